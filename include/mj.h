@@ -428,6 +428,168 @@ typedef struct mj_write_kv_args {
 
 MJ_API int mj_write_kv(const mj_write_kv_args* args, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Rotary positions. Frequency i of a token at position n turns a pair of
+ * channels by a = n * inv_freq[i]:
+ *   (x0, x1) -> scale * (x0 cos a - x1 sin a,  x1 cos a + x0 sin a)
+ * in float32, a itself in fixed point: turns[i] = inv_freq[i] / (2 pi) as a
+ * fraction of 2^64 (mj_rope_turns), n * turns[i] modulo 2^64 the angle modulo a
+ * full turn, exact to n * 2^-65 turns for any int64 n.
+ * The runner page takes queries and keys already rotated (T5DecodeRunner.run);
+ * these calls are the step before it.
+ * ---------------------------------------------------------------------- */
+typedef struct mj_rope {
+  const int64_t* positions;  /* device; token t on axis x at positions[x*axis_stride + t] */
+  int64_t axis_stride;       /* elements (unused with one axis) */
+  int num_axes;              /* 1 to 4: e.g. time, height and width of image or video tokens */
+  const uint64_t* turns;     /* device [rot_dim/2] (mj_rope_turns) */
+  const uint8_t* freq_axis;  /* device [rot_dim/2]: the axis whose position turns frequency i (an entry past
+                                the last axis means the last); may be null with one axis */
+  int rot_dim;               /* channels rotated, from channel 0: a multiple of 16, at least 16; the rest pass */
+  int interleaved;           /* 0: pairs (i, i + rot_dim/2); 1: pairs (2i, 2i + 1) */
+  float scale;               /* of cosine and sine (1 where the scheme has none) */
+} mj_rope;
+
+/* Host: turns[i] = inv_freq[i] / (2 pi) * 2^64 modulo 2^64, rounded to nearest. inv_freq and turns are host
+ * arrays of n; a frequency that is not finite or above 2^20 in size is MJ_ERR_INVALID_ARG. */
+MJ_API int mj_rope_turns(const double* inv_freq, int n, uint64_t* turns);
+
+/* ------------------------------------------------------------------------
+ * mj_rope_write_kv — mj_write_kv with the rotation on the way: rotate the
+ * queries (to bf16) and the keys, quantize keys and values and scatter them
+ * into the paged caches, in one launch.
+ *
+ * kv: as for mj_write_kv (every cache format, head size 128 or 256), except
+ * that key is rotated in float32 before its one rounding, to the cache format.
+ * q may be q_out (rotated in place, with the same strides); they must not
+ * overlap otherwise. h_q = 0: no queries. A padding token (negative slot) has
+ * its queries rotated too.
+ * Alignment: q and q_out 16 bytes, their strides multiples of 8 elements.
+ * The launch may begin before the preceding kernel on `stream` has finished
+ * and waits for it before it reads.
+ * ---------------------------------------------------------------------- */
+typedef struct mj_rope_write_kv_args {
+  mj_rope rope;               /* rot_dim <= kv.d */
+  int h_q;
+  const void* q;              /* device bf16; (t, h, c) at q[t*q_tok_stride + h*q_head_stride + c] */
+  int64_t q_tok_stride, q_head_stride;
+  void* q_out;                /* device bf16, likewise */
+  int64_t q_out_tok_stride, q_out_head_stride;
+  mj_write_kv_args kv;
+} mj_rope_write_kv_args;
+
+MJ_API int mj_rope_write_kv(const mj_rope_write_kv_args* args, void* stream);
+
+/* ------------------------------------------------------------------------
+ * The latent cache: one row a token, shared by all heads (latent attention,
+ * absorbed form). A row is MJ_LATENT_ROW_BYTES e4m3 codes: the latent vector
+ * (512 channels, value = code * scale[0]) and the rotated key part (64
+ * channels, value = code * scale[1]). Pages of 16, 32, 64 or 128 tokens.
+ * ---------------------------------------------------------------------- */
+#define MJ_LATENT_DIM 512
+#define MJ_LATENT_ROPE_DIM 64
+#define MJ_LATENT_ROW_BYTES (MJ_LATENT_DIM + MJ_LATENT_ROPE_DIM)
+
+/* mj_latent_write — append: rotate the queries' 64-channel parts (to bf16) and
+ * the keys', quantize latent and key part (x / scale, IEEE float32, to nearest
+ * even, saturating at 448) and write one row a token at slot_mapping. Slots,
+ * padding tokens, status, in-place queries and the launch as for
+ * mj_rope_write_kv. q_out is usually the last 64 channels of the absorbed
+ * query that mj_latent_attention reads.
+ * Alignment: latent, k_pe, q_pe, q_out and cache 16 bytes; element strides
+ * multiples of 8, byte strides of 16. */
+typedef struct mj_latent_write_args {
+  mj_rope rope;               /* rot_dim <= 64 */
+  int num_tokens;             /* 0: nothing to do */
+  int h;                      /* query heads; 0: no queries */
+  const void* q_pe;           /* device bf16; (t, h, c) at q_pe[t*q_tok_stride + h*q_head_stride + c], 64 channels */
+  int64_t q_tok_stride, q_head_stride;
+  void* q_out;                /* device bf16, likewise */
+  int64_t q_out_tok_stride, q_out_head_stride;
+  const void* latent;         /* device bf16; (t, c) at latent[t*latent_tok_stride + c], 512 channels */
+  int64_t latent_tok_stride;
+  const void* k_pe;           /* device bf16; (t, c) at k_pe[t*k_pe_tok_stride + c], 64 channels */
+  int64_t k_pe_tok_stride;
+  const int64_t* slot_mapping;  /* device [num_tokens] */
+  int page_size;
+  int64_t num_pages;
+  void* cache;                /* token j of page p at cache + p*stride_page + j*stride_token */
+  int64_t stride_page, stride_token;  /* bytes */
+  const float* scale;         /* device [2]: latent, key part */
+  uint32_t* status;           /* nullable device word: bit 1 for a slot past the pool (skipped) */
+} mj_latent_write_args;
+
+MJ_API int mj_latent_write(const mj_latent_write_args* args, void* stream);
+
+/* The latent plan. mj_latent_attention runs one CTA per slot and tile of 16, 32
+ * or 64 query rows (query tokens x heads); mj_latent_slots is how many slots
+ * fill sm_count SMs. mj_latent_plan cuts the requests' 128-token tiles, in
+ * order, into one contiguous piece a slot of equal cost; a request that spans
+ * slots is split and its partials joined. The plan is one buffer of
+ * mj_latent_plan_size() int32 words (a multiple of 4) with a layout fixed by
+ * slots and max_num_seqs: copy it to the device with
+ * mj_plan_upload(plan_host, NULL, plan_dev, NULL, words / 4, 0, stream).
+ * Lengths are exact or an upper bound (margin: tokens added to each that is not
+ * 0); the kernels mask by the lengths in device memory. */
+MJ_API int mj_latent_slots(int sm_count, int q_len, int h);
+MJ_API int mj_latent_plan_size(int slots, int max_num_seqs, size_t* words);
+MJ_API int mj_latent_plan(const int32_t* seq_lens_host, int num_seqs, int max_num_seqs, int slots, int margin,
+                   int32_t* plan_host, size_t plan_words);
+
+/* Bytes of mj_latent_attention's workspace: the status header (mj_workspace_init,
+ * mj_workspace_status) and two partials a slot. */
+MJ_API int mj_latent_workspace_size(int slots, int q_len, int h, size_t* bytes);
+
+/* ------------------------------------------------------------------------
+ * mj_latent_attention — decode attention over the latent cache, absorbed form:
+ *   t[r][j] = softmax_scale * (scale[0] q[r][:512] . c[j][:512] + scale[1] q[r][512:] . c[j][512:])
+ *   out[r]  = sum_j softmax_j(t[r]) * scale[0] c[j][:512]
+ * for each row r (query token, head) of each request, over its seq_lens[b]
+ * cached tokens, through the block table. Requests with seq_lens[b] == 0 are
+ * padding: nothing is written for them. A causal row that sees no key writes 0
+ * (LSE -inf). Two launches: the attention and the join of split requests.
+ *
+ * Accuracy: queries and softmax weights enter the tensor cores as two 8-bit
+ * terms each: a query value within max(2^-8 |q|, 2^-19 of its row's largest),
+ * a weight within 2^-7 of itself (0.15% rms) down to 24 binades below its
+ * row's largest, below that 0; sums in float32. A NaN code of a cached token
+ * reaches every row of its request, also one whose causal limit hides it.
+ * Status bits (workspace): as mj_workspace_status lists them.
+ * Two calls that may run at once (other streams, two captured graphs) need a
+ * workspace each. The first call of each row tile on a device raises a kernel's
+ * shared-memory limit: make it before capturing.
+ * Alignment: q, cache, block_table, seq_lens, plan, out and workspace 16 bytes.
+ * ---------------------------------------------------------------------- */
+typedef struct mj_latent_args {
+  int num_seqs, max_num_seqs;  /* requests; the plan's max_num_seqs */
+  int q_len, h;                /* query tokens a request; heads */
+  int causal;                  /* 1: query token t sees keys j <= seq_len - q_len + t; 0: all */
+  float softmax_scale;
+  const void* q;               /* device bf16; (b*q_len + t, h, c) at q[..*q_tok_stride + h*q_head_stride + c], 576
+                                  channels: 512 absorbed, 64 rotated */
+  int64_t q_tok_stride, q_head_stride;  /* elements, multiples of 8 */
+  const void* cache;
+  int64_t stride_page, stride_token;    /* bytes, multiples of 16, at least 576 */
+  int page_size;
+  int64_t num_pages;
+  const float* descale;        /* device [2]: scale[0], scale[1] */
+  const int32_t* block_table;  /* device; page of token j of request b: block_table[b*block_table_stride + j/page_size] */
+  int64_t block_table_stride;  /* elements between requests */
+  int64_t block_table_len;     /* entries a request has: a token past them is a bad page */
+  const int32_t* seq_lens;     /* device [num_seqs] */
+  const int32_t* plan;         /* device, mj_latent_plan */
+  int slots;
+  void* out;                   /* device bf16 or fp16 (out_dtype); 512 channels */
+  int64_t out_tok_stride, out_head_stride;  /* elements, multiples of 8 */
+  int out_dtype;               /* mj_out_dtype */
+  float* lse;                  /* nullable device [num_seqs][q_len*h]: natural log of the sum of exp */
+  void* workspace;
+  size_t workspace_bytes;
+  int evict_first;             /* 1: cache loads are evicted first from L2 (only with one row tile) */
+} mj_latent_args;
+
+MJ_API int mj_latent_attention(const mj_latent_args* args, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -51,9 +51,16 @@ EXPORTS = (
     "mj_quantize_q", "mj_workspace_size", "mj_workspace_init", "mj_workspace_status",
     "mj_decode_attention", "mj_merge_lse", "mj_decode_attention_noalloc", "mj_noalloc_status", "mj_write_kv",
     "mj_plan_upload", "mj_decode_kernel",
+    "mj_rope_turns", "mj_rope_write_kv", "mj_latent_write", "mj_latent_slots", "mj_latent_plan_size",
+    "mj_latent_plan", "mj_latent_workspace_size", "mj_latent_attention",
 )
 
 NOALLOC_SCRATCH_BYTES = 16 << 20
+
+# a row of the latent cache: latent channels, then the rotated key part
+LATENT_DIM = 512
+LATENT_ROPE_DIM = 64
+LATENT_ROW = LATENT_DIM + LATENT_ROPE_DIM
 
 
 class MjError(RuntimeError):
@@ -108,6 +115,60 @@ class mj_write_kv_args(ctypes.Structure):
     ]
 
 
+class mj_rope(ctypes.Structure):
+    """ctypes mirror of ``struct mj_rope`` (include/mj.h)."""
+
+    _fields_ = [
+        ("positions", ctypes.c_void_p), ("axis_stride", ctypes.c_int64), ("num_axes", ctypes.c_int),
+        ("turns", ctypes.c_void_p), ("freq_axis", ctypes.c_void_p), ("rot_dim", ctypes.c_int),
+        ("interleaved", ctypes.c_int), ("scale", ctypes.c_float),
+    ]
+
+
+class mj_rope_write_kv_args(ctypes.Structure):
+    """ctypes mirror of ``struct mj_rope_write_kv_args`` (include/mj.h)."""
+
+    _fields_ = [
+        ("rope", mj_rope), ("h_q", ctypes.c_int),
+        ("q", ctypes.c_void_p), ("q_tok_stride", ctypes.c_int64), ("q_head_stride", ctypes.c_int64),
+        ("q_out", ctypes.c_void_p), ("q_out_tok_stride", ctypes.c_int64), ("q_out_head_stride", ctypes.c_int64),
+        ("kv", mj_write_kv_args),
+    ]
+
+
+class mj_latent_write_args(ctypes.Structure):
+    """ctypes mirror of ``struct mj_latent_write_args`` (include/mj.h)."""
+
+    _fields_ = [
+        ("rope", mj_rope), ("num_tokens", ctypes.c_int), ("h", ctypes.c_int),
+        ("q_pe", ctypes.c_void_p), ("q_tok_stride", ctypes.c_int64), ("q_head_stride", ctypes.c_int64),
+        ("q_out", ctypes.c_void_p), ("q_out_tok_stride", ctypes.c_int64), ("q_out_head_stride", ctypes.c_int64),
+        ("latent", ctypes.c_void_p), ("latent_tok_stride", ctypes.c_int64),
+        ("k_pe", ctypes.c_void_p), ("k_pe_tok_stride", ctypes.c_int64),
+        ("slot_mapping", ctypes.c_void_p), ("page_size", ctypes.c_int), ("num_pages", ctypes.c_int64),
+        ("cache", ctypes.c_void_p), ("stride_page", ctypes.c_int64), ("stride_token", ctypes.c_int64),
+        ("scale", ctypes.c_void_p), ("status", ctypes.c_void_p),
+    ]
+
+
+class mj_latent_args(ctypes.Structure):
+    """ctypes mirror of ``struct mj_latent_args`` (include/mj.h)."""
+
+    _fields_ = [
+        ("num_seqs", ctypes.c_int), ("max_num_seqs", ctypes.c_int), ("q_len", ctypes.c_int), ("h", ctypes.c_int),
+        ("causal", ctypes.c_int), ("softmax_scale", ctypes.c_float),
+        ("q", ctypes.c_void_p), ("q_tok_stride", ctypes.c_int64), ("q_head_stride", ctypes.c_int64),
+        ("cache", ctypes.c_void_p), ("stride_page", ctypes.c_int64), ("stride_token", ctypes.c_int64),
+        ("page_size", ctypes.c_int), ("num_pages", ctypes.c_int64), ("descale", ctypes.c_void_p),
+        ("block_table", ctypes.c_void_p), ("block_table_stride", ctypes.c_int64), ("block_table_len", ctypes.c_int64),
+        ("seq_lens", ctypes.c_void_p),
+        ("plan", ctypes.c_void_p), ("slots", ctypes.c_int),
+        ("out", ctypes.c_void_p), ("out_tok_stride", ctypes.c_int64), ("out_head_stride", ctypes.c_int64),
+        ("out_dtype", ctypes.c_int), ("lse", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t), ("evict_first", ctypes.c_int),
+    ]
+
+
 _lib = None
 
 
@@ -139,6 +200,14 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.mj_plan_upload.argtypes = [vp, vp, vp, vp, i32, i32, vp]
     lib.mj_decode_kernel.argtypes = [ctypes.POINTER(mj_decode_args), ctypes.POINTER(ctypes.c_int)]
     lib.mj_write_kv.argtypes = [ctypes.POINTER(mj_write_kv_args), vp]
+    lib.mj_rope_turns.argtypes = [vp, i32, vp]
+    lib.mj_rope_write_kv.argtypes = [ctypes.POINTER(mj_rope_write_kv_args), vp]
+    lib.mj_latent_write.argtypes = [ctypes.POINTER(mj_latent_write_args), vp]
+    lib.mj_latent_slots.argtypes = [i32, i32, i32]
+    lib.mj_latent_plan_size.argtypes = [i32, i32, ctypes.POINTER(sz)]
+    lib.mj_latent_plan.argtypes = [vp, i32, i32, i32, i32, vp, sz]
+    lib.mj_latent_workspace_size.argtypes = [i32, i32, i32, ctypes.POINTER(sz)]
+    lib.mj_latent_attention.argtypes = [ctypes.POINTER(mj_latent_args), vp]
     _lib = lib
     return lib
 
@@ -335,4 +404,80 @@ def mj_write_kv(key, value, slot_mapping, k_cache, v_cache, kv_strides, page_siz
     _check("mj_write_kv", load_library().mj_write_kv(ctypes.byref(a), _stream(stream)))
 
 
-from .step import DecodeStep  # noqa: E402,F401
+def mj_rope_turns(inv_freq):
+    """The rotation's fixed-point frequencies: a CPU int64 tensor (the bits of
+    the C call's uint64) of ``inv_freq``'s length. ``inv_freq``: float64 values
+    (CPU tensor, numpy array or sequence), radians per position."""
+    import numpy as np
+    import torch
+
+    f = np.ascontiguousarray(np.asarray(inv_freq, dtype=np.float64).reshape(-1))
+    turns = np.zeros(f.size, dtype=np.uint64)
+    _check("mj_rope_turns", load_library().mj_rope_turns(f.ctypes.data, f.size, turns.ctypes.data))
+    return torch.from_numpy(turns.view(np.int64))
+
+
+def _on_device(args):
+    """Refuse a launch on another device than the one the tensors of ``args``
+    live on (the library launches on the current device)."""
+    import torch
+
+    dev = getattr(args, "device_index", None)
+    if dev is not None and dev != torch.cuda.current_device():
+        raise ValueError(f"the arguments' tensors are on cuda:{dev}, the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+
+
+def mj_rope_write_kv(args: mj_rope_write_kv_args, stream=None):
+    """Rotate queries and keys, append keys and values (:func:`rope_write_args` builds ``args``)."""
+    _on_device(args)
+    _check("mj_rope_write_kv", load_library().mj_rope_write_kv(ctypes.byref(args), _stream(stream)))
+
+
+def mj_latent_write(args: mj_latent_write_args, stream=None):
+    """Append latent rows and rotate the queries' part (:func:`latent_write_args` builds ``args``)."""
+    _on_device(args)
+    _check("mj_latent_write", load_library().mj_latent_write(ctypes.byref(args), _stream(stream)))
+
+
+def mj_latent_slots(sm_count: int, q_len: int, h: int) -> int:
+    return load_library().mj_latent_slots(int(sm_count), int(q_len), int(h))
+
+
+def mj_latent_plan_size(slots: int, max_num_seqs: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check("mj_latent_plan_size", load_library().mj_latent_plan_size(slots, max_num_seqs, ctypes.byref(n)))
+    return n.value
+
+
+def mj_latent_plan(seq_lens_host, num_seqs: int, max_num_seqs: int, slots: int, margin: int = 0, plan_out=None):
+    """Host plan of mj_latent_attention. ``plan_out``: an int32 host buffer
+    (numpy or a pinned CPU tensor) of ``mj_latent_plan_size`` words to write
+    into; otherwise a numpy array is returned."""
+    import numpy as np
+
+    lens = np.ascontiguousarray(np.asarray(seq_lens_host, dtype=np.int32).reshape(-1)[:num_seqs])
+    if lens.size != num_seqs:
+        raise ValueError(f"seq_lens_host holds {lens.size} lengths, num_seqs is {num_seqs}")
+    words = mj_latent_plan_size(slots, max_num_seqs)
+    if plan_out is None:
+        plan_out = np.zeros(words, dtype=np.int32)
+    addr = _host_int32(plan_out, words, "plan_out")
+    _check("mj_latent_plan", load_library().mj_latent_plan(lens.ctypes.data if num_seqs else None, num_seqs, max_num_seqs,
+                                                           slots, margin, addr, words))
+    return plan_out
+
+
+def mj_latent_workspace_size(slots: int, q_len: int, h: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check("mj_latent_workspace_size", load_library().mj_latent_workspace_size(slots, q_len, h, ctypes.byref(n)))
+    return n.value
+
+
+def mj_latent_attention(args: mj_latent_args, stream=None):
+    """Attention over the latent cache (:meth:`LatentStep.args` builds ``args``)."""
+    _on_device(args)
+    _check("mj_latent_attention", load_library().mj_latent_attention(ctypes.byref(args), _stream(stream)))
+
+
+from .step import DecodeStep, LatentStep, PagedLatent, latent_write_args, rope_write_args  # noqa: E402,F401

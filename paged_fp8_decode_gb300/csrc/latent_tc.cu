@@ -1,0 +1,781 @@
+// mj_latent_attention: decode attention over a paged cache of latent rows
+// (512 latent and 64 rotary e4m3 codes a token), in the absorbed form. All
+// query heads of a request read the same key row, and the row's first 512
+// channels are the value:
+//
+//   t[r][j] = softmax_scale (s0 q[r][:512] . c[j] + s1 q[r][512:] . c'[j])
+//   out[r]  = sum_j softmax_j(t[r]) s0 c[j]
+//
+// One persistent CTA per (plan slot, row tile): it runs through its slot's
+// work rows (request, tile range), so that every CTA streams the same number
+// of tiles whatever the lengths. The rows of a request (query tokens x heads)
+// are tiled by NR = 16, 32 or 64. Keys are the M = 128 side of both products,
+// so a few rows still fill the tensor core, and a cache byte loaded once
+// serves both:
+//
+//   S^T[key][row]  = K[key][:576] . Q[row][:576]    A = the tile (K-major),  B = Q
+//   O^T[ch][row]  += C^T[ch][key] . P^T[key][row]   A = the tile (MN-major), B = P
+//
+// kind::f8f6f4 multiplies 8-bit floats, so the bf16 queries and the softmax
+// weights enter as two terms each. A query row is scaled to amax = 448 and
+// split into hi = e4m3(x) and lo = e4m3(x - hi) (within 2^-8 of x, or 2^-19 of
+// the row's amax): two rows of the Q tile, their products added when S is
+// read. A weight p = 2^(t - m_ref + 7) is split into hi = e4m3(p) and
+// lo = e5m2(p - hi) (within 2^-7 of p and 0.15% rms, about bf16's own; e5m2
+// reaches down to 2^-17, so weights down to 24 binades below the row's max
+// count), two products into one accumulator. The row sums add the p
+// themselves in float32.
+//
+// Warps: 0 the TMA producer, 1 the MMA issuer, 4.. one or two softmax
+// warpgroups (thread x of a group: key x of S, channel x of each of the four
+// 128-channel blocks of O; a group owns RW = NR / groups rows).
+//
+// Shared memory: a ring of latent sub-tiles (128 keys x 128 channels, 128-byte
+// swizzled as tcgen05.mma reads them) and of rotary sub-tiles (128 keys x 64
+// channels, 64-byte swizzled); a latent entry is released when the PV product
+// of its channels is done, a rotary one after QK.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <atomic>
+#include <climits>
+
+#include "mj_device.cuh"
+#include "mj_internal.h"
+#include "tc_ptx.cuh"
+
+namespace mj {
+
+namespace {
+
+constexpr int kSub = 16384;       // latent sub-tile: 128 keys x 128 bytes
+constexpr int kRopeSub = 8192;    // rotary sub-tile: 128 keys x 64 bytes
+constexpr int kRow = MJ_LATENT_ROW_BYTES;
+constexpr int kLat = MJ_LATENT_DIM;
+constexpr uint64_t kWaitLimitNs = 2000000000ull;
+constexpr uint64_t kDrainLimitNs = 100000000ull;
+constexpr int kMaxDynSmem = 227 * 1024;
+
+// P is scaled so that the row's reference max has weight 2^7; the reference
+// moves once a tile's max exceeds it by more than kTau, so p <= 2^8.5 < 448.
+constexpr float kC0 = 7.f, kTau = 1.5f;
+
+template <int NR>
+struct Cfg {
+  static constexpr int kGroups = NR == 16 ? 1 : 2;  // softmax warpgroups
+  static constexpr int kRw = NR / kGroups;          // rows of a group
+  static constexpr int kThreads = 128 + 128 * kGroups;
+  static constexpr int kRing = NR == 64 ? 8 : (NR == 32 ? 9 : 11);  // latent entries
+  static constexpr int kRopeRing = NR == 64 ? 1 : 2;
+  static constexpr int kPBufs = NR == 64 ? 1 : 2;
+  static constexpr int kPBytes = 2 * NR * 128;  // hi and lo
+  static constexpr int kQSub = 2 * NR * 128;    // hi and lo rows of one 128-channel sub-tile
+  static constexpr int kQBytes = 4 * kQSub + 2 * NR * 64;
+  static constexpr int kOffRope = kRing * kSub;
+  static constexpr int kOffQ = kOffRope + kRopeRing * kRopeSub;
+  static constexpr int kOffP = kOffQ + kQBytes;
+  static constexpr int kOffCtrl = kOffP + kPBufs * kPBytes;
+  static constexpr int kSCols = 2 * NR;           // hi and lo columns of one S buffer
+  static constexpr int kCols = 2 * kSCols + 4 * NR;  // two S buffers, four O blocks
+  static constexpr uint32_t kTmemCols = kCols <= 128 ? 128 : (kCols <= 256 ? 256 : 512);
+};
+
+template <int NR>
+struct Ctrl {
+  uint64_t full[12], empty[12];
+  uint64_t rfull[2], rempty[2];
+  uint64_t s_full[2], p_full[2], o_full[2];
+  uint64_t q_ready;
+  uint64_t bound_bar[2][2];  // [group][exchange & 1]: the group's warps have posted their bounds
+  uint64_t row_bar[2];       // ... their row maxima
+  uint64_t sum_bar[2];       // ... their row sums
+  uint64_t drain;
+  uint32_t tmem_base;
+  int abort;
+  alignas(16) float bound[2][2][4];
+  alignas(16) float red[2][4][NR == 64 ? 32 : 16];  // per warp: row maxima, at the end row sums
+  alignas(16) float scale[NR];  // logit (log2 units) per unit of S
+  alignas(16) float c8[NR];     // kC0 - m_ref
+  alignas(16) float alpha[NR];  // rescale factors of the current tile
+  alignas(16) float shift[NR];  // the reference's move
+  alignas(16) int lim[NR];      // last visible key
+};
+
+template <int NR>
+constexpr int smem_bytes() {
+  return Cfg<NR>::kOffCtrl + int(sizeof(Ctrl<NR>));
+}
+static_assert(smem_bytes<64>() <= kMaxDynSmem && smem_bytes<32>() <= kMaxDynSmem && smem_bytes<16>() <= kMaxDynSmem,
+              "shared memory");
+
+// Reduce N per-lane values over the warp's lanes: row r ends up in lanes
+// r * (32 / N) .. + 32 / N - 1 (halve the rows a lane keeps, exchange the rest).
+template <int N, bool MAX>
+__device__ __forceinline__ float reduce_rows(float (&v)[N], int lane) {
+#pragma unroll
+  for (int c = N, m = 16; c > 1; c >>= 1, m >>= 1) {
+    const bool upper = (lane & m) != 0;
+#pragma unroll
+    for (int j = 0; j < c / 2; ++j) {
+      const float send = upper ? v[j] : v[c / 2 + j];
+      const float keep = upper ? v[c / 2 + j] : v[j];
+      const float recv = __shfl_xor_sync(0xFFFFFFFFu, send, m);
+      v[j] = MAX ? fmaxf(keep, recv) : keep + recv;
+    }
+  }
+  float r = v[0];
+#pragma unroll
+  for (int m = 16 / N; m > 0; m >>= 1) {
+    const float o = __shfl_xor_sync(0xFFFFFFFFu, r, m);
+    r = MAX ? fmaxf(r, o) : r + o;
+  }
+  return r;
+}
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1, int c2,
+                                            uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar), "l"(policy)
+      : "memory");
+}
+
+constexpr uint32_t kSwizzle64B = 4;      // shared-memory descriptor, bits 61-63
+constexpr uint32_t kFormatBE5m2 = 1u << 10;  // instruction descriptor: B holds e5m2 codes
+
+// One work row: keys [tb * 128, min(te * 128, L)) of request b.
+struct Work {
+  int b, part, L, ntiles;
+  int64_t k0, k1;
+};
+
+__device__ __forceinline__ Work load_work(const LatentParams& p, int row) {
+  const int4 w = reinterpret_cast<const int4*>(p.work)[row];
+  Work k;
+  k.b = w.x;
+  k.part = w.w;
+  k.L = w.x >= 0 && w.x < p.num_seqs ? p.seq_lens[w.x] : 0;
+  k.k0 = int64_t(w.y) * kKvTile;
+  k.k1 = min(int64_t(w.z) * kKvTile, int64_t(k.L));
+  k.ntiles = w.y >= 0 && k.k1 > k.k0 && w.w < 2 * p.slots ? int((k.k1 - k.k0 + kKvTile - 1) / kKvTile) : 0;
+  return k;
+}
+
+template <int NR>
+__global__ void __launch_bounds__(Cfg<NR>::kThreads, 1)
+    latent_kernel(const __grid_constant__ CUtensorMap tmap_lat, const __grid_constant__ CUtensorMap tmap_rope,
+                  LatentParams p) {
+  using C = Cfg<NR>;
+  constexpr int RW = C::kRw, G = C::kGroups;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  Ctrl<NR>& ctl = *reinterpret_cast<Ctrl<NR>*>(smem + C::kOffCtrl);
+  const uint32_t base = tc::smem_u32(smem);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (base & 1023u) {  // the swizzled layouts need it; a block without static shared memory starts so
+    if (tid == 0) atomicOr(p.status, kStatusBadPlan);
+    return;
+  }
+
+  if (tid == 0) {
+    for (int s = 0; s < C::kRing; ++s) {
+      tc::mbar_init(tc::smem_u32(&ctl.full[s]), 1);
+      tc::mbar_init(tc::smem_u32(&ctl.empty[s]), 1);
+    }
+    for (int s = 0; s < C::kRopeRing; ++s) {
+      tc::mbar_init(tc::smem_u32(&ctl.rfull[s]), 1);
+      tc::mbar_init(tc::smem_u32(&ctl.rempty[s]), 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      tc::mbar_init(tc::smem_u32(&ctl.s_full[s]), 1);
+      tc::mbar_init(tc::smem_u32(&ctl.p_full[s]), 128 * G);
+      tc::mbar_init(tc::smem_u32(&ctl.o_full[s]), 1);
+      for (int x = 0; x < 2; ++x) tc::mbar_init(tc::smem_u32(&ctl.bound_bar[s][x]), 4);
+      tc::mbar_init(tc::smem_u32(&ctl.row_bar[s]), 4);
+      tc::mbar_init(tc::smem_u32(&ctl.sum_bar[s]), 4);
+    }
+    tc::mbar_init(tc::smem_u32(&ctl.q_ready), 128 * G);
+    tc::mbar_init(tc::smem_u32(&ctl.drain), 1);
+    ctl.abort = 0;
+    tc::fence_mbar_init();
+  }
+  if (warp == 0 && lane == 0) {
+    tc::prefetch_tmap(&tmap_lat);
+    tc::prefetch_tmap(&tmap_rope);
+  }
+  if (warp == 1) {
+    tc::tmem_alloc(tc::smem_u32(&ctl.tmem_base), C::kTmemCols);
+    tc::tmem_relinquish();
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tmem = ctl.tmem_base;
+  volatile int* abort = &ctl.abort;
+
+  // programmatic dependent launch: the set-up above reads nothing that the
+  // preceding kernel on the stream may write; everything below may
+  tc::grid_dependency_wait();
+
+  const int slot = int(blockIdx.x) / p.n_row_tiles;
+  const int r0 = (int(blockIdx.x) % p.n_row_tiles) * NR;
+  const int nr = min(NR, p.n_q - r0);  // real rows of this tile
+  const int w_begin = max(0, p.cta_off[slot]), w_end = min(p.cta_off[slot + 1], p.max_work);
+  const uint32_t tO = tmem + uint32_t(2 * C::kSCols);
+
+  if (warp == 0) {
+    // ======================= TMA producer =====================================
+    const uint64_t pol = p.evict_first ? tc::l2_policy_evict_first() : tc::l2_policy_evict_normal();
+    const int ps = p.page_size, ppt = kKvTile / ps;
+    int u = 0, ur = 0;  // latent and rotary sub-tiles so far
+    bool ok = true;
+    for (int row = w_begin; row < w_end && ok; ++row) {
+      const Work w = load_work(p, row);
+      const int64_t first_page = w.k0 / ps, npages = (w.k1 + ps - 1) / ps - first_page;
+      const int32_t* bt = p.block_table + int64_t(w.b) * p.bt_stride + first_page;
+      int64_t batch = -1;
+      int entry = -1;
+      for (int i = 0; i < w.ntiles && ok; ++i) {
+        const int nvalid = int(min(int64_t(ppt), npages - int64_t(i) * ppt));
+        const int64_t e0 = int64_t(i) * ppt;
+        if (batch < 0 || e0 + nvalid > batch + 32) {
+          batch = e0;
+          entry = e0 + lane < npages && first_page + e0 + lane < p.bt_len ? bt[e0 + lane] : -1;
+        }
+        const int pg = __shfl_sync(0xFFFFFFFFu, entry, int(e0 - batch) + (lane & 7));
+        if (lane < nvalid && (pg < 0 || int64_t(pg) >= p.num_pages)) atomicOr(p.status, kStatusBadPage);
+#pragma unroll 1
+        for (int j = 0; j < 5; ++j) {
+          const bool rope = j == 4;
+          const int s = rope ? ur % C::kRopeRing : u % C::kRing;
+          const uint32_t round = uint32_t(rope ? ur / C::kRopeRing : u / C::kRing);
+          const uint32_t full = tc::smem_u32(rope ? &ctl.rfull[s] : &ctl.full[s]);
+          const uint32_t empty = tc::smem_u32(rope ? &ctl.rempty[s] : &ctl.empty[s]);
+          const uint32_t row_b = rope ? 64u : 128u;
+          if (lane == 0) {
+            ok = tc::mbar_wait(empty, (round & 1u) ^ 1u, abort, kWaitLimitNs);
+            if (ok) tc::mbar_arrive_expect_tx(full, uint32_t(nvalid * ps) * row_b);
+          }
+          ok = __shfl_sync(0xFFFFFFFFu, ok ? 1 : 0, 0) != 0;
+          if (!ok) break;
+          if (lane < nvalid) {
+            const uint32_t dst = base + (rope ? uint32_t(C::kOffRope + s * kRopeSub) : uint32_t(s * kSub)) +
+                                 uint32_t(lane * ps) * row_b;
+            tma_load_3d(dst, rope ? &tmap_rope : &tmap_lat, full, 128 * j, 0, pg, pol);
+          }
+          if (rope)
+            ++ur;
+          else
+            ++u;
+          __syncwarp();
+        }
+      }
+    }
+    if (!ok && lane == 0) {
+      // abort: wait (bounded) for the loads still in flight before the CTA exits
+      const uint64_t t0 = tc::globaltimer_ns();
+      for (int k = max(0, u - C::kRing); k < u; ++k)
+        while (!tc::mbar_try_wait(tc::smem_u32(&ctl.full[k % C::kRing]), uint32_t(k / C::kRing) & 1u) &&
+               tc::globaltimer_ns() - t0 < kDrainLimitNs) {
+        }
+      for (int k = max(0, ur - C::kRopeRing); k < ur; ++k)
+        while (!tc::mbar_try_wait(tc::smem_u32(&ctl.rfull[k % C::kRopeRing]), uint32_t(k / C::kRopeRing) & 1u) &&
+               tc::globaltimer_ns() - t0 < kDrainLimitNs) {
+        }
+    }
+  } else if (warp == 1) {
+    // ======================= MMA issuer ========================================
+    if (lane == 0) {
+      constexpr uint32_t idesc_qk = tc::idesc_e4m3(128, 2 * NR, false, false);
+      constexpr uint32_t idesc_pv = tc::idesc_e4m3(128, NR, true, true);
+      int u = 0, ur = 0, uv = 0;  // sub-tiles consumed by QK (latent, rotary) and by PV
+      int g0 = 0, nrow = 0;       // tiles of the rows before; rows with tiles so far
+      bool ok = true;
+      for (int row = w_begin; row < w_end && ok; ++row) {
+        const Work w = load_work(p, row);
+        if (w.ntiles == 0) continue;
+        ok = tc::mbar_wait(tc::smem_u32(&ctl.q_ready), uint32_t(nrow) & 1u, abort, kWaitLimitNs);
+        ++nrow;
+        int nq = 0, jq = 0, np = 0;
+        uint64_t t_idle = 0;
+        while (ok && np < w.ntiles) {
+          bool progressed = false;
+          if (nq < w.ntiles && nq <= np + 1) {
+            // QK of tile nq, sub-tile by sub-tile as they land (the S buffer is
+            // free: the softmax read tile nq - 2 before it released P of it)
+            const uint32_t d = tmem + uint32_t(((g0 + nq) & 1) * C::kSCols);
+            while (jq < 4 && tc::mbar_test_wait(tc::smem_u32(&ctl.full[u % C::kRing]), uint32_t(u / C::kRing) & 1u)) {
+              tc::tc_fence_after();
+              const uint64_t kd = tc::smem_desc(base + uint32_t((u % C::kRing) * kSub), 16, 1024, tc::kSwizzle128B);
+              const uint64_t qd = tc::smem_desc(base + uint32_t(C::kOffQ + jq * C::kQSub), 16, 1024, tc::kSwizzle128B);
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                tc::umma_f8f6f4(d, kd + uint64_t(2 * k), qd + uint64_t(2 * k), idesc_qk, jq > 0 || k > 0);
+              ++u;
+              ++jq;
+              progressed = true;
+            }
+            if (jq == 4 &&
+                tc::mbar_test_wait(tc::smem_u32(&ctl.rfull[ur % C::kRopeRing]), uint32_t(ur / C::kRopeRing) & 1u)) {
+              tc::tc_fence_after();
+              const int s = ur % C::kRopeRing;
+              const uint64_t kd = tc::smem_desc(base + uint32_t(C::kOffRope + s * kRopeSub), 16, 512, kSwizzle64B);
+              const uint64_t qd = tc::smem_desc(base + uint32_t(C::kOffQ + 4 * C::kQSub), 16, 512, kSwizzle64B);
+#pragma unroll
+              for (int k = 0; k < 2; ++k)
+                tc::umma_f8f6f4(d, kd + uint64_t(2 * k), qd + uint64_t(2 * k), idesc_qk, 1);
+              tc::umma_commit(tc::smem_u32(&ctl.s_full[(g0 + nq) & 1]));
+              tc::umma_commit(tc::smem_u32(&ctl.rempty[s]));
+              ++ur;
+              ++nq;
+              jq = 0;
+              progressed = true;
+            }
+          }
+          if (np < nq) {
+            const int gi = g0 + np;
+            if (tc::mbar_test_wait(tc::smem_u32(&ctl.p_full[gi & 1]), uint32_t(gi >> 1) & 1u)) {
+              tc::tc_fence_after();
+              // P, MN-major without swizzle: 8-key core groups 128 B apart,
+              // 16-row blocks 2 KB apart; lo after hi
+              const uint64_t pd =
+                  tc::smem_desc(base + uint32_t(C::kOffP + (gi % C::kPBufs) * C::kPBytes), 128, 2048, 0);
+#pragma unroll 1
+              for (int j = 0; j < 4; ++j) {
+                const int s = uv % C::kRing;
+                const uint64_t vd = tc::smem_desc(base + uint32_t(s * kSub), kSub, 1024, tc::kSwizzle128B);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {  // 32 keys a step
+                  tc::umma_f8f6f4(tO + uint32_t(j * NR), vd + uint64_t(256 * k), pd + uint64_t(32 * k), idesc_pv,
+                                  np > 0 || k > 0);
+                  tc::umma_f8f6f4(tO + uint32_t(j * NR), vd + uint64_t(256 * k), pd + uint64_t(NR * 8 + 32 * k),
+                                  idesc_pv | kFormatBE5m2, 1);
+                }
+                tc::umma_commit(tc::smem_u32(&ctl.empty[s]));
+                ++uv;
+              }
+              tc::umma_commit(tc::smem_u32(&ctl.o_full[gi & 1]));
+              ++np;
+              progressed = true;
+            }
+          }
+          if (progressed) {
+            t_idle = 0;
+          } else {
+            const uint64_t now = tc::globaltimer_ns();
+            if (t_idle == 0) {
+              t_idle = now;
+            } else if (now - t_idle > kWaitLimitNs || *abort) {
+              *abort = 1;
+              ok = false;
+            }
+            __nanosleep(32);
+          }
+        }
+        g0 += w.ntiles;
+      }
+      if (!ok) {
+        // abort: wait (bounded) until every MMA issued so far has completed
+        tc::umma_commit(tc::smem_u32(&ctl.drain));
+        const uint64_t t0 = tc::globaltimer_ns();
+        while (!tc::mbar_try_wait(tc::smem_u32(&ctl.drain), 0) && tc::globaltimer_ns() - t0 < kDrainLimitNs) {
+        }
+      }
+    }
+  } else if (warp >= 4) {
+    // ======================= softmax warpgroups ================================
+    const int grp = (warp - 4) >> 2, qd = warp & 3;
+    const int x = qd * 32 + lane;  // key of the tile (S), channel of a block (O)
+    const uint32_t lane_off = uint32_t(qd * 32) << 16;
+    const int rg = grp * RW;       // the group's first row in the tile
+    constexpr int kShare = 32 / RW;  // lanes that share a row after reduce_rows
+    const float ds0 = p.descale[0], ds1 = p.descale[1];
+    const float qk_log2 = p.softmax_scale * kLog2e;
+    int g0 = 0;           // tiles of the rows before
+    int xb = 0, xr = 0, xs = 0;  // bound, row and sum exchanges so far (the same in every thread of the group)
+    bool ok = true;
+    for (int row = w_begin; row < w_end && ok; ++row) {
+      const Work w = load_work(p, row);
+      if (w.ntiles == 0) {
+        // no key of this range is held any more: an empty partial
+        if (w.part >= 0 && w.part < 2 * p.slots)
+          for (int r = x; r < RW; r += 128)
+            if (rg + r < nr) p.m_part[int64_t(w.part) * p.n_q + r0 + rg + r] = -INFINITY;
+        if (w.part >= 2 * p.slots && x == 0) atomicOr(p.status, kStatusBadPlan);
+        continue;
+      }
+      // ---- Q: RW rows by 128 threads, kTpr threads a row --------------------
+      {
+        constexpr int kTpr = 128 / RW;
+        const int r = x / kTpr, part = x % kTpr;
+        const int gr = r0 + rg + r;  // row of the request
+        const bool live = rg + r < nr;
+        const int tq = live ? gr / p.h : 0, h = live ? gr - tq * p.h : 0;
+        const uint16_t* src = p.q + (int64_t(w.b) * p.q_len + tq) * p.q_ts + int64_t(h) * p.q_hs;
+        float am = 0.f;
+        if (live) {
+#pragma unroll 6
+          for (int c = part; c < kRow / 8; c += kTpr) {
+            const uint4 v = *reinterpret_cast<const uint4*>(src + c * 8);
+            const float ds = c < kLat / 8 ? ds0 : ds1;
+            const uint32_t q4[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              am = fmaxf(am, fmaxf(fabsf(__uint_as_float(q4[k] << 16) * ds), fabsf(__uint_as_float(q4[k] & 0xFFFF0000u) * ds)));
+          }
+        }
+#pragma unroll
+        for (int m = 1; m < kTpr; m <<= 1) am = fmaxf(am, __shfl_xor_sync(0xFFFFFFFFu, am, m));
+        am = fmaxf(am, 1e-30f);
+        const float inv = 448.f / am;
+#pragma unroll 3
+        for (int c = part; c < kRow / 8; c += kTpr) {
+          uint32_t hi[2] = {0u, 0u}, lo[2] = {0u, 0u};
+          if (live) {
+            const uint4 v = *reinterpret_cast<const uint4*>(src + c * 8);
+            const float f = (c < kLat / 8 ? ds0 : ds1) * inv;
+            const uint32_t q4[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float x0 = __uint_as_float(q4[k] << 16) * f, x1 = __uint_as_float(q4[k] & 0xFFFF0000u) * f;
+              const __nv_fp8x2_storage_t h2 = __nv_cvt_float2_to_fp8x2(make_float2(x0, x1), __NV_SATFINITE, __NV_E4M3);
+              const float2 hf = e4m3x2_to_float2(h2);
+              const __nv_fp8x2_storage_t l2 =
+                  __nv_cvt_float2_to_fp8x2(make_float2(x0 - hf.x, x1 - hf.y), __NV_SATFINITE, __NV_E4M3);
+              hi[k >> 1] |= uint32_t(h2) << (16 * (k & 1));
+              lo[k >> 1] |= uint32_t(l2) << (16 * (k & 1));
+            }
+          }
+          const int ch = c * 8;
+#pragma unroll
+          for (int term = 0; term < 2; ++term) {
+            const int tr = term * NR + rg + r;  // row of the Q tile
+            const uint32_t off =
+                ch < kLat ? uint32_t(C::kOffQ + (ch >> 7) * C::kQSub + tr * 128 + ((((ch & 127) >> 4) ^ (tr & 7)) << 4) + (ch & 8))
+                          : uint32_t(C::kOffQ + 4 * C::kQSub + tr * 64 + ((((ch - kLat) >> 4) ^ ((tr >> 1) & 3)) << 4) + (ch & 8));
+            *reinterpret_cast<uint2*>(smem + off) = term ? make_uint2(lo[0], lo[1]) : make_uint2(hi[0], hi[1]);
+          }
+        }
+        if (part == 0) {
+          ctl.scale[rg + r] = am * (1.f / 448.f) * qk_log2;
+          ctl.c8[rg + r] = kC0;
+          ctl.lim[rg + r] = !live ? -1 : (p.causal ? w.L - p.q_len + tq : INT_MAX);
+        }
+        tc::fence_async_smem();
+        tc::mbar_arrive(tc::smem_u32(&ctl.q_ready));
+        // the row constants are read by the whole group: any exchange below
+        // orders them; the first tile's reads come after its own wait
+      }
+      const int lim_min = p.causal ? w.L - p.q_len + r0 / p.h : INT_MAX;  // the tile's first row sees least
+      float c8_row = kC0;  // lane r < RW: row r's c8
+      float l_part[RW];
+#pragma unroll
+      for (int r = 0; r < RW; ++r) l_part[r] = 0.f;
+      bool empty_row = true;  // lane r < RW: row r has seen no key
+
+      for (int i = 0; i < w.ntiles; ++i) {
+        const int gi = g0 + i;
+        ok = tc::mbar_wait(tc::smem_u32(&ctl.s_full[gi & 1]), uint32_t(gi >> 1) & 1u, abort, kWaitLimitNs);
+        if (!ok) break;
+        tc::tc_fence_after();
+        float e[RW];
+        {
+          float lo[RW];
+          const uint32_t ts = tmem + uint32_t((gi & 1) * C::kSCols + rg) + lane_off;
+          tc::tmem_ld_cols<RW>(ts, e);
+          tc::tmem_ld_cols<RW>(ts + uint32_t(NR), lo);
+          tc::tmem_wait_ld();
+#pragma unroll
+          for (int r = 0; r < RW; ++r) e[r] += lo[r];
+        }
+        // e = t - m_ref + kC0, in log2 units; -inf where the row does not see the key
+#pragma unroll
+        for (int r = 0; r < RW; r += 4) {
+          const float4 sc = *reinterpret_cast<const float4*>(&ctl.scale[rg + r]);
+          const float4 c8 = *reinterpret_cast<const float4*>(&ctl.c8[rg + r]);
+          e[r] = fmaf(e[r], sc.x, c8.x);
+          e[r + 1] = fmaf(e[r + 1], sc.y, c8.y);
+          e[r + 2] = fmaf(e[r + 2], sc.z, c8.z);
+          e[r + 3] = fmaf(e[r + 3], sc.w, c8.w);
+        }
+        const int64_t t_end = w.k0 + int64_t(i + 1) * kKvTile;
+        const bool dead = t_end - kKvTile + x >= w.k1;  // this key is past the end
+        if (t_end > w.k1 || t_end - 1 > int64_t(lim_min)) {
+          const int key = int(t_end) - kKvTile + x;
+#pragma unroll
+          for (int r = 0; r < RW; ++r)
+            if (dead || key > ctl.lim[rg + r]) e[r] = -INFINITY;
+        }
+        bool settled = false, rescale = false;
+        if (i > 0) {
+          // one bound for all rows and keys of the group first: it holds once
+          // the references have settled, and spares the per-row maxima
+          float m = e[0];
+#pragma unroll
+          for (int r = 1; r < RW; ++r) m = fmaxf(m, e[r]);
+          m = warp_max(m);
+          if (lane == 0) ctl.bound[grp][xb & 1][qd] = m;
+          __syncwarp();
+          const uint32_t bar = tc::smem_u32(&ctl.bound_bar[grp][xb & 1]);
+          if (lane == 0) tc::mbar_arrive(bar);
+          ok = tc::mbar_wait(bar, uint32_t(xb >> 1) & 1u, abort, kWaitLimitNs);
+          if (!ok) break;
+          const float4 b = *reinterpret_cast<const float4*>(&ctl.bound[grp][xb & 1][0]);
+          settled = fmaxf(fmaxf(b.x, b.y), fmaxf(b.z, b.w)) <= kC0 + kTau;
+          ++xb;
+        }
+        if (!settled) {
+          float tmp[RW];
+#pragma unroll
+          for (int r = 0; r < RW; ++r) tmp[r] = e[r];
+          const float wm = reduce_rows<RW, true>(tmp, lane);
+          if (lane % kShare == 0) ctl.red[grp][qd][lane / kShare] = wm;
+          __syncwarp();
+          const uint32_t bar = tc::smem_u32(&ctl.row_bar[grp]);
+          if (lane == 0) tc::mbar_arrive(bar);
+          ok = tc::mbar_wait(bar, uint32_t(xr) & 1u, abort, kWaitLimitNs);
+          if (!ok) break;
+          ++xr;
+          // lane r moves row r's reference (the four warps compute and store
+          // the same values)
+          bool moved = false;
+          if (lane < RW) {
+            const float em = fmaxf(fmaxf(ctl.red[grp][0][lane], ctl.red[grp][1][lane]),
+                                   fmaxf(ctl.red[grp][2][lane], ctl.red[grp][3][lane]));
+            const float d = em - kC0;
+            moved = em != -INFINITY && (i == 0 || d > kTau);
+            empty_row = empty_row && em == -INFINITY;
+            if (moved) c8_row -= d;
+            ctl.shift[rg + lane] = moved ? d : 0.f;
+            ctl.alpha[rg + lane] = moved && i > 0 ? fast_exp2(-d) : 1.f;
+            ctl.c8[rg + lane] = c8_row;
+          }
+          rescale = __any_sync(0xFFFFFFFFu, moved) && i > 0;
+          __syncwarp();
+#pragma unroll
+          for (int r = 0; r < RW; r += 4) {
+            const float4 sh = *reinterpret_cast<const float4*>(&ctl.shift[rg + r]);
+            const float4 al = *reinterpret_cast<const float4*>(&ctl.alpha[rg + r]);
+            e[r] -= sh.x;
+            e[r + 1] -= sh.y;
+            e[r + 2] -= sh.z;
+            e[r + 3] -= sh.w;
+            l_part[r] *= al.x;
+            l_part[r + 1] *= al.y;
+            l_part[r + 2] *= al.z;
+            l_part[r + 3] *= al.w;
+          }
+        }
+        uint32_t hi[RW / 4], lo[RW / 4];
+#pragma unroll
+        for (int r = 0; r < RW; r += 2) {
+          const float p0 = fast_exp2(e[r]), p1 = fast_exp2(e[r + 1]);
+          l_part[r] += p0;
+          l_part[r + 1] += p1;
+          const __nv_fp8x2_storage_t h2 = __nv_cvt_float2_to_fp8x2(make_float2(p0, p1), __NV_SATFINITE, __NV_E4M3);
+          const float2 hf = e4m3x2_to_float2(h2);
+          const __nv_fp8x2_storage_t l2 =
+              __nv_cvt_float2_to_fp8x2(make_float2(p0 - hf.x, p1 - hf.y), __NV_SATFINITE, __NV_E5M2);
+          if ((r & 2) == 0) {
+            hi[r / 4] = uint32_t(h2);
+            lo[r / 4] = uint32_t(l2);
+          } else {
+            hi[r / 4] |= uint32_t(h2) << 16;
+            lo[r / 4] |= uint32_t(l2) << 16;
+          }
+        }
+        // the P buffer is free, and O complete up to the tile before, once
+        // that product is done
+        if (gi >= C::kPBufs) {
+          const int pi = rescale ? gi - 1 : gi - C::kPBufs;
+          ok = tc::mbar_wait(tc::smem_u32(&ctl.o_full[pi & 1]), uint32_t(pi >> 1) & 1u, abort, kWaitLimitNs);
+          if (!ok) break;
+        } else if (rescale) {
+          ok = tc::mbar_wait(tc::smem_u32(&ctl.o_full[(gi - 1) & 1]), uint32_t((gi - 1) >> 1) & 1u, abort, kWaitLimitNs);
+          if (!ok) break;
+        }
+        uint8_t* pt = smem + C::kOffP + (gi % C::kPBufs) * C::kPBytes + x * 16;
+#pragma unroll
+        for (int k = 0; k < RW / 16; ++k) {
+          const int blk = (rg / 16 + k) * 2048;
+          *reinterpret_cast<uint4*>(pt + blk) = make_uint4(hi[4 * k], hi[4 * k + 1], hi[4 * k + 2], hi[4 * k + 3]);
+          *reinterpret_cast<uint4*>(pt + NR * 128 + blk) = make_uint4(lo[4 * k], lo[4 * k + 1], lo[4 * k + 2], lo[4 * k + 3]);
+        }
+        if (dead) {
+          // value rows past the end: their weights are 0, but the bytes may be
+          // NaN codes. QK has read the tile (s_full), PV waits for p_full.
+#pragma unroll
+          for (int j = 0; j < 4 / G; ++j) {
+            const int s = (4 * gi + grp * (4 / G) + j) % C::kRing;
+            uint4* z = reinterpret_cast<uint4*>(smem + s * kSub + x * 128);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) z[k] = make_uint4(0u, 0u, 0u, 0u);
+          }
+        }
+        if (rescale) {
+          tc::tc_fence_after();
+#pragma unroll 1
+          for (int j = 0; j < 4; ++j) {
+#pragma unroll
+            for (int c = 0; c < RW; c += 16) {
+              float v[16];
+              const uint32_t at = tO + uint32_t(j * NR + rg + c) + lane_off;
+              tc::tmem_ld16(at, v);
+              tc::tmem_wait_ld();
+#pragma unroll
+              for (int k = 0; k < 16; ++k) v[k] *= ctl.alpha[rg + c + k];
+              tc::tmem_st16(at, v);
+            }
+          }
+          tc::tmem_wait_st();
+        }
+        tc::fence_async_smem();
+        tc::tc_fence_before();
+        tc::mbar_arrive(tc::smem_u32(&ctl.p_full[gi & 1]));
+      }
+      if (!ok) break;
+      g0 += w.ntiles;
+
+      // ---- epilogue of the work row --------------------------------------------
+      // (the wait: every warp has read the last tile's row maxima, whose place
+      // the sums take)
+      ok = tc::mbar_wait(tc::smem_u32(&ctl.p_full[(g0 - 1) & 1]), uint32_t((g0 - 1) >> 1) & 1u, abort, kWaitLimitNs);
+      if (!ok) break;
+      const float ws = reduce_rows<RW, false>(l_part, lane);
+      if (lane % kShare == 0) ctl.red[grp][qd][lane / kShare] = ws;
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(tc::smem_u32(&ctl.sum_bar[grp]));
+      ok = tc::mbar_wait(tc::smem_u32(&ctl.sum_bar[grp]), uint32_t(xs) & 1u, abort, kWaitLimitNs);
+      if (!ok) break;
+      ++xs;
+      if (lane < RW) {
+        const float l = (ctl.red[grp][0][lane] + ctl.red[grp][1][lane]) + (ctl.red[grp][2][lane] + ctl.red[grp][3][lane]);
+        const int gr = r0 + rg + lane;
+        ctl.alpha[rg + lane] = empty_row ? 0.f : 1.f / l;  // (the same in the four warps)
+        if (qd == 0 && rg + lane < nr) {
+          const float m = kC0 - c8_row;
+          if (w.part >= 0) {
+            p.m_part[int64_t(w.part) * p.n_q + gr] = empty_row ? -INFINITY : m;
+            p.l_part[int64_t(w.part) * p.n_q + gr] = l * (1.f / 128.f);
+          } else if (p.lse) {
+            p.lse[int64_t(w.b) * p.n_q + gr] = empty_row ? -INFINITY : (m + fast_log2(l) - kC0) * kLn2;
+          }
+        }
+      }
+      __syncwarp();
+      ok = tc::mbar_wait(tc::smem_u32(&ctl.o_full[(g0 - 1) & 1]), uint32_t((g0 - 1) >> 1) & 1u, abort, kWaitLimitNs);
+      if (!ok) break;
+      tc::tc_fence_after();
+#pragma unroll 1
+      for (int j = 0; j < 4; ++j) {
+#pragma unroll 1
+        for (int c = 0; c < RW; c += 16) {
+          float v[16];
+          tc::tmem_ld16(tO + uint32_t(j * NR + rg + c) + lane_off, v);
+          tc::tmem_wait_ld();
+          int gr = r0 + rg + c;
+          int tq = gr / p.h, h = gr - tq * p.h;
+#pragma unroll
+          for (int k = 0; k < 16; ++k, ++gr) {
+            if (rg + c + k < nr) {
+              // an empty row's accumulator may hold 0 x NaN: it is not used
+              const float il = ctl.alpha[rg + c + k];
+              const float o = il == 0.f ? 0.f : v[k] * il;
+              if (w.part >= 0)
+                p.o_part[(int64_t(w.part) * p.n_q + gr) * kLat + 128 * j + x] = o;
+              else
+                p.out[(int64_t(w.b) * p.q_len + tq) * p.out_ts + int64_t(h) * p.out_hs + 128 * j + x] =
+                    float_to_out_bits(o * ds0, p.out_f16);
+            }
+            if (++h == p.h) {
+              h = 0;
+              ++tq;
+            }
+          }
+        }
+      }
+      // all reads of O and of the row constants are done before any warp of
+      // the group stages the next row: S of it only comes after every warp's
+      // q_ready arrival, and O after every warp's p_full arrival
+      tc::tc_fence_before();
+      __syncwarp();
+    }
+  }
+
+  // ---- teardown ----------------------------------------------------------------
+  __syncthreads();
+  if (*abort && tid == 0) atomicOr(p.status, kStatusTimeout);
+  tc::tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc::tc_fence_after();
+    tc::tmem_dealloc(tmem, C::kTmemCols);
+  }
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static std::atomic<void*> fn{nullptr};
+  void* f = fn.load(std::memory_order_acquire);
+  if (!f) {
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      return nullptr;
+    fn.store(f, std::memory_order_release);
+  }
+  return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+}
+
+// 3-D byte tensor (row, token, page) of the cache; a box is `width` bytes of a page's tokens.
+bool encode_map(CUtensorMap* map, const LatentParams& p, int width, CUtensorMapSwizzle swizzle) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {cuuint64_t(kRow), cuuint64_t(p.page_size), cuuint64_t(p.num_pages)};
+  const cuuint64_t strides[2] = {cuuint64_t(p.stride_token), cuuint64_t(p.stride_page)};
+  const cuuint32_t box[3] = {cuuint32_t(width), cuuint32_t(p.page_size), 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t*>(p.cache), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int NR>
+cudaError_t launch(const CUtensorMap& ml, const CUtensorMap& mr, const LatentParams& p, cudaStream_t stream) {
+  constexpr int bytes = smem_bytes<NR>();
+  static std::atomic<bool> configured[64];  // the shared-memory limit is raised once per device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!configured[dev].load(std::memory_order_acquire)) {
+    e = cudaFuncSetAttribute(latent_kernel<NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+    configured[dev].store(true, std::memory_order_release);
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(p.slots) * unsigned(p.n_row_tiles));
+  cfg.blockDim = dim3(Cfg<NR>::kThreads);
+  cfg.dynamicSmemBytes = bytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, latent_kernel<NR>, ml, mr, p);
+}
+
+}  // namespace
+
+cudaError_t launch_latent(const LatentParams& p, cudaStream_t stream) {
+  CUtensorMap ml, mr;
+  if (!encode_map(&ml, p, 128, CU_TENSOR_MAP_SWIZZLE_128B) || !encode_map(&mr, p, 64, CU_TENSOR_MAP_SWIZZLE_64B))
+    return cudaErrorInvalidValue;
+  switch (p.row_tile) {
+    case 16: return launch<16>(ml, mr, p, stream);
+    case 32: return launch<32>(ml, mr, p, stream);
+    default: return launch<64>(ml, mr, p, stream);
+  }
+}
+
+}  // namespace mj

@@ -16,8 +16,11 @@ from dataclasses import dataclass
 import numpy as np
 import torch
 
-from . import (KV_FORMATS, MJ_IMPL_AUTO, mj_decode_args, mj_decode_attention, mj_merge_lse,
-               mj_plan_split_kv, mj_plan_upload, mj_quantize_q, mj_slots, mj_workspace_init, mj_workspace_size)
+from . import (KV_FORMATS, LATENT_DIM, LATENT_ROPE_DIM, LATENT_ROW, MJ_IMPL_AUTO, MJ_KV_E4M3, MJ_OUT_BF16, MJ_OUT_F16,
+               _check, _ptr, _stream, load_library, mj_decode_args, mj_decode_attention, mj_latent_args,
+               mj_latent_attention, mj_latent_plan, mj_latent_plan_size, mj_latent_slots, mj_latent_workspace_size,
+               mj_latent_write_args, mj_merge_lse, mj_plan_split_kv, mj_plan_upload, mj_quantize_q,
+               mj_rope_write_kv_args, mj_slots, mj_workspace_init, mj_workspace_size)
 
 
 @dataclass
@@ -171,3 +174,241 @@ def paged_kv_from_workload(w, device="cuda") -> PagedKV:
 
 def q_from_workload(w, device="cuda") -> torch.Tensor:
     return torch.from_numpy(w.q_bits.view(np.int16)).view(torch.bfloat16).to(device)
+
+
+# ----------------------------------------------------------------------------
+# the rotated cache writes
+# ----------------------------------------------------------------------------
+def _tensor(name: str, t: torch.Tensor, dtype, *shape) -> torch.Tensor:
+    """Check a tensor the library reads through a device pointer: on a GPU, of
+    the type, of the shape (None: any extent)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor: the kernels read it through a device pointer")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
+    if t.dim() != len(shape) or any(w is not None and int(n) != w for n, w in zip(t.shape, shape)):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple('*' if w is None else w for w in shape)}")
+    return t
+
+
+def _rows(name: str, t: torch.Tensor, dtype, *shape) -> torch.Tensor:
+    _tensor(name, t, dtype, *shape)
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
+        raise ValueError(f"{name}: its last dimension must be contiguous")
+    return t
+
+
+def _flat(name: str, t: torch.Tensor, dtype, *shape) -> torch.Tensor:
+    _tensor(name, t, dtype, *shape)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t
+
+
+def _hold(a, *tensors):
+    """``a`` keeps the tensors whose addresses it holds, and their one device."""
+    held = [t for t in tensors if t is not None]
+    devices = {t.device.index for t in held}
+    if len(devices) > 1:
+        raise ValueError(f"the tensors are on several devices: {sorted(devices)}")
+    a.tensors, a.device_index = held, devices.pop()
+    return a
+
+
+def _set_rope(r, positions, turns, freq_axis, interleaved: bool, scale: float, T: int, d: int):
+    axes = 1 if positions.dim() == 1 else int(positions.shape[0])
+    if positions.dim() == 1:
+        _flat("positions", positions, torch.int64, T)
+    else:
+        _rows("positions", positions, torch.int64, axes, T)
+    n = int(turns.numel())
+    _flat("turns", turns, torch.int64, n)
+    if freq_axis is not None:
+        _flat("freq_axis", freq_axis, torch.uint8, n)
+    r.positions, r.axis_stride, r.num_axes = positions.data_ptr(), positions.stride(0) if axes > 1 else 0, axes
+    r.turns, r.freq_axis = turns.data_ptr(), freq_axis.data_ptr() if freq_axis is not None else None
+    r.rot_dim, r.interleaved, r.scale = 2 * n, 1 if interleaved else 0, float(scale)
+
+
+def rope_write_args(q, key, value, positions, turns, slot_mapping, k_cache, v_cache, kv_strides, page_size: int,
+                    num_pages: int, kv_format: int, k_scale, v_scale, *, q_out=None, freq_axis=None,
+                    interleaved: bool = False, rope_scale: float = 1.0, scale_per_head: bool = False,
+                    status=None) -> mj_rope_write_kv_args:
+    """The arguments of :func:`mj_rope_write_kv`, good for as many calls as the
+    buffers keep their addresses.
+
+    ``q`` bf16 ``[T, h_q, d]`` or None (no queries) and ``q_out`` the same
+    (None: in place); ``positions`` int64 ``[T]`` or ``[axes, T]``; ``turns``
+    :func:`mj_rope_turns` of ``rot_dim / 2`` frequencies, on the device;
+    ``freq_axis`` uint8, the axis of each frequency. The rest as for
+    :func:`mj_write_kv`."""
+    T, h_k, d = (int(n) for n in key.shape)
+    _rows("key", key, torch.bfloat16, T, h_k, d)
+    _rows("value", value, torch.bfloat16, T, h_k, d)
+    _flat("slot_mapping", slot_mapping, torch.int64, T)
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        if not t.is_cuda or t.dtype != torch.uint8:
+            raise ValueError(f"{name} must be a uint8 CUDA tensor")
+    n_scale = h_k * d if kv_format != MJ_KV_E4M3 else (h_k if scale_per_head else 1)
+    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+        if not t.is_cuda or t.dtype != torch.float32 or not t.is_contiguous() or t.numel() != n_scale:
+            raise ValueError(f"{name}: {n_scale} contiguous float32 values on the GPU are required")
+    a = mj_rope_write_kv_args()
+    _set_rope(a.rope, positions, turns, freq_axis, interleaved, rope_scale, T, d)
+    if q is not None:
+        a.h_q = int(q.shape[1])
+        _rows("q", q, torch.bfloat16, T, a.h_q, d)
+        q_out = q if q_out is None else q_out
+        _rows("q_out", q_out, torch.bfloat16, T, a.h_q, d)
+        a.q, a.q_tok_stride, a.q_head_stride = q.data_ptr(), q.stride(0), q.stride(1)
+        a.q_out, a.q_out_tok_stride, a.q_out_head_stride = q_out.data_ptr(), q_out.stride(0), q_out.stride(1)
+    w = a.kv
+    w.num_tokens, w.h_k, w.d = T, h_k, d
+    w.key, w.key_tok_stride, w.key_head_stride = key.data_ptr(), key.stride(0), key.stride(1)
+    w.value, w.value_tok_stride, w.value_head_stride = value.data_ptr(), value.stride(0), value.stride(1)
+    w.slot_mapping = slot_mapping.data_ptr()
+    w.kv_format, w.page_size, w.num_pages = int(kv_format), int(page_size), int(num_pages)
+    w.k_cache, w.v_cache = k_cache.data_ptr(), v_cache.data_ptr()
+    w.k_stride_page, w.k_stride_token, w.k_stride_head = (int(x) for x in kv_strides)
+    w.v_stride_page, w.v_stride_token, w.v_stride_head = (int(x) for x in kv_strides)
+    w.k_scale, w.v_scale = k_scale.data_ptr(), v_scale.data_ptr()
+    w.scale_per_head = 1 if scale_per_head else 0
+    w.status = _ptr(status)
+    return _hold(a, q, q_out, key, value, positions, turns, freq_axis, slot_mapping, k_cache, v_cache, k_scale, v_scale,
+                 status)
+
+
+def _latent_cache(cache):
+    _rows("cache", cache, torch.uint8, None, None, LATENT_ROW)
+    return cache
+
+
+def latent_write_args(q_pe, latent, k_pe, positions, turns, slot_mapping, cache, scale, *, q_out=None, freq_axis=None,
+                      interleaved: bool = True, rope_scale: float = 1.0, status=None) -> mj_latent_write_args:
+    """The arguments of :func:`mj_latent_write`, good for as many calls as the
+    buffers keep their addresses.
+
+    ``q_pe`` bf16 ``[T, h, 64]`` or None (no queries) and ``q_out`` the same
+    (None: in place; usually the last 64 channels of the ``[T, h, 576]`` query);
+    ``latent`` bf16 ``[T, 512]``, ``k_pe`` bf16 ``[T, 64]``; ``cache`` uint8
+    ``[pages, page_size, 576]`` (any page and token strides); ``scale`` float32
+    ``[2]`` (latent, key part). Positions as for :func:`rope_write_args`."""
+    T = int(latent.shape[0])
+    _rows("latent", latent, torch.bfloat16, T, LATENT_DIM)
+    _rows("k_pe", k_pe, torch.bfloat16, T, LATENT_ROPE_DIM)
+    _flat("slot_mapping", slot_mapping, torch.int64, T)
+    _flat("scale", scale, torch.float32, 2)
+    _latent_cache(cache)
+    a = mj_latent_write_args()
+    _set_rope(a.rope, positions, turns, freq_axis, interleaved, rope_scale, T, LATENT_ROPE_DIM)
+    a.num_tokens = T
+    if q_pe is not None:
+        a.h = int(q_pe.shape[1])
+        _rows("q_pe", q_pe, torch.bfloat16, T, a.h, LATENT_ROPE_DIM)
+        q_out = q_pe if q_out is None else q_out
+        _rows("q_out", q_out, torch.bfloat16, T, a.h, LATENT_ROPE_DIM)
+        a.q_pe, a.q_tok_stride, a.q_head_stride = q_pe.data_ptr(), q_pe.stride(0), q_pe.stride(1)
+        a.q_out, a.q_out_tok_stride, a.q_out_head_stride = q_out.data_ptr(), q_out.stride(0), q_out.stride(1)
+    a.latent, a.latent_tok_stride = latent.data_ptr(), latent.stride(0)
+    a.k_pe, a.k_pe_tok_stride = k_pe.data_ptr(), k_pe.stride(0)
+    a.slot_mapping = slot_mapping.data_ptr()
+    a.page_size, a.num_pages = int(cache.shape[1]), int(cache.shape[0])
+    a.cache, a.stride_page, a.stride_token = cache.data_ptr(), cache.stride(0), cache.stride(1)
+    a.scale = scale.data_ptr()
+    a.status = _ptr(status)
+    return _hold(a, q_pe, q_out, latent, k_pe, positions, turns, freq_axis, slot_mapping, cache, scale, status)
+
+
+# ----------------------------------------------------------------------------
+# attention over the latent cache
+# ----------------------------------------------------------------------------
+@dataclass
+class PagedLatent:
+    """A paged latent cache in device memory, as mj_latent_attention sees it."""
+
+    cache: torch.Tensor  # uint8 [pages, page_size, 576]: e4m3 codes, any page and token strides
+    descale: torch.Tensor  # float32 [2]: latent, key part
+    block_table: torch.Tensor  # int32 [B, max_blocks]
+    seq_lens: torch.Tensor  # int32 [B]; 0 = padding request
+
+
+class LatentStep:
+    """Latent attention with the buffers a caller keeps between steps: the plan
+    (pinned staging and its fixed device buffer) and the workspace. One plan
+    serves every layer of a step; calls that may run at once need a LatentStep
+    each (they share its workspace)."""
+
+    def __init__(self, *, max_num_seqs: int, q_len: int, h: int, sm_count: int | None = None, margin: int = 0,
+                 causal: bool = True, evict_first: bool = True, device="cuda", with_lse: bool = False):
+        self.device = torch.device(device)
+        if sm_count is None:
+            sm_count = torch.cuda.get_device_properties(self.device).multi_processor_count
+        self.max_num_seqs, self.q_len, self.h = max_num_seqs, q_len, h
+        self.margin, self.causal, self.evict_first = margin, causal, evict_first
+        self.slots = mj_latent_slots(sm_count, q_len, h)
+        words = mj_latent_plan_size(self.slots, max_num_seqs)
+        self.plan_dev = torch.zeros(words, dtype=torch.int32, device=self.device)
+        self.plan_host = torch.zeros(words, dtype=torch.int32).pin_memory()
+        self._staged = None  # event after the last copy of the staging buffer
+        self.ws_bytes = mj_latent_workspace_size(self.slots, q_len, h)
+        with torch.cuda.device(self.device):
+            self.workspace = torch.empty(self.ws_bytes, dtype=torch.uint8, device=self.device)
+            mj_workspace_init(self.workspace)
+        self.lse = (torch.empty(max(1, max_num_seqs), q_len * h, dtype=torch.float32, device=self.device)
+                    if with_lse else None)
+
+    def plan(self, seq_lens_host, num_seqs: int, stream=None):
+        """Host plan into the pinned staging buffer, then an asynchronous copy
+        into the fixed device buffer on ``stream``."""
+        if self._staged is not None:
+            self._staged.synchronize()  # the previous copy has read the staging buffer
+        mj_latent_plan(seq_lens_host, num_seqs, self.max_num_seqs, self.slots, self.margin, plan_out=self.plan_host)
+        s = stream or torch.cuda.current_stream(self.device)
+        _check("mj_plan_upload", load_library().mj_plan_upload(
+            self.plan_host.data_ptr(), None, self.plan_dev.data_ptr(), None, self.plan_host.numel() // 4, 0, _stream(s)))
+        if self._staged is None:
+            self._staged = torch.cuda.Event()
+        self._staged.record(s)
+        return self.plan_host
+
+    def args(self, q: torch.Tensor, out: torch.Tensor, kv: PagedLatent, num_seqs: int,
+             softmax_scale: float) -> mj_latent_args:
+        """The attention call's arguments, good for as many calls as the
+        buffers keep their addresses. ``q`` bf16 ``[>= num_seqs * q_len, h, 576]``,
+        ``out`` bf16 or fp16 ``[>= num_seqs * q_len, h, 512]``."""
+        if num_seqs > self.max_num_seqs:
+            raise ValueError(f"{num_seqs} requests, the step was made for {self.max_num_seqs}")
+        _rows("q", q, torch.bfloat16, None, self.h, LATENT_ROW)
+        if out.dtype not in (torch.bfloat16, torch.float16):
+            raise ValueError("out must be bf16 or fp16")
+        _rows("out", out, out.dtype, None, self.h, LATENT_DIM)
+        _latent_cache(kv.cache)
+        _flat("descale", kv.descale, torch.float32, 2)
+        _rows("block_table", kv.block_table, torch.int32, None, None)
+        _flat("seq_lens", kv.seq_lens, torch.int32, None)
+        if min(int(q.shape[0]), int(out.shape[0])) < num_seqs * self.q_len:
+            raise ValueError(f"q and out need {num_seqs * self.q_len} rows")
+        if min(int(kv.block_table.shape[0]), int(kv.seq_lens.shape[0])) < num_seqs:
+            raise ValueError(f"block_table and seq_lens need {num_seqs} requests")
+        a = mj_latent_args()
+        a.num_seqs, a.max_num_seqs, a.q_len, a.h = num_seqs, self.max_num_seqs, self.q_len, self.h
+        a.causal, a.softmax_scale = 1 if self.causal else 0, softmax_scale
+        a.q, a.q_tok_stride, a.q_head_stride = q.data_ptr(), q.stride(0), q.stride(1)
+        a.cache, a.stride_page, a.stride_token = kv.cache.data_ptr(), kv.cache.stride(0), kv.cache.stride(1)
+        a.page_size, a.num_pages = int(kv.cache.shape[1]), int(kv.cache.shape[0])
+        a.descale = kv.descale.data_ptr()
+        a.block_table, a.block_table_stride = kv.block_table.data_ptr(), kv.block_table.stride(0)
+        a.block_table_len = int(kv.block_table.shape[1])
+        a.seq_lens, a.plan, a.slots = kv.seq_lens.data_ptr(), self.plan_dev.data_ptr(), self.slots
+        a.out, a.out_tok_stride, a.out_head_stride = out.data_ptr(), out.stride(0), out.stride(1)
+        a.out_dtype = MJ_OUT_F16 if out.dtype == torch.float16 else MJ_OUT_BF16
+        a.lse = self.lse.data_ptr() if self.lse is not None else None
+        a.workspace, a.workspace_bytes = self.workspace.data_ptr(), self.ws_bytes
+        a.evict_first = 1 if self.evict_first else 0
+        return _hold(a, q, out, kv.cache, kv.descale, kv.block_table, kv.seq_lens, self.plan_dev, self.workspace, self.lse)
+
+    def run(self, q: torch.Tensor, out: torch.Tensor, kv: PagedLatent, num_seqs: int, softmax_scale: float, stream=None,
+            args: mj_latent_args | None = None):
+        """The device part of one layer's attention; ``plan`` comes before it."""
+        mj_latent_attention(args if args is not None else self.args(q, out, kv, num_seqs, softmax_scale), stream)
+        return out
