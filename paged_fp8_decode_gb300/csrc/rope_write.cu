@@ -16,13 +16,10 @@
 // What bounds it: HBM for many tokens (each query, key and value element is
 // read once and written once), launch and load latency for few. A token's
 // cosines and sines serve all its heads, so a CTA takes whole tokens: it first
-// requests the elements of up to four items a thread (an item: 16 channels as
-// two 16-byte chunks, a pair's two sides in one thread), then computes the
-// group's cosines and sines into shared memory while they arrive.
+// requests the first slots of each thread (of each 16 channels as two 16-byte
+// chunks, a pair's two sides in one thread), then computes the tokens' cosines
+// and sines into shared memory while they arrive.
 #include <cuda_fp8.h>
-
-#include <algorithm>
-#include <atomic>
 
 #include "kv_codec.cuh"
 #include "mj_device.cuh"
@@ -33,7 +30,15 @@ namespace mj {
 
 namespace {
 
-constexpr int kItemsPerThread = 4;  // items whose loads are in flight together
+constexpr int kThreads = 128;
+// Two slots of loads in flight a thread and seven CTAs an SM: 16384 tokens of
+// 32/8 heads of 128 in 62.8 us (5.9 TB/s). Three slots and five CTAs: 65.6 us,
+// and 0.2 us less for one token; eight CTAs spill: 71 us.
+constexpr int kItemsPerThread = 2, kMinCtas = 7;
+// With many tokens a thread takes more slots, so that its cosines, addresses
+// and set-up serve more of them (up to 6 against up to 4: 69 and 78 us before
+// the packed arithmetic); with few, the shorter chain counts.
+constexpr int kManyTokens = 600, kItemsMany = 6;
 
 struct RopeWriteParams {
   // rotation
@@ -46,7 +51,7 @@ struct RopeWriteParams {
   int interleaved;
   float scale;
   // tokens
-  int num_tokens, group;  // tokens per CTA
+  int num_tokens, group, lanes;  // tokens per CTA, slot lanes per token (a power of two)
   int h_q, h_k;
   const uint16_t* q;
   uint16_t* q_out;
@@ -66,21 +71,41 @@ struct RopeWriteParams {
   uint32_t* status;
 };
 
+// Bounds of 1 / s that hold x * lo <= x / s <= x * hi in size after rounding
+// (8 units of 2^-24 either way; the reciprocal and the two products are off by
+// three). A scale so large or small that the reciprocal could overflow or
+// vanish gets bounds that never agree.
+struct Recip {
+  float lo, hi;
+};
+__device__ __forceinline__ Recip recip_bounds(float s) {
+  const float r = __frcp_rn(s);
+  const bool plain = fabsf(s) > 0x1p-100f && fabsf(s) < 0x1p100f;
+  return plain ? Recip{r * (1.f - 0x1p-21f), r * (1.f + 0x1p-21f)} : Recip{0.f, INFINITY};
+}
+
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+  const __nv_fp8x2_storage_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+  const __nv_fp8x2_storage_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
+  return uint32_t(lo) | (uint32_t(hi) << 16);
+}
+
+// The e4m3 codes of x / s (IEEE float32 division) for four values. The rounding
+// to a code is monotonic, so where both bounds of the quotient have the same
+// code it is that one; the division itself is done where they differ (a
+// quotient within 2^-21 of a border between codes, about one in 10^4).
+__device__ __forceinline__ uint32_t quotient_codes(const float* x, float s, Recip r) {
+  const uint32_t lo = e4m3x4(x[0] * r.lo, x[1] * r.lo, x[2] * r.lo, x[3] * r.lo);
+  const uint32_t hi = e4m3x4(x[0] * r.hi, x[1] * r.hi, x[2] * r.hi, x[3] * r.hi);
+  if (lo == hi) return lo;
+  return e4m3x4(__fdiv_rn(x[0], s), __fdiv_rn(x[1], s), __fdiv_rn(x[2], s), __fdiv_rn(x[3], s));
+}
+
 // 8 values of one row, channels c .. c + 7 (c a multiple of 8), to codes.
 template <int F>
-__device__ __forceinline__ void encode8(const float x[8], const float* scale, uint8_t* row, int c) {
+__device__ __forceinline__ void encode8(const float x[8], const float* scale, Recip r, uint8_t* row, int c) {
   if constexpr (F == MJ_KV_E4M3) {
-    const float s = scale[0];
-    uint32_t w[2];
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const __nv_fp8x2_storage_t lo = __nv_cvt_float2_to_fp8x2(
-          make_float2(__fdiv_rn(x[4 * k], s), __fdiv_rn(x[4 * k + 1], s)), __NV_SATFINITE, __NV_E4M3);
-      const __nv_fp8x2_storage_t hi = __nv_cvt_float2_to_fp8x2(
-          make_float2(__fdiv_rn(x[4 * k + 2], s), __fdiv_rn(x[4 * k + 3], s)), __NV_SATFINITE, __NV_E4M3);
-      w[k] = uint32_t(lo) | (uint32_t(hi) << 16);
-    }
-    *reinterpret_cast<uint2*>(row + c) = make_uint2(w[0], w[1]);
+    *reinterpret_cast<uint2*>(row + c) = make_uint2(quotient_codes(x, scale[0], r), quotient_codes(x + 4, scale[0], r));
   } else {
     const float4* sc = reinterpret_cast<const float4*>(scale + c);
     const float4 s0 = sc[0], s1 = sc[1];
@@ -104,27 +129,61 @@ __device__ __forceinline__ void encode8(const float x[8], const float* scale, ui
   }
 }
 
+// Two float32 products or fused multiply-adds in one instruction.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  uint64_t x, y, d;
+  memcpy(&x, &a, 8);
+  memcpy(&y, &b, 8);
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(x), "l"(y));
+  float2 r;
+  memcpy(&r, &d, 8);
+  return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t x, y, z, d;
+  memcpy(&x, &a, 8);
+  memcpy(&y, &b, 8);
+  memcpy(&z, &c, 8);
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(x), "l"(y), "l"(z));
+  float2 r;
+  memcpy(&r, &d, 8);
+  return r;
+}
+
 __device__ __forceinline__ uint4 pack_bf16x8(const float x[8]) {
   uint32_t w[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    w[i] = uint32_t(float_to_bf16_bits(x[2 * i])) | (uint32_t(float_to_bf16_bits(x[2 * i + 1])) << 16);
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+    memcpy(&w[i], &h, 4);
+  }
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // F: the cache format; D: channels of a rotated head (queries and keys); VD:
 // channels of a value head (the latent vector of mj_latent_write).
+//
+// A token's elements are `slots` of D channels: its query heads, its key heads
+// and VD / D slots a value head. Thread (token, lane, j) takes chunk pair j
+// (16 channels) of the slots lane, lane + lanes, ...: always the same eight
+// frequencies, whose cosines and sines it holds in registers.
 template <int F, int D, int VD>
-__global__ void __launch_bounds__(256) rope_write_kernel(RopeWriteParams p) {
+__global__ void __launch_bounds__(kThreads, kMinCtas) rope_write_kernel(RopeWriteParams p) {
   constexpr int U = kItemsPerThread;
-  constexpr int kD = D / 16, kVD = VD / 16;  // items of a rotated and of a value head
-  extern __shared__ float2 cs[];             // [group][n]: cos and sin, times the scale
-  const int tid = threadIdx.x, threads = blockDim.x;
+  constexpr int kD = D / 16;   // chunk pairs of a slot
+  constexpr int kVS = VD / D;  // slots of a value head
+  extern __shared__ __align__(16) float cs[];  // [tokens of the CTA][2][n]: cosines, sines, times the scale
+  const int tid = threadIdx.x;
+  const int j = tid % kD, lane = (tid / kD) & (p.lanes - 1), tl = tid / (kD * p.lanes);
   const int t0 = blockIdx.x * p.group;
-  const int nt = min(p.group, p.num_tokens - t0);
-  const int qk_items = (p.h_q + p.h_k) * kD;
-  const int per_token = qk_items + p.h_k * kVD;
-  const int total = nt * per_token;
+  const int tok = t0 + tl;
+  const int slots = p.h_q + p.h_k + p.h_k * kVS;
+  const int n_slots = tok < p.num_tokens ? slots : 0;
+
+  // this thread's two 8-channel chunks of a rotated slot, and of a value slot
+  const bool rot = 8 * j < p.n;
+  const int c0 = rot && !p.interleaved ? 8 * j : 16 * j;
+  const int c1 = c0 + (rot && !p.interleaved ? p.n : 8);
 
   // launched with programmatic stream serialization: everything below may be
   // the preceding kernel's output. The next kernel may launch (and waits for
@@ -132,145 +191,135 @@ __global__ void __launch_bounds__(256) rope_write_kernel(RopeWriteParams p) {
   tc::grid_launch_dependents();
   tc::grid_dependency_wait();
 
-  struct Item {
-    int tok, head, c0, c1, f;  // f: first frequency of the chunk, -1 when it is not rotated
-    int kind;                  // 0 query, 1 key, 2 value
-  };
-  auto item_of = [&](int i) {
-    Item it;
-    const int tl = p.group == 1 ? 0 : i / per_token;
-    const int r = i - tl * per_token;
-    it.tok = t0 + tl;
-    it.f = -1;
-    if (r < qk_items) {
-      const int hs = r / kD, j = r % kD;
-      it.kind = hs < p.h_q ? 0 : 1;
-      it.head = hs < p.h_q ? hs : hs - p.h_q;
-      if (8 * j < p.n) {
-        it.f = 8 * j;
-        it.c0 = p.interleaved ? 16 * j : 8 * j;
-        it.c1 = it.c0 + (p.interleaved ? 8 : p.n);
-      } else {
-        it.c0 = 16 * j;  // rot_dim / 16 items lie before: channels rot_dim + 16 (j - n / 8)
-        it.c1 = it.c0 + 8;
-      }
+  auto load = [&](int s, uint4& a, uint4& b) {
+    const uint16_t* src;
+    int o0 = c0, o1 = c1;
+    if (s < p.h_q) {
+      src = p.q + tok * p.q_ts + s * p.q_hs;
+    } else if (s < p.h_q + p.h_k) {
+      src = p.key + tok * p.k_ts + (s - p.h_q) * p.k_hs;
     } else {
-      it.kind = 2;
-      it.head = (r - qk_items) / kVD;
-      it.c0 = ((r - qk_items) % kVD) * 16;
-      it.c1 = it.c0 + 8;
+      const int v = s - p.h_q - p.h_k;
+      src = p.value + tok * p.v_ts + (v / kVS) * p.v_hs + (v % kVS) * D;
+      o0 = 16 * j;
+      o1 = o0 + 8;
     }
-    return it;
+    a = *reinterpret_cast<const uint4*>(src + o0);
+    b = *reinterpret_cast<const uint4*>(src + o1);
   };
+  uint4 a[U], b[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    if (lane + u * p.lanes < n_slots) load(lane + u * p.lanes, a[u], b[u]);
+  const int64_t slot = n_slots ? p.slots[tok] : -1;
 
-  bool ready = false;  // the cosines and sines are in shared memory (the same in every thread)
-  for (int base = 0; base < total; base += U * threads) {
-    uint4 a[U], b[U];
-    int64_t slot[U];
+  for (int e = tid; e < p.group * p.n; e += kThreads) {
+    const int el = e / p.n, f = e - el * p.n;
+    if (t0 + el >= p.num_tokens) break;
+    const int ax = p.axes > 1 ? min(int(p.freq_axis[f]), p.axes - 1) : 0;
+    const uint64_t turn = uint64_t(p.pos[int64_t(ax) * p.pos_axis + t0 + el]) * p.turns[f];
+    float sn, cn;
+    sincospif(float(int32_t(turn >> 32)) * 0x1p-31f, &sn, &cn);
+    cs[el * 2 * p.n + f] = cn * p.scale;
+    cs[el * 2 * p.n + p.n + f] = sn * p.scale;
+  }
+  __syncthreads();
+  float2 wc[4], ws[4];  // cosines and sines of frequencies 8j + 2k, 8j + 2k + 1
+  if (rot && n_slots) {
+    const float* wp = cs + tl * 2 * p.n + 8 * j;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const float4 c4 = *reinterpret_cast<const float4*>(wp + 4 * k);
+      const float4 s4 = *reinterpret_cast<const float4*>(wp + p.n + 4 * k);
+      wc[2 * k] = make_float2(c4.x, c4.y);
+      wc[2 * k + 1] = make_float2(c4.z, c4.w);
+      ws[2 * k] = make_float2(s4.x, s4.y);
+      ws[2 * k + 1] = make_float2(s4.z, s4.w);
+    }
+  }
+  if (slot >= p.num_slots && p.status && lane == 0 && j == 0) atomicOr(p.status, kStatusBadPage);
+  const bool live = slot >= 0 && slot < p.num_slots;
+  const int64_t page = slot >> p.page_shift, prow = slot & ((int64_t(1) << p.page_shift) - 1);
+
+  for (int s0 = lane; s0 < n_slots; s0 += U * p.lanes) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int i = base + u * threads + tid;
-      if (i < total) {
-        const Item it = item_of(i);
-        const uint16_t* src = it.kind == 0   ? p.q + it.tok * p.q_ts + it.head * p.q_hs
-                              : it.kind == 1 ? p.key + it.tok * p.k_ts + it.head * p.k_hs
-                                             : p.value + it.tok * p.v_ts + it.head * p.v_hs;
-        a[u] = *reinterpret_cast<const uint4*>(src + it.c0);
-        b[u] = *reinterpret_cast<const uint4*>(src + it.c1);
-        slot[u] = it.kind == 0 ? -1 : p.slots[it.tok];
-      }
-    }
-    if (!ready) {
-      for (int e = tid; e < nt * p.n; e += threads) {
-        const int tl = p.group == 1 ? 0 : e / p.n, f = e - tl * p.n;
-        const int ax = p.axes > 1 ? min(int(p.freq_axis[f]), p.axes - 1) : 0;
-        const uint64_t turn = uint64_t(p.pos[int64_t(ax) * p.pos_axis + t0 + tl]) * p.turns[f];
-        float s, c;
-        sincospif(float(int32_t(turn >> 32)) * 0x1p-31f, &s, &c);
-        cs[e] = make_float2(c * p.scale, s * p.scale);
-      }
-      __syncthreads();
-      ready = true;
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int i = base + u * threads + tid;
-      if (i >= total) break;
-      const Item it = item_of(i);
-      if (it.kind != 0) {
-        if (slot[u] < 0) continue;  // a padding token
-        if (slot[u] >= p.num_slots) {
-          if (p.status && it.kind == 2 && it.head == 0 && it.c0 == 0) atomicOr(p.status, kStatusBadPage);
-          continue;
-        }
-      }
+      const int s = s0 + u * p.lanes;
+      if (s >= n_slots) break;
+      const bool value = s >= p.h_q + p.h_k;
+      if (s >= p.h_q && !live) continue;  // a padding token, or a slot past the pool
       float x[8], y[8];
       bf16x8_to_float(a[u], x);
       bf16x8_to_float(b[u], y);
-      if (it.f >= 0) {
-        const float2* w = cs + (it.tok - t0) * p.n + it.f;
+      if (rot && !value) {
         if (p.interleaved) {  // pairs (2k, 2k + 1): x holds the first four of them, y the others
+          auto turn = [](float& x0, float& x1, float c, float sn) {
+            const float t = x0 * c - x1 * sn;
+            x1 = x1 * c + x0 * sn;
+            x0 = t;
+          };
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float2 wa = w[k], wb = w[k + 4];
-            const float x0 = x[2 * k], x1 = x[2 * k + 1], y0 = y[2 * k], y1 = y[2 * k + 1];
-            x[2 * k] = x0 * wa.x - x1 * wa.y;
-            x[2 * k + 1] = x1 * wa.x + x0 * wa.y;
-            y[2 * k] = y0 * wb.x - y1 * wb.y;
-            y[2 * k + 1] = y1 * wb.x + y0 * wb.y;
+          for (int k = 0; k < 2; ++k) {
+            turn(x[4 * k], x[4 * k + 1], wc[k].x, ws[k].x);
+            turn(x[4 * k + 2], x[4 * k + 3], wc[k].y, ws[k].y);
+            turn(y[4 * k], y[4 * k + 1], wc[k + 2].x, ws[k + 2].x);
+            turn(y[4 * k + 2], y[4 * k + 3], wc[k + 2].y, ws[k + 2].y);
           }
         } else {  // pairs (k, k + n)
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const float2 wk = w[k];
-            const float x0 = x[k], y0 = y[k];
-            x[k] = x0 * wk.x - y0 * wk.y;
-            y[k] = y0 * wk.x + x0 * wk.y;
+          for (int k = 0; k < 4; ++k) {
+            const float2 x0 = make_float2(x[2 * k], x[2 * k + 1]), y0 = make_float2(y[2 * k], y[2 * k + 1]);
+            const float2 xr = fma2(x0, wc[k], mul2(y0, make_float2(-ws[k].x, -ws[k].y)));
+            const float2 yr = fma2(y0, wc[k], mul2(x0, ws[k]));
+            x[2 * k] = xr.x;
+            x[2 * k + 1] = xr.y;
+            y[2 * k] = yr.x;
+            y[2 * k + 1] = yr.y;
           }
         }
       }
-      if (it.kind == 0) {
-        uint16_t* dst = p.q_out + it.tok * p.qo_ts + it.head * p.qo_hs;
-        *reinterpret_cast<uint4*>(dst + it.c0) = pack_bf16x8(x);
-        *reinterpret_cast<uint4*>(dst + it.c1) = pack_bf16x8(y);
+      if (s < p.h_q) {
+        uint16_t* dst = p.q_out + tok * p.qo_ts + s * p.qo_hs;
+        *reinterpret_cast<uint4*>(dst + c0) = pack_bf16x8(x);
+        *reinterpret_cast<uint4*>(dst + c1) = pack_bf16x8(y);
+      } else if (!value) {
+        const int g = s - p.h_q;
+        uint8_t* row = p.k_cache + page * p.k_sp + prow * p.k_st + g * p.k_sh;
+        const float* scale = p.k_scale + (F != MJ_KV_E4M3 ? g * D : (p.scale_per_head ? g : 0));
+        const Recip r = F == MJ_KV_E4M3 ? recip_bounds(scale[0]) : Recip{};
+        encode8<F>(x, scale, r, row, c0);
+        encode8<F>(y, scale, r, row, c1);
       } else {
-        const int64_t page = slot[u] >> p.page_shift, prow = slot[u] & ((int64_t(1) << p.page_shift) - 1);
-        const bool key = it.kind == 1;
-        uint8_t* row = key ? p.k_cache + page * p.k_sp + prow * p.k_st + it.head * p.k_sh
-                           : p.v_cache + page * p.v_sp + prow * p.v_st + it.head * p.v_sh;
-        const float* scale = (key ? p.k_scale : p.v_scale) +
-                             (F != MJ_KV_E4M3 ? it.head * D : (p.scale_per_head ? it.head : 0));
-        encode8<F>(x, scale, row, it.c0);
-        encode8<F>(y, scale, row, it.c1);
+        const int v = s - p.h_q - p.h_k, g = v / kVS, c = (v % kVS) * D + 16 * j;
+        uint8_t* row = p.v_cache + page * p.v_sp + prow * p.v_st + g * p.v_sh;
+        const float* scale = p.v_scale + (F != MJ_KV_E4M3 ? g * D : (p.scale_per_head ? g : 0));
+        const Recip r = F == MJ_KV_E4M3 ? recip_bounds(scale[0]) : Recip{};
+        encode8<F>(x, scale, r, row, c);
+        encode8<F>(y, scale, r, row, c + 8);
       }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int s = s0 + (U + u) * p.lanes;
+      if (s < n_slots) load(s, a[u], b[u]);
     }
   }
 }
 
 template <int F, int D, int VD>
 cudaError_t launch(RopeWriteParams p, cudaStream_t stream) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  static std::atomic<int> sm_count[64];  // per device, looked up once (host threads may race)
-  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  int sms = sm_count[dev].load(std::memory_order_relaxed);
-  if (sms == 0) {
-    e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (e != cudaSuccess) return e;
-    sm_count[dev].store(sms, std::memory_order_relaxed);
-  }
-  // Tokens per CTA: enough of them for four items a thread, as long as every SM
-  // still gets two CTAs; 256 threads where one token alone has more than that.
-  const int64_t per_token = int64_t(p.h_q + p.h_k) * (D / 16) + int64_t(p.h_k) * (VD / 16);
-  const int threads = per_token > 128 * kItemsPerThread ? 256 : 128;
-  int64_t g = std::max<int64_t>(1, threads * kItemsPerThread / per_token);
-  g = std::min(g, std::max<int64_t>(1, p.num_tokens / (2 * int64_t(sms))));
-  p.group = int(std::min<int64_t>(g, 16));
+  constexpr int kLanes = kThreads / (D / 16);  // slot lanes of a CTA with one token
+  const int64_t slots = int64_t(p.h_q) + p.h_k + int64_t(p.h_k) * (VD / D);
+  // Lanes a token: so many that a thread has at most that many slots, up to the
+  // CTA's; the CTA takes more tokens where that leaves room.
+  p.lanes = 1;
+  const int per_thread = p.num_tokens > kManyTokens ? kItemsMany : kItemsPerThread;
+  while (p.lanes < kLanes && p.lanes * per_thread < slots) p.lanes *= 2;
+  p.group = kLanes / p.lanes;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned((int64_t(p.num_tokens) + p.group - 1) / p.group));
-  cfg.blockDim = dim3(unsigned(threads));
-  cfg.dynamicSmemBytes = size_t(p.group) * p.n * sizeof(float2);  // at most 16 x 128 x 8 bytes
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = size_t(p.group) * p.n * 2 * sizeof(float);  // at most 8 KB: 32 tokens of 32 or 8 of 128 frequencies
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
