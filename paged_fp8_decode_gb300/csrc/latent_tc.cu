@@ -285,101 +285,112 @@ __global__ void __launch_bounds__(Cfg<NR>::kThreads, 1)
     }
   } else if (warp == 1) {
     // ======================= MMA issuer ========================================
-    if (lane == 0) {
-      constexpr uint32_t idesc_qk = tc::idesc_e4m3(128, 2 * NR, false, false);
-      constexpr uint32_t idesc_pv = tc::idesc_e4m3(128, NR, true, true);
-      int u = 0, ur = 0, uv = 0;  // sub-tiles consumed by QK (latent, rotary) and by PV
-      int g0 = 0, nrow = 0;       // tiles of the rows before; rows with tiles so far
-      bool ok = true;
-      for (int row = w_begin; row < w_end && ok; ++row) {
-        const Work w = load_work(p, row);
-        if (w.ntiles == 0) continue;
-        ok = tc::mbar_wait(tc::smem_u32(&ctl.q_ready), uint32_t(nrow) & 1u, abort, kWaitLimitNs);
-        ++nrow;
-        int nq = 0, jq = 0, np = 0;
-        uint64_t t_idle = 0;
-        while (ok && np < w.ntiles) {
-          bool progressed = false;
-          if (nq < w.ntiles && nq <= np + 1) {
-            // QK of tile nq, sub-tile by sub-tile as they land (the S buffer is
-            // free: the softmax read tile nq - 2 before it released P of it)
-            const uint32_t d = tmem + uint32_t(((g0 + nq) & 1) * C::kSCols);
-            while (jq < 4 && tc::mbar_test_wait(tc::smem_u32(&ctl.full[u % C::kRing]), uint32_t(u / C::kRing) & 1u)) {
-              tc::tc_fence_after();
-              const uint64_t kd = tc::smem_desc(base + uint32_t((u % C::kRing) * kSub), 16, 1024, tc::kSwizzle128B);
-              const uint64_t qd = tc::smem_desc(base + uint32_t(C::kOffQ + jq * C::kQSub), 16, 1024, tc::kSwizzle128B);
+    // The whole warp runs the loop and one elected lane issues: with a single
+    // thread's loop the descriptors had to be moved to uniform registers for
+    // every MMA, and issuing a tile's 50 took 5000 cycles instead of 2050.
+    constexpr uint32_t idesc_qk = tc::idesc_e4m3(128, 2 * NR, false, false);
+    constexpr uint32_t idesc_pv = tc::idesc_e4m3(128, NR, true, true);
+    const uint64_t kd0 = tc::smem_desc(base, 16, 1024, tc::kSwizzle128B);
+    const uint64_t qd0 = tc::smem_desc(base + uint32_t(C::kOffQ), 16, 1024, tc::kSwizzle128B);
+    const uint64_t krd0 = tc::smem_desc(base + uint32_t(C::kOffRope), 16, 512, kSwizzle64B);
+    const uint64_t qrd = tc::smem_desc(base + uint32_t(C::kOffQ + 4 * C::kQSub), 16, 512, kSwizzle64B);
+    const uint64_t vd0 = tc::smem_desc(base, kSub, 1024, tc::kSwizzle128B);
+    // P, MN-major without swizzle: 8-key core groups 128 B apart, 16-row blocks
+    // 2 KB apart; lo after hi
+    const uint64_t pd0 = tc::smem_desc(base + uint32_t(C::kOffP), 128, 2048, 0);
+    auto ready = [&](uint64_t& bar, uint32_t parity) {
+      return __all_sync(0xFFFFFFFFu, tc::mbar_test_wait(tc::smem_u32(&bar), parity)) != 0;
+    };
+    int sk = 0, sr = 0, sv = 0;           // ring entries QK (latent, rotary) and PV take next
+    uint32_t fk = 0, fr = 0;              // and their phases
+    int g0 = 0, nrow = 0;                 // tiles of the rows before; rows with tiles so far
+    bool ok = true;
+    for (int row = w_begin; row < w_end && ok; ++row) {
+      const int ntiles = __shfl_sync(0xFFFFFFFFu, load_work(p, row).ntiles, 0);
+      if (ntiles == 0) continue;
+      ok = __all_sync(0xFFFFFFFFu, tc::mbar_wait(tc::smem_u32(&ctl.q_ready), uint32_t(nrow) & 1u, abort, kWaitLimitNs));
+      ++nrow;
+      int nq = 0, jq = 0, np = 0;
+      uint64_t t_idle = 0;
+      while (ok && np < ntiles) {
+        bool progressed = false;
+        if (nq < ntiles && nq <= np + 1) {
+          // QK of tile nq, sub-tile by sub-tile as they land (the S buffer is
+          // free: the softmax read tile nq - 2 before it released P of it)
+          const uint32_t d = tmem + uint32_t(((g0 + nq) & 1) * C::kSCols);
+          while (jq < 4 && ready(ctl.full[sk], fk)) {
+            tc::tc_fence_after();
+            const uint64_t kd = kd0 + uint64_t(sk * (kSub >> 4)), qd = qd0 + uint64_t(jq * (C::kQSub >> 4));
 #pragma unroll
-              for (int k = 0; k < 4; ++k)
-                tc::umma_f8f6f4(d, kd + uint64_t(2 * k), qd + uint64_t(2 * k), idesc_qk, jq > 0 || k > 0);
-              ++u;
-              ++jq;
-              progressed = true;
+            for (int k = 0; k < 4; ++k)
+              tc::umma_f8f6f4_warp(d, kd + uint64_t(2 * k), qd + uint64_t(2 * k), idesc_qk, jq > 0 || k > 0);
+            if (++sk == C::kRing) {
+              sk = 0;
+              fk ^= 1u;
             }
-            if (jq == 4 &&
-                tc::mbar_test_wait(tc::smem_u32(&ctl.rfull[ur % C::kRopeRing]), uint32_t(ur / C::kRopeRing) & 1u)) {
-              tc::tc_fence_after();
-              const int s = ur % C::kRopeRing;
-              const uint64_t kd = tc::smem_desc(base + uint32_t(C::kOffRope + s * kRopeSub), 16, 512, kSwizzle64B);
-              const uint64_t qd = tc::smem_desc(base + uint32_t(C::kOffQ + 4 * C::kQSub), 16, 512, kSwizzle64B);
-#pragma unroll
-              for (int k = 0; k < 2; ++k)
-                tc::umma_f8f6f4(d, kd + uint64_t(2 * k), qd + uint64_t(2 * k), idesc_qk, 1);
-              tc::umma_commit(tc::smem_u32(&ctl.s_full[(g0 + nq) & 1]));
-              tc::umma_commit(tc::smem_u32(&ctl.rempty[s]));
-              ++ur;
-              ++nq;
-              jq = 0;
-              progressed = true;
-            }
+            ++jq;
+            progressed = true;
           }
-          if (np < nq) {
-            const int gi = g0 + np;
-            if (tc::mbar_test_wait(tc::smem_u32(&ctl.p_full[gi & 1]), uint32_t(gi >> 1) & 1u)) {
-              tc::tc_fence_after();
-              // P, MN-major without swizzle: 8-key core groups 128 B apart,
-              // 16-row blocks 2 KB apart; lo after hi
-              const uint64_t pd =
-                  tc::smem_desc(base + uint32_t(C::kOffP + (gi % C::kPBufs) * C::kPBytes), 128, 2048, 0);
-#pragma unroll 1
-              for (int j = 0; j < 4; ++j) {
-                const int s = uv % C::kRing;
-                const uint64_t vd = tc::smem_desc(base + uint32_t(s * kSub), kSub, 1024, tc::kSwizzle128B);
+          if (jq == 4 && ready(ctl.rfull[sr], fr)) {
+            tc::tc_fence_after();
+            const uint64_t kd = krd0 + uint64_t(sr * (kRopeSub >> 4));
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {  // 32 keys a step
-                  tc::umma_f8f6f4(tO + uint32_t(j * NR), vd + uint64_t(256 * k), pd + uint64_t(32 * k), idesc_pv,
-                                  np > 0 || k > 0);
-                  tc::umma_f8f6f4(tO + uint32_t(j * NR), vd + uint64_t(256 * k), pd + uint64_t(NR * 8 + 32 * k),
-                                  idesc_pv | kFormatBE5m2, 1);
-                }
-                tc::umma_commit(tc::smem_u32(&ctl.empty[s]));
-                ++uv;
+            for (int k = 0; k < 2; ++k) tc::umma_f8f6f4_warp(d, kd + uint64_t(2 * k), qrd + uint64_t(2 * k), idesc_qk, 1);
+            tc::umma_commit_warp(tc::smem_u32(&ctl.s_full[(g0 + nq) & 1]));
+            tc::umma_commit_warp(tc::smem_u32(&ctl.rempty[sr]));
+            if (++sr == C::kRopeRing) {
+              sr = 0;
+              fr ^= 1u;
+            }
+            ++nq;
+            jq = 0;
+            progressed = true;
+          }
+        }
+        if (np < nq) {
+          const int gi = g0 + np;
+          if (ready(ctl.p_full[gi & 1], uint32_t(gi >> 1) & 1u)) {
+            tc::tc_fence_after();
+            const uint64_t pd = pd0 + uint64_t((gi % C::kPBufs) * (C::kPBytes >> 4));
+            const uint32_t acc = np > 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const uint64_t vd = vd0 + uint64_t(sv * (kSub >> 4));
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {  // 32 keys a step
+                tc::umma_f8f6f4_warp(tO + uint32_t(j * NR), vd + uint64_t(256 * k), pd + uint64_t(32 * k), idesc_pv,
+                                     k > 0 ? 1u : acc);
+                tc::umma_f8f6f4_warp(tO + uint32_t(j * NR), vd + uint64_t(256 * k), pd + uint64_t(NR * 8 + 32 * k),
+                                     idesc_pv | kFormatBE5m2, 1);
               }
-              tc::umma_commit(tc::smem_u32(&ctl.o_full[gi & 1]));
-              ++np;
-              progressed = true;
+              tc::umma_commit_warp(tc::smem_u32(&ctl.empty[sv]));
+              if (++sv == C::kRing) sv = 0;
             }
-          }
-          if (progressed) {
-            t_idle = 0;
-          } else {
-            const uint64_t now = tc::globaltimer_ns();
-            if (t_idle == 0) {
-              t_idle = now;
-            } else if (now - t_idle > kWaitLimitNs || *abort) {
-              *abort = 1;
-              ok = false;
-            }
-            __nanosleep(32);
+            tc::umma_commit_warp(tc::smem_u32(&ctl.o_full[gi & 1]));
+            ++np;
+            progressed = true;
           }
         }
-        g0 += w.ntiles;
+        if (progressed) {
+          t_idle = 0;
+        } else {
+          const uint64_t now = tc::globaltimer_ns();
+          if (t_idle == 0) {
+            t_idle = now;
+          } else if (__any_sync(0xFFFFFFFFu, now - t_idle > kWaitLimitNs || *abort)) {
+            *abort = 1;
+            ok = false;
+          }
+          __nanosleep(32);
+        }
       }
-      if (!ok) {
-        // abort: wait (bounded) until every MMA issued so far has completed
-        tc::umma_commit(tc::smem_u32(&ctl.drain));
-        const uint64_t t0 = tc::globaltimer_ns();
-        while (!tc::mbar_try_wait(tc::smem_u32(&ctl.drain), 0) && tc::globaltimer_ns() - t0 < kDrainLimitNs) {
-        }
+      g0 += ntiles;
+    }
+    if (!ok) {
+      // abort: wait (bounded) until every MMA issued so far has completed
+      tc::umma_commit_warp(tc::smem_u32(&ctl.drain));
+      const uint64_t t0 = tc::globaltimer_ns();
+      while (!tc::mbar_try_wait(tc::smem_u32(&ctl.drain), 0) && tc::globaltimer_ns() - t0 < kDrainLimitNs) {
       }
     }
   } else if (warp >= 4) {
