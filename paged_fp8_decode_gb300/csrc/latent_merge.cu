@@ -1,16 +1,16 @@
 // Joins the partials of mj_latent_attention's split requests: for request b
-// and row r, over its partials s (normalised output O~, max logit m in the
-// log2 domain, sum l = sum 2^(t - m)):
-//   M = max_s m_s,  w_s = 2^(m_s - M) l_s,  out = s0 sum w_s O~_s / sum w_s.
-// A partial without a key has m = -inf and is selected off (its O~ and l were
-// never written).
+// and row r, over its partials s (unnormalised output O~, reference max m in
+// the log2 domain, sum l, both scaled by 2^m):
+//   M = max_s m_s,  out = s0 sum_s 2^(m_s - M) O~_s / sum_s 2^(m_s - M) l_s.
+// A partial without a key has m = -inf and is selected off (its O~ and l may
+// never have been written).
 //
-// Bound by latency: a few megabytes of partials at most. A task is 128 channels
-// of one row (a float4 a lane). Few rows (a long request split over the whole
-// GPU): 16 warps share a task's partials and meet in shared memory, so that
-// their loads are in flight together; many rows: a warp each.
-#include <atomic>
-
+// Bound by latency and L2: tens of megabytes of partials at most, just
+// written. A task is four rows of 128 channels, one 16-byte load a thread and
+// partial. Many tasks: 128 threads each, which request four partials at a
+// time. Few (a long request split over the whole GPU): four groups of 128
+// threads share a task's partials and meet in shared memory, so that all their
+// loads are in flight together.
 #include "mj_device.cuh"
 #include "mj_internal.h"
 #include "tc_ptx.cuh"
@@ -19,95 +19,139 @@ namespace mj {
 
 namespace {
 
-constexpr int kWarps = 16;
 constexpr int kBlocks = MJ_LATENT_DIM / 128;
 
-template <int KW>  // warps per task
-__global__ void __launch_bounds__(32 * kWarps) latent_merge_kernel(LatentParams p) {
-  __shared__ float4 part[KW > 1 ? KW : 1][32];
-  tc::grid_launch_dependents();
-  tc::grid_dependency_wait();
-  const int lane = threadIdx.x & 31, wi = (threadIdx.x >> 5) % KW;
-  const int64_t task = int64_t(blockIdx.x) * (kWarps / KW) + (threadIdx.x >> 5) / KW;
-  const int64_t unit = task / kBlocks;
-  const int ch = int(task % kBlocks) * 128 + 4 * lane;
-  if (unit >= int64_t(p.num_seqs) * p.n_q) return;  // (KW > 1: the whole CTA)
-  const int b = int(unit / p.n_q), row = int(unit % p.n_q);
-  const int first = p.splits[2 * b], n = min(p.splits[2 * b + 1], 2 * p.slots - first);
-  // an unsplit request was written by the attention kernel; a padding request is left alone
-  if (n <= 0 || first < 0 || p.seq_lens[b] <= 0) return;
-  const float* mp = p.m_part + int64_t(first) * p.n_q + row;
-  const float* lp = p.l_part + int64_t(first) * p.n_q + row;
-  const float* op = p.o_part + (int64_t(first) * p.n_q + row) * MJ_LATENT_DIM + ch;
-
-  float M = -INFINITY;
-  for (int s = lane; s < n; s += 32) M = fmaxf(M, mp[int64_t(s) * p.n_q]);
-  M = warp_max(M);
-  auto weight = [&](int s) {
-    const float m = mp[int64_t(s) * p.n_q];
-    return m == -INFINITY ? 0.f : fast_exp2(m - M) * lp[int64_t(s) * p.n_q];
-  };
-  float wsum = 0.f;
-  for (int s = lane; s < n; s += 32) wsum += weight(s);
-  wsum = warp_sum(wsum);
-
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-  for (int s = wi; s < n; s += KW) {
-    const float w = weight(s);
-    const float4 o = *reinterpret_cast<const float4*>(op + int64_t(s) * p.n_q * MJ_LATENT_DIM);
-    if (w != 0.f) {
-      acc.x = fmaf(w, o.x, acc.x);
-      acc.y = fmaf(w, o.y, acc.y);
-      acc.z = fmaf(w, o.z, acc.z);
-      acc.w = fmaf(w, o.w, acc.w);
-    }
-  }
-  if constexpr (KW > 1) {
-    part[wi][lane] = acc;
-    __syncthreads();
-    if (wi != 0) return;
-#pragma unroll
-    for (int k = 1; k < KW; ++k) {
-      const float4 o = part[k][lane];
-      acc.x += o.x;
-      acc.y += o.y;
-      acc.z += o.z;
-      acc.w += o.w;
-    }
-  }
-  const float f = M == -INFINITY ? 0.f : p.descale[0] / wsum;
-  const int tq = row / p.h, h = row - tq * p.h;
-  uint2 o;
-  o.x = uint32_t(float_to_out_bits(acc.x * f, p.out_f16)) | (uint32_t(float_to_out_bits(acc.y * f, p.out_f16)) << 16);
-  o.y = uint32_t(float_to_out_bits(acc.z * f, p.out_f16)) | (uint32_t(float_to_out_bits(acc.w * f, p.out_f16)) << 16);
-  *reinterpret_cast<uint2*>(p.out + (int64_t(b) * p.q_len + tq) * p.out_ts + int64_t(h) * p.out_hs + ch) = o;
-  if (p.lse && lane == 0 && ch == 0)
-    p.lse[int64_t(b) * p.n_q + row] = M == -INFINITY ? -INFINITY : (M + fast_log2(wsum)) * kLn2;
+__device__ __forceinline__ float4 max4(float4 a, float4 b) {
+  return make_float4(fmaxf(a.x, b.x), fmaxf(a.y, b.y), fmaxf(a.z, b.z), fmaxf(a.w, b.w));
+}
+__device__ __forceinline__ float weight(float m, float M) { return m == -INFINITY ? 0.f : fast_exp2(m - M); }
+// a + w b, w = 0 selecting b off (it may be anything then)
+__device__ __forceinline__ float add_w(float a, float w, float b) { return w != 0.f ? fmaf(w, b, a) : a; }
+__device__ __forceinline__ void add_w4(float4& a, float4 w, float4 b) {
+  a.x = add_w(a.x, w.x, b.x);
+  a.y = add_w(a.y, w.y, b.y);
+  a.z = add_w(a.z, w.z, b.z);
+  a.w = add_w(a.w, w.w, b.w);
 }
 
-template <int KW>
+template <int G>  // groups of 128 threads
+__global__ void __launch_bounds__(128 * G) latent_merge_kernel(LatentParams p) {
+  constexpr int U = 4;  // partials in flight a thread
+  __shared__ float4 acc_sh[G > 1 ? G - 1 : 1][128], sum_sh[G > 1 ? G - 1 : 1];
+  tc::grid_launch_dependents();
+  tc::grid_dependency_wait();
+  const int x = threadIdx.x % 128, grp = threadIdx.x / 128;
+  const int quads = p.row_tile / 4;  // tasks of a row tile and channel block
+  int64_t task = blockIdx.x;
+  const int quad = int(task % quads);
+  task /= quads;
+  const int j = int(task % kBlocks);
+  task /= kBlocks;
+  const int tile = int(task % p.n_row_tiles), b = int(task / p.n_row_tiles);
+  const int2 sp = reinterpret_cast<const int2*>(p.splits)[b];
+  const int row = tile * p.row_tile + 4 * quad;
+  const int n = min(sp.y, 2 * p.slots - sp.x);
+  // an unsplit request was written by the attention kernel; a padding request
+  // is left alone; the rows past the last are not anyone's
+  if (n <= 0 || sp.x < 0 || p.seq_lens[b] <= 0 || row >= p.n_q) return;
+  const int rows4 = p.n_row_tiles * quads;  // float4 per partial in m_part / l_part
+  const float4* mp = reinterpret_cast<const float4*>(p.m_part) + int64_t(sp.x) * rows4 + row / 4;
+  const float4* lp = reinterpret_cast<const float4*>(p.l_part) + int64_t(sp.x) * rows4 + row / 4;
+  const int64_t ostep = int64_t(p.n_row_tiles) * kBlocks * quads * 128;
+  const float4* op = reinterpret_cast<const float4*>(p.o_part) + int64_t(sp.x) * ostep +
+                     ((int64_t(tile) * kBlocks + j) * quads + quad) * 128 + x;
+
+  const float4 none = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+  float4 M = none, sum = make_float4(0.f, 0.f, 0.f, 0.f), acc = sum;
+  float4 o[U], m[U], l[U];
+  auto load = [&](int s0) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int s = s0 + u * G;
+      if (s < n) {
+        m[u] = mp[int64_t(s) * rows4];
+        l[u] = lp[int64_t(s) * rows4];
+        o[u] = op[int64_t(s) * ostep];
+      } else {
+        m[u] = none;
+      }
+    }
+  };
+  load(grp);
+#pragma unroll 8
+  for (int s = 0; s < n; ++s) M = max4(M, mp[int64_t(s) * rows4]);
+  for (int s0 = grp; s0 < n; s0 += U * G) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const float4 w = make_float4(weight(m[u].x, M.x), weight(m[u].y, M.y), weight(m[u].z, M.z), weight(m[u].w, M.w));
+      add_w4(sum, w, l[u]);
+      add_w4(acc, w, o[u]);
+    }
+    if (s0 + U * G < n) load(s0 + U * G);
+  }
+  if constexpr (G > 1) {
+    if (grp > 0) {
+      acc_sh[grp - 1][x] = acc;
+      if (x == 0) sum_sh[grp - 1] = sum;
+    }
+    __syncthreads();
+    if (grp > 0) return;
+    const float4 one = make_float4(1.f, 1.f, 1.f, 1.f);
+#pragma unroll
+    for (int k = 0; k < G - 1; ++k) {
+      add_w4(acc, one, acc_sh[k][x]);
+      add_w4(sum, one, sum_sh[k]);
+    }
+  }
+  const float ds0 = p.descale[0];
+  // a row without a key has sum 0; a NaN among the logits leaves NaN in both
+  auto quotient = [&](float a, float s) { return s == 0.f ? 0.f : a * (ds0 / s); };
+  const float v[4] = {quotient(acc.x, sum.x), quotient(acc.y, sum.y), quotient(acc.z, sum.z), quotient(acc.w, sum.w)};
+  // two lanes trade, so that each holds two channels of one row
+  const bool odd = x & 1;
+#pragma unroll
+  for (int k = 0; k < 4; k += 2) {
+    const float other = __shfl_xor_sync(0xFFFFFFFFu, odd ? v[k] : v[k + 1], 1);
+    const float lo = odd ? other : v[k], hi = odd ? v[k + 1] : other;
+    const int r = row + k + (odd ? 1 : 0);
+    if (r < p.n_q) {
+      const int tq = r / p.h, h = r - tq * p.h;
+      *reinterpret_cast<uint32_t*>(p.out + (int64_t(b) * p.q_len + tq) * p.out_ts + int64_t(h) * p.out_hs + 128 * j +
+                                   (x & ~1)) =
+          uint32_t(float_to_out_bits(lo, p.out_f16)) | (uint32_t(float_to_out_bits(hi, p.out_f16)) << 16);
+    }
+  }
+  if (p.lse && j == 0 && x == 0) {
+    const float mv[4] = {M.x, M.y, M.z, M.w}, sv[4] = {sum.x, sum.y, sum.z, sum.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (row + k < p.n_q)
+        p.lse[int64_t(b) * p.n_q + row + k] =
+            sv[k] == 0.f ? -INFINITY : (mv[k] + fast_log2(sv[k]) - kLatentC0) * kLn2;
+  }
+}
+
+template <int G>
 cudaError_t launch(const LatentParams& p, int64_t tasks, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
-  const int64_t ctas = (tasks + kWarps / KW - 1) / (kWarps / KW);
-  if (ctas > INT32_MAX) return cudaErrorInvalidConfiguration;
-  cfg.gridDim = dim3(unsigned(ctas));
-  cfg.blockDim = dim3(32 * kWarps);
+  if (tasks > INT32_MAX) return cudaErrorInvalidConfiguration;
+  cfg.gridDim = dim3(unsigned(tasks));
+  cfg.blockDim = dim3(128 * G);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, latent_merge_kernel<KW>, p);
+  return cudaLaunchKernelEx(&cfg, latent_merge_kernel<G>, p);
 }
 
 }  // namespace
 
 cudaError_t launch_latent_merge(const LatentParams& p, cudaStream_t stream) {
-  const int64_t tasks = int64_t(p.num_seqs) * p.n_q * kBlocks;
-  // 16 warps a task while that still is at most four CTAs a slot
-  return tasks <= 4 * int64_t(p.slots) * p.n_row_tiles ? launch<kWarps>(p, tasks, stream) : launch<1>(p, tasks, stream);
+  const int64_t tasks = int64_t(p.num_seqs) * p.n_row_tiles * kBlocks * (p.row_tile / 4);
+  // four groups a task while the tasks' CTAs still fit beside each other
+  return tasks <= int64_t(p.slots) * p.n_row_tiles ? launch<4>(p, tasks, stream) : launch<1>(p, tasks, stream);
 }
 
 }  // namespace mj

@@ -56,9 +56,9 @@ constexpr uint64_t kWaitLimitNs = 2000000000ull;
 constexpr uint64_t kDrainLimitNs = 100000000ull;
 constexpr int kMaxDynSmem = 227 * 1024;
 
-// P is scaled so that the row's reference max has weight 2^7; the reference
+// P is scaled so that the row's reference max has weight 2^6; the reference
 // moves once a tile's max exceeds it by more than kTau, so p <= 2^8.5 < 448.
-constexpr float kC0 = 7.f, kTau = 1.5f;
+constexpr float kC0 = kLatentC0, kTau = 2.5f;
 
 template <int NR>
 struct Cfg {
@@ -150,12 +150,18 @@ struct Work {
   int64_t k0, k1;
 };
 
-__device__ __forceinline__ Work load_work(const LatentParams& p, int row) {
+__device__ __forceinline__ int seq_len(const LatentParams& p, int b) {
+  return b >= 0 && b < p.num_seqs ? p.seq_lens[b] : 0;
+}
+
+// b0, L0: the slot's first request and its length, read beside the work row
+// instead of after it.
+__device__ __forceinline__ Work load_work(const LatentParams& p, int row, int b0, int L0) {
   const int4 w = reinterpret_cast<const int4*>(p.work)[row];
   Work k;
   k.b = w.x;
   k.part = w.w;
-  k.L = w.x >= 0 && w.x < p.num_seqs ? p.seq_lens[w.x] : 0;
+  k.L = w.x == b0 ? L0 : seq_len(p, w.x);
   k.k0 = int64_t(w.y) * kKvTile;
   k.k1 = min(int64_t(w.z) * kKvTile, int64_t(k.L));
   k.ntiles = w.y >= 0 && k.k1 > k.k0 && w.w < 2 * p.slots ? int((k.k1 - k.k0 + kKvTile - 1) / kKvTile) : 0;
@@ -220,7 +226,9 @@ __global__ void __launch_bounds__(Cfg<NR>::kThreads, 1)
   const int slot = int(blockIdx.x) / p.n_row_tiles;
   const int r0 = (int(blockIdx.x) % p.n_row_tiles) * NR;
   const int nr = min(NR, p.n_q - r0);  // real rows of this tile
-  const int w_begin = max(0, p.cta_off[slot]), w_end = min(p.cta_off[slot + 1], p.max_work);
+  const int4 first = reinterpret_cast<const int4*>(p.slot_table)[slot];  // rows, first request, its first tile
+  const int w_begin = max(0, first.x), w_end = min(first.y, p.max_work);
+  const int b0 = first.z, L0 = seq_len(p, b0);
   const uint32_t tO = tmem + uint32_t(2 * C::kSCols);
 
   if (warp == 0) {
@@ -229,18 +237,24 @@ __global__ void __launch_bounds__(Cfg<NR>::kThreads, 1)
     const int ps = p.page_size, ppt = kKvTile / ps;
     int u = 0, ur = 0;  // latent and rotary sub-tiles so far
     bool ok = true;
+    auto table_entry = [&](int b, int64_t page) {  // -1 past the request's entries
+      return page < p.bt_len ? p.block_table[int64_t(b) * p.bt_stride + page] : -1;
+    };
+    // the first row's first entries, read beside its work row and length
+    const int64_t page0 = int64_t(max(0, first.w)) * ppt + lane;
+    const int entry0 = w_begin < w_end && b0 >= 0 && b0 < p.num_seqs ? table_entry(b0, page0) : -1;
     for (int row = w_begin; row < w_end && ok; ++row) {
-      const Work w = load_work(p, row);
+      const Work w = load_work(p, row, b0, L0);
       const int64_t first_page = w.k0 / ps, npages = (w.k1 + ps - 1) / ps - first_page;
-      const int32_t* bt = p.block_table + int64_t(w.b) * p.bt_stride + first_page;
-      int64_t batch = -1;
-      int entry = -1;
+      const bool known = row == w_begin && w.b == b0 && first_page + lane == page0;
+      int64_t batch = __all_sync(0xFFFFFFFFu, known) ? 0 : -1;
+      int entry = entry0;
       for (int i = 0; i < w.ntiles && ok; ++i) {
         const int nvalid = int(min(int64_t(ppt), npages - int64_t(i) * ppt));
         const int64_t e0 = int64_t(i) * ppt;
         if (batch < 0 || e0 + nvalid > batch + 32) {
           batch = e0;
-          entry = e0 + lane < npages && first_page + e0 + lane < p.bt_len ? bt[e0 + lane] : -1;
+          entry = e0 + lane < npages ? table_entry(w.b, first_page + e0 + lane) : -1;
         }
         const int pg = __shfl_sync(0xFFFFFFFFu, entry, int(e0 - batch) + (lane & 7));
         if (lane < nvalid && (pg < 0 || int64_t(pg) >= p.num_pages)) atomicOr(p.status, kStatusBadPage);
@@ -306,7 +320,7 @@ __global__ void __launch_bounds__(Cfg<NR>::kThreads, 1)
     int g0 = 0, nrow = 0;                 // tiles of the rows before; rows with tiles so far
     bool ok = true;
     for (int row = w_begin; row < w_end && ok; ++row) {
-      const int ntiles = __shfl_sync(0xFFFFFFFFu, load_work(p, row).ntiles, 0);
+      const int ntiles = __shfl_sync(0xFFFFFFFFu, load_work(p, row, b0, L0).ntiles, 0);
       if (ntiles == 0) continue;
       ok = __all_sync(0xFFFFFFFFu, tc::mbar_wait(tc::smem_u32(&ctl.q_ready), uint32_t(nrow) & 1u, abort, kWaitLimitNs));
       ++nrow;
@@ -402,16 +416,15 @@ __global__ void __launch_bounds__(Cfg<NR>::kThreads, 1)
     constexpr int kShare = 32 / RW;  // lanes that share a row after reduce_rows
     const float ds0 = p.descale[0], ds1 = p.descale[1];
     const float qk_log2 = p.softmax_scale * kLog2e;
+    const int rows_pad = p.n_row_tiles * NR;  // rows of a partial
     int g0 = 0;           // tiles of the rows before
     int xb = 0, xr = 0, xs = 0;  // bound, row and sum exchanges so far (the same in every thread of the group)
     bool ok = true;
     for (int row = w_begin; row < w_end && ok; ++row) {
-      const Work w = load_work(p, row);
+      const Work w = load_work(p, row, b0, L0);
       if (w.ntiles == 0) {
         // no key of this range is held any more: an empty partial
-        if (w.part >= 0 && w.part < 2 * p.slots)
-          for (int r = x; r < RW; r += 128)
-            if (rg + r < nr) p.m_part[int64_t(w.part) * p.n_q + r0 + rg + r] = -INFINITY;
+        if (w.part >= 0 && w.part < 2 * p.slots && x < RW) p.m_part[int64_t(w.part) * rows_pad + r0 + rg + x] = -INFINITY;
         if (w.part >= 2 * p.slots && x == 0) atomicOr(p.status, kStatusBadPlan);
         continue;
       }
@@ -423,38 +436,43 @@ __global__ void __launch_bounds__(Cfg<NR>::kThreads, 1)
         const bool live = rg + r < nr;
         const int tq = live ? gr / p.h : 0, h = live ? gr - tq * p.h : 0;
         const uint16_t* src = p.q + (int64_t(w.b) * p.q_len + tq) * p.q_ts + int64_t(h) * p.q_hs;
-        float am = 0.f;
-        if (live) {
-#pragma unroll 6
-          for (int c = part; c < kRow / 8; c += kTpr) {
-            const uint4 v = *reinterpret_cast<const uint4*>(src + c * 8);
-            const float ds = c < kLat / 8 ? ds0 : ds1;
-            const uint32_t q4[4] = {v.x, v.y, v.z, v.w};
+        constexpr int kCh = kRow / 8 / kTpr;  // 8-channel chunks of a thread, all loaded at once
+        uint4 qv[kCh];
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              am = fmaxf(am, fmaxf(fabsf(__uint_as_float(q4[k] << 16) * ds), fabsf(__uint_as_float(q4[k] & 0xFFFF0000u) * ds)));
-          }
+        for (int c = 0; c < kCh; ++c)
+          qv[c] = live ? *reinterpret_cast<const uint4*>(src + (part + c * kTpr) * 8) : make_uint4(0u, 0u, 0u, 0u);
+        float am = 0.f;
+#pragma unroll
+        for (int c = 0; c < kCh; ++c) {
+          const float ds = part + c * kTpr < kLat / 8 ? ds0 : ds1;
+          const uint32_t q4[4] = {qv[c].x, qv[c].y, qv[c].z, qv[c].w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            am = fmaxf(am, fmaxf(fabsf(__uint_as_float(q4[k] << 16) * ds), fabsf(__uint_as_float(q4[k] & 0xFFFF0000u) * ds)));
         }
 #pragma unroll
         for (int m = 1; m < kTpr; m <<= 1) am = fmaxf(am, __shfl_xor_sync(0xFFFFFFFFu, am, m));
         am = fmaxf(am, 1e-30f);
         const float inv = 448.f / am;
-#pragma unroll 3
-        for (int c = part; c < kRow / 8; c += kTpr) {
-          uint32_t hi[2] = {0u, 0u}, lo[2] = {0u, 0u};
-          if (live) {
-            const uint4 v = *reinterpret_cast<const uint4*>(src + c * 8);
-            const float f = (c < kLat / 8 ? ds0 : ds1) * inv;
-            const uint32_t q4[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const float x0 = __uint_as_float(q4[k] << 16) * f, x1 = __uint_as_float(q4[k] & 0xFFFF0000u) * f;
-              const __nv_fp8x2_storage_t h2 = __nv_cvt_float2_to_fp8x2(make_float2(x0, x1), __NV_SATFINITE, __NV_E4M3);
-              const float2 hf = e4m3x2_to_float2(h2);
-              const __nv_fp8x2_storage_t l2 =
-                  __nv_cvt_float2_to_fp8x2(make_float2(x0 - hf.x, x1 - hf.y), __NV_SATFINITE, __NV_E4M3);
-              hi[k >> 1] |= uint32_t(h2) << (16 * (k & 1));
-              lo[k >> 1] |= uint32_t(l2) << (16 * (k & 1));
+        for (int ci = 0; ci < kCh; ++ci) {
+          const int c = part + ci * kTpr;
+          const float f = (c < kLat / 8 ? ds0 : ds1) * inv;
+          uint32_t hi[2], lo[2];
+          const uint32_t q4[4] = {qv[ci].x, qv[ci].y, qv[ci].z, qv[ci].w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float x0 = __uint_as_float(q4[k] << 16) * f, x1 = __uint_as_float(q4[k] & 0xFFFF0000u) * f;
+            const __nv_fp8x2_storage_t h2 = __nv_cvt_float2_to_fp8x2(make_float2(x0, x1), __NV_SATFINITE, __NV_E4M3);
+            const float2 hf = e4m3x2_to_float2(h2);
+            const __nv_fp8x2_storage_t l2 =
+                __nv_cvt_float2_to_fp8x2(make_float2(x0 - hf.x, x1 - hf.y), __NV_SATFINITE, __NV_E4M3);
+            if (k & 1) {
+              hi[k >> 1] |= uint32_t(h2) << 16;
+              lo[k >> 1] |= uint32_t(l2) << 16;
+            } else {
+              hi[k >> 1] = uint32_t(h2);
+              lo[k >> 1] = uint32_t(l2);
             }
           }
           const int ch = c * 8;
@@ -489,38 +507,60 @@ __global__ void __launch_bounds__(Cfg<NR>::kThreads, 1)
         ok = tc::mbar_wait(tc::smem_u32(&ctl.s_full[gi & 1]), uint32_t(gi >> 1) & 1u, abort, kWaitLimitNs);
         if (!ok) break;
         tc::tc_fence_after();
-        float e[RW];
-        {
-          float lo[RW];
-          const uint32_t ts = tmem + uint32_t((gi & 1) * C::kSCols + rg) + lane_off;
-          tc::tmem_ld_cols<RW>(ts, e);
-          tc::tmem_ld_cols<RW>(ts + uint32_t(NR), lo);
-          tc::tmem_wait_ld();
-#pragma unroll
-          for (int r = 0; r < RW; ++r) e[r] += lo[r];
-        }
-        // e = t - m_ref + kC0, in log2 units; -inf where the row does not see the key
-#pragma unroll
-        for (int r = 0; r < RW; r += 4) {
-          const float4 sc = *reinterpret_cast<const float4*>(&ctl.scale[rg + r]);
-          const float4 c8 = *reinterpret_cast<const float4*>(&ctl.c8[rg + r]);
-          e[r] = fmaf(e[r], sc.x, c8.x);
-          e[r + 1] = fmaf(e[r + 1], sc.y, c8.y);
-          e[r + 2] = fmaf(e[r + 2], sc.z, c8.z);
-          e[r + 3] = fmaf(e[r + 3], sc.w, c8.w);
-        }
         const int64_t t_end = w.k0 + int64_t(i + 1) * kKvTile;
         const bool dead = t_end - kKvTile + x >= w.k1;  // this key is past the end
-        if (t_end > w.k1 || t_end - 1 > int64_t(lim_min)) {
-          const int key = int(t_end) - kKvTile + x;
+        const bool masked = t_end > w.k1 || t_end - 1 > int64_t(lim_min);
+        float e[RW];
+        uint32_t hi[RW / 4], lo[RW / 4];
+        // e = t - m_ref + kC0, in log2 units; -inf where the row does not see the key
+        auto logits = [&] {
+          float s_lo[RW];
+          const uint32_t ts = tmem + uint32_t((gi & 1) * C::kSCols + rg) + lane_off;
+          tc::tmem_ld_cols<RW>(ts, e);
+          tc::tmem_ld_cols<RW>(ts + uint32_t(NR), s_lo);
+          tc::tmem_wait_ld();
 #pragma unroll
-          for (int r = 0; r < RW; ++r)
-            if (dead || key > ctl.lim[rg + r]) e[r] = -INFINITY;
-        }
+          for (int r = 0; r < RW; r += 4) {
+            const float4 sc = *reinterpret_cast<const float4*>(&ctl.scale[rg + r]);
+            const float4 c8 = *reinterpret_cast<const float4*>(&ctl.c8[rg + r]);
+            e[r] = fmaf(e[r] + s_lo[r], sc.x, c8.x);
+            e[r + 1] = fmaf(e[r + 1] + s_lo[r + 1], sc.y, c8.y);
+            e[r + 2] = fmaf(e[r + 2] + s_lo[r + 2], sc.z, c8.z);
+            e[r + 3] = fmaf(e[r + 3] + s_lo[r + 3], sc.w, c8.w);
+          }
+          if (masked) {
+            const int key = int(t_end) - kKvTile + x;
+#pragma unroll
+            for (int r = 0; r < RW; ++r)
+              if (dead || key > ctl.lim[rg + r]) e[r] = -INFINITY;
+          }
+        };
+        // e becomes p = 2^e, hi and lo its terms
+        auto weights = [&] {
+#pragma unroll
+          for (int r = 0; r < RW; r += 2) {
+            e[r] = fast_exp2(e[r]);
+            e[r + 1] = fast_exp2(e[r + 1]);
+            const __nv_fp8x2_storage_t h2 = __nv_cvt_float2_to_fp8x2(make_float2(e[r], e[r + 1]), __NV_SATFINITE, __NV_E4M3);
+            const float2 hf = e4m3x2_to_float2(h2);
+            const __nv_fp8x2_storage_t l2 =
+                __nv_cvt_float2_to_fp8x2(make_float2(e[r] - hf.x, e[r + 1] - hf.y), __NV_SATFINITE, __NV_E5M2);
+            if ((r & 2) == 0) {
+              hi[r / 4] = uint32_t(h2);
+              lo[r / 4] = uint32_t(l2);
+            } else {
+              hi[r / 4] |= uint32_t(h2) << 16;
+              lo[r / 4] |= uint32_t(l2) << 16;
+            }
+          }
+        };
+        logits();
         bool settled = false, rescale = false;
         if (i > 0) {
-          // one bound for all rows and keys of the group first: it holds once
-          // the references have settled, and spares the per-row maxima
+          // One bound for all rows and keys of the group: it holds once the
+          // references have settled, and spares the per-row maxima. The weights
+          // are formed while the other warps' bounds arrive, and formed again
+          // where it does not hold.
           float m = e[0];
 #pragma unroll
           for (int r = 1; r < RW; ++r) m = fmaxf(m, e[r]);
@@ -529,11 +569,13 @@ __global__ void __launch_bounds__(Cfg<NR>::kThreads, 1)
           __syncwarp();
           const uint32_t bar = tc::smem_u32(&ctl.bound_bar[grp][xb & 1]);
           if (lane == 0) tc::mbar_arrive(bar);
+          weights();
           ok = tc::mbar_wait(bar, uint32_t(xb >> 1) & 1u, abort, kWaitLimitNs);
           if (!ok) break;
           const float4 b = *reinterpret_cast<const float4*>(&ctl.bound[grp][xb & 1][0]);
           settled = fmaxf(fmaxf(b.x, b.y), fmaxf(b.z, b.w)) <= kC0 + kTau;
           ++xb;
+          if (!settled) logits();
         }
         if (!settled) {
           float tmp[RW];
@@ -576,25 +618,10 @@ __global__ void __launch_bounds__(Cfg<NR>::kThreads, 1)
             l_part[r + 2] *= al.z;
             l_part[r + 3] *= al.w;
           }
+          weights();
         }
-        uint32_t hi[RW / 4], lo[RW / 4];
 #pragma unroll
-        for (int r = 0; r < RW; r += 2) {
-          const float p0 = fast_exp2(e[r]), p1 = fast_exp2(e[r + 1]);
-          l_part[r] += p0;
-          l_part[r + 1] += p1;
-          const __nv_fp8x2_storage_t h2 = __nv_cvt_float2_to_fp8x2(make_float2(p0, p1), __NV_SATFINITE, __NV_E4M3);
-          const float2 hf = e4m3x2_to_float2(h2);
-          const __nv_fp8x2_storage_t l2 =
-              __nv_cvt_float2_to_fp8x2(make_float2(p0 - hf.x, p1 - hf.y), __NV_SATFINITE, __NV_E5M2);
-          if ((r & 2) == 0) {
-            hi[r / 4] = uint32_t(h2);
-            lo[r / 4] = uint32_t(l2);
-          } else {
-            hi[r / 4] |= uint32_t(h2) << 16;
-            lo[r / 4] |= uint32_t(l2) << 16;
-          }
-        }
+        for (int r = 0; r < RW; ++r) l_part[r] += e[r];
         // the P buffer is free, and O complete up to the tile before, once
         // that product is done
         if (gi >= C::kPBufs) {
@@ -662,13 +689,14 @@ __global__ void __launch_bounds__(Cfg<NR>::kThreads, 1)
       if (lane < RW) {
         const float l = (ctl.red[grp][0][lane] + ctl.red[grp][1][lane]) + (ctl.red[grp][2][lane] + ctl.red[grp][3][lane]);
         const int gr = r0 + rg + lane;
-        ctl.alpha[rg + lane] = empty_row ? 0.f : 1.f / l;  // (the same in the four warps)
-        if (qd == 0 && rg + lane < nr) {
-          const float m = kC0 - c8_row;
+        // the output's factor: a partial stays as it is, an empty row becomes 0 (the same in the four warps)
+        ctl.alpha[rg + lane] = w.part >= 0 ? 1.f : (empty_row ? 0.f : ds0 / l);
+        if (qd == 0) {
+          const float m = kC0 - c8_row;  // sum of 2^(t - m + kC0) = l
           if (w.part >= 0) {
-            p.m_part[int64_t(w.part) * p.n_q + gr] = empty_row ? -INFINITY : m;
-            p.l_part[int64_t(w.part) * p.n_q + gr] = l * (1.f / 128.f);
-          } else if (p.lse) {
+            p.m_part[int64_t(w.part) * rows_pad + gr] = empty_row ? -INFINITY : m;
+            p.l_part[int64_t(w.part) * rows_pad + gr] = l;
+          } else if (p.lse && rg + lane < nr) {
             p.lse[int64_t(w.b) * p.n_q + gr] = empty_row ? -INFINITY : (m + fast_log2(l) - kC0) * kLn2;
           }
         }
@@ -677,29 +705,43 @@ __global__ void __launch_bounds__(Cfg<NR>::kThreads, 1)
       ok = tc::mbar_wait(tc::smem_u32(&ctl.o_full[(g0 - 1) & 1]), uint32_t((g0 - 1) >> 1) & 1u, abort, kWaitLimitNs);
       if (!ok) break;
       tc::tc_fence_after();
-#pragma unroll 1
-      for (int j = 0; j < 4; ++j) {
-#pragma unroll 1
-        for (int c = 0; c < RW; c += 16) {
-          float v[16];
-          tc::tmem_ld16(tO + uint32_t(j * NR + rg + c) + lane_off, v);
+      if (w.part >= 0) {
+        // a partial: four rows of a channel are one 16-byte store, a warp's 512 bytes in a row
+        float4* dst = reinterpret_cast<float4*>(p.o_part) +
+                      ((int64_t(w.part) * p.n_row_tiles + r0 / NR) * 4 * (NR / 4) + rg / 4) * 128 + x;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float v[RW];
+          tc::tmem_ld_cols<RW>(tO + uint32_t(j * NR + rg) + lane_off, v);
           tc::tmem_wait_ld();
-          int gr = r0 + rg + c;
+#pragma unroll
+          for (int c = 0; c < RW / 4; ++c)
+            dst[(j * (NR / 4) + c) * 128] = make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+        }
+      } else {
+        // the output: two lanes trade, so that each holds two channels of one
+        // row (even lanes the even rows) and a store is 4 bytes
+        const bool odd = lane & 1;
+        uint16_t* dst = p.out + (int64_t(w.b) * p.q_len) * p.out_ts + (x & ~1);
+#pragma unroll 1
+        for (int j = 0; j < 4; ++j) {
+          float v[RW];
+          tc::tmem_ld_cols<RW>(tO + uint32_t(j * NR + rg) + lane_off, v);
+          tc::tmem_wait_ld();
+          int gr = r0 + rg + (odd ? 1 : 0);
           int tq = gr / p.h, h = gr - tq * p.h;
 #pragma unroll
-          for (int k = 0; k < 16; ++k, ++gr) {
-            if (rg + c + k < nr) {
-              // an empty row's accumulator may hold 0 x NaN: it is not used
-              const float il = ctl.alpha[rg + c + k];
-              const float o = il == 0.f ? 0.f : v[k] * il;
-              if (w.part >= 0)
-                p.o_part[(int64_t(w.part) * p.n_q + gr) * kLat + 128 * j + x] = o;
-              else
-                p.out[(int64_t(w.b) * p.q_len + tq) * p.out_ts + int64_t(h) * p.out_hs + 128 * j + x] =
-                    float_to_out_bits(o * ds0, p.out_f16);
-            }
-            if (++h == p.h) {
-              h = 0;
+          for (int k = 0; k < RW; k += 2) {
+            const float2 f = *reinterpret_cast<const float2*>(&ctl.alpha[rg + k]);
+            const float a = f.x == 0.f ? 0.f : v[k] * f.x, b = f.y == 0.f ? 0.f : v[k + 1] * f.y;
+            const float other = __shfl_xor_sync(0xFFFFFFFFu, odd ? a : b, 1);
+            const float lo_c = odd ? other : a, hi_c = odd ? b : other;
+            if (rg + k + (odd ? 1 : 0) < nr)
+              *reinterpret_cast<uint32_t*>(dst + int64_t(tq) * p.out_ts + int64_t(h) * p.out_hs + 128 * j) =
+                  uint32_t(float_to_out_bits(lo_c, p.out_f16)) | (uint32_t(float_to_out_bits(hi_c, p.out_f16)) << 16);
+            h += 2;
+            while (h >= p.h) {
+              h -= p.h;
               ++tq;
             }
           }

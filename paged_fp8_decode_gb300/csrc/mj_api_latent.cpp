@@ -128,7 +128,7 @@ int mj_latent_slots(int sm_count, int q_len, int h) {
 
 int mj_latent_plan_size(int slots, int max_num_seqs, size_t* words) {
   if (!words || slots < 1 || max_num_seqs < 0) return MJ_ERR_INVALID_ARG;
-  *words = size_t(mj::latent_plan_off_words(slots) + mj::latent_plan_split_words(max_num_seqs) +
+  *words = size_t(mj::latent_plan_slot_words(slots) + mj::latent_plan_split_words(max_num_seqs) +
                   4 * mj::latent_plan_max_work(slots, max_num_seqs));
   return MJ_OK;
 }
@@ -152,8 +152,8 @@ int mj_latent_plan(const int32_t* seq_lens_host, int num_seqs, int max_num_seqs,
     return seq_lens_host[b] > 0 ? (int64_t(seq_lens_host[b]) + margin + mj::kKvTile - 1) / mj::kKvTile : 0;
   };
   std::memset(plan_host, 0, need * sizeof(int32_t));
-  int32_t* off = plan_host;
-  int32_t* splits = off + mj::latent_plan_off_words(slots);
+  int32_t* table = plan_host;
+  int32_t* splits = table + mj::latent_plan_slot_words(slots);
   int32_t* work = splits + mj::latent_plan_split_words(max_num_seqs);
 
   // The requests' tiles in order, cut so that no slot's cost (its tiles, and
@@ -169,7 +169,6 @@ int mj_latent_plan(const int32_t* seq_lens_host, int num_seqs, int max_num_seqs,
       while (at < t) {
         if (used + kRowCost + 1 > limit) {  // no room for a row here
           if (++slot >= slots) return false;
-          if (write) off[slot] = rows;
           used = 0;
         }
         const int64_t take = std::min(t - at, limit - used - kRowCost);
@@ -179,6 +178,13 @@ int mj_latent_plan(const int32_t* seq_lens_host, int num_seqs, int max_num_seqs,
           w[1] = int32_t(at);
           w[2] = int32_t(at + take);
           w[3] = -1;
+          int32_t* e = table + 4 * int64_t(slot);
+          if (used == 0) {  // the slot's first row
+            e[0] = rows;
+            e[2] = w[0];
+            e[3] = w[1];
+          }
+          e[1] = rows + 1;
         }
         ++rows;
         at += take;
@@ -193,8 +199,6 @@ int mj_latent_plan(const int32_t* seq_lens_host, int num_seqs, int max_num_seqs,
         parts += rows - first_row;
       }
     }
-    if (write)
-      for (int s = slot + 1; s <= slots; ++s) off[s] = rows;
     return true;
   };
   int64_t lo = kRowCost + 1, hi = std::max<int64_t>(lo, total);  // one slot holds everything at `total`
@@ -211,7 +215,9 @@ int mj_latent_plan(const int32_t* seq_lens_host, int num_seqs, int max_num_seqs,
 
 int mj_latent_workspace_size(int slots, int q_len, int h, size_t* bytes) {
   if (!bytes || slots < 1 || q_len < 1 || h < 1) return MJ_ERR_INVALID_ARG;
-  *bytes = mj::kWsHeader + size_t(2) * slots * size_t(q_len) * h * (MJ_LATENT_DIM + 2) * sizeof(float);
+  const int64_t tile = latent_row_tile(int64_t(q_len) * h);
+  const int64_t rows = (int64_t(q_len) * h + tile - 1) / tile * tile;
+  *bytes = mj::kWsHeader + size_t(2) * slots * size_t(rows) * (MJ_LATENT_DIM + 2) * sizeof(float);
   return MJ_OK;
 }
 
@@ -274,8 +280,8 @@ int mj_latent_attention(const mj_latent_args* a, void* stream) {
   const int64_t max_work = mj::latent_plan_max_work(a->slots, a->max_num_seqs);
   if (max_work > INT32_MAX) return MJ_ERR_INVALID_ARG;
   p.max_work = int(max_work);
-  p.cta_off = a->plan;
-  p.splits = p.cta_off + mj::latent_plan_off_words(a->slots);
+  p.slot_table = a->plan;
+  p.splits = p.slot_table + mj::latent_plan_slot_words(a->slots);
   p.work = p.splits + mj::latent_plan_split_words(a->max_num_seqs);
   p.out = static_cast<uint16_t*>(a->out);
   p.out_f16 = a->out_dtype == MJ_OUT_F16 ? 1 : 0;
@@ -284,7 +290,7 @@ int mj_latent_attention(const mj_latent_args* a, void* stream) {
   p.lse = a->lse;
   char* ws = static_cast<char*>(a->workspace);
   p.status = reinterpret_cast<uint32_t*>(ws);
-  const int64_t rows = 2 * int64_t(a->slots) * n_q;
+  const int64_t rows = 2 * int64_t(a->slots) * p.n_row_tiles * p.row_tile;
   p.o_part = reinterpret_cast<float*>(ws + mj::kWsHeader);
   p.m_part = p.o_part + rows * MJ_LATENT_DIM;
   p.l_part = p.m_part + rows;

@@ -126,7 +126,7 @@ struct LatentParams {
   int64_t bt_stride, bt_len;
   const int32_t* seq_lens;
   int slots, max_work;     // plan: slots, rows of the work list
-  const int32_t* cta_off;  // [slots + 1]
+  const int32_t* slot_table;  // [slots][4]: first work row, end, that row's request and first tile
   const int32_t* splits;   // [max_num_seqs][2]: first partial, number of them (0: not split)
   const int32_t* work;     // [max_work][4]: request, first tile, end tile, partial (-1: none)
   uint16_t* out;
@@ -134,14 +134,18 @@ struct LatentParams {
   int64_t out_ts, out_hs;
   float* lse;
   uint32_t* status;
-  float* o_part;  // [2 * slots][n_q][512]
-  float* m_part;  // [2 * slots][n_q]
-  float* l_part;
+  // partials, unnormalised: [2 * slots][row tiles][4 channel blocks][row_tile / 4][128 channels][4 rows]
+  float* o_part;
+  float* m_part;  // [2 * slots][row tiles * row_tile]: reference max (log2 units), -inf without a key
+  float* l_part;  // likewise: sum of the weights, scaled like o_part
   int evict_first;
 };
 
+// log2 of the weight that a row's reference max has in the latent kernel's sums.
+constexpr float kLatentC0 = 6.f;
+
 // Words (int32) of the plan buffer's parts, each a multiple of 4.
-inline int64_t latent_plan_off_words(int slots) { return (int64_t(slots) + 1 + 3) / 4 * 4; }
+inline int64_t latent_plan_slot_words(int slots) { return 4 * int64_t(slots); }
 inline int64_t latent_plan_split_words(int max_num_seqs) { return (2 * int64_t(max_num_seqs) + 3) / 4 * 4; }
 inline int64_t latent_plan_max_work(int slots, int max_num_seqs) { return int64_t(slots) + max_num_seqs; }
 

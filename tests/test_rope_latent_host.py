@@ -96,12 +96,19 @@ def test_turns_refuse(bad):
 
 # ---------------------------------------------------------------- the plan
 def plan_parts(plan, slots, max_num_seqs):
-    off_words = (slots + 1 + 3) // 4 * 4
     split_words = (2 * max_num_seqs + 3) // 4 * 4
-    off = plan[:slots + 1]
-    splits = plan[off_words:off_words + 2 * max_num_seqs].reshape(-1, 2)
-    work = plan[off_words + split_words:off_words + split_words + 4 * (slots + max_num_seqs)].reshape(-1, 4)
-    return off, splits, work
+    table = plan[:4 * slots].reshape(-1, 4)
+    splits = plan[4 * slots:4 * slots + 2 * max_num_seqs].reshape(-1, 2)
+    work = plan[4 * slots + split_words:4 * slots + split_words + 4 * (slots + max_num_seqs)].reshape(-1, 4)
+    # the slots' rows follow each other; a slot's entry repeats its first row's request and tile
+    off = [0]
+    for first, end, b, tile in table:
+        if end > first:
+            assert first == off[-1] and (b, tile) == tuple(work[first][:2])
+        else:
+            assert not (first or end or b or tile)
+        off.append(max(off[-1], int(end)))
+    return np.array(off), splits, work
 
 
 def check_plan(lens, slots, max_num_seqs, margin, plan):
@@ -178,7 +185,8 @@ def test_slots_and_sizes():
     assert mj.mj_latent_slots(152, 5, 128) == 15
     assert mj.mj_latent_slots(4, 8, 128) == 1
     assert mj.mj_latent_plan_size(152, 10) % 4 == 0
-    assert mj.mj_latent_workspace_size(10, 2, 3) == 256 + 2 * 10 * 6 * 514 * 4
+    assert mj.mj_latent_workspace_size(10, 2, 3) == 256 + 2 * 10 * 16 * 514 * 4
+    assert mj.mj_latent_workspace_size(10, 5, 13) == 256 + 2 * 10 * 128 * 514 * 4
 
 
 # ---------------------------------------------------------------- refusals of the C calls
