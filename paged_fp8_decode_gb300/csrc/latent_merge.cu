@@ -6,11 +6,10 @@
 // never have been written).
 //
 // Bound by latency and L2: tens of megabytes of partials at most, just
-// written. A task is four rows of 128 channels, one 16-byte load a thread and
-// partial. Many tasks: 128 threads each, which request four partials at a
-// time. Few (a long request split over the whole GPU): four groups of 128
-// threads share a task's partials and meet in shared memory, so that all their
-// loads are in flight together.
+// written. A task is four rows of 32 channels, one 16-byte load a lane and
+// partial. Many tasks: a warp each. Few (a long request split over the whole
+// GPU): the 16 warps of a CTA share a task's partials and meet in shared
+// memory, so that all their loads are in flight together.
 #include "mj_device.cuh"
 #include "mj_internal.h"
 #include "tc_ptx.cuh"
@@ -34,20 +33,25 @@ __device__ __forceinline__ void add_w4(float4& a, float4 w, float4 b) {
   a.w = add_w(a.w, w.w, b.w);
 }
 
-template <int G>  // groups of 128 threads
-__global__ void __launch_bounds__(128 * G) latent_merge_kernel(LatentParams p) {
-  constexpr int U = 4;  // partials in flight a thread
-  __shared__ float4 acc_sh[G > 1 ? G - 1 : 1][128], sum_sh[G > 1 ? G - 1 : 1];
+constexpr int kWarps = 16;
+
+template <int G>  // warps a task
+__global__ void __launch_bounds__(32 * kWarps) latent_merge_kernel(LatentParams p) {
+  constexpr int U = 4;  // partials in flight a warp
+  __shared__ float4 acc_sh[G > 1 ? G : 1][32], sum_sh[G > 1 ? G : 1];
   tc::grid_launch_dependents();
   tc::grid_dependency_wait();
-  const int x = threadIdx.x % 128, grp = threadIdx.x / 128;
-  const int quads = p.row_tile / 4;  // tasks of a row tile and channel block
-  int64_t task = blockIdx.x;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, grp = warp % G;
+  const int quads = p.row_tile / 4;  // row groups of a tile
+  int64_t task = int64_t(blockIdx.x) * (kWarps / G) + warp / G;
+  const int x = int(task & 3) * 32 + lane;  // channel of the block
+  task >>= 2;
   const int quad = int(task % quads);
   task /= quads;
   const int j = int(task % kBlocks);
   task /= kBlocks;
   const int tile = int(task % p.n_row_tiles), b = int(task / p.n_row_tiles);
+  if (b >= p.num_seqs) return;  // (G > 1: whole CTAs; the grid is exact)
   const int2 sp = reinterpret_cast<const int2*>(p.splits)[b];
   const int row = tile * p.row_tile + 4 * quad;
   const int n = min(sp.y, 2 * p.slots - sp.x);
@@ -78,8 +82,13 @@ __global__ void __launch_bounds__(128 * G) latent_merge_kernel(LatentParams p) {
     }
   };
   load(grp);
-#pragma unroll 8
-  for (int s = 0; s < n; ++s) M = max4(M, mp[int64_t(s) * rows4]);
+  if (G == 1 && n <= U) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) M = max4(M, m[u]);
+  } else {
+    for (int s = lane; s < n; s += 32) M = max4(M, mp[int64_t(s) * rows4]);
+    M = make_float4(warp_max(M.x), warp_max(M.y), warp_max(M.z), warp_max(M.w));
+  }
   for (int s0 = grp; s0 < n; s0 += U * G) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -90,16 +99,14 @@ __global__ void __launch_bounds__(128 * G) latent_merge_kernel(LatentParams p) {
     if (s0 + U * G < n) load(s0 + U * G);
   }
   if constexpr (G > 1) {
-    if (grp > 0) {
-      acc_sh[grp - 1][x] = acc;
-      if (x == 0) sum_sh[grp - 1] = sum;
-    }
+    acc_sh[grp][lane] = acc;
+    if (lane == 0) sum_sh[grp] = sum;
     __syncthreads();
     if (grp > 0) return;
     const float4 one = make_float4(1.f, 1.f, 1.f, 1.f);
 #pragma unroll
-    for (int k = 0; k < G - 1; ++k) {
-      add_w4(acc, one, acc_sh[k][x]);
+    for (int k = 1; k < G; ++k) {
+      add_w4(acc, one, acc_sh[k][lane]);
       add_w4(sum, one, sum_sh[k]);
     }
   }
@@ -134,9 +141,10 @@ __global__ void __launch_bounds__(128 * G) latent_merge_kernel(LatentParams p) {
 template <int G>
 cudaError_t launch(const LatentParams& p, int64_t tasks, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
-  if (tasks > INT32_MAX) return cudaErrorInvalidConfiguration;
-  cfg.gridDim = dim3(unsigned(tasks));
-  cfg.blockDim = dim3(128 * G);
+  const int64_t ctas = (tasks + kWarps / G - 1) / (kWarps / G);
+  if (ctas > INT32_MAX) return cudaErrorInvalidConfiguration;
+  cfg.gridDim = dim3(unsigned(ctas));
+  cfg.blockDim = dim3(32 * kWarps);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -149,9 +157,9 @@ cudaError_t launch(const LatentParams& p, int64_t tasks, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_latent_merge(const LatentParams& p, cudaStream_t stream) {
-  const int64_t tasks = int64_t(p.num_seqs) * p.n_row_tiles * kBlocks * (p.row_tile / 4);
-  // four groups a task while the tasks' CTAs still fit beside each other
-  return tasks <= int64_t(p.slots) * p.n_row_tiles ? launch<4>(p, tasks, stream) : launch<1>(p, tasks, stream);
+  const int64_t tasks = int64_t(p.num_seqs) * p.n_row_tiles * kBlocks * p.row_tile;  // x 4 channel quarters / 4 rows
+  // a CTA a task while those CTAs are few
+  return tasks <= 2 * int64_t(p.slots) * p.n_row_tiles ? launch<kWarps>(p, tasks, stream) : launch<1>(p, tasks, stream);
 }
 
 }  // namespace mj

@@ -59,6 +59,7 @@ constexpr int kMaxDynSmem = 227 * 1024;
 // P is scaled so that the row's reference max has weight 2^6; the reference
 // moves once a tile's max exceeds it by more than kTau, so p <= 2^8.5 < 448.
 constexpr float kC0 = kLatentC0, kTau = 2.5f;
+constexpr float kFar = 100.f;  // binades: a longer move starts again from the row maxima
 
 template <int NR>
 struct Cfg {
@@ -82,22 +83,23 @@ struct Cfg {
 
 template <int NR>
 struct Ctrl {
-  uint64_t full[12], empty[12];
-  uint64_t rfull[2], rempty[2];
+  uint64_t full[Cfg<NR>::kRing], empty[Cfg<NR>::kRing];
+  uint64_t rfull[Cfg<NR>::kRopeRing], rempty[Cfg<NR>::kRopeRing];
   uint64_t s_full[2], p_full[2], o_full[2];
   uint64_t q_ready;
-  uint64_t bound_bar[2][2];  // [group][exchange & 1]: the group's warps have posted their bounds
+  uint64_t bound_bar[2][2];  // [group][exchange & 1]: the group's warps have posted their rows
   uint64_t row_bar[2];       // ... their row maxima
   uint64_t sum_bar[2];       // ... their row sums
   uint64_t drain;
   uint32_t tmem_base;
   int abort;
-  alignas(16) float bound[2][2][4];
-  alignas(16) float red[2][4][NR == 64 ? 32 : 16];  // per warp: row maxima, at the end row sums
+  alignas(16) uint32_t above[2][2][4];  // [group][exchange & 1]: per warp, the rows whose reference it asks to move
+  alignas(16) uint8_t by[2][2][4][NR == 64 ? 32 : 16];  // ... and by how many binades
+  alignas(16) float red[2][4][NR == 64 ? 32 : 16];      // per warp: row maxima, at the end row sums
   alignas(16) float scale[NR];  // logit (log2 units) per unit of S
   alignas(16) float c8[NR];     // kC0 - m_ref
-  alignas(16) float alpha[NR];  // rescale factors of the current tile
-  alignas(16) float shift[NR];  // the reference's move
+  alignas(16) float move[NR];   // first tile of a work row: the reference's move; later ones: 2^-move; at the end:
+                                // the output's factor
   alignas(16) int lim[NR];      // last visible key
 };
 
@@ -107,6 +109,13 @@ constexpr int smem_bytes() {
 }
 static_assert(smem_bytes<64>() <= kMaxDynSmem && smem_bytes<32>() <= kMaxDynSmem && smem_bytes<16>() <= kMaxDynSmem,
               "shared memory");
+
+// max over the warp, in every lane (NaN lanes do not count)
+__device__ __forceinline__ float redux_max(float v) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
 
 // Reduce N per-lane values over the warp's lanes: row r ends up in lanes
 // r * (32 / N) .. + 32 / N - 1 (halve the rows a lane keeps, exchange the rest).
@@ -535,49 +544,99 @@ __global__ void __launch_bounds__(Cfg<NR>::kThreads, 1)
               if (dead || key > ctl.lim[rg + r]) e[r] = -INFINITY;
           }
         };
-        // e becomes p = 2^e, hi and lo its terms
-        auto weights = [&] {
+        auto exps = [&] {
 #pragma unroll
-          for (int r = 0; r < RW; r += 2) {
-            e[r] = fast_exp2(e[r]);
-            e[r + 1] = fast_exp2(e[r + 1]);
-            const __nv_fp8x2_storage_t h2 = __nv_cvt_float2_to_fp8x2(make_float2(e[r], e[r + 1]), __NV_SATFINITE, __NV_E4M3);
-            const float2 hf = e4m3x2_to_float2(h2);
-            const __nv_fp8x2_storage_t l2 =
-                __nv_cvt_float2_to_fp8x2(make_float2(e[r] - hf.x, e[r + 1] - hf.y), __NV_SATFINITE, __NV_E5M2);
-            if ((r & 2) == 0) {
-              hi[r / 4] = uint32_t(h2);
-              lo[r / 4] = uint32_t(l2);
-            } else {
-              hi[r / 4] |= uint32_t(h2) << 16;
-              lo[r / 4] |= uint32_t(l2) << 16;
-            }
+          for (int r = 0; r < RW; ++r) e[r] = fast_exp2(e[r]);
+        };
+        // the two terms of p = e
+        auto terms_of = [&](int r) {  // rows r, r + 1
+          const __nv_fp8x2_storage_t h2 = __nv_cvt_float2_to_fp8x2(make_float2(e[r], e[r + 1]), __NV_SATFINITE, __NV_E4M3);
+          const float2 hf = e4m3x2_to_float2(h2);
+          const __nv_fp8x2_storage_t l2 =
+              __nv_cvt_float2_to_fp8x2(make_float2(e[r] - hf.x, e[r + 1] - hf.y), __NV_SATFINITE, __NV_E5M2);
+          if ((r & 2) == 0) {
+            hi[r / 4] = uint32_t(h2);
+            lo[r / 4] = uint32_t(l2);
+          } else {
+            hi[r / 4] |= uint32_t(h2) << 16;
+            lo[r / 4] |= uint32_t(l2) << 16;
           }
         };
+        auto terms = [&] {
+#pragma unroll
+          for (int r = 0; r < RW; r += 2) terms_of(r);
+        };
         logits();
-        bool settled = false, rescale = false;
+        // Rows whose reference moves (bits; the same in every thread of the
+        // group). A warp that finds weights above the limit posts the rows and
+        // how many binades each has to move; the weights are formed while the
+        // other warps' rows arrive, and scaled by the moves.
+        uint32_t moving = 0;
+        bool anew = i == 0;  // from the row maxima: a first tile, or a move too far for a byte
         if (i > 0) {
-          // One bound for all rows and keys of the group: it holds once the
-          // references have settled, and spares the per-row maxima. The weights
-          // are formed while the other warps' bounds arrive, and formed again
-          // where it does not hold.
           float m = e[0];
 #pragma unroll
           for (int r = 1; r < RW; ++r) m = fmaxf(m, e[r]);
-          m = warp_max(m);
-          if (lane == 0) ctl.bound[grp][xb & 1][qd] = m;
+          uint32_t above = 0;
+          if (__any_sync(0xFFFFFFFFu, m > kC0 + kTau)) {
+#pragma unroll
+            for (int r = 0; r < RW; ++r) above |= e[r] > kC0 + kTau ? 1u << r : 0u;
+            above = __reduce_or_sync(0xFFFFFFFFu, above);
+#pragma unroll
+            for (int r = 0; r < RW; ++r)
+              if (above >> r & 1u) {
+                const float v = redux_max(e[r]) - kC0;
+                if (lane == 0) ctl.by[grp][xb & 1][qd][r] = uint8_t(fminf(ceilf(v), kFar));
+              }
+          }
+          if (lane == 0) ctl.above[grp][xb & 1][qd] = above;
           __syncwarp();
           const uint32_t bar = tc::smem_u32(&ctl.bound_bar[grp][xb & 1]);
           if (lane == 0) tc::mbar_arrive(bar);
-          weights();
+          exps();
+          terms();
           ok = tc::mbar_wait(bar, uint32_t(xb >> 1) & 1u, abort, kWaitLimitNs);
           if (!ok) break;
-          const float4 b = *reinterpret_cast<const float4*>(&ctl.bound[grp][xb & 1][0]);
-          settled = fmaxf(fmaxf(b.x, b.y), fmaxf(b.z, b.w)) <= kC0 + kTau;
+          const uint4 b = *reinterpret_cast<const uint4*>(&ctl.above[grp][xb & 1][0]);
+          moving = (b.x | b.y) | (b.z | b.w);
+          if (moving) {
+            // lane r moves row r's reference (the four warps compute and store the same values)
+            int d = 0;
+            if (lane < RW) {
+              if (b.x >> lane & 1u) d = max(d, int(ctl.by[grp][xb & 1][0][lane]));
+              if (b.y >> lane & 1u) d = max(d, int(ctl.by[grp][xb & 1][1][lane]));
+              if (b.z >> lane & 1u) d = max(d, int(ctl.by[grp][xb & 1][2][lane]));
+              if (b.w >> lane & 1u) d = max(d, int(ctl.by[grp][xb & 1][3][lane]));
+            }
+            anew = __any_sync(0xFFFFFFFFu, d >= int(kFar));
+            if (!anew) {
+              const float f = __int_as_float((127 - d) << 23);  // 2^-d
+              if (lane < RW) {
+                c8_row -= float(d);
+                ctl.c8[rg + lane] = c8_row;
+                ctl.move[rg + lane] = f;
+              }
+              __syncwarp();
+#pragma unroll
+              for (int r = 0; r < RW; r += 4) {
+                if (moving >> r & 0xFu) {
+                  const float4 al = *reinterpret_cast<const float4*>(&ctl.move[rg + r]);
+                  const float a4[4] = {al.x, al.y, al.z, al.w};
+#pragma unroll
+                  for (int k = 0; k < 4; ++k) {
+                    l_part[r + k] *= a4[k];
+                    e[r + k] *= a4[k];
+                  }
+                  terms_of(r);
+                  terms_of(r + 2);
+                }
+              }
+            }
+          }
           ++xb;
-          if (!settled) logits();
         }
-        if (!settled) {
+        if (anew) {
+          if (i > 0) logits();
           float tmp[RW];
 #pragma unroll
           for (int r = 0; r < RW; ++r) tmp[r] = e[r];
@@ -589,37 +648,37 @@ __global__ void __launch_bounds__(Cfg<NR>::kThreads, 1)
           ok = tc::mbar_wait(bar, uint32_t(xr) & 1u, abort, kWaitLimitNs);
           if (!ok) break;
           ++xr;
-          // lane r moves row r's reference (the four warps compute and store
-          // the same values)
           bool moved = false;
           if (lane < RW) {
             const float em = fmaxf(fmaxf(ctl.red[grp][0][lane], ctl.red[grp][1][lane]),
                                    fmaxf(ctl.red[grp][2][lane], ctl.red[grp][3][lane]));
-            const float d = em - kC0;
-            moved = em != -INFINITY && (i == 0 || d > kTau);
-            empty_row = empty_row && em == -INFINITY;
-            if (moved) c8_row -= d;
-            ctl.shift[rg + lane] = moved ? d : 0.f;
-            ctl.alpha[rg + lane] = moved && i > 0 ? fast_exp2(-d) : 1.f;
+            moved = em != -INFINITY && (i == 0 || em > kC0 + kTau);
+            const float d = moved ? em - kC0 : 0.f;
+            if (i == 0) empty_row = em == -INFINITY;
+            c8_row -= d;
             ctl.c8[rg + lane] = c8_row;
+            ctl.move[rg + lane] = i == 0 ? d : fast_exp2(-d);
           }
-          rescale = __any_sync(0xFFFFFFFFu, moved) && i > 0;
+          moving = __ballot_sync(0xFFFFFFFFu, moved);
           __syncwarp();
+          if (i == 0) {
 #pragma unroll
-          for (int r = 0; r < RW; r += 4) {
-            const float4 sh = *reinterpret_cast<const float4*>(&ctl.shift[rg + r]);
-            const float4 al = *reinterpret_cast<const float4*>(&ctl.alpha[rg + r]);
-            e[r] -= sh.x;
-            e[r + 1] -= sh.y;
-            e[r + 2] -= sh.z;
-            e[r + 3] -= sh.w;
-            l_part[r] *= al.x;
-            l_part[r + 1] *= al.y;
-            l_part[r + 2] *= al.z;
-            l_part[r + 3] *= al.w;
+            for (int r = 0; r < RW; r += 4) {
+              const float4 sh = *reinterpret_cast<const float4*>(&ctl.move[rg + r]);
+              e[r] -= sh.x;
+              e[r + 1] -= sh.y;
+              e[r + 2] -= sh.z;
+              e[r + 3] -= sh.w;
+            }
+          } else {
+            logits();
+#pragma unroll
+            for (int r = 0; r < RW; ++r) l_part[r] *= ctl.move[rg + r];
           }
-          weights();
+          exps();
+          terms();
         }
+        const bool rescale = i > 0 && moving != 0;
 #pragma unroll
         for (int r = 0; r < RW; ++r) l_part[r] += e[r];
         // the P buffer is free, and O complete up to the tile before, once
@@ -652,18 +711,16 @@ __global__ void __launch_bounds__(Cfg<NR>::kThreads, 1)
         }
         if (rescale) {
           tc::tc_fence_after();
-#pragma unroll 1
-          for (int j = 0; j < 4; ++j) {
+          for (uint32_t left = moving; left; left &= left - 1) {
+            const int r = __ffs(int(left)) - 1;
+            const uint32_t at = tO + uint32_t(rg + r) + lane_off;
+            const float f = ctl.move[rg + r];
+            float v[4];
 #pragma unroll
-            for (int c = 0; c < RW; c += 16) {
-              float v[16];
-              const uint32_t at = tO + uint32_t(j * NR + rg + c) + lane_off;
-              tc::tmem_ld16(at, v);
-              tc::tmem_wait_ld();
+            for (int j = 0; j < 4; ++j) v[j] = tc::tmem_ld1(at + uint32_t(j * NR));
+            tc::tmem_wait_ld();
 #pragma unroll
-              for (int k = 0; k < 16; ++k) v[k] *= ctl.alpha[rg + c + k];
-              tc::tmem_st16(at, v);
-            }
+            for (int j = 0; j < 4; ++j) tc::tmem_st1(at + uint32_t(j * NR), v[j] * f);
           }
           tc::tmem_wait_st();
         }
@@ -690,7 +747,7 @@ __global__ void __launch_bounds__(Cfg<NR>::kThreads, 1)
         const float l = (ctl.red[grp][0][lane] + ctl.red[grp][1][lane]) + (ctl.red[grp][2][lane] + ctl.red[grp][3][lane]);
         const int gr = r0 + rg + lane;
         // the output's factor: a partial stays as it is, an empty row becomes 0 (the same in the four warps)
-        ctl.alpha[rg + lane] = w.part >= 0 ? 1.f : (empty_row ? 0.f : ds0 / l);
+        ctl.move[rg + lane] = w.part >= 0 ? 1.f : (empty_row ? 0.f : ds0 / l);
         if (qd == 0) {
           const float m = kC0 - c8_row;  // sum of 2^(t - m + kC0) = l
           if (w.part >= 0) {
@@ -732,7 +789,7 @@ __global__ void __launch_bounds__(Cfg<NR>::kThreads, 1)
           int tq = gr / p.h, h = gr - tq * p.h;
 #pragma unroll
           for (int k = 0; k < RW; k += 2) {
-            const float2 f = *reinterpret_cast<const float2*>(&ctl.alpha[rg + k]);
+            const float2 f = *reinterpret_cast<const float2*>(&ctl.move[rg + k]);
             const float a = f.x == 0.f ? 0.f : v[k] * f.x, b = f.y == 0.f ? 0.f : v[k + 1] * f.y;
             const float other = __shfl_xor_sync(0xFFFFFFFFu, odd ? a : b, 1);
             const float lo_c = odd ? other : a, hi_c = odd ? b : other;
