@@ -134,7 +134,7 @@ __global__ void __launch_bounds__(32 * kWarps) latent_merge_kernel(LatentParams 
     for (int k = 0; k < 4; ++k)
       if (row + k < p.n_q)
         p.lse[int64_t(b) * p.n_q + row + k] =
-            sv[k] == 0.f ? -INFINITY : (mv[k] + fast_log2(sv[k]) - kLatentC0) * kLn2;
+            sv[k] == 0.f ? -INFINITY : (mv[k] + fast_log2(sv[k])) * kLn2;
   }
 }
 

@@ -20,11 +20,9 @@
 // weights enter as two terms each. A query row is scaled to amax = 448 and
 // split into hi = e4m3(x) and lo = e4m3(x - hi) (within 2^-8 of x, or 2^-19 of
 // the row's amax): two rows of the Q tile, their products added when S is
-// read. A weight p = 2^(t - m_ref + 7) is split into hi = e4m3(p) and
-// lo = e5m2(p - hi) (within 2^-7 of p and 0.15% rms, about bf16's own; e5m2
-// reaches down to 2^-17, so weights down to 24 binades below the row's max
-// count), two products into one accumulator. The row sums add the p
-// themselves in float32.
+// read. A weight p is split into hi = e4m3(p) and lo = e5m2(p - hi) (within
+// 2^-7 of p and 0.15% rms, about bf16's own; e5m2 reaches down to 2^-17), two
+// products into one accumulator. The row sums add the p themselves in float32.
 //
 // Warps: 0 the TMA producer, 1 the MMA issuer, 4.. one or two softmax
 // warpgroups (thread x of a group: key x of S, channel x of each of the four
@@ -56,9 +54,14 @@ constexpr uint64_t kWaitLimitNs = 2000000000ull;
 constexpr uint64_t kDrainLimitNs = 100000000ull;
 constexpr int kMaxDynSmem = 227 * 1024;
 
-// P is scaled so that the row's reference max has weight 2^6; the reference
-// moves once a tile's max exceeds it by more than kTau, so p <= 2^8.5 < 448.
-constexpr float kC0 = kLatentC0, kTau = 2.5f;
+// A weight is 2^e, e = t + c8 with a constant c8 per row (minus the reference)
+// that moves when some e of a tile exceeds kTop (2^8.5 < 448). At the row's first
+// tile the largest e is put at kBase, so that later tiles seldom exceed kTop
+// (moving costs about as much as a tile's softmax: with a base of 6 every
+// second tile of 64 rows of normal logits moved one); where it stands out by
+// more than kStandsOut from the smallest of the four warps' maxima (a sink), at
+// kBaseSink, which leaves more binades below it. A later move also puts it there.
+constexpr float kTop = 8.5f, kBase = 4.f, kBaseSink = 6.f, kStandsOut = 8.f;
 constexpr float kFar = 100.f;  // binades: a longer move starts again from the row maxima
 
 template <int NR>
@@ -97,7 +100,7 @@ struct Ctrl {
   alignas(16) uint8_t by[2][2][4][NR == 64 ? 32 : 16];  // ... and by how many binades
   alignas(16) float red[2][4][NR == 64 ? 32 : 16];      // per warp: row maxima, at the end row sums
   alignas(16) float scale[NR];  // logit (log2 units) per unit of S
-  alignas(16) float c8[NR];     // kC0 - m_ref
+  alignas(16) float c8[NR];     // minus the reference
   alignas(16) float move[NR];   // first tile of a work row: the reference's move; later ones: 2^-move; at the end:
                                 // the output's factor
   alignas(16) int lim[NR];      // last visible key
@@ -243,7 +246,7 @@ __global__ void __launch_bounds__(Cfg<NR>::kThreads, 1)
   if (warp == 0) {
     // ======================= TMA producer =====================================
     const uint64_t pol = p.evict_first ? tc::l2_policy_evict_first() : tc::l2_policy_evict_normal();
-    const int ps = p.page_size, ppt = kKvTile / ps;
+    const int ps = p.page_size, shift = p.page_shift, ppt = kKvTile >> shift;
     int u = 0, ur = 0;  // latent and rotary sub-tiles so far
     bool ok = true;
     auto table_entry = [&](int b, int64_t page) {  // -1 past the request's entries
@@ -254,7 +257,7 @@ __global__ void __launch_bounds__(Cfg<NR>::kThreads, 1)
     const int entry0 = w_begin < w_end && b0 >= 0 && b0 < p.num_seqs ? table_entry(b0, page0) : -1;
     for (int row = w_begin; row < w_end && ok; ++row) {
       const Work w = load_work(p, row, b0, L0);
-      const int64_t first_page = w.k0 / ps, npages = (w.k1 + ps - 1) / ps - first_page;
+      const int64_t first_page = w.k0 >> shift, npages = ((w.k1 + ps - 1) >> shift) - first_page;
       const bool known = row == w_begin && w.b == b0 && first_page + lane == page0;
       int64_t batch = __all_sync(0xFFFFFFFFu, known) ? 0 : -1;
       int entry = entry0;
@@ -496,7 +499,7 @@ __global__ void __launch_bounds__(Cfg<NR>::kThreads, 1)
         }
         if (part == 0) {
           ctl.scale[rg + r] = am * (1.f / 448.f) * qk_log2;
-          ctl.c8[rg + r] = kC0;
+          ctl.c8[rg + r] = 0.f;
           ctl.lim[rg + r] = !live ? -1 : (p.causal ? w.L - p.q_len + tq : INT_MAX);
         }
         tc::fence_async_smem();
@@ -505,7 +508,7 @@ __global__ void __launch_bounds__(Cfg<NR>::kThreads, 1)
         // orders them; the first tile's reads come after its own wait
       }
       const int lim_min = p.causal ? w.L - p.q_len + r0 / p.h : INT_MAX;  // the tile's first row sees least
-      float c8_row = kC0;  // lane r < RW: row r's c8
+      float c8_row = 0.f;  // lane r < RW: row r's c8
       float l_part[RW];
 #pragma unroll
       for (int r = 0; r < RW; ++r) l_part[r] = 0.f;
@@ -521,7 +524,7 @@ __global__ void __launch_bounds__(Cfg<NR>::kThreads, 1)
         const bool masked = t_end > w.k1 || t_end - 1 > int64_t(lim_min);
         float e[RW];
         uint32_t hi[RW / 4], lo[RW / 4];
-        // e = t - m_ref + kC0, in log2 units; -inf where the row does not see the key
+        // e = t + c8, in log2 units; -inf where the row does not see the key
         auto logits = [&] {
           float s_lo[RW];
           const uint32_t ts = tmem + uint32_t((gi & 1) * C::kSCols + rg) + lane_off;
@@ -578,14 +581,14 @@ __global__ void __launch_bounds__(Cfg<NR>::kThreads, 1)
 #pragma unroll
           for (int r = 1; r < RW; ++r) m = fmaxf(m, e[r]);
           uint32_t above = 0;
-          if (__any_sync(0xFFFFFFFFu, m > kC0 + kTau)) {
+          if (__any_sync(0xFFFFFFFFu, m > kTop)) {
 #pragma unroll
-            for (int r = 0; r < RW; ++r) above |= e[r] > kC0 + kTau ? 1u << r : 0u;
+            for (int r = 0; r < RW; ++r) above |= e[r] > kTop ? 1u << r : 0u;
             above = __reduce_or_sync(0xFFFFFFFFu, above);
 #pragma unroll
             for (int r = 0; r < RW; ++r)
               if (above >> r & 1u) {
-                const float v = redux_max(e[r]) - kC0;
+                const float v = redux_max(e[r]) - kBaseSink;
                 if (lane == 0) ctl.by[grp][xb & 1][qd][r] = uint8_t(fminf(ceilf(v), kFar));
               }
           }
@@ -650,10 +653,11 @@ __global__ void __launch_bounds__(Cfg<NR>::kThreads, 1)
           ++xr;
           bool moved = false;
           if (lane < RW) {
-            const float em = fmaxf(fmaxf(ctl.red[grp][0][lane], ctl.red[grp][1][lane]),
-                                   fmaxf(ctl.red[grp][2][lane], ctl.red[grp][3][lane]));
-            moved = em != -INFINITY && (i == 0 || em > kC0 + kTau);
-            const float d = moved ? em - kC0 : 0.f;
+            const float m0 = ctl.red[grp][0][lane], m1 = ctl.red[grp][1][lane];
+            const float m2 = ctl.red[grp][2][lane], m3 = ctl.red[grp][3][lane];
+            const float em = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)), least = fminf(fminf(m0, m1), fminf(m2, m3));
+            moved = em != -INFINITY && (i == 0 || em > kTop);
+            const float d = moved ? em - (i == 0 && em - least <= kStandsOut ? kBase : kBaseSink) : 0.f;
             if (i == 0) empty_row = em == -INFINITY;
             c8_row -= d;
             ctl.c8[rg + lane] = c8_row;
@@ -749,12 +753,12 @@ __global__ void __launch_bounds__(Cfg<NR>::kThreads, 1)
         // the output's factor: a partial stays as it is, an empty row becomes 0 (the same in the four warps)
         ctl.move[rg + lane] = w.part >= 0 ? 1.f : (empty_row ? 0.f : ds0 / l);
         if (qd == 0) {
-          const float m = kC0 - c8_row;  // sum of 2^(t - m + kC0) = l
+          const float m = -c8_row;  // l = sum of 2^(t - m)
           if (w.part >= 0) {
             p.m_part[int64_t(w.part) * rows_pad + gr] = empty_row ? -INFINITY : m;
             p.l_part[int64_t(w.part) * rows_pad + gr] = l;
           } else if (p.lse && rg + lane < nr) {
-            p.lse[int64_t(w.b) * p.n_q + gr] = empty_row ? -INFINITY : (m + fast_log2(l) - kC0) * kLn2;
+            p.lse[int64_t(w.b) * p.n_q + gr] = empty_row ? -INFINITY : (m + fast_log2(l)) * kLn2;
           }
         }
       }

@@ -119,7 +119,7 @@ struct LatentParams {
   int64_t q_ts, q_hs;
   const uint8_t* cache;
   int64_t stride_page, stride_token;
-  int page_size;
+  int page_size, page_shift;
   int64_t num_pages;
   const float* descale;
   const int32_t* block_table;
@@ -140,9 +140,6 @@ struct LatentParams {
   float* l_part;  // likewise: sum of the weights, scaled like o_part
   int evict_first;
 };
-
-// log2 of the weight that a row's reference max has in the latent kernel's sums.
-constexpr float kLatentC0 = 6.f;
 
 // Words (int32) of the plan buffer's parts, each a multiple of 4.
 inline int64_t latent_plan_slot_words(int slots) { return 4 * int64_t(slots); }
