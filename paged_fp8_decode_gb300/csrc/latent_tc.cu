@@ -24,7 +24,7 @@
 // 2^-7 of p and 0.15% rms, about bf16's own; e5m2 reaches down to 2^-17), two
 // products into one accumulator. The row sums add the p themselves in float32.
 //
-// Warps: 0 the TMA producer, 1 the MMA issuer, 4.. one or two softmax
+// Warps: 0, 2, 3 the TMA producers, 1 the MMA issuer, 4.. one or two softmax
 // warpgroups (thread x of a group: key x of S, channel x of each of the four
 // 128-channel blocks of O; a group owns RW = NR / groups rows).
 //
@@ -144,11 +144,13 @@ __device__ __forceinline__ float reduce_rows(float (&v)[N], int lane) {
   return r;
 }
 
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1, int c2,
-                                            uint64_t policy) {
+// Called by a whole converged warp: one elected lane issues.
+__device__ __forceinline__ void tma_load_3d_warp(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1, int c2,
+                                                 uint64_t policy) {
   asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
-      " [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(dst),
+      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%2, %3, %4}], [%5], %6;\n\t}" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar), "l"(policy)
       : "memory");
 }
@@ -243,11 +245,17 @@ __global__ void __launch_bounds__(Cfg<NR>::kThreads, 1)
   const int b0 = first.z, L0 = seq_len(p, b0);
   const uint32_t tO = tmem + uint32_t(2 * C::kSCols);
 
-  if (warp == 0) {
-    // ======================= TMA producer =====================================
+  if (warp == 0 || warp == 2 || warp == 3) {
+    // ======================= TMA producers =====================================
+    // Issuing a tensor load takes a warp 110 to 200 cycles (280 where one lane
+    // of a diverged warp issues), and a tile is 5 sub-tiles of 1 to 8 pages: one
+    // warp's issue alone held the stream at 20 bytes a cycle. Three warps share
+    // a tile's sub-tiles: 0 and 3, 1 and the rotary one, 2.
+    const int j_first = warp == 0 ? 0 : warp - 1;
     const uint64_t pol = p.evict_first ? tc::l2_policy_evict_first() : tc::l2_policy_evict_normal();
     const int ps = p.page_size, shift = p.page_shift, ppt = kKvTile >> shift;
-    int u = 0, ur = 0;  // latent and rotary sub-tiles so far
+    int gt = 0;      // tiles so far
+    int issued = 0;  // sub-tiles this warp has begun to load, in order of (tile, sub-tile)
     bool ok = true;
     auto table_entry = [&](int b, int64_t page) {  // -1 past the request's entries
       return page < p.bt_len ? p.block_table[int64_t(b) * p.bt_stride + page] : -1;
@@ -261,53 +269,51 @@ __global__ void __launch_bounds__(Cfg<NR>::kThreads, 1)
       const bool known = row == w_begin && w.b == b0 && first_page + lane == page0;
       int64_t batch = __all_sync(0xFFFFFFFFu, known) ? 0 : -1;
       int entry = entry0;
-      for (int i = 0; i < w.ntiles && ok; ++i) {
+      for (int i = 0; i < w.ntiles && ok; ++i, ++gt) {
         const int nvalid = int(min(int64_t(ppt), npages - int64_t(i) * ppt));
         const int64_t e0 = int64_t(i) * ppt;
         if (batch < 0 || e0 + nvalid > batch + 32) {
           batch = e0;
           entry = e0 + lane < npages ? table_entry(w.b, first_page + e0 + lane) : -1;
         }
-        const int pg = __shfl_sync(0xFFFFFFFFu, entry, int(e0 - batch) + (lane & 7));
-        if (lane < nvalid && (pg < 0 || int64_t(pg) >= p.num_pages)) atomicOr(p.status, kStatusBadPage);
-#pragma unroll 1
-        for (int j = 0; j < 5; ++j) {
+        const int at = int(e0 - batch);
+        const int mine = __shfl_sync(0xFFFFFFFFu, entry, at + (lane & 7));
+        if (warp == 0 && lane < nvalid && (mine < 0 || int64_t(mine) >= p.num_pages)) atomicOr(p.status, kStatusBadPage);
+        for (int j = j_first; j < 5 && ok; j += 3) {
           const bool rope = j == 4;
-          const int s = rope ? ur % C::kRopeRing : u % C::kRing;
-          const uint32_t round = uint32_t(rope ? ur / C::kRopeRing : u / C::kRing);
+          const int u = rope ? gt : 4 * gt + j;
+          const int s = rope ? u % C::kRopeRing : u % C::kRing;
+          const uint32_t round = uint32_t(rope ? u / C::kRopeRing : u / C::kRing);
           const uint32_t full = tc::smem_u32(rope ? &ctl.rfull[s] : &ctl.full[s]);
           const uint32_t empty = tc::smem_u32(rope ? &ctl.rempty[s] : &ctl.empty[s]);
-          const uint32_t row_b = rope ? 64u : 128u;
-          if (lane == 0) {
-            ok = tc::mbar_wait(empty, (round & 1u) ^ 1u, abort, kWaitLimitNs);
-            if (ok) tc::mbar_arrive_expect_tx(full, uint32_t(nvalid * ps) * row_b);
-          }
-          ok = __shfl_sync(0xFFFFFFFFu, ok ? 1 : 0, 0) != 0;
+          const uint32_t page_bytes = uint32_t(ps) * (rope ? 64u : 128u);
+          uint32_t dst = base + (rope ? uint32_t(C::kOffRope + s * kRopeSub) : uint32_t(s * kSub));
+          // (with a ring that is no multiple of four, another warp may have
+          // loaded the entry before; this warp's own wait four sub-tiles ago
+          // was for a later release than the one before that, so the parity
+          // cannot be mistaken)
+          ok = __all_sync(0xFFFFFFFFu, tc::mbar_wait(empty, (round & 1u) ^ 1u, abort, kWaitLimitNs));
           if (!ok) break;
-          if (lane < nvalid) {
-            const uint32_t dst = base + (rope ? uint32_t(C::kOffRope + s * kRopeSub) : uint32_t(s * kSub)) +
-                                 uint32_t(lane * ps) * row_b;
-            tma_load_3d(dst, rope ? &tmap_rope : &tmap_lat, full, 128 * j, 0, pg, pol);
-          }
-          if (rope)
-            ++ur;
-          else
-            ++u;
+          if (lane == 0) tc::mbar_arrive_expect_tx(full, uint32_t(nvalid) * page_bytes);
           __syncwarp();
+          for (int k = 0; k < nvalid; ++k, dst += page_bytes)
+            tma_load_3d_warp(dst, rope ? &tmap_rope : &tmap_lat, full, 128 * j, 0,
+                             __shfl_sync(0xFFFFFFFFu, entry, at + k), pol);
+          ++issued;
         }
       }
     }
     if (!ok && lane == 0) {
-      // abort: wait (bounded) for the loads still in flight before the CTA exits
+      // abort: wait (bounded) for this warp's loads still in flight before the CTA exits
       const uint64_t t0 = tc::globaltimer_ns();
-      for (int k = max(0, u - C::kRing); k < u; ++k)
-        while (!tc::mbar_try_wait(tc::smem_u32(&ctl.full[k % C::kRing]), uint32_t(k / C::kRing) & 1u) &&
-               tc::globaltimer_ns() - t0 < kDrainLimitNs) {
+      const int per = j_first == 2 ? 1 : 2;  // sub-tiles of a tile that are this warp's
+      for (int n = max(0, issued - C::kRing); n < issued; ++n) {
+        const int t = n / per, j = j_first + 3 * (n % per);
+        uint64_t* bar = j == 4 ? &ctl.rfull[t % C::kRopeRing] : &ctl.full[(4 * t + j) % C::kRing];
+        const uint32_t round = uint32_t(j == 4 ? t / C::kRopeRing : (4 * t + j) / C::kRing);
+        while (!tc::mbar_try_wait(tc::smem_u32(bar), round & 1u) && tc::globaltimer_ns() - t0 < kDrainLimitNs) {
         }
-      for (int k = max(0, ur - C::kRopeRing); k < ur; ++k)
-        while (!tc::mbar_try_wait(tc::smem_u32(&ctl.rfull[k % C::kRopeRing]), uint32_t(k / C::kRopeRing) & 1u) &&
-               tc::globaltimer_ns() - t0 < kDrainLimitNs) {
-        }
+      }
     }
   } else if (warp == 1) {
     // ======================= MMA issuer ========================================
