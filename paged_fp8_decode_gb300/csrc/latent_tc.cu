@@ -438,88 +438,189 @@ __global__ void __launch_bounds__(Cfg<NR>::kThreads, 1)
     int g0 = 0;           // tiles of the rows before
     int xb = 0, xr = 0, xs = 0;  // bound, row and sum exchanges so far (the same in every thread of the group)
     bool ok = true;
-    for (int row = w_begin; row < w_end && ok; ++row) {
-      const Work w = load_work(p, row, b0, L0);
-      if (w.ntiles == 0) {
-        // no key of this range is held any more: an empty partial
+    int row = w_begin;
+    // The next work row that holds keys; empty partials are written on the way.
+    auto next_row = [&](Work& w) {
+      for (; row < w_end; ++row) {
+        w = load_work(p, row, b0, L0);
+        if (w.ntiles > 0) {
+          ++row;
+          return true;
+        }
+        // no key of this range is held any more
         if (w.part >= 0 && w.part < 2 * p.slots && x < RW) p.m_part[int64_t(w.part) * rows_pad + r0 + rg + x] = -INFINITY;
         if (w.part >= 2 * p.slots && x == 0) atomicOr(p.status, kStatusBadPlan);
-        continue;
       }
-      // ---- Q: RW rows by 128 threads, kTpr threads a row --------------------
-      {
-        constexpr int kTpr = 128 / RW;
-        const int r = x / kTpr, part = x % kTpr;
-        const int gr = r0 + rg + r;  // row of the request
-        const bool live = rg + r < nr;
-        const int tq = live ? gr / p.h : 0, h = live ? gr - tq * p.h : 0;
-        const uint16_t* src = p.q + (int64_t(w.b) * p.q_len + tq) * p.q_ts + int64_t(h) * p.q_hs;
-        constexpr int kCh = kRow / 8 / kTpr;  // 8-channel chunks of a thread, all loaded at once
-        uint4 qv[kCh];
+      return false;
+    };
+    Work w = {}, wn = {};
+    bool have = false;  // w's tiles are done
+    float l_part[RW];
+    float c8_row = 0.f;      // lane r < RW: row r's c8
+    bool empty_row = true;   // lane r < RW: row r has seen no key
+    // One turn: post w's sums, stage the next row's queries (the tensor core
+    // still works on w's last product), then w's output (it already works on
+    // the next row's first scores), then the next row's tiles.
+    for (;;) {
+      if (have) {
+        // (every warp has read the last tile's row maxima, whose place the sums
+        // take, and the row constants, which the next row's replace)
+        ok = tc::mbar_wait(tc::smem_u32(&ctl.p_full[(g0 - 1) & 1]), uint32_t((g0 - 1) >> 1) & 1u, abort, kWaitLimitNs);
+        if (!ok) break;
+        const float ws = reduce_rows<RW, false>(l_part, lane);
+        if (lane % kShare == 0) ctl.red[grp][qd][lane / kShare] = ws;
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(tc::smem_u32(&ctl.sum_bar[grp]));
+      }
+      const bool more = next_row(wn);
+      if (more) {
+        // ---- Q: RW rows by 128 threads, kTpr threads a row --------------------
+        {
+          constexpr int kTpr = 128 / RW;
+          const int r = x / kTpr, part = x % kTpr;
+          const int gr = r0 + rg + r;  // row of the request
+          const bool live = rg + r < nr;
+          const int tq = live ? gr / p.h : 0, h = live ? gr - tq * p.h : 0;
+          const uint16_t* src = p.q + (int64_t(wn.b) * p.q_len + tq) * p.q_ts + int64_t(h) * p.q_hs;
+          constexpr int kCh = kRow / 8 / kTpr;  // 8-channel chunks of a thread, all loaded at once
+          uint4 qv[kCh];
 #pragma unroll
-        for (int c = 0; c < kCh; ++c)
-          qv[c] = live ? *reinterpret_cast<const uint4*>(src + (part + c * kTpr) * 8) : make_uint4(0u, 0u, 0u, 0u);
-        float am = 0.f;
+          for (int c = 0; c < kCh; ++c)
+            qv[c] = live ? *reinterpret_cast<const uint4*>(src + (part + c * kTpr) * 8) : make_uint4(0u, 0u, 0u, 0u);
+          float am = 0.f;
 #pragma unroll
-        for (int c = 0; c < kCh; ++c) {
-          const float ds = part + c * kTpr < kLat / 8 ? ds0 : ds1;
-          const uint32_t q4[4] = {qv[c].x, qv[c].y, qv[c].z, qv[c].w};
+          for (int c = 0; c < kCh; ++c) {
+            const float ds = part + c * kTpr < kLat / 8 ? ds0 : ds1;
+            const uint32_t q4[4] = {qv[c].x, qv[c].y, qv[c].z, qv[c].w};
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            am = fmaxf(am, fmaxf(fabsf(__uint_as_float(q4[k] << 16) * ds), fabsf(__uint_as_float(q4[k] & 0xFFFF0000u) * ds)));
-        }
+            for (int k = 0; k < 4; ++k)
+              am = fmaxf(am, fmaxf(fabsf(__uint_as_float(q4[k] << 16) * ds), fabsf(__uint_as_float(q4[k] & 0xFFFF0000u) * ds)));
+          }
 #pragma unroll
-        for (int m = 1; m < kTpr; m <<= 1) am = fmaxf(am, __shfl_xor_sync(0xFFFFFFFFu, am, m));
-        am = fmaxf(am, 1e-30f);
-        const float inv = 448.f / am;
+          for (int m = 1; m < kTpr; m <<= 1) am = fmaxf(am, __shfl_xor_sync(0xFFFFFFFFu, am, m));
+          am = fmaxf(am, 1e-30f);
+          const float inv = 448.f / am;
 #pragma unroll
-        for (int ci = 0; ci < kCh; ++ci) {
-          const int c = part + ci * kTpr;
-          const float f = (c < kLat / 8 ? ds0 : ds1) * inv;
-          uint32_t hi[2], lo[2];
-          const uint32_t q4[4] = {qv[ci].x, qv[ci].y, qv[ci].z, qv[ci].w};
+          for (int ci = 0; ci < kCh; ++ci) {
+            const int c = part + ci * kTpr;
+            const float f = (c < kLat / 8 ? ds0 : ds1) * inv;
+            uint32_t hi[2], lo[2];
+            const uint32_t q4[4] = {qv[ci].x, qv[ci].y, qv[ci].z, qv[ci].w};
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float x0 = __uint_as_float(q4[k] << 16) * f, x1 = __uint_as_float(q4[k] & 0xFFFF0000u) * f;
-            const __nv_fp8x2_storage_t h2 = __nv_cvt_float2_to_fp8x2(make_float2(x0, x1), __NV_SATFINITE, __NV_E4M3);
-            const float2 hf = e4m3x2_to_float2(h2);
-            const __nv_fp8x2_storage_t l2 =
-                __nv_cvt_float2_to_fp8x2(make_float2(x0 - hf.x, x1 - hf.y), __NV_SATFINITE, __NV_E4M3);
-            if (k & 1) {
-              hi[k >> 1] |= uint32_t(h2) << 16;
-              lo[k >> 1] |= uint32_t(l2) << 16;
-            } else {
-              hi[k >> 1] = uint32_t(h2);
-              lo[k >> 1] = uint32_t(l2);
+            for (int k = 0; k < 4; ++k) {
+              const float x0 = __uint_as_float(q4[k] << 16) * f, x1 = __uint_as_float(q4[k] & 0xFFFF0000u) * f;
+              const __nv_fp8x2_storage_t h2 = __nv_cvt_float2_to_fp8x2(make_float2(x0, x1), __NV_SATFINITE, __NV_E4M3);
+              const float2 hf = e4m3x2_to_float2(h2);
+              const __nv_fp8x2_storage_t l2 =
+                  __nv_cvt_float2_to_fp8x2(make_float2(x0 - hf.x, x1 - hf.y), __NV_SATFINITE, __NV_E4M3);
+              if (k & 1) {
+                hi[k >> 1] |= uint32_t(h2) << 16;
+                lo[k >> 1] |= uint32_t(l2) << 16;
+              } else {
+                hi[k >> 1] = uint32_t(h2);
+                lo[k >> 1] = uint32_t(l2);
+              }
+            }
+            const int ch = c * 8;
+#pragma unroll
+            for (int term = 0; term < 2; ++term) {
+              const int tr = term * NR + rg + r;  // row of the Q tile
+              const uint32_t off =
+                  ch < kLat ? uint32_t(C::kOffQ + (ch >> 7) * C::kQSub + tr * 128 + ((((ch & 127) >> 4) ^ (tr & 7)) << 4) + (ch & 8))
+                            : uint32_t(C::kOffQ + 4 * C::kQSub + tr * 64 + ((((ch - kLat) >> 4) ^ ((tr >> 1) & 3)) << 4) + (ch & 8));
+              *reinterpret_cast<uint2*>(smem + off) = term ? make_uint2(lo[0], lo[1]) : make_uint2(hi[0], hi[1]);
             }
           }
-          const int ch = c * 8;
-#pragma unroll
-          for (int term = 0; term < 2; ++term) {
-            const int tr = term * NR + rg + r;  // row of the Q tile
-            const uint32_t off =
-                ch < kLat ? uint32_t(C::kOffQ + (ch >> 7) * C::kQSub + tr * 128 + ((((ch & 127) >> 4) ^ (tr & 7)) << 4) + (ch & 8))
-                          : uint32_t(C::kOffQ + 4 * C::kQSub + tr * 64 + ((((ch - kLat) >> 4) ^ ((tr >> 1) & 3)) << 4) + (ch & 8));
-            *reinterpret_cast<uint2*>(smem + off) = term ? make_uint2(lo[0], lo[1]) : make_uint2(hi[0], hi[1]);
+          if (part == 0) {
+            ctl.scale[rg + r] = am * (1.f / 448.f) * qk_log2;
+            ctl.c8[rg + r] = 0.f;
+            ctl.lim[rg + r] = !live ? -1 : (p.causal ? wn.L - p.q_len + tq : INT_MAX);
           }
         }
-        if (part == 0) {
-          ctl.scale[rg + r] = am * (1.f / 448.f) * qk_log2;
-          ctl.c8[rg + r] = 0.f;
-          ctl.lim[rg + r] = !live ? -1 : (p.causal ? w.L - p.q_len + tq : INT_MAX);
+      }
+      if (have) {
+        ok = tc::mbar_wait(tc::smem_u32(&ctl.sum_bar[grp]), uint32_t(xs) & 1u, abort, kWaitLimitNs);
+        if (!ok) break;
+        ++xs;
+        if (lane < RW) {
+          const float l = (ctl.red[grp][0][lane] + ctl.red[grp][1][lane]) + (ctl.red[grp][2][lane] + ctl.red[grp][3][lane]);
+          const int gr = r0 + rg + lane;
+          // the output's factor: a partial stays as it is, an empty row becomes 0 (the same in the four warps)
+          ctl.move[rg + lane] = w.part >= 0 ? 1.f : (empty_row ? 0.f : ds0 / l);
+          if (qd == 0) {
+            const float m = -c8_row;  // l = sum of 2^(t - m)
+            if (w.part >= 0) {
+              p.m_part[int64_t(w.part) * rows_pad + gr] = empty_row ? -INFINITY : m;
+              p.l_part[int64_t(w.part) * rows_pad + gr] = l;
+            } else if (p.lse && rg + lane < nr) {
+              p.lse[int64_t(w.b) * p.n_q + gr] = empty_row ? -INFINITY : (m + fast_log2(l)) * kLn2;
+            }
+          }
         }
+        __syncwarp();
+      }
+      if (more) {
+        // (after the sums are read: the next row's first maxima take their place)
         tc::fence_async_smem();
         tc::mbar_arrive(tc::smem_u32(&ctl.q_ready));
-        // the row constants are read by the whole group: any exchange below
-        // orders them; the first tile's reads come after its own wait
       }
-      const int lim_min = p.causal ? w.L - p.q_len + r0 / p.h : INT_MAX;  // the tile's first row sees least
-      float c8_row = 0.f;  // lane r < RW: row r's c8
-      float l_part[RW];
+      if (have) {
+        ok = tc::mbar_wait(tc::smem_u32(&ctl.o_full[(g0 - 1) & 1]), uint32_t((g0 - 1) >> 1) & 1u, abort, kWaitLimitNs);
+        if (!ok) break;
+        tc::tc_fence_after();
+        if (w.part >= 0) {
+          // a partial: four rows of a channel are one 16-byte store, a warp's 512 bytes in a row
+          float4* dst = reinterpret_cast<float4*>(p.o_part) +
+                        ((int64_t(w.part) * p.n_row_tiles + r0 / NR) * 4 * (NR / 4) + rg / 4) * 128 + x;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            float v[RW];
+            tc::tmem_ld_cols<RW>(tO + uint32_t(j * NR + rg) + lane_off, v);
+            tc::tmem_wait_ld();
+#pragma unroll
+            for (int c = 0; c < RW / 4; ++c)
+              dst[(j * (NR / 4) + c) * 128] = make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+          }
+        } else {
+          // the output: two lanes trade, so that each holds two channels of one
+          // row (even lanes the even rows) and a store is 4 bytes
+          const bool odd = lane & 1;
+          uint16_t* dst = p.out + (int64_t(w.b) * p.q_len) * p.out_ts + (x & ~1);
+#pragma unroll 1
+          for (int j = 0; j < 4; ++j) {
+            float v[RW];
+            tc::tmem_ld_cols<RW>(tO + uint32_t(j * NR + rg) + lane_off, v);
+            tc::tmem_wait_ld();
+            int gr = r0 + rg + (odd ? 1 : 0);
+            int tq = gr / p.h, h = gr - tq * p.h;
+#pragma unroll
+            for (int k = 0; k < RW; k += 2) {
+              const float2 f = *reinterpret_cast<const float2*>(&ctl.move[rg + k]);
+              const float a = f.x == 0.f ? 0.f : v[k] * f.x, b = f.y == 0.f ? 0.f : v[k + 1] * f.y;
+              const float other = __shfl_xor_sync(0xFFFFFFFFu, odd ? a : b, 1);
+              const float lo_c = odd ? other : a, hi_c = odd ? b : other;
+              if (rg + k + (odd ? 1 : 0) < nr)
+                *reinterpret_cast<uint32_t*>(dst + int64_t(tq) * p.out_ts + int64_t(h) * p.out_hs + 128 * j) =
+                    uint32_t(float_to_out_bits(lo_c, p.out_f16)) | (uint32_t(float_to_out_bits(hi_c, p.out_f16)) << 16);
+              h += 2;
+              while (h >= p.h) {
+                h -= p.h;
+                ++tq;
+              }
+            }
+          }
+        }
+        tc::tc_fence_before();
+        __syncwarp();
+      }
+      if (!more) break;
+      w = wn;
+      have = true;
+      c8_row = 0.f;
+      empty_row = true;
 #pragma unroll
       for (int r = 0; r < RW; ++r) l_part[r] = 0.f;
-      bool empty_row = true;  // lane r < RW: row r has seen no key
-
+      const int lim_min = p.causal ? w.L - p.q_len + r0 / p.h : INT_MAX;  // the tile's first row sees least
       for (int i = 0; i < w.ntiles; ++i) {
         const int gi = g0 + i;
         ok = tc::mbar_wait(tc::smem_u32(&ctl.s_full[gi & 1]), uint32_t(gi >> 1) & 1u, abort, kWaitLimitNs);
@@ -740,85 +841,6 @@ __global__ void __launch_bounds__(Cfg<NR>::kThreads, 1)
       }
       if (!ok) break;
       g0 += w.ntiles;
-
-      // ---- epilogue of the work row --------------------------------------------
-      // (the wait: every warp has read the last tile's row maxima, whose place
-      // the sums take)
-      ok = tc::mbar_wait(tc::smem_u32(&ctl.p_full[(g0 - 1) & 1]), uint32_t((g0 - 1) >> 1) & 1u, abort, kWaitLimitNs);
-      if (!ok) break;
-      const float ws = reduce_rows<RW, false>(l_part, lane);
-      if (lane % kShare == 0) ctl.red[grp][qd][lane / kShare] = ws;
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(tc::smem_u32(&ctl.sum_bar[grp]));
-      ok = tc::mbar_wait(tc::smem_u32(&ctl.sum_bar[grp]), uint32_t(xs) & 1u, abort, kWaitLimitNs);
-      if (!ok) break;
-      ++xs;
-      if (lane < RW) {
-        const float l = (ctl.red[grp][0][lane] + ctl.red[grp][1][lane]) + (ctl.red[grp][2][lane] + ctl.red[grp][3][lane]);
-        const int gr = r0 + rg + lane;
-        // the output's factor: a partial stays as it is, an empty row becomes 0 (the same in the four warps)
-        ctl.move[rg + lane] = w.part >= 0 ? 1.f : (empty_row ? 0.f : ds0 / l);
-        if (qd == 0) {
-          const float m = -c8_row;  // l = sum of 2^(t - m)
-          if (w.part >= 0) {
-            p.m_part[int64_t(w.part) * rows_pad + gr] = empty_row ? -INFINITY : m;
-            p.l_part[int64_t(w.part) * rows_pad + gr] = l;
-          } else if (p.lse && rg + lane < nr) {
-            p.lse[int64_t(w.b) * p.n_q + gr] = empty_row ? -INFINITY : (m + fast_log2(l)) * kLn2;
-          }
-        }
-      }
-      __syncwarp();
-      ok = tc::mbar_wait(tc::smem_u32(&ctl.o_full[(g0 - 1) & 1]), uint32_t((g0 - 1) >> 1) & 1u, abort, kWaitLimitNs);
-      if (!ok) break;
-      tc::tc_fence_after();
-      if (w.part >= 0) {
-        // a partial: four rows of a channel are one 16-byte store, a warp's 512 bytes in a row
-        float4* dst = reinterpret_cast<float4*>(p.o_part) +
-                      ((int64_t(w.part) * p.n_row_tiles + r0 / NR) * 4 * (NR / 4) + rg / 4) * 128 + x;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          float v[RW];
-          tc::tmem_ld_cols<RW>(tO + uint32_t(j * NR + rg) + lane_off, v);
-          tc::tmem_wait_ld();
-#pragma unroll
-          for (int c = 0; c < RW / 4; ++c)
-            dst[(j * (NR / 4) + c) * 128] = make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
-        }
-      } else {
-        // the output: two lanes trade, so that each holds two channels of one
-        // row (even lanes the even rows) and a store is 4 bytes
-        const bool odd = lane & 1;
-        uint16_t* dst = p.out + (int64_t(w.b) * p.q_len) * p.out_ts + (x & ~1);
-#pragma unroll 1
-        for (int j = 0; j < 4; ++j) {
-          float v[RW];
-          tc::tmem_ld_cols<RW>(tO + uint32_t(j * NR + rg) + lane_off, v);
-          tc::tmem_wait_ld();
-          int gr = r0 + rg + (odd ? 1 : 0);
-          int tq = gr / p.h, h = gr - tq * p.h;
-#pragma unroll
-          for (int k = 0; k < RW; k += 2) {
-            const float2 f = *reinterpret_cast<const float2*>(&ctl.move[rg + k]);
-            const float a = f.x == 0.f ? 0.f : v[k] * f.x, b = f.y == 0.f ? 0.f : v[k + 1] * f.y;
-            const float other = __shfl_xor_sync(0xFFFFFFFFu, odd ? a : b, 1);
-            const float lo_c = odd ? other : a, hi_c = odd ? b : other;
-            if (rg + k + (odd ? 1 : 0) < nr)
-              *reinterpret_cast<uint32_t*>(dst + int64_t(tq) * p.out_ts + int64_t(h) * p.out_hs + 128 * j) =
-                  uint32_t(float_to_out_bits(lo_c, p.out_f16)) | (uint32_t(float_to_out_bits(hi_c, p.out_f16)) << 16);
-            h += 2;
-            while (h >= p.h) {
-              h -= p.h;
-              ++tq;
-            }
-          }
-        }
-      }
-      // all reads of O and of the row constants are done before any warp of
-      // the group stages the next row: S of it only comes after every warp's
-      // q_ready arrival, and O after every warp's p_full arrival
-      tc::tc_fence_before();
-      __syncwarp();
     }
   }
 
