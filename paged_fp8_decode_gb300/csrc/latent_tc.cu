@@ -113,6 +113,15 @@ constexpr int smem_bytes() {
 static_assert(smem_bytes<64>() <= kMaxDynSmem && smem_bytes<32>() <= kMaxDynSmem && smem_bytes<16>() <= kMaxDynSmem,
               "shared memory");
 
+// Bounded wait, the loop out of line: the kernel has some twenty of them, and
+// code that runs once is bound by its fetch from L2.
+__device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile int* abort) {
+  return tc::mbar_wait(bar, parity, abort, kWaitLimitNs);
+}
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int* abort) {
+  return tc::mbar_try_wait(bar, parity) || wait_slow(bar, parity, abort);
+}
+
 // max over the warp, in every lane (NaN lanes do not count)
 __device__ __forceinline__ float redux_max(float v) {
   float r;
@@ -157,6 +166,11 @@ __device__ __forceinline__ void tma_load_3d_warp(uint32_t dst, const CUtensorMap
 
 constexpr uint32_t kSwizzle64B = 4;      // shared-memory descriptor, bits 61-63
 constexpr uint32_t kFormatBE5m2 = 1u << 10;  // instruction descriptor: B holds e5m2 codes
+
+// The larger magnitudes of two bf16 pairs, as bit patterns (a NaN counts as above infinity).
+__device__ __forceinline__ uint32_t max_abs_bf16x2(uint32_t a, uint32_t b) {
+  return __vmaxu2(a & 0x7FFF7FFFu, b & 0x7FFF7FFFu);
+}
 
 // One work row: keys [tb * 128, min(te * 128, L)) of request b.
 struct Work {
@@ -279,6 +293,7 @@ __global__ void __launch_bounds__(Cfg<NR>::kThreads, 1)
         const int at = int(e0 - batch);
         const int mine = __shfl_sync(0xFFFFFFFFu, entry, at + (lane & 7));
         if (warp == 0 && lane < nvalid && (mine < 0 || int64_t(mine) >= p.num_pages)) atomicOr(p.status, kStatusBadPage);
+#pragma unroll 1
         for (int j = j_first; j < 5 && ok; j += 3) {
           const bool rope = j == 4;
           const int u = rope ? gt : 4 * gt + j;
@@ -292,10 +307,11 @@ __global__ void __launch_bounds__(Cfg<NR>::kThreads, 1)
           // loaded the entry before; this warp's own wait four sub-tiles ago
           // was for a later release than the one before that, so the parity
           // cannot be mistaken)
-          ok = __all_sync(0xFFFFFFFFu, tc::mbar_wait(empty, (round & 1u) ^ 1u, abort, kWaitLimitNs));
+          ok = __all_sync(0xFFFFFFFFu, wait(empty, (round & 1u) ^ 1u, abort));
           if (!ok) break;
           if (lane == 0) tc::mbar_arrive_expect_tx(full, uint32_t(nvalid) * page_bytes);
           __syncwarp();
+#pragma unroll 1
           for (int k = 0; k < nvalid; ++k, dst += page_bytes)
             tma_load_3d_warp(dst, rope ? &tmap_rope : &tmap_lat, full, 128 * j, 0,
                              __shfl_sync(0xFFFFFFFFu, entry, at + k), pol);
@@ -340,7 +356,7 @@ __global__ void __launch_bounds__(Cfg<NR>::kThreads, 1)
     for (int row = w_begin; row < w_end && ok; ++row) {
       const int ntiles = __shfl_sync(0xFFFFFFFFu, load_work(p, row, b0, L0).ntiles, 0);
       if (ntiles == 0) continue;
-      ok = __all_sync(0xFFFFFFFFu, tc::mbar_wait(tc::smem_u32(&ctl.q_ready), uint32_t(nrow) & 1u, abort, kWaitLimitNs));
+      ok = __all_sync(0xFFFFFFFFu, wait(tc::smem_u32(&ctl.q_ready), uint32_t(nrow) & 1u, abort));
       ++nrow;
       int nq = 0, jq = 0, np = 0;
       uint64_t t_idle = 0;
@@ -385,7 +401,7 @@ __global__ void __launch_bounds__(Cfg<NR>::kThreads, 1)
             tc::tc_fence_after();
             const uint64_t pd = pd0 + uint64_t((gi % C::kPBufs) * (C::kPBytes >> 4));
             const uint32_t acc = np > 0;
-#pragma unroll
+#pragma unroll 1
             for (int j = 0; j < 4; ++j) {
               const uint64_t vd = vd0 + uint64_t(sv * (kSub >> 4));
 #pragma unroll
@@ -465,7 +481,7 @@ __global__ void __launch_bounds__(Cfg<NR>::kThreads, 1)
       if (have) {
         // (every warp has read the last tile's row maxima, whose place the sums
         // take, and the row constants, which the next row's replace)
-        ok = tc::mbar_wait(tc::smem_u32(&ctl.p_full[(g0 - 1) & 1]), uint32_t((g0 - 1) >> 1) & 1u, abort, kWaitLimitNs);
+        ok = wait(tc::smem_u32(&ctl.p_full[(g0 - 1) & 1]), uint32_t((g0 - 1) >> 1) & 1u, abort);
         if (!ok) break;
         const float ws = reduce_rows<RW, false>(l_part, lane);
         if (lane % kShare == 0) ctl.red[grp][qd][lane / kShare] = ws;
@@ -482,30 +498,53 @@ __global__ void __launch_bounds__(Cfg<NR>::kThreads, 1)
           const bool live = rg + r < nr;
           const int tq = live ? gr / p.h : 0, h = live ? gr - tq * p.h : 0;
           const uint16_t* src = p.q + (int64_t(wn.b) * p.q_len + tq) * p.q_ts + int64_t(h) * p.q_hs;
-          constexpr int kCh = kRow / 8 / kTpr;  // 8-channel chunks of a thread, all loaded at once
+          // The 8 bytes of a chunk's hi codes: row tr of its sub-tile of the Q
+          // tile; the lo codes NR rows on (a multiple of 8, so swizzled alike).
+          const int tr = rg + r;
+          auto hi_at = [&](int c) {
+            const int ch = c * 8;
+            return ch < kLat ? uint32_t(C::kOffQ + (ch >> 7) * C::kQSub + tr * 128 + ((((ch & 127) >> 4) ^ (tr & 7)) << 4) + (ch & 8))
+                             : uint32_t(C::kOffQ + 4 * C::kQSub + tr * 64 + ((((ch - kLat) >> 4) ^ ((tr >> 1) & 3)) << 4) + (ch & 8));
+          };
+          auto lo_step = [&](int c) { return uint32_t(NR * (c < kLat / 8 ? 128 : 64)); };
+          constexpr int kCh = kRow / 8 / kTpr;  // 8-channel chunks of a thread, requested at once
           uint4 qv[kCh];
 #pragma unroll
           for (int c = 0; c < kCh; ++c)
             qv[c] = live ? *reinterpret_cast<const uint4*>(src + (part + c * kTpr) * 8) : make_uint4(0u, 0u, 0u, 0u);
-          float am = 0.f;
+          // the raw chunks wait in the places of their codes, so that the
+          // conversion can be a rolled loop (a thread's registers could not be
+          // indexed, and there is no L1 to speak of beside this shared memory)
+#pragma unroll
+          for (int ci = 0; ci < kCh; ++ci) {
+            const int c = part + ci * kTpr;
+            *reinterpret_cast<uint2*>(smem + hi_at(c)) = make_uint2(qv[ci].x, qv[ci].y);
+            *reinterpret_cast<uint2*>(smem + hi_at(c) + lo_step(c)) = make_uint2(qv[ci].z, qv[ci].w);
+          }
+          // |q| of two channels as bf16 bit patterns, which order like the values
+          uint32_t am_lat = 0, am_rope = 0;
 #pragma unroll
           for (int c = 0; c < kCh; ++c) {
-            const float ds = part + c * kTpr < kLat / 8 ? ds0 : ds1;
-            const uint32_t q4[4] = {qv[c].x, qv[c].y, qv[c].z, qv[c].w};
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              am = fmaxf(am, fmaxf(fabsf(__uint_as_float(q4[k] << 16) * ds), fabsf(__uint_as_float(q4[k] & 0xFFFF0000u) * ds)));
+            const uint32_t m = max_abs_bf16x2(max_abs_bf16x2(qv[c].x, qv[c].y), max_abs_bf16x2(qv[c].z, qv[c].w));
+            if (part + c * kTpr < kLat / 8)
+              am_lat = max_abs_bf16x2(am_lat, m);
+            else
+              am_rope = max_abs_bf16x2(am_rope, m);
           }
+          float am = fmaxf(fmaxf(__uint_as_float(am_lat << 16), __uint_as_float(am_lat & 0xFFFF0000u)) * fabsf(ds0),
+                           fmaxf(__uint_as_float(am_rope << 16), __uint_as_float(am_rope & 0xFFFF0000u)) * fabsf(ds1));
 #pragma unroll
           for (int m = 1; m < kTpr; m <<= 1) am = fmaxf(am, __shfl_xor_sync(0xFFFFFFFFu, am, m));
           am = fmaxf(am, 1e-30f);
           const float inv = 448.f / am;
-#pragma unroll
-          for (int ci = 0; ci < kCh; ++ci) {
-            const int c = part + ci * kTpr;
+#pragma unroll 1
+          for (int c = part; c < kRow / 8; c += kTpr) {
+            uint2* const at_hi = reinterpret_cast<uint2*>(smem + hi_at(c));
+            uint2* const at_lo = reinterpret_cast<uint2*>(smem + hi_at(c) + lo_step(c));
+            const uint2 q0 = *at_hi, q1 = *at_lo;
             const float f = (c < kLat / 8 ? ds0 : ds1) * inv;
             uint32_t hi[2], lo[2];
-            const uint32_t q4[4] = {qv[ci].x, qv[ci].y, qv[ci].z, qv[ci].w};
+            const uint32_t q4[4] = {q0.x, q0.y, q1.x, q1.y};
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               const float x0 = __uint_as_float(q4[k] << 16) * f, x1 = __uint_as_float(q4[k] & 0xFFFF0000u) * f;
@@ -521,15 +560,8 @@ __global__ void __launch_bounds__(Cfg<NR>::kThreads, 1)
                 lo[k >> 1] = uint32_t(l2);
               }
             }
-            const int ch = c * 8;
-#pragma unroll
-            for (int term = 0; term < 2; ++term) {
-              const int tr = term * NR + rg + r;  // row of the Q tile
-              const uint32_t off =
-                  ch < kLat ? uint32_t(C::kOffQ + (ch >> 7) * C::kQSub + tr * 128 + ((((ch & 127) >> 4) ^ (tr & 7)) << 4) + (ch & 8))
-                            : uint32_t(C::kOffQ + 4 * C::kQSub + tr * 64 + ((((ch - kLat) >> 4) ^ ((tr >> 1) & 3)) << 4) + (ch & 8));
-              *reinterpret_cast<uint2*>(smem + off) = term ? make_uint2(lo[0], lo[1]) : make_uint2(hi[0], hi[1]);
-            }
+            *at_hi = make_uint2(hi[0], hi[1]);
+            *at_lo = make_uint2(lo[0], lo[1]);
           }
           if (part == 0) {
             ctl.scale[rg + r] = am * (1.f / 448.f) * qk_log2;
@@ -539,7 +571,7 @@ __global__ void __launch_bounds__(Cfg<NR>::kThreads, 1)
         }
       }
       if (have) {
-        ok = tc::mbar_wait(tc::smem_u32(&ctl.sum_bar[grp]), uint32_t(xs) & 1u, abort, kWaitLimitNs);
+        ok = wait(tc::smem_u32(&ctl.sum_bar[grp]), uint32_t(xs) & 1u, abort);
         if (!ok) break;
         ++xs;
         if (lane < RW) {
@@ -565,48 +597,55 @@ __global__ void __launch_bounds__(Cfg<NR>::kThreads, 1)
         tc::mbar_arrive(tc::smem_u32(&ctl.q_ready));
       }
       if (have) {
-        ok = tc::mbar_wait(tc::smem_u32(&ctl.o_full[(g0 - 1) & 1]), uint32_t((g0 - 1) >> 1) & 1u, abort, kWaitLimitNs);
+        ok = wait(tc::smem_u32(&ctl.o_full[(g0 - 1) & 1]), uint32_t((g0 - 1) >> 1) & 1u, abort);
         if (!ok) break;
         tc::tc_fence_after();
         if (w.part >= 0) {
-          // a partial: four rows of a channel are one 16-byte store, a warp's 512 bytes in a row
+            // a partial: four rows of a channel are one 16-byte store, a warp's 512 bytes in a row
           float4* dst = reinterpret_cast<float4*>(p.o_part) +
                         ((int64_t(w.part) * p.n_row_tiles + r0 / NR) * 4 * (NR / 4) + rg / 4) * 128 + x;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            float v[RW];
-            tc::tmem_ld_cols<RW>(tO + uint32_t(j * NR + rg) + lane_off, v);
+#pragma unroll 1
+          for (int k = 0; k < 4 * (RW / 16); ++k) {  // 16 rows of a channel block
+            const int j = k / (RW / 16), c = k % (RW / 16) * 16;
+            float v[16];
+            tc::tmem_ld16(tO + uint32_t(j * NR + rg + c) + lane_off, v);
             tc::tmem_wait_ld();
 #pragma unroll
-            for (int c = 0; c < RW / 4; ++c)
-              dst[(j * (NR / 4) + c) * 128] = make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+            for (int q = 0; q < 4; ++q)
+              dst[(j * (NR / 4) + c / 4 + q) * 128] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
           }
         } else {
           // the output: two lanes trade, so that each holds two channels of one
           // row (even lanes the even rows) and a store is 4 bytes
           const bool odd = lane & 1;
-          uint16_t* dst = p.out + (int64_t(w.b) * p.q_len) * p.out_ts + (x & ~1);
+          uint16_t* dst = p.out + int64_t(w.b) * p.q_len * p.out_ts + (x & ~1);
+          const int rows = min(RW, nr - rg);
+          int gr = r0 + rg + (odd ? 1 : 0);
+          int tq = gr / p.h, h = gr - tq * p.h;
 #pragma unroll 1
-          for (int j = 0; j < 4; ++j) {
-            float v[RW];
-            tc::tmem_ld_cols<RW>(tO + uint32_t(j * NR + rg) + lane_off, v);
-            tc::tmem_wait_ld();
-            int gr = r0 + rg + (odd ? 1 : 0);
-            int tq = gr / p.h, h = gr - tq * p.h;
+          for (int c = 0; c < rows; c += 2) {
+            float v[8];
 #pragma unroll
-            for (int k = 0; k < RW; k += 2) {
-              const float2 f = *reinterpret_cast<const float2*>(&ctl.move[rg + k]);
-              const float a = f.x == 0.f ? 0.f : v[k] * f.x, b = f.y == 0.f ? 0.f : v[k + 1] * f.y;
+            for (int j = 0; j < 4; ++j) {
+              v[2 * j] = tc::tmem_ld1(tO + uint32_t(j * NR + rg + c) + lane_off);
+              v[2 * j + 1] = tc::tmem_ld1(tO + uint32_t(j * NR + rg + c + 1) + lane_off);
+            }
+            tc::tmem_wait_ld();
+            const float2 f = *reinterpret_cast<const float2*>(&ctl.move[rg + c]);
+            uint16_t* at = dst + int64_t(tq) * p.out_ts + int64_t(h) * p.out_hs;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float a = f.x == 0.f ? 0.f : v[2 * j] * f.x, b = f.y == 0.f ? 0.f : v[2 * j + 1] * f.y;
               const float other = __shfl_xor_sync(0xFFFFFFFFu, odd ? a : b, 1);
               const float lo_c = odd ? other : a, hi_c = odd ? b : other;
-              if (rg + k + (odd ? 1 : 0) < nr)
-                *reinterpret_cast<uint32_t*>(dst + int64_t(tq) * p.out_ts + int64_t(h) * p.out_hs + 128 * j) =
+              if (c + (odd ? 1 : 0) < rows)
+                *reinterpret_cast<uint32_t*>(at + 128 * j) =
                     uint32_t(float_to_out_bits(lo_c, p.out_f16)) | (uint32_t(float_to_out_bits(hi_c, p.out_f16)) << 16);
-              h += 2;
-              while (h >= p.h) {
-                h -= p.h;
-                ++tq;
-              }
+            }
+            h += 2;
+            while (h >= p.h) {
+              h -= p.h;
+              ++tq;
             }
           }
         }
@@ -623,7 +662,7 @@ __global__ void __launch_bounds__(Cfg<NR>::kThreads, 1)
       const int lim_min = p.causal ? w.L - p.q_len + r0 / p.h : INT_MAX;  // the tile's first row sees least
       for (int i = 0; i < w.ntiles; ++i) {
         const int gi = g0 + i;
-        ok = tc::mbar_wait(tc::smem_u32(&ctl.s_full[gi & 1]), uint32_t(gi >> 1) & 1u, abort, kWaitLimitNs);
+        ok = wait(tc::smem_u32(&ctl.s_full[gi & 1]), uint32_t(gi >> 1) & 1u, abort);
         if (!ok) break;
         tc::tc_fence_after();
         const int64_t t_end = w.k0 + int64_t(i + 1) * kKvTile;
@@ -676,103 +715,72 @@ __global__ void __launch_bounds__(Cfg<NR>::kThreads, 1)
 #pragma unroll
           for (int r = 0; r < RW; r += 2) terms_of(r);
         };
-        logits();
         // Rows whose reference moves (bits; the same in every thread of the
-        // group). A warp that finds weights above the limit posts the rows and
-        // how many binades each has to move; the weights are formed while the
-        // other warps' rows arrive, and scaled by the moves.
+        // group). A later tile's weights are formed from the references as they
+        // stand while the warps exchange which rows have weights above the limit
+        // and by how many binades; where some do (few tiles), the references move
+        // and the tile is done once more. A first tile, and a move too far for a
+        // byte, start from the rows' maxima. (One copy of the code for all: code
+        // that is seldom run comes from L2, some 25 cycles an instruction.)
         uint32_t moving = 0;
-        bool anew = i == 0;  // from the row maxima: a first tile, or a move too far for a byte
-        if (i > 0) {
-          float m = e[0];
+        enum { kCheck, kMaxima, kDone } phase = i == 0 ? kMaxima : kCheck;
+#pragma unroll 1
+        for (;;) {
+          logits();
+          if (phase == kCheck) {
+            float m = e[0];
 #pragma unroll
-          for (int r = 1; r < RW; ++r) m = fmaxf(m, e[r]);
-          uint32_t above = 0;
-          if (__any_sync(0xFFFFFFFFu, m > kTop)) {
+            for (int r = 1; r < RW; ++r) m = fmaxf(m, e[r]);
+            uint32_t above = 0;
+            if (__any_sync(0xFFFFFFFFu, m > kTop)) {
 #pragma unroll
-            for (int r = 0; r < RW; ++r) above |= e[r] > kTop ? 1u << r : 0u;
-            above = __reduce_or_sync(0xFFFFFFFFu, above);
-#pragma unroll
-            for (int r = 0; r < RW; ++r)
-              if (above >> r & 1u) {
-                const float v = redux_max(e[r]) - kBaseSink;
+              for (int r = 0; r < RW; ++r) above |= e[r] > kTop ? 1u << r : 0u;
+              above = __reduce_or_sync(0xFFFFFFFFu, above);
+              const uint32_t ts = tmem + uint32_t((gi & 1) * C::kSCols + rg) + lane_off;
+#pragma unroll 1
+              for (uint32_t left = above; left; left &= left - 1) {
+                const int r = __ffs(int(left)) - 1;
+                const float s0 = tc::tmem_ld1(ts + uint32_t(r)), s1 = tc::tmem_ld1(ts + uint32_t(NR + r));
+                tc::tmem_wait_ld();
+                float v = fmaf(s0 + s1, ctl.scale[rg + r], ctl.c8[rg + r]);
+                if (masked && (dead || int(t_end) - kKvTile + x > ctl.lim[rg + r])) v = -INFINITY;
+                v = redux_max(v) - kBaseSink;
                 if (lane == 0) ctl.by[grp][xb & 1][qd][r] = uint8_t(fminf(ceilf(v), kFar));
               }
-          }
-          if (lane == 0) ctl.above[grp][xb & 1][qd] = above;
-          __syncwarp();
-          const uint32_t bar = tc::smem_u32(&ctl.bound_bar[grp][xb & 1]);
-          if (lane == 0) tc::mbar_arrive(bar);
-          exps();
-          terms();
-          ok = tc::mbar_wait(bar, uint32_t(xb >> 1) & 1u, abort, kWaitLimitNs);
-          if (!ok) break;
-          const uint4 b = *reinterpret_cast<const uint4*>(&ctl.above[grp][xb & 1][0]);
-          moving = (b.x | b.y) | (b.z | b.w);
-          if (moving) {
-            // lane r moves row r's reference (the four warps compute and store the same values)
-            int d = 0;
+            }
+            if (lane == 0) ctl.above[grp][xb & 1][qd] = above;
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(tc::smem_u32(&ctl.bound_bar[grp][xb & 1]));
+          } else if (phase == kMaxima) {
+            float tmp[RW];
+#pragma unroll
+            for (int r = 0; r < RW; ++r) tmp[r] = e[r];
+            const float wm = reduce_rows<RW, true>(tmp, lane);
+            if (lane % kShare == 0) ctl.red[grp][qd][lane / kShare] = wm;
+            __syncwarp();
+            const uint32_t bar = tc::smem_u32(&ctl.row_bar[grp]);
+            if (lane == 0) tc::mbar_arrive(bar);
+            ok = wait(bar, uint32_t(xr) & 1u, abort);
+            if (!ok) break;
+            ++xr;
+            // lane r moves row r's reference (the four warps compute and store
+            // the same values)
+            bool moved = false;
             if (lane < RW) {
-              if (b.x >> lane & 1u) d = max(d, int(ctl.by[grp][xb & 1][0][lane]));
-              if (b.y >> lane & 1u) d = max(d, int(ctl.by[grp][xb & 1][1][lane]));
-              if (b.z >> lane & 1u) d = max(d, int(ctl.by[grp][xb & 1][2][lane]));
-              if (b.w >> lane & 1u) d = max(d, int(ctl.by[grp][xb & 1][3][lane]));
+              const float m0 = ctl.red[grp][0][lane], m1 = ctl.red[grp][1][lane];
+              const float m2 = ctl.red[grp][2][lane], m3 = ctl.red[grp][3][lane];
+              const float em = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)), least = fminf(fminf(m0, m1), fminf(m2, m3));
+              moved = em != -INFINITY && (i == 0 || em > kTop);
+              const float d = moved ? em - (i == 0 && em - least <= kStandsOut ? kBase : kBaseSink) : 0.f;
+              if (i == 0) empty_row = em == -INFINITY;
+              c8_row -= d;
+              ctl.c8[rg + lane] = c8_row;
+              ctl.move[rg + lane] = i == 0 ? d : fast_exp2(-d);
             }
-            anew = __any_sync(0xFFFFFFFFu, d >= int(kFar));
-            if (!anew) {
-              const float f = __int_as_float((127 - d) << 23);  // 2^-d
-              if (lane < RW) {
-                c8_row -= float(d);
-                ctl.c8[rg + lane] = c8_row;
-                ctl.move[rg + lane] = f;
-              }
-              __syncwarp();
-#pragma unroll
-              for (int r = 0; r < RW; r += 4) {
-                if (moving >> r & 0xFu) {
-                  const float4 al = *reinterpret_cast<const float4*>(&ctl.move[rg + r]);
-                  const float a4[4] = {al.x, al.y, al.z, al.w};
-#pragma unroll
-                  for (int k = 0; k < 4; ++k) {
-                    l_part[r + k] *= a4[k];
-                    e[r + k] *= a4[k];
-                  }
-                  terms_of(r);
-                  terms_of(r + 2);
-                }
-              }
-            }
-          }
-          ++xb;
-        }
-        if (anew) {
-          if (i > 0) logits();
-          float tmp[RW];
-#pragma unroll
-          for (int r = 0; r < RW; ++r) tmp[r] = e[r];
-          const float wm = reduce_rows<RW, true>(tmp, lane);
-          if (lane % kShare == 0) ctl.red[grp][qd][lane / kShare] = wm;
-          __syncwarp();
-          const uint32_t bar = tc::smem_u32(&ctl.row_bar[grp]);
-          if (lane == 0) tc::mbar_arrive(bar);
-          ok = tc::mbar_wait(bar, uint32_t(xr) & 1u, abort, kWaitLimitNs);
-          if (!ok) break;
-          ++xr;
-          bool moved = false;
-          if (lane < RW) {
-            const float m0 = ctl.red[grp][0][lane], m1 = ctl.red[grp][1][lane];
-            const float m2 = ctl.red[grp][2][lane], m3 = ctl.red[grp][3][lane];
-            const float em = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)), least = fminf(fminf(m0, m1), fminf(m2, m3));
-            moved = em != -INFINITY && (i == 0 || em > kTop);
-            const float d = moved ? em - (i == 0 && em - least <= kStandsOut ? kBase : kBaseSink) : 0.f;
-            if (i == 0) empty_row = em == -INFINITY;
-            c8_row -= d;
-            ctl.c8[rg + lane] = c8_row;
-            ctl.move[rg + lane] = i == 0 ? d : fast_exp2(-d);
-          }
-          moving = __ballot_sync(0xFFFFFFFFu, moved);
-          __syncwarp();
-          if (i == 0) {
+            moving = __ballot_sync(0xFFFFFFFFu, moved);
+            __syncwarp();
+            phase = kDone;
+            if (i > 0) continue;
 #pragma unroll
             for (int r = 0; r < RW; r += 4) {
               const float4 sh = *reinterpret_cast<const float4*>(&ctl.move[rg + r]);
@@ -781,25 +789,54 @@ __global__ void __launch_bounds__(Cfg<NR>::kThreads, 1)
               e[r + 2] -= sh.z;
               e[r + 3] -= sh.w;
             }
-          } else {
-            logits();
-#pragma unroll
-            for (int r = 0; r < RW; ++r) l_part[r] *= ctl.move[rg + r];
           }
           exps();
           terms();
+          if (phase == kDone) break;
+          ok = wait(tc::smem_u32(&ctl.bound_bar[grp][xb & 1]), uint32_t(xb >> 1) & 1u, abort);
+          if (!ok) break;
+          const uint4 b = *reinterpret_cast<const uint4*>(&ctl.above[grp][xb & 1][0]);
+          moving = (b.x | b.y) | (b.z | b.w);
+          if (!moving) {
+            ++xb;
+            break;
+          }
+          int d = 0;
+          if (lane < RW) {
+            if (b.x >> lane & 1u) d = max(d, int(ctl.by[grp][xb & 1][0][lane]));
+            if (b.y >> lane & 1u) d = max(d, int(ctl.by[grp][xb & 1][1][lane]));
+            if (b.z >> lane & 1u) d = max(d, int(ctl.by[grp][xb & 1][2][lane]));
+            if (b.w >> lane & 1u) d = max(d, int(ctl.by[grp][xb & 1][3][lane]));
+          }
+          ++xb;
+          phase = kDone;
+          if (__any_sync(0xFFFFFFFFu, d >= int(kFar))) {
+            phase = kMaxima;
+          } else {
+            if (lane < RW) {
+              c8_row -= float(d);
+              ctl.c8[rg + lane] = c8_row;
+              ctl.move[rg + lane] = __int_as_float((127 - d) << 23);  // 2^-d
+            }
+            __syncwarp();
+          }
         }
+        if (!ok) break;
         const bool rescale = i > 0 && moving != 0;
+        if (rescale) {
+#pragma unroll
+          for (int r = 0; r < RW; ++r) l_part[r] *= ctl.move[rg + r];
+        }
 #pragma unroll
         for (int r = 0; r < RW; ++r) l_part[r] += e[r];
         // the P buffer is free, and O complete up to the tile before, once
         // that product is done
         if (gi >= C::kPBufs) {
           const int pi = rescale ? gi - 1 : gi - C::kPBufs;
-          ok = tc::mbar_wait(tc::smem_u32(&ctl.o_full[pi & 1]), uint32_t(pi >> 1) & 1u, abort, kWaitLimitNs);
+          ok = wait(tc::smem_u32(&ctl.o_full[pi & 1]), uint32_t(pi >> 1) & 1u, abort);
           if (!ok) break;
         } else if (rescale) {
-          ok = tc::mbar_wait(tc::smem_u32(&ctl.o_full[(gi - 1) & 1]), uint32_t((gi - 1) >> 1) & 1u, abort, kWaitLimitNs);
+          ok = wait(tc::smem_u32(&ctl.o_full[(gi - 1) & 1]), uint32_t((gi - 1) >> 1) & 1u, abort);
           if (!ok) break;
         }
         uint8_t* pt = smem + C::kOffP + (gi % C::kPBufs) * C::kPBytes + x * 16;
