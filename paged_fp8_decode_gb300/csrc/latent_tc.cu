@@ -72,6 +72,7 @@ struct Cfg {
   static constexpr int kRing = NR == 64 ? 8 : (NR == 32 ? 9 : 11);  // latent entries
   static constexpr int kRopeRing = NR == 64 ? 1 : 2;
   static constexpr int kPBufs = NR == 64 ? 1 : 2;
+  static constexpr int kPrefetchTiles = 2;      // before the wait for the preceding kernel; at most 4 (32 pages)
   static constexpr int kPBytes = 2 * NR * 128;  // hi and lo
   static constexpr int kQSub = 2 * NR * 128;    // hi and lo rows of one 128-channel sub-tile
   static constexpr int kQBytes = 4 * kQSub + 2 * NR * 64;
@@ -112,6 +113,15 @@ constexpr int smem_bytes() {
 }
 static_assert(smem_bytes<64>() <= kMaxDynSmem && smem_bytes<32>() <= kMaxDynSmem && smem_bytes<16>() <= kMaxDynSmem,
               "shared memory");
+
+__device__ __forceinline__ void prefetch_l2(const void* at) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(at));
+}
+
+// `bytes` (a multiple of 16) from a 16-byte aligned address into L2, asynchronously.
+__device__ __forceinline__ void prefetch_bulk_l2(const void* at, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(at), "r"(bytes) : "memory");
+}
 
 // Bounded wait, the loop out of line: the kernel has some twenty of them, and
 // code that runs once is bound by its fetch from L2.
@@ -167,6 +177,28 @@ __device__ __forceinline__ void tma_load_3d_warp(uint32_t dst, const CUtensorMap
 constexpr uint32_t kSwizzle64B = 4;      // shared-memory descriptor, bits 61-63
 constexpr uint32_t kFormatBE5m2 = 1u << 10;  // instruction descriptor: B holds e5m2 codes
 
+// Two values as two 8-bit terms each: hi = e4m3(v), lo = e4m3 or e5m2(v - hi).
+// By way of f16, whose 2^-12 is far inside the terms' own steps and whose range
+// holds every v here (weights and scaled queries are at most 448; below 2^-14
+// it keeps 2^-25, the terms 2^-18), because the difference and the conversions
+// take both values at once there.
+template <bool E5M2>
+__device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
+  const __half2 h = __floats2half2_rn(a, b);
+  uint32_t hb, back, d;
+  uint16_t hc, lc;
+  memcpy(&hb, &h, 4);
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(hc) : "r"(hb));
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(back) : "h"(hc));
+  asm("sub.f16x2 %0, %1, %2;" : "=r"(d) : "r"(hb), "r"(back));
+  if constexpr (E5M2)
+    asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(lc) : "r"(d));
+  else
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(lc) : "r"(d));
+  hi = hc;
+  lo = lc;
+}
+
 // The larger magnitudes of two bf16 pairs, as bit patterns (a NaN counts as above infinity).
 __device__ __forceinline__ uint32_t max_abs_bf16x2(uint32_t a, uint32_t b) {
   return __vmaxu2(a & 0x7FFF7FFFu, b & 0x7FFF7FFFu);
@@ -211,6 +243,19 @@ __global__ void __launch_bounds__(Cfg<NR>::kThreads, 1)
     return;
   }
 
+  // The queries of rows r_from .. r_to - 1 of the tile, of request b, into L2
+  // (n threads, this one the t-th).
+  auto prefetch_rows = [&](int b, int t, int n, int r_from, int r_to) {
+    constexpr int kLines = kRow * 2 / 128;
+    const int tile0 = (int(blockIdx.x) % p.n_row_tiles) * NR;
+#pragma unroll 1
+    for (int k = t; k < (r_to - r_from) * kLines; k += n) {
+      const int r = tile0 + r_from + k / kLines, tq = r / p.h, h = r - tq * p.h;
+      if (r < p.n_q)
+        prefetch_l2(p.q + (int64_t(b) * p.q_len + tq) * p.q_ts + int64_t(h) * p.q_hs + (k % kLines) * 64);
+    }
+  };
+
   if (tid == 0) {
     for (int s = 0; s < C::kRing; ++s) {
       tc::mbar_init(tc::smem_u32(&ctl.full[s]), 1);
@@ -247,13 +292,35 @@ __global__ void __launch_bounds__(Cfg<NR>::kThreads, 1)
   const uint32_t tmem = ctl.tmem_base;
   volatile int* abort = &ctl.abort;
 
-  // programmatic dependent launch: the set-up above reads nothing that the
-  // preceding kernel on the stream may write; everything below may
-  tc::grid_dependency_wait();
-
   const int slot = int(blockIdx.x) / p.n_row_tiles;
   const int r0 = (int(blockIdx.x) % p.n_row_tiles) * NR;
   const int nr = min(NR, p.n_q - r0);  // real rows of this tile
+
+  // Programmatic dependent launch: the set-up above reads nothing that the
+  // preceding kernel on the stream may write; everything after the wait may.
+  // Before it, L2 is asked for the pages of the first kPrefetchTiles tiles and
+  // the queries of the first row, so that the memory streams them while the
+  // preceding kernel finishes. A prefetch returns no data, and that kernel's
+  // writes land in L2: the plan and block table that it is aimed with are only a
+  // guess (bounds-checked), and all of it is read again after the wait.
+  if (warp == 3 || warp >= 4) {
+    const int4 f = reinterpret_cast<const int4*>(p.slot_table)[slot];
+    if (f.y > f.x && f.x >= 0 && f.x < p.max_work && f.z >= 0 && f.z < p.num_seqs && f.w >= 0) {
+      if (warp == 3 && r0 == 0) {
+        const int4 w = reinterpret_cast<const int4*>(p.work)[f.x];
+        const int64_t page = (int64_t(f.w) << (7 - p.page_shift)) + lane;
+        const int64_t end = int64_t(min(w.z, f.w + C::kPrefetchTiles)) << (7 - p.page_shift);
+        if (p.page_span && page < end && page < p.bt_len) {
+          const int pg = p.block_table[int64_t(f.z) * p.bt_stride + page];
+          if (pg >= 0 && pg < p.num_pages) prefetch_bulk_l2(p.cache + int64_t(pg) * p.stride_page, p.page_span);
+        }
+      } else if (warp >= 4) {
+        prefetch_rows(f.z, tid - 128, 128 * G, 0, NR);
+      }
+    }
+  }
+  tc::grid_dependency_wait();
+
   const int4 first = reinterpret_cast<const int4*>(p.slot_table)[slot];  // rows, first request, its first tile
   const int w_begin = max(0, first.x), w_end = min(first.y, p.max_work);
   const int b0 = first.z, L0 = seq_len(p, b0);
@@ -470,7 +537,8 @@ __global__ void __launch_bounds__(Cfg<NR>::kThreads, 1)
       return false;
     };
     Work w = {}, wn = {};
-    bool have = false;  // w's tiles are done
+    bool have = false;            // w's tiles are done
+    bool more = next_row(wn);     // wn is the row after it
     float l_part[RW];
     float c8_row = 0.f;      // lane r < RW: row r's c8
     bool empty_row = true;   // lane r < RW: row r has seen no key
@@ -488,7 +556,6 @@ __global__ void __launch_bounds__(Cfg<NR>::kThreads, 1)
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(tc::smem_u32(&ctl.sum_bar[grp]));
       }
-      const bool more = next_row(wn);
       if (more) {
         // ---- Q: RW rows by 128 threads, kTpr threads a row --------------------
         {
@@ -538,30 +605,29 @@ __global__ void __launch_bounds__(Cfg<NR>::kThreads, 1)
           am = fmaxf(am, 1e-30f);
           const float inv = 448.f / am;
 #pragma unroll 1
-          for (int c = part; c < kRow / 8; c += kTpr) {
-            uint2* const at_hi = reinterpret_cast<uint2*>(smem + hi_at(c));
-            uint2* const at_lo = reinterpret_cast<uint2*>(smem + hi_at(c) + lo_step(c));
-            const uint2 q0 = *at_hi, q1 = *at_lo;
-            const float f = (c < kLat / 8 ? ds0 : ds1) * inv;
-            uint32_t hi[2], lo[2];
-            const uint32_t q4[4] = {q0.x, q0.y, q1.x, q1.y};
+          for (int c = part; c < kRow / 8; c += 3 * kTpr) {  // three chunks at a time
+            uint2 q0[3], q1[3];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const float x0 = __uint_as_float(q4[k] << 16) * f, x1 = __uint_as_float(q4[k] & 0xFFFF0000u) * f;
-              const __nv_fp8x2_storage_t h2 = __nv_cvt_float2_to_fp8x2(make_float2(x0, x1), __NV_SATFINITE, __NV_E4M3);
-              const float2 hf = e4m3x2_to_float2(h2);
-              const __nv_fp8x2_storage_t l2 =
-                  __nv_cvt_float2_to_fp8x2(make_float2(x0 - hf.x, x1 - hf.y), __NV_SATFINITE, __NV_E4M3);
-              if (k & 1) {
-                hi[k >> 1] |= uint32_t(h2) << 16;
-                lo[k >> 1] |= uint32_t(l2) << 16;
-              } else {
-                hi[k >> 1] = uint32_t(h2);
-                lo[k >> 1] = uint32_t(l2);
-              }
+            for (int t = 0; t < 3; ++t) {
+              q0[t] = *reinterpret_cast<const uint2*>(smem + hi_at(c + t * kTpr));
+              q1[t] = *reinterpret_cast<const uint2*>(smem + hi_at(c + t * kTpr) + lo_step(c + t * kTpr));
             }
-            *at_hi = make_uint2(hi[0], hi[1]);
-            *at_lo = make_uint2(lo[0], lo[1]);
+#pragma unroll
+            for (int t = 0; t < 3; ++t) {
+              const float f = (c + t * kTpr < kLat / 8 ? ds0 : ds1) * inv;
+              const uint32_t q4[4] = {q0[t].x, q0[t].y, q1[t].x, q1[t].y};
+              uint32_t h[4], l[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                split2<false>(__uint_as_float(q4[k] << 16) * f, __uint_as_float(q4[k] & 0xFFFF0000u) * f, h[k], l[k]);
+              q0[t] = make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
+              q1[t] = make_uint2(l[0] | l[1] << 16, l[2] | l[3] << 16);
+            }
+#pragma unroll
+            for (int t = 0; t < 3; ++t) {
+              *reinterpret_cast<uint2*>(smem + hi_at(c + t * kTpr)) = q0[t];
+              *reinterpret_cast<uint2*>(smem + hi_at(c + t * kTpr) + lo_step(c + t * kTpr)) = q1[t];
+            }
           }
           if (part == 0) {
             ctl.scale[rg + r] = am * (1.f / 448.f) * qk_log2;
@@ -655,6 +721,11 @@ __global__ void __launch_bounds__(Cfg<NR>::kThreads, 1)
       if (!more) break;
       w = wn;
       have = true;
+      more = next_row(wn);
+      if (more) {
+        // its queries, into L2: they are staged right after this row's last tile
+        prefetch_rows(wn.b, x, 128, rg, rg + RW);
+      }
       c8_row = 0.f;
       empty_row = true;
 #pragma unroll
@@ -699,16 +770,14 @@ __global__ void __launch_bounds__(Cfg<NR>::kThreads, 1)
         };
         // the two terms of p = e
         auto terms_of = [&](int r) {  // rows r, r + 1
-          const __nv_fp8x2_storage_t h2 = __nv_cvt_float2_to_fp8x2(make_float2(e[r], e[r + 1]), __NV_SATFINITE, __NV_E4M3);
-          const float2 hf = e4m3x2_to_float2(h2);
-          const __nv_fp8x2_storage_t l2 =
-              __nv_cvt_float2_to_fp8x2(make_float2(e[r] - hf.x, e[r + 1] - hf.y), __NV_SATFINITE, __NV_E5M2);
+          uint32_t h2, l2;
+          split2<true>(e[r], e[r + 1], h2, l2);
           if ((r & 2) == 0) {
-            hi[r / 4] = uint32_t(h2);
-            lo[r / 4] = uint32_t(l2);
+            hi[r / 4] = h2;
+            lo[r / 4] = l2;
           } else {
-            hi[r / 4] |= uint32_t(h2) << 16;
-            lo[r / 4] |= uint32_t(l2) << 16;
+            hi[r / 4] |= h2 << 16;
+            lo[r / 4] |= l2 << 16;
           }
         };
         auto terms = [&] {

@@ -271,6 +271,9 @@ int mj_latent_attention(const mj_latent_args* a, void* stream) {
   p.stride_token = a->stride_token;
   p.page_size = a->page_size;
   p.page_shift = a->page_size == 16 ? 4 : (a->page_size == 32 ? 5 : (a->page_size == 64 ? 6 : 7));
+  p.page_span = a->stride_token <= 2 * MJ_LATENT_ROW_BYTES
+                    ? uint32_t((a->page_size - 1) * a->stride_token + MJ_LATENT_ROW_BYTES)
+                    : 0;
   p.num_pages = a->num_pages;
   p.descale = a->descale;
   p.block_table = a->block_table;

@@ -120,6 +120,7 @@ struct LatentParams {
   const uint8_t* cache;
   int64_t stride_page, stride_token;
   int page_size, page_shift;
+  uint32_t page_span;  // bytes from a page's first row to the end of its last; 0 where its rows lie far apart
   int64_t num_pages;
   const float* descale;
   const int32_t* block_table;
