@@ -533,8 +533,8 @@ MJ_API int mj_latent_write(const mj_latent_write_args* args, void* stream);
  * 0); the kernels mask by the lengths in device memory. */
 MJ_API int mj_latent_slots(int sm_count, int q_len, int h);
 MJ_API int mj_latent_plan_size(int slots, int max_num_seqs, size_t* words);
-MJ_API int mj_latent_plan(const int32_t* seq_lens_host, int num_seqs, int max_num_seqs, int slots, int margin,
-                   int32_t* plan_host, size_t plan_words);
+MJ_API int mj_latent_plan(const int32_t* seq_lens_host, int num_seqs, int max_num_seqs, int slots, int q_len, int h,
+                   int margin, int32_t* plan_host, size_t plan_words);
 
 /* Bytes of mj_latent_attention's workspace: the status header (mj_workspace_init,
  * mj_workspace_status) and two partials a slot. */

@@ -205,7 +205,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.mj_latent_write.argtypes = [ctypes.POINTER(mj_latent_write_args), vp]
     lib.mj_latent_slots.argtypes = [i32, i32, i32]
     lib.mj_latent_plan_size.argtypes = [i32, i32, ctypes.POINTER(sz)]
-    lib.mj_latent_plan.argtypes = [vp, i32, i32, i32, i32, vp, sz]
+    lib.mj_latent_plan.argtypes = [vp, i32, i32, i32, i32, i32, i32, vp, sz]
     lib.mj_latent_workspace_size.argtypes = [i32, i32, i32, ctypes.POINTER(sz)]
     lib.mj_latent_attention.argtypes = [ctypes.POINTER(mj_latent_args), vp]
     _lib = lib
@@ -450,7 +450,8 @@ def mj_latent_plan_size(slots: int, max_num_seqs: int) -> int:
     return n.value
 
 
-def mj_latent_plan(seq_lens_host, num_seqs: int, max_num_seqs: int, slots: int, margin: int = 0, plan_out=None):
+def mj_latent_plan(seq_lens_host, num_seqs: int, max_num_seqs: int, slots: int, q_len: int, h: int, margin: int = 0,
+                   plan_out=None):
     """Host plan of mj_latent_attention. ``plan_out``: an int32 host buffer
     (numpy or a pinned CPU tensor) of ``mj_latent_plan_size`` words to write
     into; otherwise a numpy array is returned."""
@@ -464,7 +465,7 @@ def mj_latent_plan(seq_lens_host, num_seqs: int, max_num_seqs: int, slots: int, 
         plan_out = np.zeros(words, dtype=np.int32)
     addr = _host_int32(plan_out, words, "plan_out")
     _check("mj_latent_plan", load_library().mj_latent_plan(lens.ctypes.data if num_seqs else None, num_seqs, max_num_seqs,
-                                                           slots, margin, addr, words))
+                                                           slots, q_len, h, margin, addr, words))
     return plan_out
 
 

@@ -19,9 +19,9 @@ int status_of(cudaError_t e) { return e == cudaSuccess ? MJ_OK : MJ_ERR_CUDA; }
 
 bool page_size_ok(int ps) { return ps == 16 || ps == 32 || ps == 64 || ps == 128; }
 
-// A plan's cost of starting a work row, in tiles: staging Q, filling the
-// pipeline and writing the rows out.
-constexpr int kRowCost = 2;
+// A plan's cost of a work row beside its tiles, in tiles: staging the queries,
+// refilling the pipeline, writing the rows out.
+constexpr int kCost16 = 1, kCost32 = 3, kCost64 = 5;
 
 int latent_row_tile(int64_t n_q) { return n_q <= 16 ? 16 : (n_q <= 32 ? 32 : 64); }
 
@@ -133,20 +133,22 @@ int mj_latent_plan_size(int slots, int max_num_seqs, size_t* words) {
   return MJ_OK;
 }
 
-int mj_latent_plan(const int32_t* seq_lens_host, int num_seqs, int max_num_seqs, int slots, int margin,
-                   int32_t* plan_host, size_t plan_words) {
+int mj_latent_plan(const int32_t* seq_lens_host, int num_seqs, int max_num_seqs, int slots, int q_len, int h,
+                   int margin, int32_t* plan_host, size_t plan_words) {
   const mj::NvtxRange range("mj_latent_plan");
-  if (num_seqs < 0 || max_num_seqs < num_seqs || slots < 1 || margin < 0 || !plan_host ||
+  if (num_seqs < 0 || max_num_seqs < num_seqs || slots < 1 || q_len < 1 || h < 1 || margin < 0 || !plan_host ||
       (num_seqs > 0 && !seq_lens_host))
     return MJ_ERR_INVALID_ARG;
   size_t need = 0;
   const int st = mj_latent_plan_size(slots, max_num_seqs, &need);
   if (st != MJ_OK) return st;
   if (plan_words < need) return MJ_ERR_CAPACITY;
+  const int tile = latent_row_tile(int64_t(q_len) * h);
+  const int row_cost = tile == 16 ? kCost16 : (tile == 32 ? kCost32 : kCost64);
   int64_t total = 0;
   for (int b = 0; b < num_seqs; ++b) {
     if (seq_lens_host[b] < 0 || int64_t(seq_lens_host[b]) + margin > INT32_MAX) return MJ_ERR_INVALID_ARG;
-    total += (int64_t(seq_lens_host[b]) + margin + mj::kKvTile - 1) / mj::kKvTile + kRowCost;
+    total += (int64_t(seq_lens_host[b]) + margin + mj::kKvTile - 1) / mj::kKvTile + row_cost;
   }
   auto tiles = [&](int b) -> int64_t {  // a padding request has none
     return seq_lens_host[b] > 0 ? (int64_t(seq_lens_host[b]) + margin + mj::kKvTile - 1) / mj::kKvTile : 0;
@@ -157,7 +159,7 @@ int mj_latent_plan(const int32_t* seq_lens_host, int num_seqs, int max_num_seqs,
   int32_t* work = splits + mj::latent_plan_split_words(max_num_seqs);
 
   // The requests' tiles in order, cut so that no slot's cost (its tiles, and
-  // kRowCost for each of its rows) exceeds `limit`; false when that takes more
+  // row_cost for each of its rows) exceeds `limit`; false when that takes more
   // slots than there are. With `write`, the plan.
   auto cut = [&](int64_t limit, bool write) {
     int slot = 0, rows = 0, parts = 0;
@@ -167,11 +169,11 @@ int mj_latent_plan(const int32_t* seq_lens_host, int num_seqs, int max_num_seqs,
       int64_t at = 0;
       const int first_row = rows, first_part = parts;
       while (at < t) {
-        if (used + kRowCost + 1 > limit) {  // no room for a row here
+        if (used + row_cost + 1 > limit) {  // no room for a row here
           if (++slot >= slots) return false;
           used = 0;
         }
-        const int64_t take = std::min(t - at, limit - used - kRowCost);
+        const int64_t take = std::min(t - at, limit - used - row_cost);
         if (write) {
           int32_t* w = work + 4 * int64_t(rows);
           w[0] = b;
@@ -188,7 +190,7 @@ int mj_latent_plan(const int32_t* seq_lens_host, int num_seqs, int max_num_seqs,
         }
         ++rows;
         at += take;
-        used += take + kRowCost;
+        used += take + row_cost;
       }
       if (rows - first_row > 1) {
         if (write) {
@@ -201,7 +203,7 @@ int mj_latent_plan(const int32_t* seq_lens_host, int num_seqs, int max_num_seqs,
     }
     return true;
   };
-  int64_t lo = kRowCost + 1, hi = std::max<int64_t>(lo, total);  // one slot holds everything at `total`
+  int64_t lo = row_cost + 1, hi = std::max<int64_t>(lo, total);  // one slot holds everything at `total`
   while (lo < hi) {
     const int64_t mid = lo + (hi - lo) / 2;
     if (cut(mid, false))

@@ -362,7 +362,8 @@ class LatentStep:
         into the fixed device buffer on ``stream``."""
         if self._staged is not None:
             self._staged.synchronize()  # the previous copy has read the staging buffer
-        mj_latent_plan(seq_lens_host, num_seqs, self.max_num_seqs, self.slots, self.margin, plan_out=self.plan_host)
+        mj_latent_plan(seq_lens_host, num_seqs, self.max_num_seqs, self.slots, self.q_len, self.h, self.margin,
+                       plan_out=self.plan_host)
         s = stream or torch.cuda.current_stream(self.device)
         _check("mj_plan_upload", load_library().mj_plan_upload(
             self.plan_host.data_ptr(), None, self.plan_dev.data_ptr(), None, self.plan_host.numel() // 4, 0, _stream(s)))

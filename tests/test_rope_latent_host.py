@@ -145,37 +145,41 @@ def test_plan_covers_every_tile_once(seed):
     lens[rng.random(n) < 0.1] = 0
     slots, margin = int(rng.choice([1, 2, 9, 38, 76, 152])), int(rng.integers(0, 4))
     extra = int(rng.integers(0, 5))
-    plan = mj.mj_latent_plan(lens, n, n + extra, slots, margin)
+    h, cost = [(16, 1), (32, 3), (128, 5)][seed // 3 % 3]
+    plan = mj.mj_latent_plan(lens, n, n + extra, slots, 1, h, margin)
     off, rows = check_plan(lens, slots, n + extra, margin, plan)
     # balance: no slot holds more than what an even cut of all rows would give, and a row's cost
-    cost = [sum(int(w[2] - w[1]) + 2 for w in rows[off[s]:off[s + 1]]) for s in range(slots)]
+    held = [sum(int(w[2] - w[1]) + cost for w in rows[off[s]:off[s + 1]]) for s in range(slots)]
     tiles = sum(-(-(int(x) + margin) // 128) for x in lens if x)
     if tiles:
-        assert max(cost) <= (tiles + 2 * (int((lens > 0).sum()) + slots)) / slots + 4
+        assert max(held) <= (tiles + cost * (int((lens > 0).sum()) + slots)) / slots + 2 + cost
 
 
 def test_plan_of_one_long_request_fills_the_slots():
-    plan = mj.mj_latent_plan(np.array([131072], np.int32), 1, 1, 152)
+    plan = mj.mj_latent_plan(np.array([131072], np.int32), 1, 1, 152, 1, 16)
     off, rows = check_plan([131072], 152, 1, 0, plan)
     assert len(rows) >= 140 and max(int(w[2] - w[1]) for w in rows) == 7
 
 
 def test_plan_refusals():
     with pytest.raises(mj.MjError):
-        mj.mj_latent_plan(np.array([5, -1], np.int32), 2, 2, 4)
+        mj.mj_latent_plan(np.array([5, -1], np.int32), 2, 2, 4, 1, 16)
     with pytest.raises(mj.MjError):
-        mj.mj_latent_plan(np.array([5, 1], np.int32), 2, 1, 4)
+        mj.mj_latent_plan(np.array([5, 1], np.int32), 2, 1, 4, 1, 16)
     with pytest.raises(mj.MjError):
-        mj.mj_latent_plan(np.array([5], np.int32), 1, 1, 0)
+        mj.mj_latent_plan(np.array([5], np.int32), 1, 1, 0, 1, 16)
+    for q_len, h in ((0, 16), (1, 0)):
+        with pytest.raises(mj.MjError):
+            mj.mj_latent_plan(np.array([5], np.int32), 1, 1, 4, q_len, h)
     with pytest.raises(ValueError):
-        mj.mj_latent_plan(np.array([5], np.int32), 1, 1, 4, plan_out=np.zeros(8, np.int32))
+        mj.mj_latent_plan(np.array([5], np.int32), 1, 1, 4, 1, 16, plan_out=np.zeros(8, np.int32))
     with pytest.raises(ValueError):
-        mj.mj_latent_plan(np.array([5], np.int32), 2, 2, 4)
+        mj.mj_latent_plan(np.array([5], np.int32), 2, 2, 4, 1, 16)
     lib, lens, out = mj.load_library(), np.array([5], np.int32), np.zeros(64, np.int32)
-    assert lib.mj_latent_plan(lens.ctypes.data, 1, 1, 4, 0, out.ctypes.data, 8) == mj.MJ_ERR_CAPACITY
+    assert lib.mj_latent_plan(lens.ctypes.data, 1, 1, 4, 1, 16, 0, out.ctypes.data, 8) == mj.MJ_ERR_CAPACITY
     # a length that its margin takes past 32 bits
     lens[0] = 2 ** 31 - 2
-    assert lib.mj_latent_plan(lens.ctypes.data, 1, 1, 4, 5, out.ctypes.data, 64) == mj.MJ_ERR_INVALID_ARG
+    assert lib.mj_latent_plan(lens.ctypes.data, 1, 1, 4, 1, 16, 5, out.ctypes.data, 64) == mj.MJ_ERR_INVALID_ARG
 
 
 def test_slots_and_sizes():
