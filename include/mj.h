@@ -462,7 +462,8 @@ MJ_API int mj_rope_turns(const double* inv_freq, int n, uint64_t* turns);
  * kv: as for mj_write_kv (every cache format, head size 128 or 256), except
  * that key is rotated in float32 before its one rounding, to the cache format.
  * q may be q_out (rotated in place, with the same strides); they must not
- * overlap otherwise. h_q = 0: no queries. A padding token (negative slot) has
+ * overlap otherwise. The slots of live tokens are distinct: of two tokens with
+ * one slot, the row holds parts of both. h_q = 0: no queries. A padding token (negative slot) has
  * its queries rotated too.
  * Alignment: q and q_out 16 bytes, their strides multiples of 8 elements.
  * The launch may begin before the preceding kernel on `stream` has finished
@@ -551,8 +552,9 @@ MJ_API int mj_latent_workspace_size(int slots, int q_len, int h, size_t* bytes);
  *
  * Accuracy: queries and softmax weights enter the tensor cores as two 8-bit
  * terms each: a query value within max(2^-8 |q|, 2^-19 of its row's largest),
- * a weight within 2^-7 of itself (0.15% rms) down to 24 binades below its
- * row's largest, below that 0; sums in float32. A NaN code of a cached token
+ * a weight within 2^-7 of itself (0.15% rms) down to 14 binades below its row's
+ * largest, to a fixed step below that, and 0 from 21 binades below it (23 where
+ * the largest stands out); sums in float32. A NaN code of a cached token
  * reaches every row of its request, also one whose causal limit hides it.
  * Status bits (workspace): as mj_workspace_status lists them.
  * Two calls that may run at once (other streams, two captured graphs) need a

@@ -253,7 +253,8 @@ def _stream(stream) -> int | None:
     import torch
 
     if stream is None:
-        stream = torch.cuda.current_stream()
+        # the raw handle: a Stream object takes longer to make than a small launch
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()) or None
     return int(stream.cuda_stream) or None
 
 

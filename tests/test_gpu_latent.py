@@ -233,6 +233,36 @@ def test_lengths_below_the_plan():
     c.check(out, lse, lens=real)
 
 
+def test_padding_alone_and_no_requests():
+    import paged_fp8_decode_gb300 as mj
+
+    c = Case([0, 0, 0], 2, 16, 64, seed=25)
+    out, lse = c.run()
+    c.check(out, lse)
+    step = c.step()
+    step.plan(c.lens, 0)
+    step.run(c.q.cuda(), out, c.device(), 0, c.scale)
+    torch.cuda.synchronize()
+    assert bool((out == SENTINEL).all()) and mj.mj_workspace_status(step.workspace) == 0
+
+
+def test_other_shapes_than_the_step_was_made_for_are_refused():
+    c = Case([100, 200], 1, 16, 64, seed=26)
+    kv, q, out = c.device(), c.q.cuda(), c.outputs()
+    step = c.step()
+    with pytest.raises(ValueError, match="requests"):
+        step.args(q, out, kv, 3, c.scale)
+    with pytest.raises(ValueError, match="rows"):
+        step.args(q[:1], out, kv, 2, c.scale)
+    with pytest.raises(ValueError, match="q"):
+        step.args(q[:, :8], out, kv, 2, c.scale)
+    with pytest.raises(ValueError, match="out"):
+        step.args(q, out.float(), kv, 2, c.scale)
+    with pytest.raises(ValueError, match="seq_lens"):
+        kv.seq_lens = kv.seq_lens.long()
+        step.args(q, out, kv, 2, c.scale)
+
+
 def test_bad_page_is_reported():
     import paged_fp8_decode_gb300 as mj
 

@@ -88,6 +88,8 @@ def make(c, seed):
     pos[:, T // 2] = -7  # a negative position turns backwards
     w["pos"] = pos if axes > 1 else pos[0]
     w["axis"] = rng.integers(0, axes, size=c["rot"] // 2).astype(np.uint8)
+    if axes > 1:
+        w["axis"][-1] = 200  # past the last axis: the last
     slots = rng.permutation(pages * ps)[:T].astype(np.int64)
     if c.get("pad"):
         slots[::c["pad"]] = -1
@@ -199,6 +201,22 @@ def test_slot_past_the_pool_is_skipped_and_reported():
     w["slots"][4] = -1
     check_rotated(w, *out)
     assert int(status.item()) == 1
+
+
+def test_no_tokens_and_no_live_token():
+    import paged_fp8_decode_gb300 as mj
+
+    w = make(CASES[2], 9)
+    w["slots"][:] = -1
+    check_rotated(w, *call(w))  # queries rotated, caches as they were
+    z = torch.zeros(0, 2, 128, dtype=torch.bfloat16, device="cuda")
+    i = torch.zeros(0, dtype=torch.int64, device="cuda")
+    pool = torch.full((4096,), 9, dtype=torch.uint8, device="cuda")
+    one = torch.ones(1, device="cuda")
+    mj.mj_rope_write_kv(mj.rope_write_args(z, z, z, i, mj.mj_rope_turns([1.0] * 8).cuda(), i, pool, pool,
+                                           (4096, 128, 2048), 16, 1, 0, one, one))
+    torch.cuda.synchronize()
+    assert bool((pool == 9).all())
 
 
 def test_nan_and_infinite_inputs_stay_in_their_pairs():
