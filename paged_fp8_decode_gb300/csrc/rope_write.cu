@@ -71,6 +71,27 @@ struct RopeWriteParams {
   uint32_t* status;
 };
 
+// Two float32 products or fused multiply-adds in one instruction.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  uint64_t x, y, d;
+  memcpy(&x, &a, 8);
+  memcpy(&y, &b, 8);
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(x), "l"(y));
+  float2 r;
+  memcpy(&r, &d, 8);
+  return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t x, y, z, d;
+  memcpy(&x, &a, 8);
+  memcpy(&y, &b, 8);
+  memcpy(&z, &c, 8);
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(x), "l"(y), "l"(z));
+  float2 r;
+  memcpy(&r, &d, 8);
+  return r;
+}
+
 // Bounds of 1 / s that hold x * lo <= x / s <= x * hi in size after rounding
 // (8 units of 2^-24 either way; the reciprocal and the two products are off by
 // three). A scale so large or small that the reciprocal could overflow or
@@ -95,8 +116,10 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
 // code it is that one; the division itself is done where they differ (a
 // quotient within 2^-21 of a border between codes, about one in 10^4).
 __device__ __forceinline__ uint32_t quotient_codes(const float* x, float s, Recip r) {
-  const uint32_t lo = e4m3x4(x[0] * r.lo, x[1] * r.lo, x[2] * r.lo, x[3] * r.lo);
-  const uint32_t hi = e4m3x4(x[0] * r.hi, x[1] * r.hi, x[2] * r.hi, x[3] * r.hi);
+  const float2 a = make_float2(x[0], x[1]), b = make_float2(x[2], x[3]);
+  const float2 rl = make_float2(r.lo, r.lo), rh = make_float2(r.hi, r.hi);
+  const float2 al = mul2(a, rl), bl = mul2(b, rl), ah = mul2(a, rh), bh = mul2(b, rh);
+  const uint32_t lo = e4m3x4(al.x, al.y, bl.x, bl.y), hi = e4m3x4(ah.x, ah.y, bh.x, bh.y);
   if (lo == hi) return lo;
   return e4m3x4(__fdiv_rn(x[0], s), __fdiv_rn(x[1], s), __fdiv_rn(x[2], s), __fdiv_rn(x[3], s));
 }
@@ -127,27 +150,6 @@ __device__ __forceinline__ void encode8(const float x[8], const float* scale, Re
       o[2] = uint16_t(bits >> 32);
     }
   }
-}
-
-// Two float32 products or fused multiply-adds in one instruction.
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  uint64_t x, y, d;
-  memcpy(&x, &a, 8);
-  memcpy(&y, &b, 8);
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(x), "l"(y));
-  float2 r;
-  memcpy(&r, &d, 8);
-  return r;
-}
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  uint64_t x, y, z, d;
-  memcpy(&x, &a, 8);
-  memcpy(&y, &b, 8);
-  memcpy(&z, &c, 8);
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(x), "l"(y), "l"(z));
-  float2 r;
-  memcpy(&r, &d, 8);
-  return r;
 }
 
 __device__ __forceinline__ uint4 pack_bf16x8(const float x[8]) {
