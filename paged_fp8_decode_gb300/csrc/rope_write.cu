@@ -21,6 +21,8 @@
 // and sines into shared memory while they arrive.
 #include <cuda_fp8.h>
 
+#include <atomic>
+
 #include "kv_codec.cuh"
 #include "mj_device.cuh"
 #include "mj_internal.h"
@@ -35,10 +37,11 @@ constexpr int kThreads = 128;
 // 32/8 heads of 128 in 62.8 us (5.9 TB/s). Three slots and five CTAs: 65.6 us,
 // and 0.2 us less for one token; eight CTAs spill: 71 us.
 constexpr int kItemsPerThread = 2, kMinCtas = 7;
-// With many tokens a thread takes more slots, so that its cosines, addresses
-// and set-up serve more of them (up to 6 against up to 4: 69 and 78 us before
-// the packed arithmetic); with few, the shorter chain counts.
-constexpr int kManyTokens = 600, kItemsMany = 6;
+// Where the CTAs of that would not be resident at once, a thread takes up to
+// six slots, so that its cosines, addresses and set-up serve more of them
+// (16384 tokens: 62.8 against 70.2 us); where they are, the shorter chain counts
+// (32/8 heads, 900 tokens: 5.1 against 7.2 us, 1500 tokens: 9.1 against 8.6).
+constexpr int kItemsMany = 6;
 
 struct RopeWriteParams {
   // rotation
@@ -314,12 +317,31 @@ cudaError_t launch(RopeWriteParams p, cudaStream_t stream) {
   const int64_t slots = int64_t(p.h_q) + p.h_k + int64_t(p.h_k) * (VD / D);
   // Lanes a token: so many that a thread has at most that many slots, up to the
   // CTA's; the CTA takes more tokens where that leaves room.
-  p.lanes = 1;
-  const int per_thread = p.num_tokens > kManyTokens ? kItemsMany : kItemsPerThread;
-  while (p.lanes < kLanes && p.lanes * per_thread < slots) p.lanes *= 2;
+  auto lanes_for = [&](int per_thread) {
+    int lanes = 1;
+    while (lanes < kLanes && lanes * per_thread < slots) lanes *= 2;
+    return lanes;
+  };
+  auto ctas = [&] { return (int64_t(p.num_tokens) + p.group - 1) / p.group; };
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  static std::atomic<int> sm_count[64];  // per device, looked up once (host threads may race)
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  int sms = sm_count[dev].load(std::memory_order_relaxed);
+  if (sms == 0) {
+    e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    sm_count[dev].store(sms, std::memory_order_relaxed);
+  }
+  p.lanes = lanes_for(kItemsPerThread);
   p.group = kLanes / p.lanes;
+  if (ctas() > int64_t(kMinCtas) * sms) {
+    p.lanes = lanes_for(kItemsMany);
+    p.group = kLanes / p.lanes;
+  }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned((int64_t(p.num_tokens) + p.group - 1) / p.group));
+  cfg.gridDim = dim3(unsigned(ctas()));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = size_t(p.group) * p.n * 2 * sizeof(float);  // at most 8 KB: 32 tokens of 32 or 8 of 128 frequencies
   cfg.stream = stream;
