@@ -20,7 +20,10 @@ int status_of(cudaError_t e) { return e == cudaSuccess ? MJ_OK : MJ_ERR_CUDA; }
 bool page_size_ok(int ps) { return ps == 16 || ps == 32 || ps == 64 || ps == 128; }
 
 // A plan's cost of a work row beside its tiles, in tiles: staging the queries,
-// refilling the pipeline, writing the rows out.
+// refilling the pipeline, writing the rows out and joining them. Measured (us):
+// 64 x 4096 tokens, 16 heads: 35.8, 34.5, 35.7 at 0, 1, 2; 96 requests of 300 to
+// 5000 tokens, 32 heads: 55.2, 49.8, 48.8, 50.6 at 1, 2, 3, 6; 48 of 1024 to
+// 16384, 128 heads: 136, 125, 116, 121 at 1, 2, 5, 9.
 constexpr int kCost16 = 1, kCost32 = 3, kCost64 = 5;
 
 int latent_row_tile(int64_t n_q) { return n_q <= 16 ? 16 : (n_q <= 32 ? 32 : 64); }
@@ -144,7 +147,7 @@ int mj_latent_plan(const int32_t* seq_lens_host, int num_seqs, int max_num_seqs,
   if (st != MJ_OK) return st;
   if (plan_words < need) return MJ_ERR_CAPACITY;
   const int tile = latent_row_tile(int64_t(q_len) * h);
-  const int row_cost = tile == 16 ? kCost16 : (tile == 32 ? kCost32 : kCost64);
+  const int row_cost = tile == 16 ? kCost16 : (tile == 32 ? kCost32 : kCost64), least = std::min(row_cost, 3);
   int64_t total = 0;
   for (int b = 0; b < num_seqs; ++b) {
     if (seq_lens_host[b] < 0 || int64_t(seq_lens_host[b]) + margin > INT32_MAX) return MJ_ERR_INVALID_ARG;
@@ -169,7 +172,8 @@ int mj_latent_plan(const int32_t* seq_lens_host, int num_seqs, int max_num_seqs,
       int64_t at = 0;
       const int first_row = rows, first_part = parts;
       while (at < t) {
-        if (used + row_cost + 1 > limit) {  // no room for a row here
+        // no room for a row here, or for so few tiles only that starting it costs more
+        if (used > 0 && used + row_cost + std::min<int64_t>(t - at, least) > limit) {
           if (++slot >= slots) return false;
           used = 0;
         }
