@@ -11,7 +11,7 @@
 // request split over the whole GPU): four rows of 32 channels to a CTA, whose 16
 // warps share the partials and meet in shared memory.
 #include "mj_device.cuh"
-#include "mj_internal.h"
+#include "mj_latent.h"
 #include "tc_ptx.cuh"
 
 namespace mj {

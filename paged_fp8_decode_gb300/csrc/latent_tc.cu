@@ -38,9 +38,9 @@
 #include <atomic>
 #include <climits>
 
+#include "latent_ptx.cuh"
 #include "mj_device.cuh"
-#include "mj_internal.h"
-#include "tc_ptx.cuh"
+#include "mj_latent.h"
 
 namespace mj {
 
@@ -114,15 +114,6 @@ constexpr int smem_bytes() {
 static_assert(smem_bytes<64>() <= kMaxDynSmem && smem_bytes<32>() <= kMaxDynSmem && smem_bytes<16>() <= kMaxDynSmem,
               "shared memory");
 
-__device__ __forceinline__ void prefetch_l2(const void* at) {
-  asm volatile("prefetch.global.L2 [%0];" ::"l"(at));
-}
-
-// `bytes` (a multiple of 16) from a 16-byte aligned address into L2, asynchronously.
-__device__ __forceinline__ void prefetch_bulk_l2(const void* at, uint32_t bytes) {
-  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(at), "r"(bytes) : "memory");
-}
-
 // Bounded wait, the loop out of line: the kernel has some twenty of them, and
 // code that runs once is bound by its fetch from L2.
 __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile int* abort) {
@@ -130,13 +121,6 @@ __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile i
 }
 __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int* abort) {
   return tc::mbar_try_wait(bar, parity) || wait_slow(bar, parity, abort);
-}
-
-// max over the warp, in every lane (NaN lanes do not count)
-__device__ __forceinline__ float redux_max(float v) {
-  float r;
-  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
-  return r;
 }
 
 // Reduce N per-lane values over the warp's lanes: row r ends up in lanes
@@ -162,20 +146,6 @@ __device__ __forceinline__ float reduce_rows(float (&v)[N], int lane) {
   }
   return r;
 }
-
-// Called by a whole converged warp: one elected lane issues.
-__device__ __forceinline__ void tma_load_3d_warp(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1, int c2,
-                                                 uint64_t policy) {
-  asm volatile(
-      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
-      "@e cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
-      " [%0], [%1, {%2, %3, %4}], [%5], %6;\n\t}" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar), "l"(policy)
-      : "memory");
-}
-
-constexpr uint32_t kSwizzle64B = 4;      // shared-memory descriptor, bits 61-63
-constexpr uint32_t kFormatBE5m2 = 1u << 10;  // instruction descriptor: B holds e5m2 codes
 
 // Two values as two 8-bit terms each: hi = e4m3(v), lo = e4m3 or e5m2(v - hi).
 // By way of f16, whose 2^-12 is far inside the terms' own steps and whose range
@@ -252,7 +222,7 @@ __global__ void __launch_bounds__(Cfg<NR>::kThreads, 1)
     for (int k = t; k < (r_to - r_from) * kLines; k += n) {
       const int r = tile0 + r_from + k / kLines, tq = r / p.h, h = r - tq * p.h;
       if (r < p.n_q)
-        prefetch_l2(p.q + (int64_t(b) * p.q_len + tq) * p.q_ts + int64_t(h) * p.q_hs + (k % kLines) * 64);
+        tc::prefetch_l2(p.q + (int64_t(b) * p.q_len + tq) * p.q_ts + int64_t(h) * p.q_hs + (k % kLines) * 64);
     }
   };
 
@@ -312,7 +282,7 @@ __global__ void __launch_bounds__(Cfg<NR>::kThreads, 1)
         const int64_t end = int64_t(min(w.z, f.w + C::kPrefetchTiles)) << (7 - p.page_shift);
         if (p.page_span && page < end && page < p.bt_len) {
           const int pg = p.block_table[int64_t(f.z) * p.bt_stride + page];
-          if (pg >= 0 && pg < p.num_pages) prefetch_bulk_l2(p.cache + int64_t(pg) * p.stride_page, p.page_span);
+          if (pg >= 0 && pg < p.num_pages) tc::prefetch_bulk_l2(p.cache + int64_t(pg) * p.stride_page, p.page_span);
         }
       } else if (warp >= 4) {
         prefetch_rows(f.z, tid - 128, 128 * G, 0, NR);
@@ -380,7 +350,7 @@ __global__ void __launch_bounds__(Cfg<NR>::kThreads, 1)
           __syncwarp();
 #pragma unroll 1
           for (int k = 0; k < nvalid; ++k, dst += page_bytes)
-            tma_load_3d_warp(dst, rope ? &tmap_rope : &tmap_lat, full, 128 * j, 0,
+            tc::tma_load_3d_warp(dst, rope ? &tmap_rope : &tmap_lat, full, 128 * j, 0,
                              __shfl_sync(0xFFFFFFFFu, entry, at + k), pol);
           ++issued;
         }
@@ -407,8 +377,8 @@ __global__ void __launch_bounds__(Cfg<NR>::kThreads, 1)
     constexpr uint32_t idesc_pv = tc::idesc_e4m3(128, NR, true, true);
     const uint64_t kd0 = tc::smem_desc(base, 16, 1024, tc::kSwizzle128B);
     const uint64_t qd0 = tc::smem_desc(base + uint32_t(C::kOffQ), 16, 1024, tc::kSwizzle128B);
-    const uint64_t krd0 = tc::smem_desc(base + uint32_t(C::kOffRope), 16, 512, kSwizzle64B);
-    const uint64_t qrd = tc::smem_desc(base + uint32_t(C::kOffQ + 4 * C::kQSub), 16, 512, kSwizzle64B);
+    const uint64_t krd0 = tc::smem_desc(base + uint32_t(C::kOffRope), 16, 512, tc::kSwizzle64B);
+    const uint64_t qrd = tc::smem_desc(base + uint32_t(C::kOffQ + 4 * C::kQSub), 16, 512, tc::kSwizzle64B);
     const uint64_t vd0 = tc::smem_desc(base, kSub, 1024, tc::kSwizzle128B);
     // P, MN-major without swizzle: 8-key core groups 128 B apart, 16-row blocks
     // 2 KB apart; lo after hi
@@ -476,7 +446,7 @@ __global__ void __launch_bounds__(Cfg<NR>::kThreads, 1)
                 tc::umma_f8f6f4_warp(tO + uint32_t(j * NR), vd + uint64_t(256 * k), pd + uint64_t(32 * k), idesc_pv,
                                      k > 0 ? 1u : acc);
                 tc::umma_f8f6f4_warp(tO + uint32_t(j * NR), vd + uint64_t(256 * k), pd + uint64_t(NR * 8 + 32 * k),
-                                     idesc_pv | kFormatBE5m2, 1);
+                                     idesc_pv | tc::kFormatBE5m2, 1);
               }
               tc::umma_commit_warp(tc::smem_u32(&ctl.empty[sv]));
               if (++sv == C::kRing) sv = 0;
@@ -813,7 +783,7 @@ __global__ void __launch_bounds__(Cfg<NR>::kThreads, 1)
                 tc::tmem_wait_ld();
                 float v = fmaf(s0 + s1, ctl.scale[rg + r], ctl.c8[rg + r]);
                 if (masked && (dead || int(t_end) - kKvTile + x > ctl.lim[rg + r])) v = -INFINITY;
-                v = redux_max(v) - kBaseSink;
+                v = tc::redux_max(v) - kBaseSink;
                 if (lane == 0) ctl.by[grp][xb & 1][qd][r] = uint8_t(fminf(ceilf(v), kFar));
               }
             }

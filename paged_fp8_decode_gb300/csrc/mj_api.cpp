@@ -10,6 +10,7 @@
 #include <cstring>
 
 #include "mj_internal.h"
+#include "mj_latent.h"
 
 namespace {
 

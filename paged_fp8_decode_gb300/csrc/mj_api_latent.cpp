@@ -9,7 +9,7 @@
 #include <cstdint>
 #include <cstring>
 
-#include "mj_internal.h"
+#include "mj_latent.h"
 
 namespace {
 

@@ -25,7 +25,7 @@
 
 #include "kv_codec.cuh"
 #include "mj_device.cuh"
-#include "mj_internal.h"
+#include "mj_latent.h"
 #include "tc_ptx.cuh"
 
 namespace mj {
