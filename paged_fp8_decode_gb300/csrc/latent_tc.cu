@@ -650,7 +650,7 @@ __global__ void __launch_bounds__(Cfg<NR>::kThreads, 1)
         if (!ok) break;
         tc::tc_fence_after();
         if (w.part >= 0) {
-            // a partial: four rows of a channel are one 16-byte store, a warp's 512 bytes in a row
+          // a partial: four rows of a channel are one 16-byte store, a warp's 512 bytes in a row
           float4* dst = reinterpret_cast<float4*>(p.o_part) +
                         ((int64_t(w.part) * p.n_row_tiles + r0 / NR) * 4 * (NR / 4) + rg / 4) * 128 + x;
 #pragma unroll 1
