@@ -824,7 +824,8 @@ __global__ void __launch_bounds__(Cfg<NR>::kThreads, 1)
               const float em = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)), least = fminf(fminf(m0, m1), fminf(m2, m3));
               moved = em != -INFINITY && (i == 0 || em > kTop);
               const float d = moved ? em - (i == 0 && em - least <= kStandsOut ? kBase : kBaseSink) : 0.f;
-              if (i == 0) empty_row = em == -INFINITY;
+              // (by the mask, not by em: NaN logits beside masked keys leave em at -inf too)
+              if (i == 0) empty_row = int64_t(ctl.lim[rg + lane]) < w.k0;
               c8_row -= d;
               ctl.c8[rg + lane] = c8_row;
               ctl.move[rg + lane] = i == 0 ? d : fast_exp2(-d);

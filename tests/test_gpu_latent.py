@@ -304,6 +304,25 @@ def test_nan_query_stays_in_its_row():
     assert bad.nonzero()[:, 0].tolist() == [3, 4]
 
 
+@pytest.mark.parametrize("n,h", [(1, 8), (37, 20), (200, 16), (70, 128)])
+def test_nan_query_of_a_request_that_ends_inside_a_tile(n, h):
+    """Masked keys beside NaN logits: the row is not taken for one without a key."""
+    c = Case([n], 1, h, 64, seed=31)
+    c.q[0, 3, 100] = float("nan")
+    out, lse = c.run(sm_count=1)
+    bad = torch.isnan(out[0]).all(dim=1).cpu()
+    assert bad.nonzero()[:, 0].tolist() == [3]
+    assert torch.isnan(lse[0]).nonzero()[:, 0].tolist() == [3]
+    assert bool(torch.isfinite(out[0][~bad.cuda()]).all())
+
+
+def test_nan_code_of_the_only_token():
+    c = Case([1], 1, 8, 16, seed=32)
+    c.cache[c.table[0, 0], 0, 5] = 0x7F
+    out, lse = c.run()
+    assert bool(torch.isnan(out).all()) and bool(torch.isnan(lse).all())
+
+
 def test_offsets_past_32_bits():
     """Pages at the far end of a pool larger than 4 GiB."""
     c = Case([130, 500], 1, 16, 64, seed=18)
