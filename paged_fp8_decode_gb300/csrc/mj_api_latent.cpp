@@ -26,6 +26,9 @@ bool page_size_ok(int ps) { return ps == 16 || ps == 32 || ps == 64 || ps == 128
 // 16384, 128 heads: 136, 125, 116, 121 at 1, 2, 5, 9.
 constexpr int kCost16 = 1, kCost32 = 3, kCost64 = 5;
 
+// The writes' kernel indexes tokens, rounded up to whole CTAs, with 32 bits.
+constexpr int kMaxTokens = 1 << 30;
+
 int latent_row_tile(int64_t n_q) { return n_q <= 16 ? 16 : (n_q <= 32 ? 32 : 64); }
 
 int check_rope(const mj_rope& r, int d) {
@@ -90,6 +93,7 @@ int mj_rope_turns(const double* inv_freq, int n, uint64_t* turns) {
 int mj_rope_write_kv(const mj_rope_write_kv_args* a, void* stream) {
   const mj::NvtxRange range("mj_rope_write_kv");
   if (!a) return MJ_ERR_INVALID_ARG;
+  if (a->kv.num_tokens > kMaxTokens) return MJ_ERR_CAPACITY;
   int st = mj::check_write_kv(&a->kv);
   if (st != MJ_OK || a->kv.num_tokens == 0) return st;
   st = check_rope(a->rope, a->kv.d);
@@ -104,6 +108,7 @@ int mj_latent_write(const mj_latent_write_args* a, void* stream) {
   const mj::NvtxRange range("mj_latent_write");
   if (!a) return MJ_ERR_INVALID_ARG;
   if (a->num_tokens < 0 || a->num_pages < 0) return MJ_ERR_INVALID_ARG;
+  if (a->num_tokens > kMaxTokens) return MJ_ERR_CAPACITY;
   if (!page_size_ok(a->page_size)) return MJ_ERR_UNSUPPORTED;
   if (a->num_tokens == 0) return MJ_OK;
   int st = check_rope(a->rope, MJ_LATENT_ROPE_DIM);

@@ -293,6 +293,16 @@ def test_latent_attention_refusals(path, value, status):
     assert mj.load_library().mj_latent_attention(ctypes.byref(a), None) == status
 
 
+def test_more_tokens_than_a_launch_indexes_are_refused():
+    lib = mj.load_library()
+    a, b = rope_write(), latent_write()
+    a.kv.num_tokens, a.kv.h_k, b.num_tokens = (1 << 30) + 1, 1, (1 << 30) + 1
+    a.kv.slot_mapping = b.slot_mapping = None  # (a call that passed the limit would stop here, by another status)
+    a.rope.rot_dim = b.rope.rot_dim = 24
+    assert lib.mj_rope_write_kv(ctypes.byref(a), None) == mj.MJ_ERR_CAPACITY
+    assert lib.mj_latent_write(ctypes.byref(b), None) == mj.MJ_ERR_CAPACITY
+
+
 def test_nothing_to_do_is_ok():
     lib = mj.load_library()
     a, b, c = rope_write(), latent_write(), latent()
