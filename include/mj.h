@@ -524,7 +524,7 @@ typedef struct mj_latent_write_args {
   int page_size;
   int64_t num_pages;
   void* cache;                /* token j of page p at cache + p*stride_page + j*stride_token */
-  int64_t stride_page, stride_token;  /* bytes */
+  int64_t stride_page, stride_token;  /* bytes, at least 576 */
   const float* scale;         /* device [2]: latent, key part */
   uint32_t* status;           /* nullable device word: bit 1 for a slot past the pool (skipped) */
 } mj_latent_write_args;

@@ -117,7 +117,8 @@ int mj_latent_write(const mj_latent_write_args* a, void* stream) {
   if (st != MJ_OK) return st;
   if (a->h > (1 << 16)) return MJ_ERR_INVALID_ARG;
   if (!a->latent || !a->k_pe || !a->slot_mapping || !a->cache || !a->scale) return MJ_ERR_INVALID_ARG;
-  if (a->latent_tok_stride < 0 || a->k_pe_tok_stride < 0 || a->stride_page < 0 || a->stride_token < 0)
+  if (a->latent_tok_stride < 0 || a->k_pe_tok_stride < 0 || a->stride_page < MJ_LATENT_ROW_BYTES ||
+      a->stride_token < MJ_LATENT_ROW_BYTES)
     return MJ_ERR_INVALID_ARG;
   if (!aligned(a->latent, 16) || !aligned(a->k_pe, 16) || !aligned(a->cache, 16) || !aligned(a->slot_mapping, 8) ||
       !aligned(a->scale, 4) || (a->status && !aligned(a->status, 4)))

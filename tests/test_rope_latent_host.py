@@ -293,6 +293,15 @@ def test_latent_attention_refusals(path, value, status):
     assert mj.load_library().mj_latent_attention(ctypes.byref(a), None) == status
 
 
+@pytest.mark.parametrize("path,value", [("stride_token", 560), ("stride_token", 0), ("stride_page", 560), ("stride_page", 0)])
+def test_latent_write_refuses_rows_that_overlap(path, value):
+    a = latent_write()
+    set_path(a, path, value)
+    a.rope.scale = 1.0
+    a.latent_tok_stride = 4  # (stops a call that passed the check, by another status)
+    assert mj.load_library().mj_latent_write(ctypes.byref(a), None) == I
+
+
 def test_more_tokens_than_a_launch_indexes_are_refused():
     lib = mj.load_library()
     a, b = rope_write(), latent_write()
