@@ -547,7 +547,7 @@ MJ_API int mj_latent_plan(const int32_t* seq_lens_host, int num_seqs, int max_nu
                    int margin, int32_t* plan_host, size_t plan_words);
 
 /* Bytes of mj_latent_attention's workspace: the status header (mj_workspace_init,
- * mj_workspace_status) and two partials a slot. */
+ * mj_workspace_status) and two partials a slot. q_len * h is at most 2^20. */
 MJ_API int mj_latent_workspace_size(int slots, int q_len, int h, size_t* bytes);
 
 /* ------------------------------------------------------------------------

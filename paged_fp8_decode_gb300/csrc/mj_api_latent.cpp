@@ -29,6 +29,9 @@ constexpr int kCost16 = 1, kCost32 = 3, kCost64 = 5;
 // The writes' kernel indexes tokens, rounded up to whole CTAs, with 32 bits.
 constexpr int kMaxTokens = 1 << 30;
 
+// Query rows of a request (its partials' sizes stay far inside 64 bits).
+constexpr int64_t kMaxRows = 1 << 20;
+
 int latent_row_tile(int64_t n_q) { return n_q <= 16 ? 16 : (n_q <= 32 ? 32 : 64); }
 
 int check_rope(const mj_rope& r, int d) {
@@ -226,7 +229,7 @@ int mj_latent_plan(const int32_t* seq_lens_host, int num_seqs, int max_num_seqs,
 }
 
 int mj_latent_workspace_size(int slots, int q_len, int h, size_t* bytes) {
-  if (!bytes || slots < 1 || q_len < 1 || h < 1) return MJ_ERR_INVALID_ARG;
+  if (!bytes || slots < 1 || q_len < 1 || h < 1 || int64_t(q_len) * h > kMaxRows) return MJ_ERR_INVALID_ARG;
   const int64_t tile = latent_row_tile(int64_t(q_len) * h);
   const int64_t rows = (int64_t(q_len) * h + tile - 1) / tile * tile;
   *bytes = mj::kWsHeader + size_t(2) * slots * size_t(rows) * (MJ_LATENT_DIM + 2) * sizeof(float);
@@ -244,7 +247,7 @@ int mj_latent_attention(const mj_latent_args* a, void* stream) {
   if (!(a->softmax_scale > 0.f) || !std::isfinite(a->softmax_scale)) return MJ_ERR_INVALID_ARG;
   if (a->out_dtype != MJ_OUT_BF16 && a->out_dtype != MJ_OUT_F16) return MJ_ERR_UNSUPPORTED;
   const int64_t n_q = int64_t(a->q_len) * a->h;
-  if (n_q > (1 << 20)) return MJ_ERR_INVALID_ARG;
+  if (n_q > kMaxRows) return MJ_ERR_INVALID_ARG;
   const void* need[] = {a->q, a->cache, a->descale, a->block_table, a->seq_lens, a->plan, a->out, a->workspace};
   for (const void* ptr : need)
     if (!ptr) return MJ_ERR_INVALID_ARG;

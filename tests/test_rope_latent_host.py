@@ -312,6 +312,13 @@ def test_more_tokens_than_a_launch_indexes_are_refused():
     assert lib.mj_latent_write(ctypes.byref(b), None) == mj.MJ_ERR_CAPACITY
 
 
+def test_workspace_of_more_rows_than_the_attention_takes_is_refused():
+    lib, n = mj.load_library(), ctypes.c_size_t(0)
+    assert lib.mj_latent_workspace_size(152, 8192, 128, ctypes.byref(n)) == mj.MJ_OK
+    assert lib.mj_latent_workspace_size(152, 8193, 128, ctypes.byref(n)) == I
+    assert lib.mj_latent_workspace_size(2**31 - 1, 2**31 - 1, 2**31 - 1, ctypes.byref(n)) == I
+
+
 def test_nothing_to_do_is_ok():
     lib = mj.load_library()
     a, b, c = rope_write(), latent_write(), latent()
