@@ -196,7 +196,13 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) rope_write_kernel(RopeWrit
   tc::grid_launch_dependents();
   tc::grid_dependency_wait();
 
-  auto load = [&](int s, uint4& a, uint4& b) {
+  // The n-th slot in the order taken: queries, keys, values; of a latent row
+  // (one key, one value head) values, queries, key, as its eight value slots
+  // fill a warp's lanes and the key then shares no pass with them (8191 tokens:
+  // 14.7 against 16.6 us; 40 tokens of 128 heads 4.1 against 4.4).
+  auto slot_at = [&](int n) { return VD == D ? n : (n < kVS ? p.h_q + 1 + n : n - kVS); };
+  auto load = [&](int n, uint4& a, uint4& b) {
+    const int s = slot_at(n);
     const uint16_t* src;
     int o0 = c0, o1 = c1;
     if (s < p.h_q) {
@@ -205,7 +211,7 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) rope_write_kernel(RopeWrit
       src = p.key + tok * p.k_ts + (s - p.h_q) * p.k_hs;
     } else {
       const int v = s - p.h_q - p.h_k;
-      src = p.value + tok * p.v_ts + (v / kVS) * p.v_hs + (v % kVS) * D;
+      src = p.value + tok * p.v_ts + (VD == D ? v * p.v_hs : v * D);
       o0 = 16 * j;
       o1 = o0 + 8;
     }
@@ -249,8 +255,8 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) rope_write_kernel(RopeWrit
   for (int s0 = lane; s0 < n_slots; s0 += U * p.lanes) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int s = s0 + u * p.lanes;
-      if (s >= n_slots) break;
+      if (s0 + u * p.lanes >= n_slots) break;
+      const int s = slot_at(s0 + u * p.lanes);
       const bool value = s >= p.h_q + p.h_k;
       if (s >= p.h_q && !live) continue;  // a padding token, or a slot past the pool
       float x[8], y[8];
@@ -288,14 +294,14 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) rope_write_kernel(RopeWrit
         *reinterpret_cast<uint4*>(dst + c0) = pack_bf16x8(x);
         *reinterpret_cast<uint4*>(dst + c1) = pack_bf16x8(y);
       } else if (!value) {
-        const int g = s - p.h_q;
+        const int g = VD == D ? s - p.h_q : 0;
         uint8_t* row = p.k_cache + page * p.k_sp + prow * p.k_st + g * p.k_sh;
         const float* scale = p.k_scale + (F != MJ_KV_E4M3 ? g * D : (p.scale_per_head ? g : 0));
         const Recip r = F == MJ_KV_E4M3 ? recip_bounds(scale[0]) : Recip{};
         encode8<F>(x, scale, r, row, c0);
         encode8<F>(y, scale, r, row, c1);
       } else {
-        const int v = s - p.h_q - p.h_k, g = v / kVS, c = (v % kVS) * D + 16 * j;
+        const int v = s - p.h_q - p.h_k, g = VD == D ? v : 0, c = (VD == D ? 0 : v * D) + 16 * j;
         uint8_t* row = p.v_cache + page * p.v_sp + prow * p.v_st + g * p.v_sh;
         const float* scale = p.v_scale + (F != MJ_KV_E4M3 ? g * D : (p.scale_per_head ? g : 0));
         const Recip r = F == MJ_KV_E4M3 ? recip_bounds(scale[0]) : Recip{};
