@@ -560,11 +560,16 @@ MJ_API int mj_latent_workspace_size(int slots, int q_len, int h, size_t* bytes);
  * (LSE -inf). Two launches: the attention and the join of split requests.
  *
  * Accuracy: queries and softmax weights enter the tensor cores as two 8-bit
- * terms each: a query value within max(2^-8 |q|, 2^-19 of its row's largest),
- * a weight within 2^-7 of itself (0.15% rms) down to 14 binades below its row's
- * largest, to a fixed step below that, and 0 from 21 binades below it (23 where
- * the largest stands out); sums in float32. A NaN code of a cached token
- * reaches every row of its request, also one whose causal limit hides it.
+ * terms each, sums are float32. A query value is within max(2^-8 |q|, 2^-18 of
+ * its row's largest). A weight is within 2^-7.8 of itself (0.15% rms) down to 10
+ * binades below its row's largest (12 where the largest stands out); below that
+ * it is rounded up or down by a dither that depends on its key's index alone, by
+ * 2^-2 of itself or 2^-20 of the largest at most and right on average but for
+ * 2^-29 of the largest. So N such weights, equal ones too, are off by some
+ * sqrt(N) times one of them at random and N 2^-29 together: less than 0.2% of
+ * max|V| in the output at 131072 keys. Weights from 29 binades below on are 0.
+ * A NaN code of a cached token reaches every row of its request, also one whose
+ * causal limit hides it.
  * Status bits (workspace): as mj_workspace_status lists them.
  * Two calls that may run at once (other streams, two captured graphs) need a
  * workspace each. The first call of each row tile on a device raises a kernel's

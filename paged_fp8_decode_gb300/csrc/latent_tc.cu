@@ -20,9 +20,14 @@
 // weights enter as two terms each. A query row is scaled to amax = 448 and
 // split into hi = e4m3(x) and lo = e4m3(x - hi) (within 2^-8 of x, or 2^-19 of
 // the row's amax): two rows of the Q tile, their products added when S is
-// read. A weight p is split into hi = e4m3(p) and lo = e5m2(p - hi) (within
-// 2^-7 of p and 0.15% rms, about bf16's own; e5m2 reaches down to 2^-17), two
-// products into one accumulator. The row sums add the p themselves in float32.
+// read. A weight p is split into hi = e4m3(p) and lo, the rest in e5m2: two
+// products into one accumulator. From 2^-6 on that is within 2^-7.8 of p, 0.15%
+// rms, about bf16's own. Below 2^-6 hi is on a fixed step and lo alone has two
+// bits, so that many equal small weights, all off alike, would change their
+// share of a row (131071 keys 16.8 binades below one: the output by 2% of
+// max|V|); there lo is rounded up or down by a dither, 8 bits of a hash of the
+// key's index, and the errors cancel (0.01%). The row sums add the p themselves
+// in float32.
 //
 // Warps: 0, 2, 3 the TMA producers, 1 the MMA issuer, 4.. one or two softmax
 // warpgroups (thread x of a group: key x of S, channel x of each of the four
@@ -160,26 +165,56 @@ __device__ __forceinline__ float reduce_rows(float (&v)[N], int lane) {
   return r;
 }
 
-// Two values as two 8-bit terms each: hi = e4m3(v), lo = e4m3 or e5m2(v - hi).
-// By way of f16, whose 2^-12 is far inside the terms' own steps and whose range
-// holds every v here (weights and scaled queries are at most 448; below 2^-14
-// it keeps 2^-25, the terms 2^-18), because the difference and the conversions
-// take both values at once there.
-template <bool E5M2>
-__device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
-  const __half2 h = __floats2half2_rn(a, b);
-  uint32_t hb, back, d;
-  uint16_t hc, lc;
+// The e4m3 codes of two values and what they leave, as float16 pairs. By way of
+// f16, whose 2^-11 is far inside the terms' own steps and whose range holds every
+// value here (weights and scaled queries are at most 448; below 2^-14 it keeps
+// 2^-25), because the difference (exact) and the conversions take both values at
+// once there.
+__device__ __forceinline__ uint32_t split2(float a, float b, __half2& h, uint32_t& rest) {
+  h = __floats2half2_rn(a, b);
+  uint32_t hb, back;
+  uint16_t hc;
   memcpy(&hb, &h, 4);
   asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(hc) : "r"(hb));
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(back) : "h"(hc));
-  asm("sub.f16x2 %0, %1, %2;" : "=r"(d) : "r"(hb), "r"(back));
-  if constexpr (E5M2)
-    asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(lc) : "r"(d));
-  else
-    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(lc) : "r"(d));
-  hi = hc;
+  asm("sub.f16x2 %0, %1, %2;" : "=r"(rest) : "r"(hb), "r"(back));
+  return hc;
+}
+
+// Two query values: hi = e4m3(v), lo = e4m3(v - hi).
+__device__ __forceinline__ void query_terms(float a, float b, uint32_t& hi, uint32_t& lo) {
+  __half2 h;
+  uint32_t rest;
+  uint16_t lc;
+  hi = split2(a, b, h, rest);
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(lc) : "r"(rest));
   lo = lc;
+}
+
+// Four weights: hi = e4m3(p), lo = e5m2(p - hi). An e5m2 code is the upper byte of
+// a float16, so lo is rounded by adding to the lower byte: 0x80, to nearest, from
+// 2^-6 on; `dither` (the key's 8 bits, in both halves) below, where over its 256
+// values the two terms add up to the float16 weight on average. A weight of 0
+// stays 0. (A NaN's hi is NaN whatever becomes of lo.)
+__device__ __forceinline__ void weight_terms(const float* p, uint32_t dither, uint32_t& hi, uint32_t& lo) {
+  uint32_t hc[2], rest[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    __half2 h;
+    hc[k] = split2(p[2 * k], p[2 * k + 1], h, rest[k]);
+    const uint32_t small = __hlt2_mask(h, __float2half2_rn(0x1p-6f));
+    rest[k] += (dither & small) | (0x00800080u & ~small);
+  }
+  hi = __byte_perm(hc[0], hc[1], 0x5410);
+  lo = __byte_perm(rest[0], rest[1], 0x7531);
+}
+
+// 8 bits of a key's index, in both halves: the dither of its weights. Every
+// value alike often in any 16 tiles, also among every 2nd, 3rd, ... key.
+__device__ __forceinline__ uint32_t key_dither(uint32_t key) {
+  uint32_t u = key * 0x9E3779B1u;  // 2^32 / golden ratio
+  u ^= u >> 16;
+  return (u * 0x9E3779B1u >> 24) * 0x00010001u;
 }
 
 // The larger magnitudes of two bf16 pairs, as bit patterns (a NaN counts as above infinity).
@@ -602,7 +637,7 @@ __global__ void __launch_bounds__(Cfg<NR>::kThreads, 1)
               uint32_t h[4], l[4];
 #pragma unroll
               for (int k = 0; k < 4; ++k)
-                split2<false>(__uint_as_float(q4[k] << 16) * f, __uint_as_float(q4[k] & 0xFFFF0000u) * f, h[k], l[k]);
+                query_terms(__uint_as_float(q4[k] << 16) * f, __uint_as_float(q4[k] & 0xFFFF0000u) * f, h[k], l[k]);
               q0[t] = make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
               q1[t] = make_uint2(l[0] | l[1] << 16, l[2] | l[3] << 16);
             }
@@ -751,21 +786,10 @@ __global__ void __launch_bounds__(Cfg<NR>::kThreads, 1)
 #pragma unroll
           for (int r = 0; r < RW; ++r) e[r] = fast_exp2(e[r]);
         };
-        // the two terms of p = e
-        auto terms_of = [&](int r) {  // rows r, r + 1
-          uint32_t h2, l2;
-          split2<true>(e[r], e[r + 1], h2, l2);
-          if ((r & 2) == 0) {
-            hi[r / 4] = h2;
-            lo[r / 4] = l2;
-          } else {
-            hi[r / 4] |= h2 << 16;
-            lo[r / 4] |= l2 << 16;
-          }
-        };
-        auto terms = [&] {
+        auto terms = [&] {  // of p = e
+          const uint32_t dither = key_dither(uint32_t(t_end) - kKvTile + x);
 #pragma unroll
-          for (int r = 0; r < RW; r += 2) terms_of(r);
+          for (int r = 0; r < RW; r += 4) weight_terms(e + r, dither, hi[r / 4], lo[r / 4]);
         };
         // Rows whose reference moves (bits; the same in every thread of the
         // group). A later tile's weights are formed from the references as they
