@@ -17,10 +17,14 @@
 //   O^T[ch][row]  += C^T[ch][key] . P^T[key][row]   A = the tile (MN-major), B = P
 //
 // kind::f8f6f4 multiplies 8-bit floats, so the bf16 queries and the softmax
-// weights enter as two terms each. A query row is scaled to amax = 448 and
-// split into hi = e4m3(x) and lo = e4m3(x - hi) (within 2^-8 of x, or 2^-19 of
-// the row's amax): two rows of the Q tile, their products added when S is
-// read. A weight p is split into hi = e4m3(p) and lo, the rest in e5m2: two
+// weights enter as two terms each. A query row is scaled by the power of two that
+// puts its largest value between 224 and 448 and split into hi = e4m3(x) and
+// lo = e4m3(x - hi), two rows of the Q tile, their products added when S is read.
+// bf16 has 8 bits and the terms 4 each, so a latent channel from 1/4 on is exact,
+// a smaller one within 2^-10; s0 goes into the row's logit scale, and the rotary
+// channels, which take s1 / s0, are within 2^-8 of themselves. (Scaled to
+// 448 by s0 448 / amax, no power of two, all were within 2^-8 only: logits of 6
+// nats off by 0.01.) A weight p is split into hi = e4m3(p) and lo, the rest in e5m2: two
 // products into one accumulator. From 2^-6 on that is within 2^-7.8 of p, 0.15%
 // rms, about bf16's own. Below 2^-6 hi is on a fixed step and lo alone has two
 // bits, so that many equal small weights, all off alike, would change their
@@ -534,7 +538,11 @@ __global__ void __launch_bounds__(Cfg<NR>::kThreads, 1)
     const int rg = grp * RW;       // the group's first row in the tile
     constexpr int kShare = 32 / RW;  // lanes that share a row after reduce_rows
     const float ds0 = p.descale[0], ds1 = p.descale[1];
-    const float qk_log2 = p.softmax_scale * kLog2e;
+    // Queries enter in units of one descale: the latent channels', unless it is 0
+    // or vanishes beside the other (their ratio stays finite then).
+    const float unit = ds0 != 0.f && fabsf(ds1) <= fabsf(ds0) * 0x1p64f ? ds0 : (ds1 != 0.f ? ds1 : 1.f);
+    const float rel0 = ds0 / unit, rel1 = ds1 / unit;
+    const float qk_log2 = p.softmax_scale * kLog2e * unit;
     const int rows_pad = p.n_row_tiles * NR;  // rows of a partial
     int g0 = 0;           // tiles of the rows before
     int xb = 0, xr = 0, xs = 0;  // bound, row and sum exchanges so far (the same in every thread of the group)
@@ -616,12 +624,14 @@ __global__ void __launch_bounds__(Cfg<NR>::kThreads, 1)
             else
               am_rope = max_abs_bf16x2(am_rope, m);
           }
-          float am = fmaxf(fmaxf(__uint_as_float(am_lat << 16), __uint_as_float(am_lat & 0xFFFF0000u)) * fabsf(ds0),
-                           fmaxf(__uint_as_float(am_rope << 16), __uint_as_float(am_rope & 0xFFFF0000u)) * fabsf(ds1));
+          float am = fmaxf(fmaxf(__uint_as_float(am_lat << 16), __uint_as_float(am_lat & 0xFFFF0000u)) * fabsf(rel0),
+                           fmaxf(__uint_as_float(am_rope << 16), __uint_as_float(am_rope & 0xFFFF0000u)) * fabsf(rel1));
 #pragma unroll
           for (int m = 1; m < kTpr; m <<= 1) am = fmaxf(am, __shfl_xor_sync(0xFFFFFFFFu, am, m));
           am = fmaxf(am, 1e-30f);
-          const float inv = 448.f / am;
+          // 2^(8 - k), 2^k the power below am 8/7: am goes to [224, 448]
+          const uint32_t k2 = __float_as_uint(am * (8.f / 7.f)) & 0x7F800000u;
+          const float up = __uint_as_float((262u << 23) - k2);
 #pragma unroll 1
           for (int c = part; c < kRow / 8; c += 3 * kTpr) {  // three chunks at a time
             uint2 q0[3], q1[3];
@@ -632,7 +642,7 @@ __global__ void __launch_bounds__(Cfg<NR>::kThreads, 1)
             }
 #pragma unroll
             for (int t = 0; t < 3; ++t) {
-              const float f = (c + t * kTpr < kLat / 8 ? ds0 : ds1) * inv;
+              const float f = (c + t * kTpr < kLat / 8 ? rel0 : rel1) * up;
               const uint32_t q4[4] = {q0[t].x, q0[t].y, q1[t].x, q1[t].y};
               uint32_t h[4], l[4];
 #pragma unroll
@@ -648,7 +658,8 @@ __global__ void __launch_bounds__(Cfg<NR>::kThreads, 1)
             }
           }
           if (part == 0) {
-            ctl.scale[rg + r] = am * (1.f / 448.f) * qk_log2;
+            // (NaN for a row with an infinity)
+            ctl.scale[rg + r] = __uint_as_float(k2 - (8u << 23)) * qk_log2 + (am - am);
             ctl.c8[rg + r] = 0.f;
             ctl.lim[rg + r] = !live ? -1 : (p.causal ? wn.L - p.q_len + tq : INT_MAX);
           }

@@ -1,10 +1,12 @@
 """The latent attention's two 8-bit terms where they could go wrong: many equal
-small weights below a few large ones in one piece.
-tests/test_latent_arithmetic.py has the terms' own properties."""
+small weights below a few large ones in one piece, and queries whose logits are
+large. tests/test_latent_arithmetic.py has the terms' own properties."""
 
 import numpy as np
 import pytest
 import torch
+
+from oracle import rope as OR
 
 pytestmark = pytest.mark.gpu
 
@@ -87,3 +89,45 @@ def test_many_equal_keys_far_below_a_few(values, n, sms, high, h):
         err = (out - want[None]).abs()
         assert bool((err <= tol[None]).all()), (gap, float(err.max()) / vmax, float(tol.max()) / vmax)
         assert float((got_lse - lse).abs().max()) <= 1e-3, gap
+
+
+@pytest.mark.parametrize("h", [7, 32, 64])
+@pytest.mark.parametrize("descale", [(4 / 448, 5 / 448), (-4 / 448, 5 / 448), (0.75 / 448, 5 / 448)])
+def test_large_logits_of_exact_queries(h, descale):
+    """Queries without a rotary part: bf16 has 8 bits, the two terms 4 each, so
+    the logits (6 nats rms) are as exact as their sums: 18 products of a row, each
+    rounded to 2^-22 of the terms' sum of sizes, some 20 times the logit's rms:
+    18 * 2^-22 * 120 = 5e-4 nats; the LSE as much, and its own 2^-18. Values of a
+    thousandth of the row's largest are exact too."""
+    n = 700
+    rng = np.random.default_rng(h)
+    codes = torch.from_numpy(rng.standard_normal((n, 576)) * 112).clamp(-448, 448).float().to(torch.float8_e4m3fn)
+    f = codes.double().numpy()
+    rows = np.concatenate([f[:, :512] * np.float32(descale[0]), f[:, 512:] * np.float32(descale[1])], axis=1)
+    x = rng.standard_normal((1, h, 576)) * 2.0 ** rng.uniform(-8, 0, (1, h, 576))
+    x[:, :, 512:] = 0
+    q = torch.from_numpy(x).to(torch.bfloat16)
+    t = q[0].double().numpy() @ rows.T
+    scale = float(np.float32(6 / t.std()))
+    want, lse = OR.latent_attention(q.double().numpy(), rows, scale, n, True)
+    out, got = attend(codes.view(torch.uint8).cuda(), q.cuda(), torch.tensor(descale, dtype=torch.float32).cuda(), scale, 1)
+    assert np.abs(got.numpy() - lse[0]).max() <= 1e-3
+    # weights within 2^-7.8 (0.0016 rms), few of them large; bf16
+    assert np.linalg.norm(out.numpy() - want[0]) <= 0.0045 * np.linalg.norm(want[0])
+
+
+@pytest.mark.parametrize("descale", [(0.0, 5 / 448), (4 / 448, 0.0), (0.0, 0.0), (2.0 ** -90, 1.0), (1.0, 2.0 ** -90)])
+def test_descales_of_zero_and_far_apart(descale):
+    n, h = 300, 16
+    rng = np.random.default_rng(8)
+    codes = torch.from_numpy(rng.standard_normal((n, 576)) * 112).clamp(-448, 448).float().to(torch.float8_e4m3fn)
+    f = codes.double().numpy()
+    rows = np.concatenate([f[:, :512] * np.float32(descale[0]), f[:, 512:] * np.float32(descale[1])], axis=1)
+    q = torch.from_numpy(rng.standard_normal((1, h, 576))).to(torch.bfloat16)
+    spread = (q[0].double().numpy() @ rows.T).std()
+    scale = float(np.float32(1 / spread)) if spread else 1.0
+    want, lse = OR.latent_attention(q.double().numpy(), rows, scale, n, True)
+    out, got = attend(codes.view(torch.uint8).cuda(), q.cuda(), torch.tensor(descale, dtype=torch.float32).cuda(), scale, 1)
+    # a logit (1 nat rms) off by 2^-8 of a query value at most, 0.0013 rms: 5 sigma
+    assert np.abs(got.numpy() - lse[0]).max() <= 0.0065
+    assert np.linalg.norm(out.numpy() - want[0]) <= 0.0065 * np.linalg.norm(want[0])

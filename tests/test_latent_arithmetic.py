@@ -10,10 +10,14 @@ made of; tests/test_gpu_latent_far.py checks the kernel itself.
     index) says so. Over the dither's 256 values the two terms add up to the
     float16 weight exactly, so the errors of many equal weights cancel; one
     weight is within max(2^-12, where it holds no hi term its own 2^-2).
+* A query value q * 2^k, its row's largest put between 224 and 448, as two e4m3
+  terms is exact from 1/4 on (bf16 has 8 bits, the terms 4 each), else within
+  2^-10; a rotary value times the descales' ratio within max(2^-8, 2^-10).
 """
 
 import numpy as np
 import pytest
+import torch
 
 from oracle import formats as F
 
@@ -102,3 +106,22 @@ def test_many_equal_weights_far_below_one(gap, n, base):
     exact = (p[:, None].astype(np.float64) * v).sum(0) / p.sum(dtype=np.float64)
     got = (weight(p, dither(np.arange(n)))[:, None] * v).sum(0) / p.sum(dtype=np.float64)
     assert np.abs(got - exact).max() <= 1.5e-3 * np.abs(v).max()
+
+
+def test_query_terms_are_exact_for_bf16():
+    rng = np.random.default_rng(1)
+    q = torch.from_numpy((rng.standard_normal(200000) * 2.0 ** rng.uniform(-14, 0, 200000)).astype(np.float32))
+    q = q.to(torch.bfloat16).double().numpy()
+    for top in (1.0, 1.74, 1.75, 1.7578125, 1.9921875, 3e5, 7e-12):
+        x = np.append(q / np.abs(q).max(), 0) * top
+        x = torch.from_numpy(x).to(torch.bfloat16).double().numpy()
+        am = np.float32(np.abs(x).max())
+        k = 8 - int(np.frexp(np.float32(am * np.float32(8 / 7)))[1] - 1)
+        y = x * 2.0 ** k
+        assert 223.9 <= np.abs(y).max() <= 448
+        hi = e4(y)
+        err = np.abs(hi + e4(y - hi) - y)
+        assert np.all(err[np.abs(y) >= 0.25] == 0) and err.max() <= 2.0 ** -10
+        z = y * 0.8137  # a rotary value: times the descales' ratio
+        hi = e4(z)
+        assert np.all(np.abs(hi + e4(z - hi) - z) <= np.maximum(2.0 ** -8 * np.abs(z), 2.0 ** -10))
