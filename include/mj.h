@@ -540,7 +540,8 @@ MJ_API int mj_latent_write(const mj_latent_write_args* args, void* stream);
  * slots and max_num_seqs: copy it to the device with
  * mj_plan_upload(plan_host, NULL, plan_dev, NULL, words / 4, 0, stream).
  * Lengths are exact or an upper bound (margin: tokens added to each that is not
- * 0); the kernels mask by the lengths in device memory. */
+ * 0); the kernels mask by the lengths in device memory, and report one that
+ * reaches past the plan's tiles of its request (mj_latent_attention). */
 MJ_API int mj_latent_slots(int sm_count, int q_len, int h);
 MJ_API int mj_latent_plan_size(int slots, int max_num_seqs, size_t* words);
 MJ_API int mj_latent_plan(const int32_t* seq_lens_host, int num_seqs, int max_num_seqs, int slots, int q_len, int h,
@@ -572,7 +573,10 @@ MJ_API int mj_latent_workspace_size(int slots, int q_len, int h, size_t* bytes);
  * max|V| in the output at 131072 keys. Weights from 29 binades below on are 0.
  * A NaN code of a cached token reaches every row of its request, also one whose
  * causal limit hides it.
- * Status bits (workspace): as mj_workspace_status lists them.
+ * Status bits (workspace): as mj_workspace_status lists them; bit 4 also where a
+ * request's device length reaches past the tiles that the plan has of it (a plan
+ * of shorter lengths, or of none): the tokens past them are not attended to, and
+ * a request that the plan has as padding is not written.
  * Two calls that may run at once (other streams, two captured graphs) need a
  * workspace each. The first call of each row tile on a device raises a kernel's
  * shared-memory limit: make it before capturing.

@@ -3,7 +3,8 @@
 // the log2 domain, sum l, both scaled by 2^m):
 //   M = max_s m_s,  out = s0 sum_s 2^(m_s - M) O~_s / sum_s 2^(m_s - M) l_s.
 // A partial without a key has m = -inf and is selected off (its O~ and l may
-// never have been written).
+// never have been written). One lane a request compares its length with the
+// tiles that the plan covers, and reports tokens past them: no CTA read those.
 //
 // Bound by latency and L2: tens of megabytes of partials at most, just
 // written. Many tasks: a warp joins four rows of 128 channels, four 16-byte
@@ -64,6 +65,8 @@ __global__ void __launch_bounds__(G > 1 ? 32 * G : 32 * kWarps) latent_merge_ker
   const int2 sp = reinterpret_cast<const int2*>(p.splits)[b];
   const int len = p.seq_lens[b];
   const int row = tile * p.row_tile + 4 * quad;
+  if (j == 0 && quad == 0 && tile == 0 && x == 0 && (G == 1 || warp == 0) && int64_t(len) > int64_t(p.planned[b]) * kKvTile)
+    atomicOr(p.status, kStatusBadPlan);
   const int n = min(sp.y, 2 * p.slots - sp.x);
   // an unsplit request was written by the attention kernel; a padding request
   // is left alone; the rows past the last are not anyone's

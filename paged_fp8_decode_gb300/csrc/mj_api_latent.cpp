@@ -141,7 +141,7 @@ int mj_latent_slots(int sm_count, int q_len, int h) {
 int mj_latent_plan_size(int slots, int max_num_seqs, size_t* words) {
   if (!words || slots < 1 || max_num_seqs < 0) return MJ_ERR_INVALID_ARG;
   *words = size_t(mj::latent_plan_slot_words(slots) + mj::latent_plan_split_words(max_num_seqs) +
-                  4 * mj::latent_plan_max_work(slots, max_num_seqs));
+                  4 * mj::latent_plan_max_work(slots, max_num_seqs) + mj::latent_plan_tile_words(max_num_seqs));
   return MJ_OK;
 }
 
@@ -169,6 +169,8 @@ int mj_latent_plan(const int32_t* seq_lens_host, int num_seqs, int max_num_seqs,
   int32_t* table = plan_host;
   int32_t* splits = table + mj::latent_plan_slot_words(slots);
   int32_t* work = splits + mj::latent_plan_split_words(max_num_seqs);
+  int32_t* planned = work + 4 * mj::latent_plan_max_work(slots, max_num_seqs);
+  for (int b = 0; b < num_seqs; ++b) planned[b] = int32_t(tiles(b));
 
   // The requests' tiles in order, cut so that no slot's cost (its tiles, and
   // row_cost for each of its rows) exceeds `limit`; false when that takes more
@@ -302,6 +304,7 @@ int mj_latent_attention(const mj_latent_args* a, void* stream) {
   p.slot_table = a->plan;
   p.splits = p.slot_table + mj::latent_plan_slot_words(a->slots);
   p.work = p.splits + mj::latent_plan_split_words(a->max_num_seqs);
+  p.planned = p.work + 4 * max_work;
   p.out = static_cast<uint16_t*>(a->out);
   p.out_f16 = a->out_dtype == MJ_OUT_F16 ? 1 : 0;
   p.out_ts = a->out_tok_stride;

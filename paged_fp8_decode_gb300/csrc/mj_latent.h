@@ -27,6 +27,7 @@ struct LatentParams {
   const int32_t* slot_table;  // [slots][4]: first work row, end, that row's request and first tile
   const int32_t* splits;   // [max_num_seqs][2]: first partial, number of them (0: not split)
   const int32_t* work;     // [max_work][4]: request, first tile, end tile, partial (-1: none)
+  const int32_t* planned;  // [max_num_seqs]: tiles the plan covers
   uint16_t* out;
   int out_f16;
   int64_t out_ts, out_hs;
@@ -43,6 +44,7 @@ struct LatentParams {
 inline int64_t latent_plan_slot_words(int slots) { return 4 * int64_t(slots); }
 inline int64_t latent_plan_split_words(int max_num_seqs) { return (2 * int64_t(max_num_seqs) + 3) / 4 * 4; }
 inline int64_t latent_plan_max_work(int slots, int max_num_seqs) { return int64_t(slots) + max_num_seqs; }
+inline int64_t latent_plan_tile_words(int max_num_seqs) { return (int64_t(max_num_seqs) + 3) / 4 * 4; }
 
 cudaError_t launch_rope_write(const mj_rope_write_kv_args& a, cudaStream_t stream);
 cudaError_t launch_latent_write(const mj_latent_write_args& a, cudaStream_t stream);

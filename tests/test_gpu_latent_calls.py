@@ -1,0 +1,57 @@
+"""The latent attention's calls as programs make them: plans that no longer hold
+the lengths."""
+
+import numpy as np
+import pytest
+import torch
+
+from tests.test_gpu_latent import SENTINEL, Case
+
+pytestmark = pytest.mark.gpu
+
+BAD_PLAN = 4
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from paged_fp8_decode_gb300.build import build
+
+    build()
+
+
+def attend(c, plan_lens, planned_seqs=None, **kw):
+    import paged_fp8_decode_gb300 as mj
+
+    step = c.step(**kw)
+    step.lse.fill_(SENTINEL)
+    step.plan(plan_lens, len(plan_lens) if planned_seqs is None else planned_seqs)
+    out = c.outputs()
+    step.run(c.q.cuda(), out, c.device(), c.B, c.scale)
+    torch.cuda.synchronize()
+    return out, step.lse[:c.B], mj.mj_workspace_status(step.workspace)
+
+
+@pytest.mark.parametrize("h", [16, 128])
+@pytest.mark.parametrize("sms", [1, 40, None])
+def test_length_past_the_plan_is_reported(h, sms):
+    c = Case([300, 1281, 0, 5], 1, h, 64, seed=1)
+    # 1281 tokens reach into an eleventh tile: a plan for ten drops the newest one
+    assert attend(c, np.array([300, 1280, 0, 5], np.int32), sm_count=sms)[2] == BAD_PLAN
+    # growth inside the last planned tile is served
+    out, lse, status = attend(c, np.array([257, 1281, 0, 1], np.int32), sm_count=sms)
+    assert status == 0
+    c.check(out, lse)
+    # a margin that covers it
+    out, lse, status = attend(c, np.array([300, 1280, 0, 5], np.int32), sm_count=sms, margin=1)
+    assert status == 0
+    c.check(out, lse)
+
+
+@pytest.mark.parametrize("planned", [[300, 700, 0], [300, 700]])
+def test_live_request_without_a_plan_is_reported(planned):
+    c = Case([300, 700, 90], 1, 16, 64, seed=2)
+    out, _, status = attend(c, np.array(planned, np.int32))
+    assert status == BAD_PLAN
+    assert bool((out[2] == SENTINEL).all())
