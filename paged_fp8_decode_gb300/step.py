@@ -356,6 +356,8 @@ class LatentStep:
             mj_workspace_init(self.workspace)
         self.lse = (torch.empty(max(1, max_num_seqs), q_len * h, dtype=torch.float32, device=self.device)
                     if with_lse else None)
+        # the buffers may be used on any stream from here on: their clearing is done
+        torch.cuda.current_stream(self.device).synchronize()
 
     def plan(self, seq_lens_host, num_seqs: int, stream=None):
         """Host plan into the pinned staging buffer, then an asynchronous copy

@@ -1,5 +1,5 @@
 """The latent attention's calls as programs make them: plans that no longer hold
-the lengths."""
+the lengths, a step made on a busy stream."""
 
 import numpy as np
 import pytest
@@ -55,3 +55,20 @@ def test_live_request_without_a_plan_is_reported(planned):
     out, _, status = attend(c, np.array(planned, np.int32))
     assert status == BAD_PLAN
     assert bool((out[2] == SENTINEL).all())
+
+
+def test_step_made_on_a_busy_stream_and_used_on_another():
+    """The buffers of a new step are ready when it is: work that is still queued
+    on the stream where it was made does not clear its plan later."""
+    c = Case([700, 2000], 1, 16, 64, seed=3)
+    kv, q, out, s = c.device(), c.q.cuda(), c.outputs(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(200_000_000)  # a tenth of a second
+    step = c.step()
+    step.plan(c.lens, c.B, stream=s)
+    torch.cuda.synchronize()
+    step.lse.fill_(SENTINEL)
+    torch.cuda.synchronize()
+    step.run(q, out, kv, c.B, c.scale, stream=s)
+    torch.cuda.synchronize()
+    c.check(out, step.lse)
