@@ -418,15 +418,17 @@ def mj_rope_turns(inv_freq):
     return torch.from_numpy(turns.view(np.int64))
 
 
-def _on_device(args):
-    """Refuse a launch on another device than the one the tensors of ``args``
-    live on (the library launches on the current device)."""
+def _same_device(what: str, dev: int | None):
+    """Refuse a call on another device than the one (``dev``) its tensors live
+    on (the library launches on the current device)."""
     import torch
 
-    dev = getattr(args, "device_index", None)
     if dev is not None and dev != torch.cuda.current_device():
-        raise ValueError(f"the arguments' tensors are on cuda:{dev}, the current device is "
-                         f"cuda:{torch.cuda.current_device()}")
+        raise ValueError(f"{what} are on cuda:{dev}, the current device is cuda:{torch.cuda.current_device()}")
+
+
+def _on_device(args):
+    _same_device("the arguments' tensors", getattr(args, "device_index", None))
 
 
 def mj_rope_write_kv(args: mj_rope_write_kv_args, stream=None):

@@ -17,7 +17,7 @@ import numpy as np
 import torch
 
 from . import (KV_FORMATS, LATENT_DIM, LATENT_ROPE_DIM, LATENT_ROW, MJ_IMPL_AUTO, MJ_KV_E4M3, MJ_OUT_BF16, MJ_OUT_F16,
-               _check, _ptr, _stream, load_library, mj_decode_args, mj_decode_attention, mj_latent_args,
+               _check, _ptr, _same_device, _stream, load_library, mj_decode_args, mj_decode_attention, mj_latent_args,
                mj_latent_attention, mj_latent_plan, mj_latent_plan_size, mj_latent_slots, mj_latent_workspace_size,
                mj_latent_write_args, mj_merge_lse, mj_plan_split_kv, mj_plan_upload, mj_quantize_q,
                mj_rope_write_kv_args, mj_slots, mj_workspace_init, mj_workspace_size)
@@ -361,7 +361,9 @@ class LatentStep:
 
     def plan(self, seq_lens_host, num_seqs: int, stream=None):
         """Host plan into the pinned staging buffer, then an asynchronous copy
-        into the fixed device buffer on ``stream``."""
+        into the fixed device buffer on ``stream``. The step's device must be the
+        current one (a default stream is the current device's)."""
+        _same_device("the step's buffers", self.plan_dev.device.index)
         if self._staged is not None:
             self._staged.synchronize()  # the previous copy has read the staging buffer
         mj_latent_plan(seq_lens_host, num_seqs, self.max_num_seqs, self.slots, self.q_len, self.h, self.margin,
