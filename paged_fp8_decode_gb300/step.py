@@ -16,8 +16,8 @@ from dataclasses import dataclass
 import numpy as np
 import torch
 
-from . import (KV_FORMATS, LATENT_DIM, LATENT_ROPE_DIM, LATENT_ROW, MJ_IMPL_AUTO, MJ_KV_E4M3, MJ_OUT_BF16, MJ_OUT_F16,
-               _check, _ptr, _same_device, _stream, load_library, mj_decode_args, mj_decode_attention, mj_latent_args,
+from . import (KV_FORMATS, LATENT_DIM, LATENT_ROPE_DIM, LATENT_ROW, MJ_IMPL_AUTO, MJ_KV_E2M1, MJ_KV_E4M3, MJ_OUT_BF16,
+               MJ_OUT_F16, _check, _ptr, _same_device, _stream, load_library, mj_decode_args, mj_decode_attention, mj_latent_args,
                mj_latent_attention, mj_latent_plan, mj_latent_plan_size, mj_latent_slots, mj_latent_workspace_size,
                mj_latent_write_args, mj_merge_lse, mj_plan_split_kv, mj_plan_upload, mj_quantize_q,
                mj_rope_write_kv_args, mj_slots, mj_workspace_init, mj_workspace_size)
@@ -205,6 +205,18 @@ def _flat(name: str, t: torch.Tensor, dtype, *shape) -> torch.Tensor:
     return t
 
 
+def _pool(name: str, t: torch.Tensor, strides, page_size: int, num_pages: int, heads: int, row_bytes: int):
+    """Check a cache that the library writes through a pointer and strides: on a
+    GPU, uint8, and its last row ends inside the tensor."""
+    if not t.is_cuda or t.dtype != torch.uint8:
+        raise ValueError(f"{name} must be a uint8 CUDA tensor")
+    page, token, head = strides
+    need = (num_pages - 1) * page + (page_size - 1) * token + (heads - 1) * head + row_bytes if num_pages > 0 else 0
+    have = 1 + sum((n - 1) * s for n, s in zip(t.shape, t.stride())) if t.numel() else 0
+    if need > have:
+        raise ValueError(f"{name}: {num_pages} pages of {page_size} tokens end at byte {need}, the tensor at {have}")
+
+
 def _hold(a, *tensors):
     """``a`` keeps the tensors whose addresses it holds, and their one device."""
     held = [t for t in tensors if t is not None]
@@ -241,14 +253,15 @@ def rope_write_args(q, key, value, positions, turns, slot_mapping, k_cache, v_ca
     (None: in place); ``positions`` int64 ``[T]`` or ``[axes, T]``; ``turns``
     :func:`mj_rope_turns` of ``rot_dim / 2`` frequencies, on the device;
     ``freq_axis`` uint8, the axis of each frequency. The rest as for
-    :func:`mj_write_kv`."""
+    :func:`mj_write_kv`; the pages and strides must lie inside the caches."""
     T, h_k, d = (int(n) for n in key.shape)
     _rows("key", key, torch.bfloat16, T, h_k, d)
     _rows("value", value, torch.bfloat16, T, h_k, d)
     _flat("slot_mapping", slot_mapping, torch.int64, T)
+    strides = tuple(int(x) for x in kv_strides)
+    bits = {MJ_KV_E4M3: 8, MJ_KV_E2M1: 4}.get(int(kv_format), 6)
     for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        if not t.is_cuda or t.dtype != torch.uint8:
-            raise ValueError(f"{name} must be a uint8 CUDA tensor")
+        _pool(name, t, strides, int(page_size), int(num_pages), h_k, d * bits // 8)
     n_scale = h_k * d if kv_format != MJ_KV_E4M3 else (h_k if scale_per_head else 1)
     for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
         if not t.is_cuda or t.dtype != torch.float32 or not t.is_contiguous() or t.numel() != n_scale:
@@ -269,8 +282,8 @@ def rope_write_args(q, key, value, positions, turns, slot_mapping, k_cache, v_ca
     w.slot_mapping = slot_mapping.data_ptr()
     w.kv_format, w.page_size, w.num_pages = int(kv_format), int(page_size), int(num_pages)
     w.k_cache, w.v_cache = k_cache.data_ptr(), v_cache.data_ptr()
-    w.k_stride_page, w.k_stride_token, w.k_stride_head = (int(x) for x in kv_strides)
-    w.v_stride_page, w.v_stride_token, w.v_stride_head = (int(x) for x in kv_strides)
+    w.k_stride_page, w.k_stride_token, w.k_stride_head = strides
+    w.v_stride_page, w.v_stride_token, w.v_stride_head = strides
     w.k_scale, w.v_scale = k_scale.data_ptr(), v_scale.data_ptr()
     w.scale_per_head = 1 if scale_per_head else 0
     w.status = _ptr(status)

@@ -34,3 +34,48 @@ def test_a_plan_on_another_device_is_refused(monkeypatch):
     step.plan_dev = types.SimpleNamespace(device=torch.device("cuda", 1))
     with pytest.raises(ValueError, match="cuda:1"):
         step.plan(np.array([5], np.int32), 1)
+
+
+class OnGpu(torch.Tensor):
+    """A host tensor that says it is on a GPU: what the argument builders look at, without one."""
+
+    is_cuda = True
+
+
+def on_gpu(*shape, dtype=torch.bfloat16):
+    return torch.zeros(*shape, dtype=dtype).as_subclass(OnGpu)
+
+
+def rope_args(fmt=0, T=3, h_k=2, d=128, k_bytes=None, v_bytes=None, page=16, pages=4, strides=None, pools=None):
+    row = d * {0: 8, 1: 6, 2: 6, 3: 4}[fmt] // 8
+    strides = strides or (h_k * page * row, row, page * row)
+    full = pages * page * h_k * row
+    k, v = pools or (on_gpu(k_bytes or full, dtype=torch.uint8), on_gpu(v_bytes or full, dtype=torch.uint8))
+    n = 1 if fmt == 0 else h_k * d
+    scale = on_gpu(n, dtype=torch.float32)
+    x = on_gpu(T, h_k, d)
+    return mj.rope_write_args(x, x.clone(), x.clone(), on_gpu(T, dtype=torch.int64), mj.mj_rope_turns([1.0] * 64).as_subclass(OnGpu),
+                              on_gpu(T, dtype=torch.int64), k, v, strides, page, pages, fmt, scale, scale)
+
+
+@pytest.mark.parametrize("fmt", [0, 1, 2, 3])
+def test_caches_that_end_before_their_pages_are_refused(fmt):
+    row = 128 * {0: 8, 1: 6, 2: 6, 3: 4}[fmt] // 8
+    full = 4 * 16 * 2 * row
+    a = rope_args(fmt)
+    assert (a.kv.k_stride_page, a.kv.k_stride_token, a.kv.k_stride_head) == (32 * row, row, 16 * row)
+    for bad in (dict(k_bytes=full - 1), dict(v_bytes=full - 1), dict(k_bytes=full, v_bytes=full, pages=5),
+                dict(k_bytes=full, v_bytes=full, page=32), dict(strides=(32 * row, row, 64 * row)),
+                dict(strides=(64 * row, row, 16 * row))):
+        with pytest.raises(ValueError, match="_cache"):
+            rope_args(fmt, **bad)
+
+
+def test_caches_may_be_views_of_one_pool():
+    # keys and values side by side in each page: a view's extent ends with its own last row
+    pool = on_gpu(4, 2, 2, 16, 128, dtype=torch.uint8)
+    k, v = pool[:, 0], pool[:, 1]
+    rope_args(pools=(k, v), strides=(8192, 128, 2048))
+    with pytest.raises(ValueError, match="v_cache"):
+        rope_args(pools=(k, v[:3]), strides=(8192, 128, 2048))
+    rope_args(pools=(on_gpu(0, dtype=torch.uint8), on_gpu(0, dtype=torch.uint8)), pages=0)
