@@ -471,8 +471,10 @@ MJ_API int mj_rope_turns(const double* inv_freq, int n, uint64_t* turns);
  * kv: as for mj_write_kv (every cache format, head size 128 or 256), except
  * that key is rotated in float32 before its one rounding, to the cache format.
  * q may be q_out (rotated in place, with the same strides); they must not
- * overlap otherwise. The slots of live tokens are distinct: of two tokens with
- * one slot, the row holds parts of both. h_q = 0: no queries. A padding token
+ * overlap otherwise. The caches' rows lie apart: of the page, token and head
+ * strides each holds all steps of the next smaller, the smallest a row. The slots
+ * of live tokens are distinct: of two tokens with one slot, the row holds parts of
+ * both. h_q = 0: no queries. A padding token
  * (negative slot) has its queries rotated too. At most 2^30 tokens.
  * Alignment: q and q_out 16 bytes, their strides multiples of 8 elements.
  * The launch may begin before the preceding kernel on `stream` has finished
@@ -502,7 +504,7 @@ MJ_API int mj_rope_write_kv(const mj_rope_write_kv_args* args, void* stream);
 
 /* mj_latent_write — append: rotate the queries' 64-channel parts (to bf16) and
  * the keys', quantize latent and key part (x / scale, IEEE float32, to nearest
- * even, saturating at 448) and write one row a token at slot_mapping. Slots,
+ * even, saturating at 448) and write one row a token at slot_mapping. Rows, slots,
  * padding tokens, status, in-place queries, token limit and the launch as for
  * mj_rope_write_kv. q_out is usually the last 64 channels of the absorbed
  * query that mj_latent_attention reads.

@@ -34,6 +34,23 @@ constexpr int64_t kMaxRows = 1 << 20;
 
 int latent_row_tile(int64_t n_q) { return n_q <= 16 ? 16 : (n_q <= 32 ? 32 : 64); }
 
+// Rows of `row` units at two or three strides, as many of each as its count:
+// whether they lie apart, the steps of each stride inside one of the next larger.
+struct Dim {
+  int64_t stride, count;
+};
+template <int N>
+bool rows_apart(int64_t row, Dim (&&d)[N]) {
+  std::sort(d, d + N, [](const Dim& a, const Dim& b) { return a.stride < b.stride; });
+  __int128 extent = row;
+  for (const Dim& k : d) {
+    if (k.count <= 1) continue;
+    if (k.stride < extent) return false;
+    extent += static_cast<__int128>(k.stride) * (k.count - 1);
+  }
+  return true;
+}
+
 int check_rope(const mj_rope& r, int d) {
   if (r.num_axes < 1 || r.num_axes > 4 || r.axis_stride < 0) return MJ_ERR_INVALID_ARG;
   if (r.rot_dim < 16 || r.rot_dim > d || r.rot_dim % 16) return MJ_ERR_UNSUPPORTED;
@@ -103,7 +120,12 @@ int mj_rope_write_kv(const mj_rope_write_kv_args* a, void* stream) {
   if (st != MJ_OK) return st;
   st = check_query(a->h_q, a->q, a->q_out, a->q_tok_stride, a->q_head_stride, a->q_out_tok_stride, a->q_out_head_stride);
   if (st != MJ_OK) return st;
-  if ((int64_t(a->h_q) + 2 * int64_t(a->kv.h_k)) * a->kv.d > (int64_t(1) << 24)) return MJ_ERR_INVALID_ARG;
+  const mj_write_kv_args& w = a->kv;
+  if ((int64_t(a->h_q) + 2 * int64_t(w.h_k)) * w.d > (int64_t(1) << 24)) return MJ_ERR_INVALID_ARG;
+  const int64_t row = int64_t(w.d) * (w.kv_format == MJ_KV_E4M3 ? 8 : (w.kv_format == MJ_KV_E2M1 ? 4 : 6)) / 8;
+  if (!rows_apart(row, {{w.k_stride_page, w.num_pages}, {w.k_stride_token, w.page_size}, {w.k_stride_head, w.h_k}}) ||
+      !rows_apart(row, {{w.v_stride_page, w.num_pages}, {w.v_stride_token, w.page_size}, {w.v_stride_head, w.h_k}}))
+    return MJ_ERR_INVALID_ARG;
   return status_of(mj::launch_rope_write(*a, static_cast<cudaStream_t>(stream)));
 }
 
@@ -128,6 +150,8 @@ int mj_latent_write(const mj_latent_write_args* a, void* stream) {
     return MJ_ERR_ALIGNMENT;
   if (a->latent_tok_stride % 8 || a->k_pe_tok_stride % 8 || a->stride_page % 16 || a->stride_token % 16)
     return MJ_ERR_ALIGNMENT;
+  if (!rows_apart(MJ_LATENT_ROW_BYTES, {{a->stride_page, a->num_pages}, {a->stride_token, a->page_size}}))
+    return MJ_ERR_INVALID_ARG;
   return status_of(mj::launch_latent_write(*a, static_cast<cudaStream_t>(stream)));
 }
 

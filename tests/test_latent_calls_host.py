@@ -1,6 +1,7 @@
 """The rotated writes and the latent attention on the host, beside
 test_rope_latent_host.py: what the plan says of its lengths, refusals."""
 
+import ctypes
 import types
 
 import numpy as np
@@ -8,6 +9,7 @@ import pytest
 import torch
 
 import paged_fp8_decode_gb300 as mj
+from tests import test_rope_latent_host as H
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -79,3 +81,45 @@ def test_caches_may_be_views_of_one_pool():
     with pytest.raises(ValueError, match="v_cache"):
         rope_args(pools=(k, v[:3]), strides=(8192, 128, 2048))
     rope_args(pools=(on_gpu(0, dtype=torch.uint8), on_gpu(0, dtype=torch.uint8)), pages=0)
+
+
+def set_all(a, **fields):
+    for path, value in fields.items():
+        H.set_path(a, path.replace("__", "."), value)
+    return a
+
+
+# (a call that passed the check would stop at the launch, which needs a GPU; on one it must not get there)
+no_gpu = pytest.mark.skipif(torch.cuda.is_available(), reason="the pointers are not real")
+
+
+@no_gpu
+@pytest.mark.parametrize("which", ["k", "v"])
+@pytest.mark.parametrize("page,token,head", [(4096, 112, 2048), (4096, 128, 112), (4096, 128, 128), (4096, 128, 1024),
+                                             (2048, 128, 4096), (0, 128, 2048), (4096, 0, 2048), (4096, 128, 0)])
+def test_rope_write_refuses_cache_rows_that_overlap(which, page, token, head):
+    a = H.rope_write()  # 4 pages of 16 tokens, 2 heads of 128 bytes
+    set_all(a, **{f"kv__{which}_stride_page": page, f"kv__{which}_stride_token": token, f"kv__{which}_stride_head": head})
+    assert mj.load_library().mj_rope_write_kv(ctypes.byref(a), None) == mj.MJ_ERR_INVALID_ARG
+
+
+@no_gpu
+def test_cache_rows_in_any_order_of_strides_are_taken():
+    # past every check, the call fails at the launch: there is no GPU
+    for page, token, head in ((4096, 128, 2048), (4096, 256, 128), (2048, 128, 8192), (256, 1024, 128), (8192, 144, 2560)):
+        a = set_all(H.rope_write(), **{f"kv__{w}_stride_{n}": x for w in "kv" for n, x in
+                                       (("page", page), ("token", token), ("head", head))})
+        assert mj.load_library().mj_rope_write_kv(ctypes.byref(a), None) == mj.MJ_ERR_CUDA
+    one = set_all(H.rope_write(), kv__h_k=1, kv__num_pages=1, kv__k_stride_head=0, kv__v_stride_head=0, kv__k_stride_page=0)
+    assert mj.load_library().mj_rope_write_kv(ctypes.byref(one), None) == mj.MJ_ERR_CUDA
+    six = set_all(H.rope_write(), kv__kv_format=1, **{f"kv__{w}_stride_{n}": x for w in "kv" for n, x in
+                                                      (("page", 4096), ("token", 96), ("head", 2048))})
+    assert mj.load_library().mj_rope_write_kv(ctypes.byref(six), None) == mj.MJ_ERR_CUDA
+
+
+@no_gpu
+@pytest.mark.parametrize("page,token,ok", [(9216, 576, True), (576, 2304, True), (9200, 576, False), (576, 576, False),
+                                           (1152, 2304, False)])
+def test_latent_write_refuses_pages_that_overlap(page, token, ok):
+    a = set_all(H.latent_write(), stride_page=page, stride_token=token)  # 4 pages of 16 tokens
+    assert mj.load_library().mj_latent_write(ctypes.byref(a), None) == (mj.MJ_ERR_CUDA if ok else mj.MJ_ERR_INVALID_ARG)
