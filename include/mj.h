@@ -471,11 +471,12 @@ MJ_API int mj_rope_turns(const double* inv_freq, int n, uint64_t* turns);
  * kv: as for mj_write_kv (every cache format, head size 128 or 256), except
  * that key is rotated in float32 before its one rounding, to the cache format.
  * q may be q_out (rotated in place, with the same strides); they must not
- * overlap otherwise. The caches' rows lie apart: of the page, token and head
- * strides each holds all steps of the next smaller, the smallest a row. The slots
- * of live tokens are distinct: of two tokens with one slot, the row holds parts of
- * both. h_q = 0: no queries. A padding token
- * (negative slot) has its queries rotated too. At most 2^30 tokens.
+ * overlap otherwise. What is written lies apart: of the page, token and head
+ * strides of a cache, and the token and head strides of q_out, each holds all
+ * steps of the next smaller, the smallest a row. The slots of live tokens are
+ * distinct: of two tokens with one slot, the row holds parts of both. h_q = 0: no
+ * queries. A padding token (negative slot) has its queries rotated too. At most
+ * 2^30 tokens.
  * Alignment: q and q_out 16 bytes, their strides multiples of 8 elements.
  * The launch may begin before the preceding kernel on `stream` has finished
  * and waits for it before it reads.

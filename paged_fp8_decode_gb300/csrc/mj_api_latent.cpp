@@ -60,12 +60,14 @@ int check_rope(const mj_rope& r, int d) {
   return MJ_OK;
 }
 
-// The query part of a write: h heads in, h heads out.
-int check_query(int h, const void* q, const void* q_out, int64_t ts, int64_t hs, int64_t ots, int64_t ohs) {
+// The query part of a write: h heads of d channels in, h heads out.
+int check_query(int T, int h, int d, const void* q, const void* q_out, int64_t ts, int64_t hs, int64_t ots, int64_t ohs) {
   if (h < 0) return MJ_ERR_INVALID_ARG;
   if (h == 0) return MJ_OK;
   if (!q || !q_out || ts < 0 || hs < 0 || ots < 0 || ohs < 0) return MJ_ERR_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(q_out, 16) || ts % 8 || hs % 8 || ots % 8 || ohs % 8) return MJ_ERR_ALIGNMENT;
+  if (!rows_apart(d, {{ots, T}, {ohs, h}})) return MJ_ERR_INVALID_ARG;
+  if (q == q_out && ((T > 1 && ts != ots) || (h > 1 && hs != ohs))) return MJ_ERR_INVALID_ARG;
   return MJ_OK;
 }
 
@@ -118,7 +120,8 @@ int mj_rope_write_kv(const mj_rope_write_kv_args* a, void* stream) {
   if (st != MJ_OK || a->kv.num_tokens == 0) return st;
   st = check_rope(a->rope, a->kv.d);
   if (st != MJ_OK) return st;
-  st = check_query(a->h_q, a->q, a->q_out, a->q_tok_stride, a->q_head_stride, a->q_out_tok_stride, a->q_out_head_stride);
+  st = check_query(a->kv.num_tokens, a->h_q, a->kv.d, a->q, a->q_out, a->q_tok_stride, a->q_head_stride,
+                   a->q_out_tok_stride, a->q_out_head_stride);
   if (st != MJ_OK) return st;
   const mj_write_kv_args& w = a->kv;
   if ((int64_t(a->h_q) + 2 * int64_t(w.h_k)) * w.d > (int64_t(1) << 24)) return MJ_ERR_INVALID_ARG;
@@ -138,7 +141,8 @@ int mj_latent_write(const mj_latent_write_args* a, void* stream) {
   if (a->num_tokens == 0) return MJ_OK;
   int st = check_rope(a->rope, MJ_LATENT_ROPE_DIM);
   if (st != MJ_OK) return st;
-  st = check_query(a->h, a->q_pe, a->q_out, a->q_tok_stride, a->q_head_stride, a->q_out_tok_stride, a->q_out_head_stride);
+  st = check_query(a->num_tokens, a->h, MJ_LATENT_ROPE_DIM, a->q_pe, a->q_out, a->q_tok_stride, a->q_head_stride,
+                   a->q_out_tok_stride, a->q_out_head_stride);
   if (st != MJ_OK) return st;
   if (a->h > (1 << 16)) return MJ_ERR_INVALID_ARG;
   if (!a->latent || !a->k_pe || !a->slot_mapping || !a->cache || !a->scale) return MJ_ERR_INVALID_ARG;

@@ -123,3 +123,33 @@ def test_cache_rows_in_any_order_of_strides_are_taken():
 def test_latent_write_refuses_pages_that_overlap(page, token, ok):
     a = set_all(H.latent_write(), stride_page=page, stride_token=token)  # 4 pages of 16 tokens
     assert mj.load_library().mj_latent_write(ctypes.byref(a), None) == (mj.MJ_ERR_CUDA if ok else mj.MJ_ERR_INVALID_ARG)
+
+
+@no_gpu
+@pytest.mark.parametrize("fn,make,d,q", [("mj_rope_write_kv", H.rope_write, 128, "q"), ("mj_latent_write", H.latent_write, 64, "q_pe")])
+def test_queries_written_over_each_other_are_refused(fn, make, d, q):
+    call = getattr(mj.load_library(), fn)
+    for tok, head in ((8 * d, 0), (0, d), (8 * d, d - 8), (8 * d - 8, d), (d, d), (d, 2 * d)):  # 3 tokens of 8 heads
+        a = set_all(make(), q_out_tok_stride=tok, q_out_head_stride=head)
+        assert call(ctypes.byref(a), None) == mj.MJ_ERR_INVALID_ARG
+        a = set_all(make(), q_out_tok_stride=tok, q_out_head_stride=head, q_tok_stride=tok, q_head_stride=head)
+        a.q_out = getattr(a, q)  # in place
+        assert call(ctypes.byref(a), None) == mj.MJ_ERR_INVALID_ARG
+    a = set_all(make(), q_out_tok_stride=16 * d)
+    a.q_out = getattr(a, q)  # in place, at other strides
+    assert call(ctypes.byref(a), None) == mj.MJ_ERR_INVALID_ARG
+    for tok, head in ((d, 3 * d), (9 * d + 8, d + 8)):
+        assert call(ctypes.byref(set_all(make(), q_out_tok_stride=tok, q_out_head_stride=head)), None) == mj.MJ_ERR_CUDA
+    # queries read twice are no fault
+    assert call(ctypes.byref(set_all(make(), q_tok_stride=0, q_head_stride=0)), None) == mj.MJ_ERR_CUDA
+
+
+@no_gpu
+def test_an_expanded_query_is_not_rotated_in_place():
+    x = on_gpu(1, 2, 128).expand(3, 2, 128)
+    pool = on_gpu(16384, dtype=torch.uint8)
+    i, one = on_gpu(3, dtype=torch.int64), on_gpu(1, dtype=torch.float32)
+    key = on_gpu(3, 2, 128)
+    a = mj.rope_write_args(x, key, key, i, mj.mj_rope_turns([1.0] * 8).as_subclass(OnGpu), i, pool, pool,
+                           (4096, 128, 2048), 16, 4, 0, one, one)
+    assert mj.load_library().mj_rope_write_kv(ctypes.byref(a), None) == mj.MJ_ERR_INVALID_ARG
