@@ -580,6 +580,8 @@ MJ_API int mj_latent_workspace_size(int slots, int q_len, int h, size_t* bytes);
  * request's device length reaches past the tiles that the plan has of it (a plan
  * of shorter lengths, or of none): the tokens past them are not attended to, and
  * a request that the plan has as padding is not written.
+ * out overlaps nothing that the call reads; its rows lie apart (of its strides the
+ * larger holds all steps of the smaller, the smaller a row).
  * Two calls that may run at once (other streams, two captured graphs) need a
  * workspace each. The first call of each row tile on a device raises a kernel's
  * shared-memory limit: make it before capturing.

@@ -293,6 +293,8 @@ int mj_latent_attention(const mj_latent_args* a, void* stream) {
   for (int k = 0; k < 4; ++k)
     if (strides[k] % 8) return MJ_ERR_ALIGNMENT;
   if (a->stride_page % 16 || a->stride_token % 16) return MJ_ERR_ALIGNMENT;
+  if (!rows_apart(MJ_LATENT_DIM, {{a->out_tok_stride, int64_t(a->num_seqs) * a->q_len}, {a->out_head_stride, a->h}}))
+    return MJ_ERR_INVALID_ARG;
   size_t bytes = 0;
   const int st = mj_latent_workspace_size(a->slots, a->q_len, a->h, &bytes);
   if (st != MJ_OK) return st;

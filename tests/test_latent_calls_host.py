@@ -153,3 +153,15 @@ def test_an_expanded_query_is_not_rotated_in_place():
     a = mj.rope_write_args(x, key, key, i, mj.mj_rope_turns([1.0] * 8).as_subclass(OnGpu), i, pool, pool,
                            (4096, 128, 2048), 16, 4, 0, one, one)
     assert mj.load_library().mj_rope_write_kv(ctypes.byref(a), None) == mj.MJ_ERR_INVALID_ARG
+
+
+@no_gpu
+def test_attention_rows_written_over_each_other_are_refused():
+    lib = mj.load_library()
+    for tok, head in ((4096, 0), (0, 512), (4096, 504), (4088, 512), (512, 512), (512, 768)):  # 2 requests of 8 heads
+        a = set_all(H.latent(), out_tok_stride=tok, out_head_stride=head)
+        a.workspace_bytes = 256  # (stops a call that passed the check, by another status)
+        assert lib.mj_latent_attention(ctypes.byref(a), None) == mj.MJ_ERR_INVALID_ARG
+    for tok, head in ((4096, 512), (512, 1024), (4800, 600)):
+        a = set_all(H.latent(), out_tok_stride=tok, out_head_stride=head, workspace_bytes=256)
+        assert lib.mj_latent_attention(ctypes.byref(a), None) == mj.MJ_ERR_CAPACITY
