@@ -1,5 +1,6 @@
 """The latent attention's calls as programs make them: plans that no longer hold
-the lengths, a step made on a busy stream."""
+the lengths, a step made on a busy stream, and what the kernel reads before it
+waits for the preceding one."""
 
 import numpy as np
 import pytest
@@ -72,3 +73,50 @@ def test_step_made_on_a_busy_stream_and_used_on_another():
     step.run(q, out, kv, c.B, c.scale, stream=s)
     torch.cuda.synchronize()
     c.check(out, step.lse)
+
+
+@pytest.mark.parametrize("h,q_len,sms", [(16, 1, None), (16, 1, 2), (32, 1, None), (128, 1, None), (16, 4, None)])
+def test_inputs_rewritten_right_before_the_attention(h, q_len, sms):
+    """Before the kernel waits for the preceding one it reads plan, lengths' owner
+    and block table to aim prefetches. Here the kernels right before each call
+    rewrite the table (to a second copy of the pages; the copy that it leaves holds
+    NaN codes), the plan (cut finely, or not at all), the lengths and the queries."""
+    import paged_fp8_decode_gb300 as mj
+
+    long, short = np.array([3000, 700, 1290], np.int32), np.array([140, 0, 900], np.int32)
+    c = Case(long, q_len, h, 64, seed=4)
+    kv = c.device()
+    P, pool = c.pages, kv.cache.contiguous()
+    both = torch.cat([pool, pool]).contiguous()
+    kv.cache = both
+    tables = [kv.block_table.clone(), torch.where(kv.block_table >= 0, kv.block_table + P, kv.block_table)]
+    step = c.step(sm_count=sms)
+    lens = [torch.from_numpy(x).cuda() for x in (long, short)]
+    plans = []
+    for x in (long, short):
+        step.plan(x, c.B)
+        torch.cuda.synchronize()
+        plans.append(step.plan_dev.clone())
+    q, out = c.q.cuda(), c.outputs()
+    qs = [q.clone(), (-q).contiguous()]
+    aa = step.args(q, out, kv, c.B, c.scale)
+    wants = []
+    for x, sign in ((long, 1), (short, -1)):
+        c.q = c.q * sign
+        wants.append(c.expected(x))
+        c.q = c.q * sign
+    for i in range(6):
+        use = i % 2
+        out.fill_(SENTINEL)
+        step.lse.fill_(SENTINEL)
+        stale = both[:P] if use else both[P:]
+        stale.fill_(0x7F)
+        q.copy_(qs[use])
+        kv.seq_lens.copy_(lens[use])
+        step.plan_dev.copy_(plans[use])
+        kv.block_table.copy_(tables[use])  # the last kernel before the attention
+        mj.mj_latent_attention(aa)
+        torch.cuda.synchronize()
+        assert mj.mj_workspace_status(step.workspace) == 0
+        c.check(out, step.lse, lens=(long, short)[use], want=wants[use])
+        stale.copy_(pool)
