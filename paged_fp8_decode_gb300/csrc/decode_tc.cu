@@ -5,12 +5,7 @@
 
 namespace mj {
 
-namespace {
-
-// ---------------------------------------------------------------------------
-// host side
-// ---------------------------------------------------------------------------
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encode_fn() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
   static std::once_flag once;
   std::call_once(once, [] {
@@ -24,12 +19,17 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
+namespace {
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
 // 4-D byte tensor (row, token, head, page) of one K or V cache; the smaller of
 // the token / head strides goes to dimension 1 (a box extent of 1 in the head
 // dimension leaves the shared-memory layout [token][128 B] either way).
 bool encode_kv_map(CUtensorMap* map, const void* base, const DecodeParams& p, int64_t sp, int64_t st, int64_t sh,
                    bool head_inner) {
-  auto fn = encode_fn();
+  auto fn = tensor_map_encode_fn();
   if (!fn) return false;
   const int64_t sh_eff = p.h_k == 1 ? (head_inner ? 32 : sp) : sh;
   cuuint64_t dims[4];
@@ -87,7 +87,7 @@ bool tc_supported(const DecodeParams& p) {
   const int64_t sm[] = {p.k_sp, p.v_sp};
   for (int64_t s : sm)
     if (s == 0) return false;
-  if (!encode_fn()) return false;
+  if (!tensor_map_encode_fn()) return false;
   return true;
 }
 

@@ -54,8 +54,6 @@
 //   cycle. 48 ragged requests of 128 heads: 115 us, 930 TFLOP/s counted once.
 //   Short requests: code that runs once comes from L2, 13 of the 25 cycles
 //   between two instructions of a warp are waits for it; hence the rolled loops.
-#include <cuda.h>
-#include <cudaTypedefs.h>
 
 #include <atomic>
 #include <climits>
@@ -980,22 +978,9 @@ __global__ void __launch_bounds__(Cfg<NR>::kThreads, 1)
   }
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-  static std::atomic<void*> fn{nullptr};
-  void* f = fn.load(std::memory_order_acquire);
-  if (!f) {
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      return nullptr;
-    fn.store(f, std::memory_order_release);
-  }
-  return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-}
-
 // 3-D byte tensor (row, token, page) of the cache; a box is `width` bytes of a page's tokens.
 bool encode_map(CUtensorMap* map, const LatentParams& p, int width, CUtensorMapSwizzle swizzle) {
-  auto fn = encode_fn();
+  auto fn = tensor_map_encode_fn();
   if (!fn) return false;
   const cuuint64_t dims[3] = {cuuint64_t(kRow), cuuint64_t(p.page_size), cuuint64_t(p.num_pages)};
   const cuuint64_t strides[2] = {cuuint64_t(p.stride_token), cuuint64_t(p.stride_page)};

@@ -125,7 +125,7 @@ int mj_rope_write_kv(const mj_rope_write_kv_args* a, void* stream) {
   if (st != MJ_OK) return st;
   const mj_write_kv_args& w = a->kv;
   if ((int64_t(a->h_q) + 2 * int64_t(w.h_k)) * w.d > (int64_t(1) << 24)) return MJ_ERR_INVALID_ARG;
-  const int64_t row = int64_t(w.d) * (w.kv_format == MJ_KV_E4M3 ? 8 : (w.kv_format == MJ_KV_E2M1 ? 4 : 6)) / 8;
+  const int64_t row = mj::kv_row_bytes(w.kv_format, w.d);
   if (!rows_apart(row, {{w.k_stride_page, w.num_pages}, {w.k_stride_token, w.page_size}, {w.k_stride_head, w.h_k}}) ||
       !rows_apart(row, {{w.v_stride_page, w.num_pages}, {w.v_stride_token, w.page_size}, {w.v_stride_head, w.h_k}}))
     return MJ_ERR_INVALID_ARG;
@@ -317,7 +317,7 @@ int mj_latent_attention(const mj_latent_args* a, void* stream) {
   p.stride_page = a->stride_page;
   p.stride_token = a->stride_token;
   p.page_size = a->page_size;
-  p.page_shift = a->page_size == 16 ? 4 : (a->page_size == 32 ? 5 : (a->page_size == 64 ? 6 : 7));
+  p.page_shift = mj::page_shift(a->page_size);
   p.page_span = a->stride_token <= 2 * MJ_LATENT_ROW_BYTES
                     ? uint32_t((a->page_size - 1) * a->stride_token + MJ_LATENT_ROW_BYTES)
                     : 0;

@@ -40,6 +40,8 @@ struct LatentParams {
   int evict_first;
 };
 
+inline int page_shift(int page_size) { return page_size == 16 ? 4 : (page_size == 32 ? 5 : (page_size == 64 ? 6 : 7)); }
+
 // Words (int32) of the plan buffer's parts, each a multiple of 4.
 inline int64_t latent_plan_slot_words(int slots) { return 4 * int64_t(slots); }
 inline int64_t latent_plan_split_words(int max_num_seqs) { return (2 * int64_t(max_num_seqs) + 3) / 4 * 4; }

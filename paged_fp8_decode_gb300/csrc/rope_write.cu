@@ -369,8 +369,6 @@ cudaError_t launch_format(int kv_format, const RopeWriteParams& p, cudaStream_t 
   }
 }
 
-int log2_of(int page_size) { return page_size == 16 ? 4 : (page_size == 32 ? 5 : (page_size == 64 ? 6 : 7)); }
-
 void set_rope(RopeWriteParams& p, const mj_rope& r) {
   p.pos = r.positions;
   p.pos_axis = r.axis_stride;
@@ -405,7 +403,7 @@ cudaError_t launch_rope_write(const mj_rope_write_kv_args& a, cudaStream_t strea
   p.v_ts = w.value_tok_stride;
   p.v_hs = w.value_head_stride;
   p.slots = w.slot_mapping;
-  p.page_shift = log2_of(w.page_size);
+  p.page_shift = page_shift(w.page_size);
   p.num_slots = w.num_pages * w.page_size;
   p.k_cache = static_cast<uint8_t*>(w.k_cache);
   p.v_cache = static_cast<uint8_t*>(w.v_cache);
@@ -442,7 +440,7 @@ cudaError_t launch_latent_write(const mj_latent_write_args& a, cudaStream_t stre
   p.k_ts = a.k_pe_tok_stride;
   p.v_ts = a.latent_tok_stride;
   p.slots = a.slot_mapping;
-  p.page_shift = log2_of(a.page_size);
+  p.page_shift = page_shift(a.page_size);
   p.num_slots = a.num_pages * a.page_size;
   p.v_cache = static_cast<uint8_t*>(a.cache);
   p.k_cache = p.v_cache + MJ_LATENT_DIM;

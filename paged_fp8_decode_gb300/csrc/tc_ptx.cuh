@@ -5,9 +5,14 @@
 #pragma once
 
 #include <cuda.h>
+#include <cudaTypedefs.h>
 #include <stdint.h>
 
 namespace mj {
+
+// The driver's cuTensorMapEncodeTiled (null where there is no driver), looked up once (decode_tc.cu).
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encode_fn();
+
 namespace tc {
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
