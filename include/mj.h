@@ -443,7 +443,8 @@ MJ_API int mj_write_kv(const mj_write_kv_args* args, void* stream);
  *   (x0, x1) -> scale * (x0 cos a - x1 sin a,  x1 cos a + x0 sin a)
  * in float32, a itself in fixed point: turns[i] = inv_freq[i] / (2 pi) as a
  * fraction of 2^64 (mj_rope_turns), n * turns[i] modulo 2^64 the angle modulo a
- * full turn, exact to n * 2^-65 turns for any int64 n.
+ * full turn, exact to n * 2^-65 turns for any int64 n; its cosine and sine are those
+ * of its nearest float32, within 1e-7 rad.
  * The runner page takes queries and keys already rotated (T5DecodeRunner.run);
  * these calls are the step before it.
  * ---------------------------------------------------------------------- */

@@ -44,15 +44,19 @@
 //
 // What bounds it (GB300, one launch and the merge; DRAM reads are the cache's
 // bytes, 152.3 MB for 151.0 MB of 64 x 4096 tokens):
-//   16 rows: HBM. 64 x 4096 tokens, 16 heads: 34.5 us, 4.4 TB/s in all; once it
+//   16 rows: HBM. 64 x 4096 tokens, 16 heads: 34.9 us, 4.4 TB/s in all; once it
 //   streams, a tile takes 3400 cycles an SM, 6.3 TB/s. The rest is the start
 //   (7500 cycles to the first scores), the last tile and the merge (3 us).
 //   64 rows: the chain load, QK, softmax, PV of a ring that holds two tiles
-//   beside the 72 KB of Q's two terms, 4300 cycles a tile; the products alone
+//   beside the 72 KB of Q's two terms, 4400 cycles a tile; the products alone
 //   take 3055 (18 MMAs of N = 128 at 65 cycles and 32 of N = 64 at 49 + issue),
 //   and at N = 64 both operands' reads fill the shared memory's 128 bytes a
-//   cycle. 48 ragged requests of 128 heads: 115 us, 930 TFLOP/s counted once.
-//   Short requests: code that runs once comes from L2, 13 of the 25 cycles
+//   cycle. 48 ragged requests of 128 heads: 119 us, 900 TFLOP/s counted once.
+//   A change of work row there is serial: after a row's last tile the softmax
+//   warps stage the next row's queries and write the row's output while the
+//   tensor pipe idles, so many short requests are slowest (128 of 1024 tokens,
+//   128 heads: 64 us for 19 of operations).
+//   Short requests: code that runs once comes from L2, 10 of the 23 cycles
 //   between two instructions of a warp are waits for it; hence the rolled loops.
 
 #include <atomic>

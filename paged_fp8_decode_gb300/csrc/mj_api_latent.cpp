@@ -20,7 +20,9 @@ int status_of(cudaError_t e) { return e == cudaSuccess ? MJ_OK : MJ_ERR_CUDA; }
 bool page_size_ok(int ps) { return ps == 16 || ps == 32 || ps == 64 || ps == 128; }
 
 // A plan's cost of a work row beside its tiles, in tiles: staging the queries,
-// refilling the pipeline, writing the rows out and joining them. Measured (us):
+// refilling the pipeline, writing the rows out and joining them (a row of an
+// unsplit request has no partial to join, but is charged alike). Fitted, each to
+// one batch, not derived; in us:
 // 64 x 4096 tokens, 16 heads: 35.8, 34.5, 35.7 at 0, 1, 2; 96 requests of 300 to
 // 5000 tokens, 32 heads: 55.2, 49.8, 48.8, 50.6 at 1, 2, 3, 6; 48 of 1024 to
 // 16384, 128 heads: 136, 125, 116, 121 at 1, 2, 5, 9.

@@ -8,8 +8,9 @@
 // the angle is formed in turns, in fixed point: `turns[i]` is
 // inv_freq[i] / (2 pi) as a fraction of 2^64, and position * turns[i] modulo 2^64
 // is the angle modulo a full turn, off by at most position * 2^-65 of a turn. Its
-// upper 32 bits, read as a signed number of 2^-31 half turns (below 1e-9 rad),
-// go to sincospif. Everything after is float32, with one rounding at the end: to
+// upper 32 bits, a signed number of 2^-31 half turns, go to sincospif as a float32:
+// that rounds an angle near half a turn by 2^-25 of one, 1e-7 rad, far inside the
+// output's own rounding. Everything after is float32, with one rounding at the end: to
 // bf16 (queries) or to the cache format (keys and values, the division IEEE
 // float32, as mj_write_kv does it).
 //
@@ -34,8 +35,10 @@ namespace {
 
 constexpr int kThreads = 128;
 // Two slots of loads in flight a thread and seven CTAs an SM: 16384 tokens of
-// 32/8 heads of 128 in 62.8 us (5.9 TB/s). Three slots and five CTAs: 65.6 us,
-// and 0.2 us less for one token; eight CTAs spill: 71 us.
+// 32/8 heads of 128 in 62.6 us (5.9 TB/s; e2m3, e3m2, e2m1, which divide every
+// element: 92, 87, 89 us, 4.0 TB/s). Three slots and five CTAs: 65.6 us, and 0.2
+// us less for one token; eight CTAs: 71 us. (Seven leave 72 registers: 8 bytes
+// are spilled for e4m3, 24 for the packed formats, more at eight.)
 constexpr int kItemsPerThread = 2, kMinCtas = 7;
 // Where the CTAs of that would not be resident at once, a thread takes up to
 // six slots, so that its cosines, addresses and set-up serve more of them
