@@ -541,8 +541,8 @@ __global__ void __launch_bounds__(Cfg<NR>::kThreads, 1)
     constexpr int kShare = 32 / RW;  // lanes that share a row after reduce_rows
     const float ds0 = p.descale[0], ds1 = p.descale[1];
     // Queries enter in units of one descale: the latent channels', unless it is 0
-    // or vanishes beside the other (their ratio stays finite then).
-    const float unit = ds0 != 0.f && fabsf(ds1) <= fabsf(ds0) * 0x1p64f ? ds0 : (ds1 != 0.f ? ds1 : 1.f);
+    // or far below the other (2^16 times a row's factor, 2^108 at most, is finite).
+    const float unit = ds0 != 0.f && fabsf(ds1) <= fabsf(ds0) * 0x1p16f ? ds0 : (ds1 != 0.f ? ds1 : 1.f);
     const float rel0 = ds0 / unit, rel1 = ds1 / unit;
     const float qk_log2 = p.softmax_scale * kLog2e * unit;
     const int rows_pad = p.n_row_tiles * NR;  // rows of a partial

@@ -131,3 +131,24 @@ def test_descales_of_zero_and_far_apart(descale):
     # a logit (1 nat rms) off by 2^-8 of a query value at most, 0.0013 rms: 5 sigma
     assert np.abs(got.numpy() - lse[0]).max() <= 0.0065
     assert np.linalg.norm(out.numpy() - want[0]) <= 0.0065 * np.linalg.norm(want[0])
+
+
+@pytest.mark.parametrize("descale", [(2.0 ** -30, 1.0), (2.0 ** -60, 1.0), (2.0 ** -17, 1.0), (2.0 ** -16, 1.0), (1.0, 2.0 ** -60)])
+def test_queries_of_zero_and_tiny_beside_descales_far_apart(descale):
+    """A row's factor is largest where its queries are 0, and may meet the ratio of the descales there."""
+    n, h = 200, 16
+    rng = np.random.default_rng(9)
+    codes = torch.from_numpy(rng.standard_normal((n, 576)) * 112).clamp(-448, 448).float().to(torch.float8_e4m3fn)
+    f = codes.double().numpy()
+    rows = np.concatenate([f[:, :512] * descale[0], f[:, 512:] * descale[1]], axis=1)
+    q = torch.from_numpy(rng.standard_normal((1, h, 576)))
+    q[0, 0] = 0
+    q[0, 1] *= 2.0 ** -110
+    q[0, 2, 512:] = 0
+    q = q.to(torch.bfloat16)
+    scale = float(np.float32(1 / (q[0].double().numpy() @ rows.T).std()))
+    want, lse = OR.latent_attention(q.double().numpy(), rows, scale, n, True)
+    out, got = attend(codes.view(torch.uint8).cuda(), q.cuda(), torch.tensor(descale, dtype=torch.float32).cuda(), scale, 1)
+    # as above: logits of 1 nat rms, 5 sigma of 0.0013
+    assert np.abs(got.numpy() - lse[0]).max() <= 0.0065
+    assert np.linalg.norm(out.numpy() - want[0]) <= 0.0065 * np.linalg.norm(want[0])
