@@ -22,16 +22,15 @@
 // lo = e4m3(x - hi), two rows of the Q tile, their products added when S is read.
 // bf16 has 8 bits and the terms 4 each, so a latent channel from 1/4 on is exact,
 // a smaller one within 2^-10; s0 goes into the row's logit scale, and the rotary
-// channels, which take s1 / s0, are within 2^-8 of themselves. (Scaled to
-// 448 by s0 448 / amax, no power of two, all were within 2^-8 only: logits of 6
-// nats off by 0.01.) A weight p is split into hi = e4m3(p) and lo, the rest in e5m2: two
-// products into one accumulator. From 2^-6 on that is within 2^-7.8 of p, 0.15%
-// rms, about bf16's own. Below 2^-6 hi is on a fixed step and lo alone has two
-// bits, so that many equal small weights, all off alike, would change their
-// share of a row (131071 keys 16.8 binades below one: the output by 2% of
-// max|V|); there lo is rounded up or down by a dither, 8 bits of a hash of the
-// key's index, and the errors cancel (0.01%). The row sums add the p themselves
-// in float32.
+// channels, which take s1 / s0, are within 2^-8 of themselves. (By s0 448 / amax,
+// no power of two, all were within 2^-8 only: logits of 6 nats off by 0.01.)
+// A weight p is split into hi = e4m3(p) and lo, the rest in e5m2: two products
+// into one accumulator. From 2^-6 on that is within 2^-7.8 of p, 0.15% rms, about
+// bf16's own. Below 2^-6 hi is on a fixed step and lo alone has two bits, so that
+// many equal small weights, all off alike, would change their share of a row
+// (131071 keys 16.8 binades below one: the output by 2% of max|V|); there lo is
+// rounded up or down by a dither, 8 bits of a hash of the key's index, and the
+// errors cancel (0.01%). The row sums add the p themselves in float32.
 //
 // Warps: 0, 2, 3 the TMA producers, 1 the MMA issuer, 4.. one or two softmax
 // warpgroups (thread x of a group: key x of S, channel x of each of the four
@@ -44,14 +43,14 @@
 //
 // What bounds it (GB300, one launch and the merge; DRAM reads are the cache's
 // bytes, 152.3 MB for 151.0 MB of 64 x 4096 tokens):
-//   16 rows: HBM. 64 x 4096 tokens, 16 heads: 34.9 us, 4.4 TB/s in all; once it
+//   16 rows: HBM. 64 x 4096 tokens, 16 heads: 34.7 us, 4.4 TB/s in all; once it
 //   streams, a tile takes 3400 cycles an SM, 6.3 TB/s. The rest is the start
 //   (7500 cycles to the first scores), the last tile and the merge (3 us).
 //   64 rows: the chain load, QK, softmax, PV of a ring that holds two tiles
 //   beside the 72 KB of Q's two terms, 4400 cycles a tile; the products alone
 //   take 3055 (18 MMAs of N = 128 at 65 cycles and 32 of N = 64 at 49 + issue),
 //   and at N = 64 both operands' reads fill the shared memory's 128 bytes a
-//   cycle. 48 ragged requests of 128 heads: 119 us, 900 TFLOP/s counted once.
+//   cycle. 48 ragged requests of 128 heads: 119.5 us, 900 TFLOP/s counted once.
 //   A change of work row there is serial: after a row's last tile the softmax
 //   warps stage the next row's queries and write the row's output while the
 //   tensor pipe idles, so many short requests are slowest (128 of 1024 tokens,
@@ -215,8 +214,8 @@ __device__ __forceinline__ void weight_terms(const float* p, uint32_t dither, ui
   lo = __byte_perm(rest[0], rest[1], 0x7531);
 }
 
-// 8 bits of a key's index, in both halves: the dither of its weights. Every
-// value alike often in any 16 tiles, also among every 2nd, 3rd, ... key.
+// 8 bits of a key's index, in both halves: the dither of its weights. A hash, so
+// that every 2nd, 16th, ... key takes all values about alike often too.
 __device__ __forceinline__ uint32_t key_dither(uint32_t key) {
   uint32_t u = key * 0x9E3779B1u;  // 2^32 / golden ratio
   u ^= u >> 16;

@@ -17,10 +17,10 @@ import numpy as np
 import torch
 
 from . import (KV_FORMATS, LATENT_DIM, LATENT_ROPE_DIM, LATENT_ROW, MJ_IMPL_AUTO, MJ_KV_E2M1, MJ_KV_E4M3, MJ_OUT_BF16,
-               MJ_OUT_F16, _check, _ptr, _same_device, _stream, load_library, mj_decode_args, mj_decode_attention, mj_latent_args,
-               mj_latent_attention, mj_latent_plan, mj_latent_plan_size, mj_latent_slots, mj_latent_workspace_size,
-               mj_latent_write_args, mj_merge_lse, mj_plan_split_kv, mj_plan_upload, mj_quantize_q,
-               mj_rope_write_kv_args, mj_slots, mj_workspace_init, mj_workspace_size)
+               MJ_OUT_F16, _check, _ptr, _same_device, _stream, load_library, mj_decode_args, mj_decode_attention,
+               mj_latent_args, mj_latent_attention, mj_latent_plan, mj_latent_plan_size, mj_latent_slots,
+               mj_latent_workspace_size, mj_latent_write_args, mj_merge_lse, mj_plan_split_kv, mj_plan_upload,
+               mj_quantize_q, mj_rope_write_kv_args, mj_slots, mj_workspace_init, mj_workspace_size)
 
 
 @dataclass
