@@ -570,9 +570,10 @@ MJ_API int mj_latent_workspace_size(int slots, int q_len, int h, size_t* bytes);
  * and within 2^-17.8 of it below, its rotary channels within 2^-8 of themselves or
  * 2^-17.8 of it (the other way round where scale[1] is above 2^16 scale[0]).
  * A weight is within 2^-7.8 of itself (0.15% rms) down to 10 binades below its
- * row's largest (12 where the largest stands out); below that it is rounded up or down by a dither that depends on its key's index alone, by
- * 2^-2 of itself or 2^-20 of the largest at most and right on average but for
- * 2^-29 of the largest. So N such weights, equal ones too, are off by some
+ * row's largest (12 where the largest stands out); below that it is rounded up or
+ * down by a dither that depends on its key's index alone, by 2^-2 of itself or
+ * 2^-20 of the largest at most and right on average but for 2^-29 of the largest.
+ * So N such weights, equal ones too, are off by some
  * sqrt(N) times one of them at random and N 2^-29 together: less than 0.2% of
  * max|V| in the output at 131072 keys. Weights from 29 binades below on are 0.
  * A NaN code of a cached token reaches every row of its request, also one whose
