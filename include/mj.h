@@ -24,6 +24,15 @@
  *   mj_latent_plan      (host)   equal shares of all requests' tiles
  *   mj_latent_attention (device) attention in the absorbed form, split and joined
  *
+ * A block-scaled cache (e4m3 codes, a power-of-two scale for each block of
+ * tokens and KV head, found at the write) has its own calls:
+ *
+ *   mj_block_write_kv   (device) append keys and values, growing blocks' scales
+ *   mj_block_read_kv    (device) bring requests' tokens back as bf16 or fp16 rows
+ *   mj_block_plan       (host)   each request in equal pieces, however many requests
+ *   mj_block_attention  (device) decode attention, split and joined
+ *   mj_block_prompt     (device) attention of ragged prompt chunks
+ *
  * Conventions (all calls):
  *  - Every call returns an mj_status; 0 is success, negative is an error.
  *    Nothing throws, aborts or prints.
@@ -618,6 +627,211 @@ typedef struct mj_latent_args {
 } mj_latent_args;
 
 MJ_API int mj_latent_attention(const mj_latent_args* args, void* stream);
+
+/* ------------------------------------------------------------------------
+ * The block-scaled cache: e4m3 codes with one power-of-two scale for each block
+ * of `block` tokens and KV head, found as the tokens are written (no
+ * calibration). A scale is an exponent byte e: a code c of its block stands for
+ * c * 2^(e - 127), with e from MJ_BLOCK_EXP_MIN (2^-32) to MJ_BLOCK_EXP_MAX
+ * (2^32); a byte outside them is read as the nearer one. Pages of 16, 32, 64 or
+ * 128 tokens hold whole blocks: block is 16, 32, 64 or 128, at most page_size.
+ * Alignment: caches 16 bytes, their byte strides multiples of 16.
+ * ---------------------------------------------------------------------- */
+#define MJ_BLOCK_EXP_MIN 95
+#define MJ_BLOCK_EXP_MAX 159
+
+typedef struct mj_block_cache {
+  int h_k, d;                 /* KV heads; head size: 128 or 256 */
+  int page_size, block;       /* tokens of a page, and of a scale */
+  int64_t num_pages;
+  void* k_cache;              /* channel c of token j of page p, KV head g: byte p*stride_page + j*stride_token + g*stride_head + c */
+  void* v_cache;
+  int64_t k_stride_page, k_stride_token, k_stride_head;  /* bytes */
+  int64_t v_stride_page, v_stride_token, v_stride_head;
+  uint8_t* k_exp;             /* block i of page p, KV head g: byte p*exp_stride_page + g*exp_stride_head + i */
+  uint8_t* v_exp;
+  int64_t k_exp_stride_page, k_exp_stride_head;
+  int64_t v_exp_stride_page, v_exp_stride_head;
+} mj_block_cache;
+
+/* ------------------------------------------------------------------------
+ * mj_block_write_kv — quantize the new tokens' keys and values and append them
+ * at slot_mapping (page s / page_size, row s % page_size), in one launch. For
+ * each block and KV head that the call writes into, K and V apart:
+ *   need = the smallest e with max |x| <= 448 * 2^(e - 127) over the call's
+ *          finite values of the block, within the range above
+ *   e'   = need               where the call writes the block's first row (it
+ *                             begins anew, whatever it held)
+ *          max(e, need)       else: the rows before the call's first one are the
+ *                             block's earlier tokens
+ *   new rows:     c  = e4m3(x * 2^(127 - e'))
+ *   earlier rows: c' = e4m3(c * 2^(e - e'))  (exact but for subnormal results)
+ * rounded to nearest even, saturating at 448 (infinities too; NaN stays NaN).
+ * Every other byte of the caches keeps its value; rows of a block behind the
+ * ones written are of no value until they are written. The result does not
+ * depend on the tokens' order.
+ * The call's slots are distinct, and its tokens of one block follow one another
+ * (padding tokens between two of them: at most 128): a block's tokens that do
+ * not are written as if by several calls at once, in no order. Negative slots
+ * are padding, a slot past the pool is skipped and reported (status bit 1). The
+ * rows of a cache, and its exponent bytes, lie apart: each stride holds all
+ * steps of the next smaller. At most 2^30 tokens.
+ * Alignment: key and value 16 bytes, their strides multiples of 8 elements.
+ * The launch may begin before the preceding kernel on `stream` has finished
+ * and waits for it before it reads.
+ * ---------------------------------------------------------------------- */
+typedef struct mj_block_write_args {
+  int num_tokens;             /* 0: nothing to do */
+  const void* key;            /* device bf16; (t, g, c) at key[t*key_tok_stride + g*key_head_stride + c] */
+  const void* value;
+  int64_t key_tok_stride, key_head_stride;      /* elements */
+  int64_t value_tok_stride, value_head_stride;
+  const int64_t* slot_mapping;  /* device [num_tokens] */
+  mj_block_cache cache;
+  uint32_t* status;           /* nullable device word */
+} mj_block_write_args;
+
+MJ_API int mj_block_write_kv(const mj_block_write_args* args, void* stream);
+
+/* ------------------------------------------------------------------------
+ * mj_block_read_kv — bring cached tokens back: row starts[b] + i of k_out and
+ * v_out, for i < starts[b + 1] - starts[b], is the value of token first[b] + i of
+ * request b (token i without `first`), as bf16 (exact) or fp16 (to nearest even). Rows
+ * from starts[num_seqs] on, and
+ * rows past num_rows, are left as they are. A page outside the pool or the block table reads as zeros
+ * and is reported (status bit 1), as is a token past the table.
+ * starts rises from 0; num_rows is at least starts[num_seqs] and sizes the grid.
+ * Alignment: outputs 16 bytes, their strides multiples of 8 elements; the
+ * outputs' rows lie apart.
+ * ---------------------------------------------------------------------- */
+typedef struct mj_block_read_args {
+  int num_seqs;
+  int64_t num_rows;           /* rows of the outputs (0: nothing to do) */
+  mj_block_cache cache;
+  const int32_t* block_table; /* device; page of token j of request b: block_table[b*block_table_stride + j/page_size] */
+  int64_t block_table_stride, block_table_len;  /* elements between requests; entries a request has */
+  const int32_t* starts;      /* device [num_seqs + 1] */
+  const int32_t* first;       /* nullable device [num_seqs]: each request's first token to read */
+  void* k_out;                /* device bf16 or fp16 (out_dtype); (t, g, c) at k_out[t*tok_stride + g*head_stride + c]; */
+  void* v_out;                /* either may be null */
+  int64_t k_tok_stride, k_head_stride;  /* elements */
+  int64_t v_tok_stride, v_head_stride;
+  int out_dtype;              /* mj_out_dtype */
+  uint32_t* status;           /* nullable device word */
+} mj_block_read_args;
+
+MJ_API int mj_block_read_kv(const mj_block_read_args* args, void* stream);
+
+/* ------------------------------------------------------------------------
+ * The block-scaled plan: like mj_plan_split_kv's, but every request is cut into
+ * pieces of its own equal length, so that a long request among short ones is
+ * split however many requests there are. slots: mj_slots(...). The plan is one
+ * buffer of mj_block_plan_size() int32 words (a multiple of 4): copy it with
+ * mj_plan_upload(plan_host, NULL, plan_dev, NULL, words / 4, 0, stream). Lengths
+ * are exact or an upper bound (margin: tokens added to each that is not 0).
+ * mj_block_workspace_size: bytes of mj_block_attention's workspace, the status
+ * header (mj_workspace_init, mj_workspace_status) and the pieces' partials.
+ * ---------------------------------------------------------------------- */
+MJ_API int mj_block_plan_size(int slots, int max_num_seqs, size_t* words);
+MJ_API int mj_block_plan(const int32_t* seq_lens_host, int num_seqs, int max_num_seqs, int slots, int margin,
+                  int32_t* plan_host, size_t plan_words);
+MJ_API int mj_block_workspace_size(int slots, int q_len, int h_q, int h_k, int d, size_t* bytes);
+
+/* ------------------------------------------------------------------------
+ * mj_block_attention — decode attention over the block-scaled cache:
+ *   t[r][j] = softmax_scale * q[r] . k[j]      out[r] = sum_j softmax_j(t[r]) v[j]
+ * for each query row r (query token, head) of each request, over its seq_lens[b]
+ * cached tokens. Two launches: the attention, and the join of split requests.
+ * Requests with seq_lens[b] == 0 are padding: nothing is written for them. A
+ * causal row that sees no key writes 0 (LSE -inf).
+ *
+ * Accuracy: a query enters the tensor cores as two 8-bit terms, exact down to
+ * 2^-14 of the largest |q| among the rows of its request and KV head (within 2^-22
+ * of it below); a value's weight, softmax weight times its block's scale, as two 8-bit
+ * terms, within 2^-8 of itself down to 10 binades below its row's largest (below
+ * that, where such keys are many, by two more terms, down to 28 binades). A row of
+ * N keys is off by at most (2^-7 + N 2^-28) times its largest weight times 448. A query that is not finite makes its
+ * row NaN; a NaN code of a cached token reaches every row of its request, also
+ * one whose causal limit hides it.
+ * Status bits (workspace): as mj_workspace_status lists them; bit 1 also for a
+ * token past block_table_len, bit 4 also where a request's device length reaches
+ * past the plan's tiles of it (the tokens past them are not attended to).
+ * Two calls that may run at once (other streams, two captured graphs) need a
+ * workspace each. out overlaps nothing that the call reads; its rows lie apart.
+ * Make one call of each head size and row count before capturing.
+ * Alignment: q, block_table, seq_lens, plan, out and workspace 16 bytes.
+ * ---------------------------------------------------------------------- */
+typedef struct mj_block_args {
+  int num_seqs, max_num_seqs;  /* requests; the plan's max_num_seqs */
+  int q_len, h_q;              /* query tokens a request; query heads (a multiple of cache.h_k) */
+  int causal;                  /* 1: query token t sees keys j <= seq_len - q_len + t; 0: all */
+  float softmax_scale;
+  const void* q;               /* device bf16; (b*q_len + t, h, c) at q[..*q_tok_stride + h*q_head_stride + c] */
+  int64_t q_tok_stride, q_head_stride;  /* elements, multiples of 8 */
+  mj_block_cache cache;
+  const int32_t* block_table;
+  int64_t block_table_stride, block_table_len;
+  const int32_t* seq_lens;     /* device [num_seqs] */
+  const int32_t* plan;         /* device, mj_block_plan */
+  int slots;
+  void* out;                   /* device bf16 or fp16 (out_dtype) */
+  int64_t out_tok_stride, out_head_stride;  /* elements, multiples of 8 */
+  int out_dtype;               /* mj_out_dtype */
+  float* lse;                  /* nullable device [num_seqs][h_k][q_len*h_q/h_k], as mj_decode_args' */
+  void* workspace;
+  size_t workspace_bytes;
+  int evict_first;             /* 1: cache loads are evicted first from L2 */
+} mj_block_args;
+
+MJ_API int mj_block_attention(const mj_block_args* args, void* stream);
+
+/* ------------------------------------------------------------------------
+ * mj_block_prompt — attention of ragged prompt chunks over the block-scaled
+ * cache, the chunk's own tokens already written there: query tokens
+ * q_starts[b] .. q_starts[b + 1] - 1 are the last ones of request b's seq_lens[b]
+ * tokens, and (causal) query token i of its n sees keys j <= seq_lens[b] - n + i.
+ * Rows from q_starts[num_seqs] on are left as they are; a row that sees no key
+ * writes 0 (LSE -inf).
+ * max_q_len bounds a request's query tokens on the host and sizes the grid; query
+ * tokens past it are not computed, and reported (status bit 4). splits: into how
+ * many pieces the keys of a row tile are cut, each piece a CTA, joined by a second
+ * launch where there is more than one: any number from 1 to MJ_BLOCK_MAX_SPLITS, or
+ * what mj_block_prompt_splits gives, which fills sm_count SMs where the chunks
+ * alone do not (max_len: the longest request).
+ *
+ * Accuracy: queries as in mj_block_attention, but exact down to 2^-10 of the
+ * row's largest |q| (within 2^-18 of it below); weights in fp16, relative to a
+ * running reference of their row, so that keys down to 24 binades below its largest count;
+ * sums in float32. What that call says about values that are not finite, status
+ * bits, workspaces and overlaps holds here.
+ * ---------------------------------------------------------------------- */
+typedef struct mj_block_prompt_args {
+  int num_seqs;
+  int num_tokens;              /* rows of q and out (0: nothing to do) */
+  int max_q_len;
+  int splits;
+  int h_q;                     /* query heads (a multiple of cache.h_k) */
+  int causal;
+  float softmax_scale;
+  const void* q;               /* device bf16; (t, h, c) at q[t*q_tok_stride + h*q_head_stride + c] */
+  int64_t q_tok_stride, q_head_stride;  /* elements, multiples of 8 */
+  const int32_t* q_starts;     /* device [num_seqs + 1], rising from 0 */
+  mj_block_cache cache;
+  const int32_t* block_table;
+  int64_t block_table_stride, block_table_len;
+  const int32_t* seq_lens;     /* device [num_seqs] */
+  void* out;                   /* device bf16 or fp16 (out_dtype) */
+  int64_t out_tok_stride, out_head_stride;  /* elements, multiples of 8 */
+  int out_dtype;
+  float* lse;                  /* nullable device [num_tokens][h_q]: natural log of the sum of exp */
+  void* workspace;
+  size_t workspace_bytes;
+} mj_block_prompt_args;
+
+#define MJ_BLOCK_MAX_SPLITS 64
+MJ_API int mj_block_prompt_splits(int sm_count, int num_seqs, int max_q_len, int max_len, int h_q, int h_k, int d);
+MJ_API int mj_block_prompt_workspace_size(int num_tokens, int h_q, int d, int splits, size_t* bytes);
+MJ_API int mj_block_prompt(const mj_block_prompt_args* args, void* stream);
 
 #ifdef __cplusplus
 }

@@ -33,6 +33,8 @@ Modules:
   (bit-exact target).
 * :mod:`oracle.attention` — exact fp64 paged decode attention, split
   partials and the LSE merge.
+* :mod:`oracle.block`   — the block-scaled cache: its write, its values and the
+  attention over them.
 
 Parity status: every function here is pinned by ``tests/test_oracle_*.py``
 against values and properties fixed by the format definitions, the pages

@@ -53,6 +53,8 @@ EXPORTS = (
     "mj_plan_upload", "mj_decode_kernel",
     "mj_rope_turns", "mj_rope_write_kv", "mj_latent_write", "mj_latent_slots", "mj_latent_plan_size",
     "mj_latent_plan", "mj_latent_workspace_size", "mj_latent_attention",
+    "mj_block_write_kv", "mj_block_read_kv", "mj_block_plan_size", "mj_block_plan", "mj_block_workspace_size",
+    "mj_block_attention", "mj_block_prompt_splits", "mj_block_prompt_workspace_size", "mj_block_prompt",
 )
 
 NOALLOC_SCRATCH_BYTES = 16 << 20
@@ -61,6 +63,12 @@ NOALLOC_SCRATCH_BYTES = 16 << 20
 LATENT_DIM = 512
 LATENT_ROPE_DIM = 64
 LATENT_ROW = LATENT_DIM + LATENT_ROPE_DIM
+
+# exponent bytes of a block-scaled cache: a code c of a block with byte e stands for c * 2^(e - BLOCK_EXP_BIAS)
+BLOCK_EXP_BIAS = 127
+BLOCK_EXP_MIN = 95
+BLOCK_EXP_MAX = 159
+BLOCK_MAX_SPLITS = 64
 
 
 class MjError(RuntimeError):
@@ -169,6 +177,76 @@ class mj_latent_args(ctypes.Structure):
     ]
 
 
+class mj_block_cache(ctypes.Structure):
+    """ctypes mirror of ``struct mj_block_cache`` (include/mj.h)."""
+
+    _fields_ = [
+        ("h_k", ctypes.c_int), ("d", ctypes.c_int), ("page_size", ctypes.c_int), ("block", ctypes.c_int),
+        ("num_pages", ctypes.c_int64), ("k_cache", ctypes.c_void_p), ("v_cache", ctypes.c_void_p),
+        ("k_stride_page", ctypes.c_int64), ("k_stride_token", ctypes.c_int64), ("k_stride_head", ctypes.c_int64),
+        ("v_stride_page", ctypes.c_int64), ("v_stride_token", ctypes.c_int64), ("v_stride_head", ctypes.c_int64),
+        ("k_exp", ctypes.c_void_p), ("v_exp", ctypes.c_void_p),
+        ("k_exp_stride_page", ctypes.c_int64), ("k_exp_stride_head", ctypes.c_int64),
+        ("v_exp_stride_page", ctypes.c_int64), ("v_exp_stride_head", ctypes.c_int64),
+    ]
+
+
+class mj_block_write_args(ctypes.Structure):
+    """ctypes mirror of ``struct mj_block_write_args`` (include/mj.h)."""
+
+    _fields_ = [
+        ("num_tokens", ctypes.c_int), ("key", ctypes.c_void_p), ("value", ctypes.c_void_p),
+        ("key_tok_stride", ctypes.c_int64), ("key_head_stride", ctypes.c_int64),
+        ("value_tok_stride", ctypes.c_int64), ("value_head_stride", ctypes.c_int64),
+        ("slot_mapping", ctypes.c_void_p), ("cache", mj_block_cache), ("status", ctypes.c_void_p),
+    ]
+
+
+class mj_block_read_args(ctypes.Structure):
+    """ctypes mirror of ``struct mj_block_read_args`` (include/mj.h)."""
+
+    _fields_ = [
+        ("num_seqs", ctypes.c_int), ("num_rows", ctypes.c_int64), ("cache", mj_block_cache),
+        ("block_table", ctypes.c_void_p), ("block_table_stride", ctypes.c_int64), ("block_table_len", ctypes.c_int64),
+        ("starts", ctypes.c_void_p), ("first", ctypes.c_void_p), ("k_out", ctypes.c_void_p), ("v_out", ctypes.c_void_p),
+        ("k_tok_stride", ctypes.c_int64), ("k_head_stride", ctypes.c_int64),
+        ("v_tok_stride", ctypes.c_int64), ("v_head_stride", ctypes.c_int64),
+        ("out_dtype", ctypes.c_int), ("status", ctypes.c_void_p),
+    ]
+
+
+class mj_block_args(ctypes.Structure):
+    """ctypes mirror of ``struct mj_block_args`` (include/mj.h)."""
+
+    _fields_ = [
+        ("num_seqs", ctypes.c_int), ("max_num_seqs", ctypes.c_int), ("q_len", ctypes.c_int), ("h_q", ctypes.c_int),
+        ("causal", ctypes.c_int), ("softmax_scale", ctypes.c_float),
+        ("q", ctypes.c_void_p), ("q_tok_stride", ctypes.c_int64), ("q_head_stride", ctypes.c_int64),
+        ("cache", mj_block_cache),
+        ("block_table", ctypes.c_void_p), ("block_table_stride", ctypes.c_int64), ("block_table_len", ctypes.c_int64),
+        ("seq_lens", ctypes.c_void_p), ("plan", ctypes.c_void_p), ("slots", ctypes.c_int),
+        ("out", ctypes.c_void_p), ("out_tok_stride", ctypes.c_int64), ("out_head_stride", ctypes.c_int64),
+        ("out_dtype", ctypes.c_int), ("lse", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t), ("evict_first", ctypes.c_int),
+    ]
+
+
+class mj_block_prompt_args(ctypes.Structure):
+    """ctypes mirror of ``struct mj_block_prompt_args`` (include/mj.h)."""
+
+    _fields_ = [
+        ("num_seqs", ctypes.c_int), ("num_tokens", ctypes.c_int), ("max_q_len", ctypes.c_int), ("splits", ctypes.c_int),
+        ("h_q", ctypes.c_int), ("causal", ctypes.c_int), ("softmax_scale", ctypes.c_float),
+        ("q", ctypes.c_void_p), ("q_tok_stride", ctypes.c_int64), ("q_head_stride", ctypes.c_int64),
+        ("q_starts", ctypes.c_void_p), ("cache", mj_block_cache),
+        ("block_table", ctypes.c_void_p), ("block_table_stride", ctypes.c_int64), ("block_table_len", ctypes.c_int64),
+        ("seq_lens", ctypes.c_void_p),
+        ("out", ctypes.c_void_p), ("out_tok_stride", ctypes.c_int64), ("out_head_stride", ctypes.c_int64),
+        ("out_dtype", ctypes.c_int), ("lse", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
 _lib = None
 
 
@@ -208,6 +286,15 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.mj_latent_plan.argtypes = [vp, i32, i32, i32, i32, i32, i32, vp, sz]
     lib.mj_latent_workspace_size.argtypes = [i32, i32, i32, ctypes.POINTER(sz)]
     lib.mj_latent_attention.argtypes = [ctypes.POINTER(mj_latent_args), vp]
+    lib.mj_block_write_kv.argtypes = [ctypes.POINTER(mj_block_write_args), vp]
+    lib.mj_block_read_kv.argtypes = [ctypes.POINTER(mj_block_read_args), vp]
+    lib.mj_block_plan_size.argtypes = [i32, i32, ctypes.POINTER(sz)]
+    lib.mj_block_plan.argtypes = [vp, i32, i32, i32, i32, vp, sz]
+    lib.mj_block_workspace_size.argtypes = [i32, i32, i32, i32, i32, ctypes.POINTER(sz)]
+    lib.mj_block_attention.argtypes = [ctypes.POINTER(mj_block_args), vp]
+    lib.mj_block_prompt_splits.argtypes = [i32, i32, i32, i32, i32, i32, i32]
+    lib.mj_block_prompt_workspace_size.argtypes = [i32, i32, i32, i32, ctypes.POINTER(sz)]
+    lib.mj_block_prompt.argtypes = [ctypes.POINTER(mj_block_prompt_args), vp]
     _lib = lib
     return lib
 
@@ -484,4 +571,70 @@ def mj_latent_attention(args: mj_latent_args, stream=None):
     _check("mj_latent_attention", load_library().mj_latent_attention(ctypes.byref(args), _stream(stream)))
 
 
+def mj_block_write_kv(args: mj_block_write_args, stream=None):
+    """Quantize and append keys and values to a block-scaled cache (:func:`block_write_args` builds ``args``)."""
+    _on_device(args)
+    _check("mj_block_write_kv", load_library().mj_block_write_kv(ctypes.byref(args), _stream(stream)))
+
+
+def mj_block_read_kv(args: mj_block_read_args, stream=None):
+    """Bring cached tokens back as rows (:func:`block_read_args` builds ``args``)."""
+    _on_device(args)
+    _check("mj_block_read_kv", load_library().mj_block_read_kv(ctypes.byref(args), _stream(stream)))
+
+
+def mj_block_plan_size(slots: int, max_num_seqs: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check("mj_block_plan_size", load_library().mj_block_plan_size(slots, max_num_seqs, ctypes.byref(n)))
+    return n.value
+
+
+def mj_block_plan(seq_lens_host, num_seqs: int, max_num_seqs: int, slots: int, margin: int = 0, plan_out=None):
+    """Host plan of mj_block_attention. ``plan_out``: an int32 host buffer
+    (numpy or a pinned CPU tensor) of ``mj_block_plan_size`` words to write
+    into; otherwise a numpy array is returned."""
+    import numpy as np
+
+    lens = np.ascontiguousarray(np.asarray(seq_lens_host, dtype=np.int32).reshape(-1)[:num_seqs])
+    if lens.size != num_seqs:
+        raise ValueError(f"seq_lens_host holds {lens.size} lengths, num_seqs is {num_seqs}")
+    words = mj_block_plan_size(slots, max_num_seqs)
+    if plan_out is None:
+        plan_out = np.zeros(words, dtype=np.int32)
+    addr = _host_int32(plan_out, words, "plan_out")
+    _check("mj_block_plan", load_library().mj_block_plan(lens.ctypes.data if num_seqs else None, num_seqs, max_num_seqs,
+                                                         slots, margin, addr, words))
+    return plan_out
+
+
+def mj_block_workspace_size(slots: int, q_len: int, h_q: int, h_k: int, d: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check("mj_block_workspace_size", load_library().mj_block_workspace_size(slots, q_len, h_q, h_k, d, ctypes.byref(n)))
+    return n.value
+
+
+def mj_block_attention(args: mj_block_args, stream=None):
+    """Decode attention over a block-scaled cache (:meth:`BlockStep.args` builds ``args``)."""
+    _on_device(args)
+    _check("mj_block_attention", load_library().mj_block_attention(ctypes.byref(args), _stream(stream)))
+
+
+def mj_block_prompt_splits(sm_count: int, num_seqs: int, max_q_len: int, max_len: int, h_q: int, h_k: int, d: int) -> int:
+    return load_library().mj_block_prompt_splits(sm_count, num_seqs, max_q_len, max_len, h_q, h_k, d)
+
+
+def mj_block_prompt_workspace_size(num_tokens: int, h_q: int, d: int, splits: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check("mj_block_prompt_workspace_size", load_library().mj_block_prompt_workspace_size(num_tokens, h_q, d, splits,
+                                                                                           ctypes.byref(n)))
+    return n.value
+
+
+def mj_block_prompt(args: mj_block_prompt_args, stream=None):
+    """Prompt attention over a block-scaled cache (:meth:`PromptStep.args` builds ``args``)."""
+    _on_device(args)
+    _check("mj_block_prompt", load_library().mj_block_prompt(ctypes.byref(args), _stream(stream)))
+
+
 from .step import DecodeStep, LatentStep, PagedLatent, latent_write_args, rope_write_args  # noqa: E402,F401
+from .block import BlockKV, BlockStep, PromptStep, block_read_args, block_write_args  # noqa: E402,F401

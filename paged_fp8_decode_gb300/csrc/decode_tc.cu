@@ -113,6 +113,16 @@ bool decode_tc_supported(const DecodeParams& p0) {
   return tc_prepare(p, &mk, &mv);
 }
 
+cudaError_t launch_decode_block(DecodeParams p, cudaStream_t stream, bool* unsupported) {
+  *unsupported = false;
+  CUtensorMap mk, mv;
+  if (!tc_prepare(p, &mk, &mv)) {
+    *unsupported = true;
+    return cudaSuccess;
+  }
+  return p.num_work == 0 ? cudaSuccess : launch_tc_block(mk, mv, p, stream);
+}
+
 cudaError_t launch_decode_tc(DecodeParams p, cudaStream_t stream, bool* unsupported) {
   *unsupported = false;
   CUtensorMap mk, mv;

@@ -232,7 +232,16 @@ __host__ __device__ constexpr uint32_t tc_tmem_alloc_cols(int cols) {
 
 // QM, how Q arrives (mj_q_mode): 0 e4m3 codes from mj_quantize_q; 1 bf16 Q
 // as is, represented as two e4m3 terms per value; 2 bf16 Q quantized here
-// with mj_quantize_q's recipe (see the Q staging in the softmax warps).
+// with mj_quantize_q's recipe (see the Q staging in the softmax warps); 3
+// (kQBlock) bf16 Q as two terms over the block-scaled cache:
+//   A key's row of the tile has one scale 2^ek for K and one, 2^ev, for V, and
+//   the thread that owns the key folds them in: its logits are (S_hi + S_lo / 16) c 2^ek,
+//   and the operand of the PV product is 2^(u - m + 8) with u = t + ev, the key's
+//   weight on its V codes; m is the running reference of u, so that the operand
+//   keeps the same range and terms as the others' weights whatever the blocks'
+//   scales. The softmax sum wants 2^t and adds the operand times 2^-ev (both within 32 binades: no
+//   overflow). Each thread loads its key's two exponent bytes one iteration
+//   ahead and the page id they need two ahead, behind the softmax of a tile.
 // D, the head size (128 or 256): a K or V row of D channels is DH = D / 128
 // sub-tiles of 128 bytes; QK accumulates over the sub-tiles and PV runs once
 // per sub-tile into its own O accumulator (channel 128 * dh + lane).
@@ -249,12 +258,14 @@ __global__ void __launch_bounds__(KF != MJ_KV_E4M3 ? kThreadsTcFp6 : kThreadsTc,
   // P columns: term k (A hi, A lo, B hi, B lo) of row r at column k * NR + r
   static_assert(NPV == 4 * NR && NR <= NQK && NR >= 4 && (NR & (NR - 1)) == 0, "row tile");
   constexpr bool PK = KF != MJ_KV_E4M3;  // a packed (narrow) format: no NaN codes, V widened
-  static_assert(QM != 1 || (!PK && 2 * NR <= NQK), "bf16 Q: e4m3 KV, hi and lo rows in the Q tile");
+  constexpr bool BS = QM == kQBlock;   // the block-scaled cache
+  constexpr bool Q2 = QM == 1 || BS;    // Q as two terms
+  static_assert(!Q2 || (!PK && 2 * NR <= NQK), "bf16 Q: e4m3 KV, hi and lo rows in the Q tile");
   static_assert((D == 128 || D == 256) && (!PK || D == 128), "head size (packed formats: 128)");
   // TP tiles per softmax iteration; NSB S and P buffers let QK run up to
   // NSB - 1 tiles ahead of PV, so the softmax of a tile never waits for
   // the QK product of the next.
-  constexpr int TP = (NR <= 8 || (NR == 16 && QM != 1 && !PK)) ? 2 : 1;
+  constexpr int TP = (NR <= 8 || (NR == 16 && !Q2 && !PK)) ? 2 : 1;
   constexpr int NSB = tc_nsb(NR);
   static_assert(NSB >= 2 * TP, "S / P buffers");
   constexpr int NPB = tc_npb(NR);  // P buffers: P_j in buffer j % NPB
@@ -377,11 +388,25 @@ __global__ void __launch_bounds__(KF != MJ_KV_E4M3 ? kThreadsTcFp6 : kThreadsTc,
   const int4 w = reinterpret_cast<const int4*>(p.work)[blockIdx.x / unsigned(p.h_k)];
   const int b = w.x;
   bool active = w.z > w.y && b >= 0 && b < p.num_seqs;
-  if (active && p.with_reduction && (w.w < 0 || w.w >= p.max_splits || b >= p.part_seqs)) {
+  int4 req = make_int4(0, 1, 0, 0);
+  if constexpr (BS) {
+    if (active) {
+      req = p.req[b];
+      const int64_t first = req.x, n = req.y;
+      if (w.w < 0 || w.w >= n || (n > 1 && (first < 0 || first + n > p.part_cap))) {
+        if (threadIdx.x == 0) atomicOr(p.status, kStatusBadPlan);
+        active = false;
+      }
+    }
+  } else if (active && p.with_reduction && (w.w < 0 || w.w >= p.max_splits || b >= p.part_seqs)) {
     if (threadIdx.x == 0) atomicOr(p.status, kStatusBadPlan);
     active = false;
   }
   const int L = active ? p.seq_lens[b] : 0;
+  if constexpr (BS) {
+    // a length past the plan's tiles of the request, seen by its first piece
+    if (active && w.w == 0 && threadIdx.x == 0 && int64_t(L) > int64_t(req.w) * kKvTile) atomicOr(p.status, kStatusBadPlan);
+  }
   const int64_t k0 = int64_t(w.y) * kKvTile;
   const int64_t k1 = min(int64_t(w.z) * kKvTile, int64_t(L));
   const int r0 = blockIdx.y * p.tw;
@@ -425,7 +450,8 @@ __global__ void __launch_bounds__(KF != MJ_KV_E4M3 ? kThreadsTcFp6 : kThreadsTc,
         const int64_t e0 = int64_t(i) * ppt;
         if (batch < 0 || e0 + nvalid > batch + 32) {
           batch = e0;
-          entry = (e0 + lane < npages) ? bt[e0 + lane] : -1;
+          const bool held = e0 + lane < npages && (!BS || first_page + e0 + lane < p.bt_len);
+          entry = held ? bt[e0 + lane] : -1;
         }
         const int pg = __shfl_sync(0xFFFFFFFFu, entry, int(e0 - batch) + (lane & 7));
         if (half == 0 && lane < nvalid && (pg < 0 || int64_t(pg) >= p.num_pages)) atomicOr(p.status, kStatusBadPage);
@@ -667,6 +693,59 @@ __global__ void __launch_bounds__(KF != MJ_KV_E4M3 ? kThreadsTcFp6 : kThreadsTc,
           }
         }
         zero_rows(NR);  // the rows past the tile
+      } else if constexpr (BS) {
+        // bf16 Q as two e4m3 terms of x' = x * 2^(127 - e), e the smallest exponent
+        // byte with max |x'| <= 448 over the tile's finite values: hi = e4m3(x'),
+        // lo = e4m3(16 (x' - hi)). A bf16 value has 8 significant bits, hi takes the
+        // upper four and lo the rest: exact down to |x'| = 2^-6, 2^-14 of the
+        // largest, and within 2^-14 (2^-22 of it) below. A value that is not finite
+        // becomes NaN codes, which reach its own row alone.
+        constexpr int EPT = NR * DH;
+        const int row = (xq * EPT) / D, c0 = (xq * EPT) % D;
+        float xv[EPT];
+#pragma unroll
+        for (int e = 0; e < EPT; ++e) xv[e] = 0.f;
+        if (row < nr) {
+          const int rr = r0 + row, tq = rr / p.h_r, h = g * p.h_r + rr % p.h_r;
+          const uint16_t* src = p.q_bf16 + int64_t(b * p.q_len + tq) * p.q_ts + int64_t(h) * p.q_hs + c0;
+#pragma unroll
+          for (int e = 0; e < EPT; e += 4) {
+            const uint2 u = *reinterpret_cast<const uint2*>(src + e);
+            xv[e] = __uint_as_float(u.x << 16);
+            xv[e + 1] = __uint_as_float(u.x & 0xFFFF0000u);
+            xv[e + 2] = __uint_as_float(u.y << 16);
+            xv[e + 3] = __uint_as_float(u.y & 0xFFFF0000u);
+          }
+        }
+        float am = 0.f;
+#pragma unroll
+        for (int e = 0; e < EPT; ++e) {
+          const float a = fabsf(xv[e]);
+          am = fmaxf(am, a < INFINITY ? a : 0.f);
+        }
+        const int eq = max(1, int((__float_as_uint(block_max(am, 0)) + 0x1FFFFFu) >> 23) - 8);
+        const float inv = __int_as_float((254 - eq) << 23);
+        sc_hi = __int_as_float(eq << 23) * p.qk_scale_log2;
+#pragma unroll
+        for (int e = 0; e < EPT; e += 4) {
+          uint32_t hw = 0u, lw = 0u;
+#pragma unroll
+          for (int j = 0; j < 4; j += 2) {
+            float x0 = xv[e + j] * inv, x1 = xv[e + j + 1] * inv;
+            if (!(fabsf(x0) < INFINITY)) x0 = NAN;
+            if (!(fabsf(x1) < INFINITY)) x1 = NAN;
+            const __nv_fp8x2_storage_t h2 = __nv_cvt_float2_to_fp8x2(make_float2(x0, x1), __NV_SATFINITE, __NV_E4M3);
+            const float2 hv = e4m3x2_to_float2(h2);
+            const __nv_fp8x2_storage_t l2 = __nv_cvt_float2_to_fp8x2(
+                make_float2((x0 - hv.x) * 16.f, (x1 - hv.y) * 16.f), __NV_SATFINITE, __NV_E4M3);
+            hw |= uint32_t(h2) << (8 * j);
+            lw |= uint32_t(l2) << (8 * j);
+          }
+          const int c = c0 + e;
+          *reinterpret_cast<uint32_t*>(smem + q_off(row, c)) = hw;
+          *reinterpret_cast<uint32_t*>(smem + q_off(NR + row, c)) = lw;
+        }
+        zero_rows(2 * NR);  // the rows past the two terms
       } else {
         // bf16 Q as two e4m3 terms: hi = e4m3(x / s_hi) with s_hi = amax/448,
         // lo = e4m3((x - hi*s_hi) / s_lo) with s_lo = (max |residual|)/448.
@@ -739,10 +818,10 @@ __global__ void __launch_bounds__(KF != MJ_KV_E4M3 ? kThreadsTcFp6 : kThreadsTc,
       const int qd = warp & 3;          // TMEM lane quadrant of this warp
       const int x = qd * 32 + lane;     // key of the tile (S) / channel (O)
       const uint32_t lane_off = uint32_t(qd * 32) << 16;
-      const float kd = kv_descale(p.k_descale, p.ds_seq, p.ds_head, b, g);
+      const float kd = BS ? 1.f : kv_descale(p.k_descale, p.ds_seq, p.ds_head, b, g);
       // bf16 Q as two terms: the logits are formed when S is read (scale 1 below)
       const float scale =
-          QM == 1 ? 1.f : (QM == 2 ? sq : p.q_descale[int64_t(b) * p.h_k + g]) * kd * p.qk_scale_log2;
+          Q2 ? 1.f : (QM == 2 ? sq : p.q_descale[int64_t(b) * p.h_k + g]) * kd * p.qk_scale_log2;
       // last visible key of each row (query token t sees keys j <= L - q_len + t)
       int lim[NR];
 #pragma unroll
@@ -773,6 +852,32 @@ __global__ void __launch_bounds__(KF != MJ_KV_E4M3 ? kThreadsTcFp6 : kThreadsTc,
       constexpr int kSmallBudget = 8 / TP;  // iterations whose weights below 1/4 went with pair A alone
       int n_small = 0;
 
+      // block-scaled cache: the page of this thread's key in tile j (-1: none), and the
+      // key's exponent bytes there, K's low (2^0 each where there is no page)
+      auto page_of = [&](int j) {
+        const int64_t key = k0 + int64_t(j) * kKvTile + x;
+        const int64_t e = key >> p.page_shift;
+        return key < k1 && e < p.bt_len ? p.block_table[int64_t(b) * p.bt_stride + e] : -1;
+      };
+      auto exps_of = [&](int j, int page) {
+        if (page < 0 || page >= p.num_pages) return 0x7F7Fu;
+        const int64_t key = k0 + int64_t(j) * kKvTile + x;
+        const int at = int(key & ((1 << p.page_shift) - 1)) >> p.block_shift;
+        return uint32_t(p.k_exp[page * p.ke_sp + g * p.ke_sh + at]) |
+               (uint32_t(p.v_exp[page * p.ve_sp + g * p.ve_sh + at]) << 8);
+      };
+      uint32_t ex[TP];  // of this iteration's tiles, loaded in the one before
+      int pg[TP];       // of the next one's
+      if constexpr (BS) {
+#pragma unroll
+        for (int a = 0; a < TP; ++a) ex[a] = uint32_t(page_of(a));
+#pragma unroll
+        for (int a = 0; a < TP; ++a) {
+          pg[a] = page_of(TP + a);
+          ex[a] = exps_of(a, int(ex[a]));
+        }
+      }
+
       // TP tiles per iteration: with few rows, the two S buffers are processed
       // together (256 keys), so the row-max reduction, the cross-warp exchange
       // and the fences are paid once per pair and the two tiles' arithmetic
@@ -780,6 +885,18 @@ __global__ void __launch_bounds__(KF != MJ_KV_E4M3 ? kThreadsTcFp6 : kThreadsTc,
       for (int i = 0; i < ntiles; i += TP) {
         const int nt = min(TP, ntiles - i);
         float s[TP][NR];  // S columns of the real rows only
+        float ck[TP], ev[TP], inv_v[TP];  // block-scaled: the logits' scale, V's exponent and 2^-ev of this thread's keys
+        if constexpr (BS) {
+#pragma unroll
+          for (int a = 0; a < TP; ++a) {
+            ck[a] = __int_as_float(max(MJ_BLOCK_EXP_MIN, min(MJ_BLOCK_EXP_MAX, int(ex[a] & 0xFFu))) << 23) * sc_hi;
+            const int v = max(MJ_BLOCK_EXP_MIN, min(MJ_BLOCK_EXP_MAX, int(ex[a] >> 8)));
+            ev[a] = float(v - 127);
+            inv_v[a] = __int_as_float((254 - v) << 23);
+            ex[a] = exps_of(i + TP + a, pg[a]);
+            pg[a] = page_of(i + 2 * TP + a);
+          }
+        }
 #pragma unroll
         for (int a = 0; a < TP; ++a) {
           if (a < nt) {
@@ -788,7 +905,7 @@ __global__ void __launch_bounds__(KF != MJ_KV_E4M3 ? kThreadsTcFp6 : kThreadsTc,
         }
         if (!ok) break;
         tc::tc_fence_after();
-        if constexpr (QM != 1) {
+        if constexpr (!Q2) {
 #pragma unroll
           for (int a = 0; a < TP; ++a) {
             if (a < nt) {
@@ -809,7 +926,12 @@ __global__ void __launch_bounds__(KF != MJ_KV_E4M3 ? kThreadsTcFp6 : kThreadsTc,
 #pragma unroll
           for (int a = 0; a < TP; ++a)
 #pragma unroll
-            for (int c = 0; c < NR; ++c) s[a][c] = a < nt ? fmaf(s2[a][NR + c], sc_lo, s2[a][c] * sc_hi) : -INFINITY;
+            for (int c = 0; c < NR; ++c) {
+              if constexpr (BS)
+                s[a][c] = a < nt ? fmaf(fmaf(s2[a][NR + c], 1.f / 16.f, s2[a][c]), ck[a], ev[a]) : -INFINITY;
+              else
+                s[a][c] = a < nt ? fmaf(s2[a][NR + c], sc_lo, s2[a][c] * sc_hi) : -INFINITY;
+            }
         }
 
         int key[TP];
@@ -923,7 +1045,8 @@ __global__ void __launch_bounds__(KF != MJ_KV_E4M3 ? kThreadsTcFp6 : kThreadsTc,
             for (int a = 0; a < TP; ++a)
 #pragma unroll
               for (int r = 0; r < NR; ++r) {
-                const bool vis = valid[a] && key[a] <= lim[r] && m_ref[r] != -INFINITY;
+                // (block-scaled: a row of NaN logits has no reference and stays NaN)
+                const bool vis = valid[a] && key[a] <= lim[r] && (m_ref[r] != -INFINITY || (BS && s[a][r] != s[a][r]));
                 s[a][r] = vis ? fast_exp2(fmaf(s[a][r], scale, c8[r])) : 0.f;
                 pmin = fminf(pmin, vis ? s[a][r] : INFINITY);
               }
@@ -982,8 +1105,13 @@ __global__ void __launch_bounds__(KF != MJ_KV_E4M3 ? kThreadsTcFp6 : kThreadsTc,
               }
               // l sums the weights themselves; O gets them to within
               // max(2^-8 p, 2^-20) each
-              l_part[r] += x0;
-              l_part[r + 1] += x1;
+              if constexpr (BS) {
+                l_part[r] = fmaf(x0, inv_v[a], l_part[r]);
+                l_part[r + 1] = fmaf(x1, inv_v[a], l_part[r + 1]);
+              } else {
+                l_part[r] += x0;
+                l_part[r + 1] += x1;
+              }
             }
             uint8_t* pt = smem + lay.p0 + ((i + a) % NPB) * p_stride;
             constexpr int kBlkA = NR >= 8 ? NPV / 32 : NPV / 16;  // blocks always stored
@@ -1090,19 +1218,20 @@ __global__ void __launch_bounds__(KF != MJ_KV_E4M3 ? kThreadsTcFp6 : kThreadsTc,
       if (lane == 0) tc::mbar_arrive(tc::smem_u32(&ctl.sum_bar));
       ok = ok && tc::mbar_wait(tc::smem_u32(&ctl.sum_bar), 0, abort, kWaitLimitNs);
       if (ok) {
-        const bool direct = !p.with_reduction || p.n_splits[b] <= 1;
-        const float vd = kv_descale(p.v_descale, p.ds_seq, p.ds_head, b, g) * p.v_fmt;
+        const bool direct = BS ? req.y <= 1 : (!p.with_reduction || p.n_splits[b] <= 1);
+        const float vd = BS ? 1.f : kv_descale(p.v_descale, p.ds_seq, p.ds_head, b, g) * p.v_fmt;
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
           if (r >= nr) break;
           const float lr = ctl.lsum[0][r] + ctl.lsum[1][r] + ctl.lsum[2][r] + ctl.lsum[3][r];
+          const bool some = BS ? !(lr == 0.f) : lr > 0.f;  // (block-scaled: a NaN sum is one)
           const int row = r0 + r;
           const int tq = row / p.h_r, h = g * p.h_r + row % p.h_r;
-          const int64_t idx = direct ? 0 : part_index(p, b, w.w, g, row);
+          const int64_t idx = direct ? 0 : (BS ? ((int64_t(req.x) + w.w) * p.h_k + g) * p.n_q + row : part_index(p, b, w.w, g, row));
 #pragma unroll
           for (int dh = 0; dh < DH; ++dh) {
             const int ch = 128 * dh + x;
-            const float on = lr > 0.f ? o_acc[dh][r] / lr : 0.f;
+            const float on = some ? o_acc[dh][r] / lr : 0.f;
             if (direct) {
               float val = on * vd;
               if (p.o_mul) val *= p.o_mul[int64_t(h) * D + ch];
@@ -1115,9 +1244,9 @@ __global__ void __launch_bounds__(KF != MJ_KV_E4M3 ? kThreadsTcFp6 : kThreadsTc,
             if (direct) {
               if (p.lse)
                 p.lse[(int64_t(b) * p.h_k + g) * p.n_q + row] =
-                    lr > 0.f ? (m_ref[r] + fast_log2(lr) - 8.f) * kLn2 : -INFINITY;
+                    some ? (m_ref[r] + fast_log2(lr) - 8.f) * kLn2 : -INFINITY;
             } else {
-              p.m_part[idx] = lr > 0.f ? m_ref[r] : -INFINITY;
+              p.m_part[idx] = some ? (BS ? fmaxf(m_ref[r], -1e30f) : m_ref[r]) : -INFINITY;
               p.l_part[idx] = lr * (1.f / 256.f);
             }
           }
@@ -1217,7 +1346,7 @@ cudaError_t launch_tc(const CUtensorMap& mk, const CUtensorMap& mv, const Decode
 // row (two pairs of e4m3 terms).
 template <int KF, int QM, int D = 128>
 cudaError_t launch_rows(const CUtensorMap& mk, const CUtensorMap& mv, const DecodeParams& p, cudaStream_t stream) {
-  constexpr int K = QM == 1 ? 2 : 1;
+  constexpr int K = QM == 1 || QM == kQBlock ? 2 : 1;
   if (p.tw <= 16) {
     if (p.n_q <= 4) return launch_tc<16, 16, 4, KF, QM, D>(mk, mv, p, stream);
     if (p.n_q <= 8) return launch_tc<16, 32, 8, KF, QM, D>(mk, mv, p, stream);
@@ -1241,5 +1370,6 @@ cudaError_t launch_tc_e4m3_d256(const CUtensorMap& mk, const CUtensorMap& mv, co
 cudaError_t launch_tc_e2m3(const CUtensorMap& mk, const CUtensorMap& mv, const DecodeParams& p, cudaStream_t stream);
 cudaError_t launch_tc_e3m2(const CUtensorMap& mk, const CUtensorMap& mv, const DecodeParams& p, cudaStream_t stream);
 cudaError_t launch_tc_e2m1(const CUtensorMap& mk, const CUtensorMap& mv, const DecodeParams& p, cudaStream_t stream);
+cudaError_t launch_tc_block(const CUtensorMap& mk, const CUtensorMap& mv, const DecodeParams& p, cudaStream_t stream);
 
 }  // namespace mj

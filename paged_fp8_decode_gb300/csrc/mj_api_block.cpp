@@ -1,0 +1,457 @@
+// Host side of the block-scaled cache's calls (include/mj.h): argument checks,
+// the plan, the workspace layouts and the launches. Nothing here allocates,
+// synchronises or reads device memory.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+
+#include "mj_block.h"
+#include "mj_latent.h"
+
+namespace {
+
+using mj::rows_apart;
+
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+int status_of(cudaError_t e) { return e == cudaSuccess ? MJ_OK : MJ_ERR_CUDA; }
+
+bool size_ok(int n) { return n == 16 || n == 32 || n == 64 || n == 128; }
+
+constexpr int kMaxTokens = 1 << 30;
+// A prompt's row tile, and the least keys of a piece worth a CTA of its own.
+constexpr int64_t kPromptRows = 256, kPromptMinKeys = 1024;
+constexpr int64_t kMaxRows = 1 << 20;  // query rows of a request and KV head
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// The cache of a call. written: its rows and exponent bytes must lie apart.
+int check_cache(const mj_block_cache& c, bool written) {
+  if (c.h_k < 1 || c.num_pages < 1) return MJ_ERR_INVALID_ARG;
+  if (!mj::head_dim_ok(c.d) || !size_ok(c.page_size) || !size_ok(c.block)) return MJ_ERR_UNSUPPORTED;
+  if (c.block > c.page_size) return MJ_ERR_INVALID_ARG;
+  if (c.h_k > 65535 || c.num_pages > INT32_MAX) return MJ_ERR_UNSUPPORTED;
+  if (!c.k_cache || !c.v_cache || !c.k_exp || !c.v_exp) return MJ_ERR_INVALID_ARG;
+  const int64_t st[] = {c.k_stride_page, c.k_stride_token, c.k_stride_head, c.v_stride_page, c.v_stride_token, c.v_stride_head};
+  for (int64_t s : st)
+    if (s < 0) return MJ_ERR_INVALID_ARG;
+  if (c.k_exp_stride_page < 0 || c.k_exp_stride_head < 0 || c.v_exp_stride_page < 0 || c.v_exp_stride_head < 0)
+    return MJ_ERR_INVALID_ARG;
+  for (int64_t s : st)
+    if (s % 16) return MJ_ERR_ALIGNMENT;
+  if (!aligned(c.k_cache, 16) || !aligned(c.v_cache, 16)) return MJ_ERR_ALIGNMENT;
+  if (written) {
+    const int64_t blocks = c.page_size / c.block;
+    if (!rows_apart(c.d, {{c.k_stride_page, c.num_pages}, {c.k_stride_token, c.page_size}, {c.k_stride_head, c.h_k}}) ||
+        !rows_apart(c.d, {{c.v_stride_page, c.num_pages}, {c.v_stride_token, c.page_size}, {c.v_stride_head, c.h_k}}) ||
+        !rows_apart(blocks, {{c.k_exp_stride_page, c.num_pages}, {c.k_exp_stride_head, c.h_k}}) ||
+        !rows_apart(blocks, {{c.v_exp_stride_page, c.num_pages}, {c.v_exp_stride_head, c.h_k}}))
+      return MJ_ERR_INVALID_ARG;
+  }
+  return MJ_OK;
+}
+
+// bf16 rows of d channels at element strides: (t, h, c) for T tokens and H heads.
+int check_rows(const void* p, int64_t ts, int64_t hs) {
+  if (!p || ts < 0 || hs < 0) return MJ_ERR_INVALID_ARG;
+  return !aligned(p, 16) || ts % 8 || hs % 8 ? MJ_ERR_ALIGNMENT : MJ_OK;
+}
+
+int check_table(const int32_t* table, int64_t stride, int64_t len) {
+  return !table || stride < 0 || len < 0 ? MJ_ERR_INVALID_ARG : (aligned(table, 4) ? MJ_OK : MJ_ERR_ALIGNMENT);
+}
+
+void sides(const mj_block_cache& c, mj::BlockSide (&s)[2]) {
+  s[0] = {static_cast<uint8_t*>(c.k_cache), c.k_stride_page, c.k_stride_token, c.k_stride_head, c.k_exp, c.k_exp_stride_page,
+          c.k_exp_stride_head};
+  s[1] = {static_cast<uint8_t*>(c.v_cache), c.v_stride_page, c.v_stride_token, c.v_stride_head, c.v_exp, c.v_exp_stride_page,
+          c.v_exp_stride_head};
+}
+
+int64_t work_rows(int slots, int max_num_seqs) { return max_num_seqs < slots ? slots : int64_t(slots) + max_num_seqs; }
+
+// Partial rows (a piece of a split request) that a plan can have: at most 2 a slot.
+int64_t part_cap(int slots) { return 2 * int64_t(slots); }
+
+bool slots_ok(int slots) { return slots >= 1 && slots <= (1 << 20); }
+
+}  // namespace
+
+extern "C" {
+
+int mj_block_write_kv(const mj_block_write_args* a, void* stream) {
+  const mj::NvtxRange range("mj_block_write_kv");
+  if (!a || a->num_tokens < 0) return MJ_ERR_INVALID_ARG;
+  if (a->num_tokens > kMaxTokens) return MJ_ERR_CAPACITY;
+  int st = check_cache(a->cache, true);
+  if (st != MJ_OK || a->num_tokens == 0) return st;
+  st = check_rows(a->key, a->key_tok_stride, a->key_head_stride);
+  if (st == MJ_OK) st = check_rows(a->value, a->value_tok_stride, a->value_head_stride);
+  if (st != MJ_OK) return st;
+  if (!a->slot_mapping) return MJ_ERR_INVALID_ARG;
+  if (!aligned(a->slot_mapping, 8) || !aligned(a->status, 4)) return MJ_ERR_ALIGNMENT;
+  mj::BlockWriteParams p = {};
+  p.num_tokens = a->num_tokens;
+  p.h_k = a->cache.h_k;
+  p.in[0] = static_cast<const uint16_t*>(a->key);
+  p.in[1] = static_cast<const uint16_t*>(a->value);
+  p.ts[0] = a->key_tok_stride;
+  p.hs[0] = a->key_head_stride;
+  p.ts[1] = a->value_tok_stride;
+  p.hs[1] = a->value_head_stride;
+  p.slots = a->slot_mapping;
+  p.num_slots = a->cache.num_pages * a->cache.page_size;
+  p.page_shift = mj::page_shift(a->cache.page_size);
+  p.block_shift = mj::page_shift(a->cache.block);
+  sides(a->cache, p.side);
+  p.status = a->status;
+  return status_of(mj::launch_block_write(p, a->cache.d, static_cast<cudaStream_t>(stream)));
+}
+
+int mj_block_read_kv(const mj_block_read_args* a, void* stream) {
+  const mj::NvtxRange range("mj_block_read_kv");
+  if (!a || a->num_seqs < 0 || a->num_rows < 0) return MJ_ERR_INVALID_ARG;
+  if (a->num_rows > kMaxTokens) return MJ_ERR_CAPACITY;
+  int st = check_cache(a->cache, false);
+  if (st != MJ_OK) return st;
+  if (a->out_dtype != MJ_OUT_BF16 && a->out_dtype != MJ_OUT_F16) return MJ_ERR_UNSUPPORTED;
+  if (a->num_rows == 0 || a->num_seqs == 0) return MJ_OK;
+  if (!a->starts || (!a->k_out && !a->v_out)) return MJ_ERR_INVALID_ARG;
+  st = check_table(a->block_table, a->block_table_stride, a->block_table_len);
+  const mj_block_cache& c = a->cache;
+  if (st == MJ_OK && a->k_out) st = check_rows(a->k_out, a->k_tok_stride, a->k_head_stride);
+  if (st == MJ_OK && a->v_out) st = check_rows(a->v_out, a->v_tok_stride, a->v_head_stride);
+  if (st != MJ_OK) return st;
+  if ((a->k_out && !rows_apart(c.d, {{a->k_tok_stride, a->num_rows}, {a->k_head_stride, c.h_k}})) ||
+      (a->v_out && !rows_apart(c.d, {{a->v_tok_stride, a->num_rows}, {a->v_head_stride, c.h_k}})))
+    return MJ_ERR_INVALID_ARG;
+  if (!aligned(a->starts, 4) || !aligned(a->first, 4) || !aligned(a->status, 4)) return MJ_ERR_ALIGNMENT;
+  mj::BlockReadParams p = {};
+  p.num_seqs = a->num_seqs;
+  p.num_rows = a->num_rows;
+  p.h_k = c.h_k;
+  p.page_shift = mj::page_shift(c.page_size);
+  p.block_shift = mj::page_shift(c.block);
+  p.num_pages = c.num_pages;
+  sides(c, p.side);
+  p.block_table = a->block_table;
+  p.bt_stride = a->block_table_stride;
+  p.bt_len = a->block_table_len;
+  p.starts = a->starts;
+  p.first = a->first;
+  p.out[0] = static_cast<uint16_t*>(a->k_out);
+  p.out[1] = static_cast<uint16_t*>(a->v_out);
+  p.ts[0] = a->k_tok_stride;
+  p.hs[0] = a->k_head_stride;
+  p.ts[1] = a->v_tok_stride;
+  p.hs[1] = a->v_head_stride;
+  p.out_f16 = a->out_dtype == MJ_OUT_F16 ? 1 : 0;
+  p.sides = (a->k_out ? 1 : 0) + (a->v_out ? 1 : 0);
+  p.side0 = a->k_out ? 0 : 1;
+  p.status = a->status;
+  return status_of(mj::launch_block_read(p, c.d, static_cast<cudaStream_t>(stream)));
+}
+
+int mj_block_plan_size(int slots, int max_num_seqs, size_t* words) {
+  if (!words || !slots_ok(slots) || max_num_seqs < 0 || max_num_seqs > (1 << 24)) return MJ_ERR_INVALID_ARG;
+  *words = size_t(4 * (work_rows(slots, max_num_seqs) + max_num_seqs));
+  return MJ_OK;
+}
+
+int mj_block_plan(const int32_t* seq_lens_host, int num_seqs, int max_num_seqs, int slots, int margin, int32_t* plan_host,
+                  size_t plan_words) {
+  const mj::NvtxRange range("mj_block_plan");
+  if (num_seqs < 0 || num_seqs > max_num_seqs || margin < 0 || (num_seqs > 0 && !seq_lens_host) || !plan_host)
+    return MJ_ERR_INVALID_ARG;
+  size_t words = 0;
+  const int st = mj_block_plan_size(slots, max_num_seqs, &words);
+  if (st != MJ_OK) return st;
+  if (plan_words < words) return MJ_ERR_CAPACITY;
+  for (int b = 0; b < num_seqs; ++b)
+    if (seq_lens_host[b] < 0) return MJ_ERR_INVALID_ARG;
+  auto tiles = [&](int b) -> int64_t {
+    return seq_lens_host[b] > 0 ? ceil_div(int64_t(seq_lens_host[b]) + margin, mj::kKvTile) : 0;
+  };
+  int64_t total = 0, longest = 1, live = 0;
+  for (int b = 0; b < num_seqs; ++b) {
+    const int64_t t = tiles(b);
+    total += t;
+    longest = std::max(longest, t);
+    live += t > 0;
+  }
+  // Tiles a piece has at most. With fewer requests than slots: the least with which
+  // all pieces run at once (one wave). With more: a slot's share, so that no piece
+  // outlasts the rest; requests of up to a share stay whole.
+  auto pieces = [&](int64_t c) {
+    int64_t n = 0;
+    for (int b = 0; b < num_seqs; ++b) n += ceil_div(tiles(b), c);
+    return n;
+  };
+  int64_t chunk = std::max<int64_t>(1, ceil_div(total, slots));
+  if (live <= slots) {
+    int64_t lo = chunk, hi = longest;  // pieces(longest) = live
+    while (lo < hi) {
+      const int64_t mid = lo + (hi - lo) / 2;
+      if (pieces(mid) <= slots)
+        hi = mid;
+      else
+        lo = mid + 1;
+    }
+    chunk = std::max(lo, chunk);
+  }
+  const int64_t rows = work_rows(slots, max_num_seqs);
+  int32_t* work = plan_host;
+  int32_t* req = plan_host + 4 * rows;
+  std::memset(plan_host, 0, words * sizeof(int32_t));
+  int64_t part = 0;
+  for (int b = 0; b < num_seqs; ++b) {
+    const int64_t t = tiles(b);
+    const int64_t n = std::max<int64_t>(1, ceil_div(t, chunk)), each = std::max<int64_t>(1, ceil_div(t, n));
+    int32_t* r = req + 4 * int64_t(b);
+    r[0] = int32_t(part);
+    r[1] = int32_t(t > 0 ? ceil_div(t, each) : 0);
+    r[2] = int32_t(each);
+    r[3] = int32_t(t);
+    if (r[1] > 1) part += r[1];
+  }
+  if (part > part_cap(slots)) return MJ_ERR_CAPACITY;  // cannot be: a split request has over one share
+  // the longest pieces first, so that the last to start are short ones
+  struct Row {
+    int32_t b, begin, end, s;
+  };
+  Row* out = reinterpret_cast<Row*>(work);
+  int64_t at = 0;
+  for (int b = 0; b < num_seqs; ++b) {
+    const int32_t* r = req + 4 * int64_t(b);
+    for (int s = 0; s < r[1]; ++s) {
+      if (at >= rows) return MJ_ERR_CAPACITY;  // cannot be: a request has at most one piece that is no full share
+      out[at++] = {b, s * r[2], int32_t(std::min<int64_t>((s + int64_t(1)) * r[2], r[3])), s};
+    }
+  }
+  std::sort(out, out + at, [](const Row& x, const Row& y) {
+    const int32_t lx = x.end - x.begin, ly = y.end - y.begin;
+    return lx != ly ? lx > ly : (x.b != y.b ? x.b < y.b : x.s < y.s);
+  });
+  return MJ_OK;
+}
+
+int mj_block_workspace_size(int slots, int q_len, int h_q, int h_k, int d, size_t* bytes) {
+  if (!bytes || !slots_ok(slots) || q_len < 1 || h_k < 1 || h_q < 1 || h_q % h_k) return MJ_ERR_INVALID_ARG;
+  if (!mj::head_dim_ok(d)) return MJ_ERR_UNSUPPORTED;
+  const int64_t n_q = int64_t(q_len) * (h_q / h_k);
+  if (n_q > kMaxRows || h_k > 65535) return MJ_ERR_INVALID_ARG;
+  *bytes = mj::kWsHeader + size_t(part_cap(slots) * h_k * n_q) * (size_t(d) + 2) * sizeof(float);
+  return MJ_OK;
+}
+
+int mj_block_attention(const mj_block_args* a, void* stream) {
+  const mj::NvtxRange range("mj_block_attention");
+  if (!a) return MJ_ERR_INVALID_ARG;
+  int st = check_cache(a->cache, false);
+  if (st != MJ_OK) return st;
+  const mj_block_cache& c = a->cache;
+  if (a->num_seqs < 0 || a->num_seqs > a->max_num_seqs || a->q_len < 1 || a->h_q < 1 || a->h_q % c.h_k)
+    return MJ_ERR_INVALID_ARG;
+  if (!(a->softmax_scale > 0.f) || !std::isfinite(a->softmax_scale)) return MJ_ERR_INVALID_ARG;
+  if (a->out_dtype != MJ_OUT_BF16 && a->out_dtype != MJ_OUT_F16) return MJ_ERR_UNSUPPORTED;
+  size_t bytes = 0, words = 0;
+  st = mj_block_workspace_size(a->slots, a->q_len, a->h_q, c.h_k, c.d, &bytes);
+  if (st == MJ_OK) st = mj_block_plan_size(a->slots, a->max_num_seqs, &words);
+  if (st == MJ_OK) st = check_rows(a->q, a->q_tok_stride, a->q_head_stride);
+  if (st == MJ_OK) st = check_rows(a->out, a->out_tok_stride, a->out_head_stride);
+  if (st == MJ_OK) st = check_table(a->block_table, a->block_table_stride, a->block_table_len);
+  if (st != MJ_OK) return st;
+  if (!a->seq_lens || !a->plan || !a->workspace) return MJ_ERR_INVALID_ARG;
+  if (!aligned(a->seq_lens, 4) || !aligned(a->plan, 16) || !aligned(a->workspace, 16) || !aligned(a->lse, 4))
+    return MJ_ERR_ALIGNMENT;
+  if (a->workspace_bytes < bytes) return MJ_ERR_CAPACITY;
+  if (!rows_apart(c.d, {{a->out_tok_stride, int64_t(a->num_seqs) * a->q_len}, {a->out_head_stride, a->h_q}}))
+    return MJ_ERR_INVALID_ARG;
+  if (a->num_seqs == 0) return MJ_OK;
+
+  const int h_r = a->h_q / c.h_k, n_q = a->q_len * h_r;
+  mj::DecodeParams p = {};
+  p.num_seqs = a->num_seqs;
+  p.q_len = a->q_len;
+  p.h_q = a->h_q;
+  p.h_k = c.h_k;
+  p.h_r = h_r;
+  p.n_q = n_q;
+  p.d = c.d;
+  p.causal = a->causal ? 1 : 0;
+  p.kv_format = MJ_KV_E4M3;
+  p.page_size = c.page_size;
+  p.row_bytes = c.d;
+  p.num_pages = c.num_pages;
+  p.tw = mj_tile_width(n_q);
+  p.n_row_tiles = int(ceil_div(n_q, p.tw));
+  p.q_mode = mj::kQBlock;
+  p.q_bf16 = static_cast<const uint16_t*>(a->q);
+  p.q_ts = a->q_tok_stride;
+  p.q_hs = a->q_head_stride;
+  p.k_cache = static_cast<const uint8_t*>(c.k_cache);
+  p.v_cache = static_cast<const uint8_t*>(c.v_cache);
+  p.k_sp = c.k_stride_page;
+  p.k_st = c.k_stride_token;
+  p.k_sh = c.k_stride_head;
+  p.v_sp = c.v_stride_page;
+  p.v_st = c.v_stride_token;
+  p.v_sh = c.v_stride_head;
+  p.k_exp = c.k_exp;
+  p.v_exp = c.v_exp;
+  p.ke_sp = c.k_exp_stride_page;
+  p.ke_sh = c.k_exp_stride_head;
+  p.ve_sp = c.v_exp_stride_page;
+  p.ve_sh = c.v_exp_stride_head;
+  p.page_shift = mj::page_shift(c.page_size);
+  p.block_shift = mj::page_shift(c.block);
+  p.block_table = a->block_table;
+  p.bt_stride = a->block_table_stride;
+  p.bt_len = a->block_table_len;
+  p.seq_lens = a->seq_lens;
+  const int64_t rows = work_rows(a->slots, a->max_num_seqs);
+  p.work = a->plan;
+  p.req = reinterpret_cast<const int4*>(a->plan + 4 * rows);
+  p.num_work = int(rows);
+  p.with_reduction = 1;
+  p.part_cap = int(part_cap(a->slots));
+  p.qk_scale_log2 = a->softmax_scale * 1.4426950408889634f;
+  p.v_fmt = 1.f;
+  p.out = static_cast<uint16_t*>(a->out);
+  p.out_f16 = a->out_dtype == MJ_OUT_F16 ? 1 : 0;
+  p.out_ts = a->out_tok_stride;
+  p.out_hs = a->out_head_stride;
+  p.lse = a->lse;
+  char* ws = static_cast<char*>(a->workspace);
+  p.status = reinterpret_cast<uint32_t*>(ws);
+  const int64_t parts = part_cap(a->slots) * c.h_k * n_q;
+  p.o_part = reinterpret_cast<float*>(ws + mj::kWsHeader);
+  p.m_part = p.o_part + parts * c.d;
+  p.l_part = p.m_part + parts;
+  p.evict_first = a->evict_first;
+  bool unsupported = false;
+  cudaError_t e = mj::launch_decode_block(p, static_cast<cudaStream_t>(stream), &unsupported);
+  if (unsupported) return MJ_ERR_UNSUPPORTED;
+  if (e != cudaSuccess) return MJ_ERR_CUDA;
+  mj::BlockJoinParams j = {};
+  j.d = c.d;
+  j.units = int64_t(a->num_seqs) * c.h_k * n_q;
+  j.o_part = p.o_part;
+  j.m_part = p.m_part;
+  j.l_part = p.l_part;
+  j.out = p.out;
+  j.out_f16 = p.out_f16;
+  j.out_ts = p.out_ts;
+  j.out_hs = p.out_hs;
+  j.lse = p.lse;
+  j.plan = p.req;
+  j.seq_lens = p.seq_lens;
+  j.h_k = c.h_k;
+  j.h_r = h_r;
+  j.n_q = n_q;
+  j.q_len = a->q_len;
+  return status_of(mj::launch_block_join(j, static_cast<cudaStream_t>(stream)));
+}
+
+// Pieces of a row tile's keys: as many as give every SM a CTA, none below
+// kPromptMinKeys keys.
+int mj_block_prompt_splits(int sm_count, int num_seqs, int max_q_len, int max_len, int h_q, int h_k, int d) {
+  if (sm_count < 1 || num_seqs < 1 || max_q_len < 1 || max_len < 1 || h_k < 1 || h_q < h_k || h_q % h_k || !mj::head_dim_ok(d))
+    return 1;
+  const int64_t rows = int64_t(max_q_len) * (h_q / h_k);
+  const int64_t ctas = ceil_div(rows, kPromptRows) * h_k * num_seqs;
+  const int64_t by_keys = std::max<int64_t>(1, max_len / kPromptMinKeys);
+  return int(std::min<int64_t>({MJ_BLOCK_MAX_SPLITS, by_keys, std::max<int64_t>(1, sm_count / ctas)}));
+}
+
+int mj_block_prompt_workspace_size(int num_tokens, int h_q, int d, int splits, size_t* bytes) {
+  if (!bytes || num_tokens < 0 || h_q < 1 || splits < 1 || splits > MJ_BLOCK_MAX_SPLITS) return MJ_ERR_INVALID_ARG;
+  if (!mj::head_dim_ok(d)) return MJ_ERR_UNSUPPORTED;
+  if (int64_t(num_tokens) * h_q > (int64_t(1) << 31)) return MJ_ERR_INVALID_ARG;
+  *bytes = mj::kWsHeader + (splits > 1 ? size_t(splits) * num_tokens * h_q * (size_t(d) + 2) * sizeof(float) : 0);
+  return MJ_OK;
+}
+
+int mj_block_prompt(const mj_block_prompt_args* a, void* stream) {
+  const mj::NvtxRange range("mj_block_prompt");
+  if (!a) return MJ_ERR_INVALID_ARG;
+  int st = check_cache(a->cache, false);
+  if (st != MJ_OK) return st;
+  const mj_block_cache& c = a->cache;
+  if (a->num_seqs < 0 || a->num_tokens < 0 || a->max_q_len < 0 || a->h_q < 1 || a->h_q % c.h_k) return MJ_ERR_INVALID_ARG;
+  if (!(a->softmax_scale > 0.f) || !std::isfinite(a->softmax_scale)) return MJ_ERR_INVALID_ARG;
+  if (a->out_dtype != MJ_OUT_BF16 && a->out_dtype != MJ_OUT_F16) return MJ_ERR_UNSUPPORTED;
+  size_t bytes = 0;
+  st = mj_block_prompt_workspace_size(a->num_tokens, a->h_q, c.d, a->splits, &bytes);
+  if (st != MJ_OK) return st;
+  const int h_r = a->h_q / c.h_k;
+  if (a->num_seqs > 65535 || int64_t(c.h_k) * a->splits > 65535) return MJ_ERR_UNSUPPORTED;
+  if (a->num_seqs == 0 || a->num_tokens == 0 || a->max_q_len == 0) return MJ_OK;
+  st = check_rows(a->q, a->q_tok_stride, a->q_head_stride);
+  if (st == MJ_OK) st = check_rows(a->out, a->out_tok_stride, a->out_head_stride);
+  if (st == MJ_OK) st = check_table(a->block_table, a->block_table_stride, a->block_table_len);
+  if (st != MJ_OK) return st;
+  if (!a->seq_lens || !a->q_starts || !a->workspace) return MJ_ERR_INVALID_ARG;
+  if (!aligned(a->seq_lens, 4) || !aligned(a->q_starts, 4) || !aligned(a->workspace, 16) || !aligned(a->lse, 4))
+    return MJ_ERR_ALIGNMENT;
+  if (a->workspace_bytes < bytes) return MJ_ERR_CAPACITY;
+  if (!rows_apart(c.d, {{a->out_tok_stride, a->num_tokens}, {a->out_head_stride, a->h_q}})) return MJ_ERR_INVALID_ARG;
+
+  mj::BlockPromptParams p = {};
+  p.num_seqs = a->num_seqs;
+  p.num_tokens = a->num_tokens;
+  p.max_q_len = std::min(a->max_q_len, a->num_tokens);
+  p.splits = a->splits;
+  p.h_q = a->h_q;
+  p.h_k = c.h_k;
+  p.h_r = h_r;
+  p.d = c.d;
+  p.causal = a->causal ? 1 : 0;
+  p.scale_log2 = a->softmax_scale * 1.4426950408889634f;
+  p.q = static_cast<const uint16_t*>(a->q);
+  p.q_ts = a->q_tok_stride;
+  p.q_hs = a->q_head_stride;
+  p.q_starts = a->q_starts;
+  p.page_shift = mj::page_shift(c.page_size);
+  p.block_shift = mj::page_shift(c.block);
+  p.num_pages = c.num_pages;
+  sides(c, p.side);
+  p.block_table = a->block_table;
+  p.bt_stride = a->block_table_stride;
+  p.bt_len = a->block_table_len;
+  p.seq_lens = a->seq_lens;
+  p.out = static_cast<uint16_t*>(a->out);
+  p.out_f16 = a->out_dtype == MJ_OUT_F16 ? 1 : 0;
+  p.out_ts = a->out_tok_stride;
+  p.out_hs = a->out_head_stride;
+  p.lse = a->lse;
+  char* ws = static_cast<char*>(a->workspace);
+  p.status = reinterpret_cast<uint32_t*>(ws);
+  const int64_t parts = int64_t(a->splits) * a->num_tokens * a->h_q;
+  p.o_part = reinterpret_cast<float*>(ws + mj::kWsHeader);
+  p.m_part = p.o_part + parts * c.d;
+  p.l_part = p.m_part + parts;
+  cudaError_t e = mj::launch_block_prompt(p, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess || a->splits == 1) return status_of(e);
+  mj::BlockJoinParams j = {};
+  j.d = c.d;
+  j.units = int64_t(a->num_tokens) * a->h_q;
+  j.o_part = p.o_part;
+  j.m_part = p.m_part;
+  j.l_part = p.l_part;
+  j.out = p.out;
+  j.out_f16 = p.out_f16;
+  j.out_ts = p.out_ts;
+  j.out_hs = p.out_hs;
+  j.lse = p.lse;
+  j.pieces = a->splits;
+  j.h_q = a->h_q;
+  j.q_starts = p.q_starts;
+  j.num_seqs = a->num_seqs;
+  return status_of(mj::launch_block_join(j, static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"

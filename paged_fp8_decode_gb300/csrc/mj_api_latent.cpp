@@ -13,6 +13,8 @@
 
 namespace {
 
+using mj::rows_apart;
+
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 int status_of(cudaError_t e) { return e == cudaSuccess ? MJ_OK : MJ_ERR_CUDA; }
@@ -35,23 +37,6 @@ constexpr int kMaxTokens = 1 << 30;
 constexpr int64_t kMaxRows = 1 << 20;
 
 int latent_row_tile(int64_t n_q) { return n_q <= 16 ? 16 : (n_q <= 32 ? 32 : 64); }
-
-// Rows of `row` units at two or three strides, as many of each as its count:
-// whether they lie apart, the steps of each stride inside one of the next larger.
-struct Dim {
-  int64_t stride, count;
-};
-template <int N>
-bool rows_apart(int64_t row, Dim (&&d)[N]) {
-  std::sort(d, d + N, [](const Dim& a, const Dim& b) { return a.stride < b.stride; });
-  __int128 extent = row;
-  for (const Dim& k : d) {
-    if (k.count <= 1) continue;
-    if (k.stride < extent) return false;
-    extent += static_cast<__int128>(k.stride) * (k.count - 1);
-  }
-  return true;
-}
 
 int check_rope(const mj_rope& r, int d) {
   if (r.num_axes < 1 || r.num_axes > 4 || r.axis_stride < 0) return MJ_ERR_INVALID_ARG;

@@ -6,6 +6,8 @@
 #include <nvtx3/nvToolsExt.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "../../include/mj.h"
 
 namespace mj {
@@ -40,6 +42,23 @@ __host__ __device__ constexpr int kv_row_bytes(int kv_format, int d) {
 
 inline bool kv_format_ok(int f) { return f >= MJ_KV_E4M3 && f <= MJ_KV_E2M1; }
 
+// Rows of `row` units at two or three strides, as many of each as its count:
+// whether they lie apart, the steps of each stride inside one of the next larger.
+struct Dim {
+  int64_t stride, count;
+};
+template <int N>
+inline bool rows_apart(int64_t row, Dim (&&d)[N]) {
+  std::sort(d, d + N, [](const Dim& a, const Dim& b) { return a.stride < b.stride; });
+  __int128 extent = row;
+  for (const Dim& k : d) {
+    if (k.count <= 1) continue;
+    if (k.stride < extent) return false;
+    extent += static_cast<__int128>(k.stride) * (k.count - 1);
+  }
+  return true;
+}
+
 // Workspace layout: a 256-byte header (status word at offset 0), then the
 // split partials o_part [rows][d], m_part [rows], l_part [rows].
 constexpr size_t kWsHeader = 256;
@@ -48,6 +67,10 @@ constexpr size_t kWsHeader = 256;
 constexpr uint32_t kStatusBadPage = 1u;
 constexpr uint32_t kStatusTimeout = 2u;
 constexpr uint32_t kStatusBadPlan = 4u;
+
+// q_mode of the block-scaled cache's decode: bf16 Q as two e4m3 terms, scaled by
+// a power of two; beside the public modes of mj_q_mode.
+constexpr int kQBlock = 3;
 
 // Everything a decode / merge launch needs, by value (kernel parameter).
 struct DecodeParams {
@@ -94,6 +117,16 @@ struct DecodeParams {
   float* m_part;
   float* l_part;
 
+  // block-scaled cache (q_mode kQBlock): exponent bytes of K and V, the plan's
+  // requests (in place of n_splits) and the partial rows that the workspace holds
+  const uint8_t* k_exp;
+  const uint8_t* v_exp;
+  int64_t ke_sp, ke_sh, ve_sp, ve_sh;
+  int page_shift, block_shift;
+  int64_t bt_len;
+  const int4* req;  // [num_seqs]: first partial, pieces, tiles a piece, tiles planned
+  int part_cap;
+
   int kv_stages;
   int evict_first;
   int tma_head_inner;  // tensor-core kernel: head dimension is the TMA's dim 1
@@ -125,6 +158,8 @@ cudaError_t launch_write_kv(const mj_write_kv_args& a, cudaStream_t stream);
 // Tensor-core kernel; sets *unsupported (and launches nothing) when the
 // arguments are outside its envelope.
 cudaError_t launch_decode_tc(DecodeParams p, cudaStream_t stream, bool* unsupported);
+// The same for the block-scaled cache (q_mode kQBlock; one launch, without the join).
+cudaError_t launch_decode_block(DecodeParams p, cudaStream_t stream, bool* unsupported);
 // Whether the tensor-core kernel takes these arguments (launches nothing).
 bool decode_tc_supported(const DecodeParams& p);
 
