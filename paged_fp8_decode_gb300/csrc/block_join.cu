@@ -49,6 +49,7 @@ __global__ void __launch_bounds__(32 * kWarps) block_join_kernel(BlockJoinParams
   } else {
     const int64_t t = unit / p.h_q;
     if (t >= p.q_starts[p.num_seqs]) return;
+    if (__ldcg(p.l_part + unit) < 0.f) return;  // not computed
     n = p.pieces;
     step = p.units;
     first = unit;

@@ -1,150 +1,703 @@
-// mj_block_prompt: attention of ragged prompt chunks over the block-scaled cache.
+// mj_block_prompt: attention of ragged prompt chunks over the block-scaled cache, on
+// the tensor cores.
 //
-// A CTA takes 32 query rows (tokens x heads of one KV head) of one request and
-// one piece of their keys, 32 keys at a time: codes to float32 in shared memory,
-// a lane to a key for the scores, a lane to channels for the output, one pass
-// with the running maximum and sum of each row.
+// A CTA takes the query rows (tokens x the heads of one KV head) of one or two
+// 128-row tiles of a request and walks their keys once, BN at a time:
+//   S = Q K^T     kind::f8f6f4, Q as two e4m3 terms (hi + lo, exact for bf16 down to 2^-10
+//                 of the row's largest), K as it lies in the cache: 128-byte swizzled by TMA
+//   P = 2^(u - m + 6) in fp16, u = t + ev: the weight on V's codes, t = S ck 2^ek, where
+//                 2^ek and 2^ev are the scales of the key's block
+//   O += P V      kind::f16, P from tensor memory (in place of S), V's codes widened to fp16
+//                 (exact) by warps of their own
+// so both products run at the 16-bit rate, and a block's scales cost an addition
+// and a product per 16 keys and row. m is the row's running reference of u: it moves
+// only where a tile's largest u is more than 8 above it (P stays below 2^14 + 1), and
+// O, kept in tensor memory, is rescaled then. Weights keep 11 bits down to 20 binades
+// below the reference, and lose less than 2^-31 of it each below. The sum l wants 2^t: P's float32 times 2^-ev.
+//
+// Head size 128: two row tiles (256 rows) and 128 keys a step; while one tile's softmax
+// runs, the tensor cores work on the other's products. Head size 256: tensor memory
+// holds one row tile's O; 64 keys a step, two S buffers, so that the next scores
+// are ready when a softmax ends. What bounds it is the 16-bit tensor rate.
+//
+// Warps: 0-3 and 4-7 softmax of the row tiles (a thread a row), 8-11 widen V (4-11 at head size 256),
+// 12 TMA, 13 MMA, 14 the blocks' scales. Every wait is bounded (2 s): a timeout sets a status
+// bit, and the CTA drains its copies and products, frees its tensor memory and returns.
+#include <atomic>
+
+#include "latent_ptx.cuh"
 #include "mj_block.h"
 #include "mj_device.cuh"
-#include "tc_ptx.cuh"
 
 namespace mj {
 
 namespace {
 
-constexpr int kRowsWarp = 8, kWarps = 4, kRows = kRowsWarp * kWarps, kKeys = 32;
+constexpr int kThreads = 512;
+constexpr uint64_t kWaitNs = 2000000000ull, kDrainNs = 100000000ull;
+constexpr float kTau = 8.f, kLift = 6.f;  // log2 units
+constexpr int kKStages = 3;
+constexpr int kTile = 16384;              // bytes: 128 rows of 128, and a K or V tile
 
 template <int D>
-__global__ void __launch_bounds__(32 * kWarps) block_prompt_kernel(BlockPromptParams p) {
-  extern __shared__ float sm[];
-  float* qs = sm;                       // [kRows][D]
-  float* ks = qs + kRows * D;           // [kKeys][D + 1]
-  float* vs = ks + kKeys * (D + 1);     // [kKeys][D]
-  constexpr int C = D / 32;
-  tc::grid_dependency_wait();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int piece = int(blockIdx.y) % p.splits, g = int(blockIdx.y) / p.splits, b = blockIdx.z;
-  const int t0 = max(0, p.q_starts[b]), n = min(p.q_starts[b + 1], p.num_tokens) - t0;
-  const int L = p.seq_lens[b];
-  const int r0 = int(blockIdx.x) * kRows;
-  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0 && n > p.max_q_len) atomicOr(p.status, kStatusBadPlan);
-  const int rows = min(n, p.max_q_len) * p.h_r;
-  if (r0 >= rows) return;
-  const int nr = min(kRows, rows - r0);
-  const int last = p.causal ? L - n + (r0 + nr - 1) / p.h_r : L - 1;  // the last key that any row sees
-  const int tiles = max(0, min(last + 1, L) + kKeys - 1) / kKeys;
-  const int each = (tiles + p.splits - 1) / p.splits;
-  const int k0 = piece * each * kKeys, k1 = min(min(L, max(0, last + 1)), (piece + 1) * each * kKeys);
+struct Cfg {
+  static constexpr int NT = D == 128 ? 2 : 1;   // row tiles
+  static constexpr int BN = D == 128 ? 128 : 64;
+  static constexpr int DH = D / 128;
+  static constexpr int NB = BN / 16;            // 16-key groups of a tile
+  static constexpr int TB = 32 / NB;            // tiles a batch of scales covers
+  static constexpr int kConvWarp0 = 4 * NT, kConvWarps = 12 - kConvWarp0;
+  static constexpr int kRows = 128 * NT;
+  static constexpr uint32_t kO = 256;           // O's first column; S (and P) buffers from 0, BN columns each
+  static constexpr int kQ = NT * 2 * DH * kTile;
+  static constexpr int kK = kQ, kVr = kK + kKStages * kTile, kVf = kVr + 2 * kTile, kCtrl = kVf + 4 * kTile;
+  static constexpr int kBytes = kCtrl + 2048;
+};
+static_assert(Cfg<128>::kBytes == Cfg<256>::kBytes && Cfg<128>::kBytes + 1024 <= 227 * 1024, "shared memory");
 
-  for (int i = threadIdx.x; i < kRows * D; i += 32 * kWarps) {
-    const int r = i / D, row = r0 + r;
-    float v = 0.f;
-    if (r < nr)
-      v = bf16_bits_to_float(p.q[(t0 + int64_t(row / p.h_r)) * p.q_ts + (int64_t(g) * p.h_r + row % p.h_r) * p.q_hs + i % D]);
-    qs[i] = v;
-  }
-  float m[kRowsWarp], l[kRowsWarp], acc[kRowsWarp][C];
-#pragma unroll
-  for (int r = 0; r < kRowsWarp; ++r) {
-    m[r] = -INFINITY;
-    l[r] = 0.f;
-#pragma unroll
-    for (int c = 0; c < C; ++c) acc[r][c] = 0.f;
-  }
-  for (int j0 = k0; j0 < k1; j0 += kKeys) {
-    __syncthreads();
-    for (int i = threadIdx.x; i < kKeys * (D / 4); i += 32 * kWarps) {
-      const int k = i / (D / 4), c = i % (D / 4) * 4;
-      float kf[4] = {0.f, 0.f, 0.f, 0.f}, vf[4] = {0.f, 0.f, 0.f, 0.f};
-      if (j0 + k < k1) {
-        const int64_t e = int64_t(j0 + k) >> p.page_shift;
-        const int pg = e < p.bt_len ? p.block_table[b * p.bt_stride + e] : -1;
-        const int row = (j0 + k) & ((1 << p.page_shift) - 1);
-        if (pg >= 0 && pg < p.num_pages) {
-          const BlockSide &K = p.side[0], &V = p.side[1];
-          e4m3x4_to_float(*reinterpret_cast<const uint32_t*>(K.codes + pg * K.sp + row * K.st + g * K.sh + c), kf);
-          e4m3x4_to_float(*reinterpret_cast<const uint32_t*>(V.codes + pg * V.sp + row * V.st + g * V.sh + c), vf);
-          const float kx = __int_as_float(block_exp(K.exps[pg * K.esp + g * K.esh + (row >> p.block_shift)]) << 23);
-          const float vx = __int_as_float(block_exp(V.exps[pg * V.esp + g * V.esh + (row >> p.block_shift)]) << 23);
-          for (int u = 0; u < 4; ++u) kf[u] *= kx, vf[u] *= vx;
-        } else if (c == 0) {
-          atomicOr(p.status, kStatusBadPage);
-        }
-      }
-      for (int u = 0; u < 4; ++u) ks[k * (D + 1) + c + u] = kf[u], vs[k * D + c + u] = vf[u];
-    }
-    __syncthreads();
-    float s[kRowsWarp] = {};
-    const float* q = qs + warp * kRowsWarp * D;
-    for (int c = 0; c < D; ++c) {
-      const float k = ks[lane * (D + 1) + c];
-#pragma unroll
-      for (int r = 0; r < kRowsWarp; ++r) s[r] = fmaf(q[r * D + c], k, s[r]);
-    }
-#pragma unroll
-    for (int r = 0; r < kRowsWarp; ++r) {
-      const int row = r0 + warp * kRowsWarp + r, j = j0 + lane;
-      const bool see = j < k1 && (!p.causal || j <= L - n + row / p.h_r);
-      const float t = see ? s[r] * p.scale_log2 : -INFINITY;
-      const float top = fmaxf(m[r], warp_max(t));
-      const float by = m[r] == -INFINITY ? 0.f : exp2f(m[r] - top);
-      s[r] = see ? exp2f(t - top) : 0.f;
-      l[r] = l[r] * by + warp_sum(s[r]);
-      m[r] = top;
-#pragma unroll
-      for (int c = 0; c < C; ++c) acc[r][c] *= by;
-    }
-    for (int k = 0; k < kKeys; ++k) {
-      float v[C];
-#pragma unroll
-      for (int c = 0; c < C; ++c) v[c] = vs[k * D + lane + 32 * c];
-#pragma unroll
-      for (int r = 0; r < kRowsWarp; ++r) {
-        const float w = __shfl_sync(~0u, s[r], k);
-#pragma unroll
-        for (int c = 0; c < C; ++c) acc[r][c] = fmaf(w, v[c], acc[r][c]);
-      }
-    }
-  }
-#pragma unroll
-  for (int r = 0; r < kRowsWarp; ++r) {
-    const int row = r0 + warp * kRowsWarp + r;
-    if (row >= rows) break;
-    const int64_t t = t0 + int64_t(row / p.h_r), h = int64_t(g) * p.h_r + row % p.h_r;
-    const int64_t part = (int64_t(piece) * p.num_tokens + t) * p.h_q + h;
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const float o = l[r] == 0.f ? 0.f : acc[r][c] / l[r];
-      if (p.splits > 1)
-        p.o_part[part * D + lane + 32 * c] = o;
-      else
-        p.out[t * p.out_ts + h * p.out_hs + lane + 32 * c] = float_to_out_bits(o, p.out_f16);
-    }
-    if (lane == 0) {
-      if (p.splits > 1) {
-        p.m_part[part] = m[r];
-        p.l_part[part] = l[r];
-      } else if (p.lse) {
-        p.lse[t * p.h_q + h] = l[r] == 0.f ? -INFINITY : (m[r] + log2f(l[r])) * kLn2;
-      }
-    }
-  }
+struct Ctrl {
+  uint64_t k_full[kKStages], k_empty[kKStages];
+  uint64_t vr_full[2], vr_empty[2], vf_full[2], vf_empty[2];
+  uint64_t s_full[2], p_full[2], o_done[2];
+  uint64_t e_full[2], e_empty[2];
+  uint64_t q_ready, drain;
+  uint32_t tmem;
+  int abort;
+  alignas(16) float4 scale[2][32];  // batches of TB tiles: 2^ek, ev, 2^-ev of each 16-key group
+};
+static_assert(sizeof(Ctrl) <= 2048, "control block");
+
+// D[tmem] (+)= A[tmem] B[smem desc], fp16 operands; called by a converged warp (one elected lane issues).
+__device__ __forceinline__ void umma_f16_ts_warp(uint32_t d, uint32_t a, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Instruction descriptor of kind::f16 with fp16 A (K-major) and B (MN-major), f32 accumulator.
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N) {
+  return (1u << 4) | (1u << 16) | (uint32_t(N >> 3) << 17) | (uint32_t(M >> 4) << 24);
+}
+
+__device__ __forceinline__ void tmem_ld32(uint32_t at, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(at));
+}
+
+// Wait for the thread's TMEM loads; the values pass through, so that nothing uses them earlier.
+__device__ __forceinline__ void tmem_wait_ld32(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+                 "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]),
+                 "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]),
+                 "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory");
+}
+
+__device__ __forceinline__ void tmem_st32(uint32_t at, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(at),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]),
+      "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
+      "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_st16u(uint32_t at, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15, %16};" ::"r"(at),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
+// two float32 at once: a * b + c
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+      "fma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tadd.rn.f32x2 w, x, y;\n\t"
+      "mov.b64 {%0, %1}, w;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+// lo and hi to fp16, packed
+__device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// two e4m3 codes to fp16, exactly
+__device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t two) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 x, y;\n\tmov.b32 {x, y}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, x;\n\t}" : "=r"(r) : "r"(two));
+  return r;
 }
 
 template <int D>
-cudaError_t launch(const BlockPromptParams& p, cudaStream_t stream) {
-  constexpr int bytes = (kRows * D + kKeys * (2 * D + 1)) * 4;
-  cudaError_t e = cudaFuncSetAttribute(block_prompt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+__global__ void __launch_bounds__(kThreads, 1)
+    block_prompt_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
+                        BlockPromptParams p) {
+  using C = Cfg<D>;
+  constexpr int NT = C::NT, BN = C::BN, DH = C::DH, NB = C::NB, TB = C::TB;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  Ctrl& ctl = *reinterpret_cast<Ctrl*>(smem + C::kCtrl);
+  const uint32_t base = tc::smem_u32(smem);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  auto bar = [](uint64_t& b) { return tc::smem_u32(&b); };
+
+  tc::grid_dependency_wait();
+  // The CTA's rows. blockIdx: (KV head and piece, row tiles from the last one on: with a causal
+  // limit the longest, request)
+  const int piece = int(blockIdx.x) % p.splits, g = int(blockIdx.x) / p.splits, b = blockIdx.z;
+  const int t0 = max(0, p.q_starts[b]), n = min(p.q_starts[b + 1], p.num_tokens) - t0;
+  const int rows = min(n, p.max_q_len) * p.h_r;
+  const int n_tiles_rows = (rows + C::kRows - 1) / C::kRows;
+  if (n > p.max_q_len && blockIdx.x == 0 && blockIdx.y == 0) {
+    if (tid == 0) atomicOr(p.status, kStatusBadPlan);
+    if (p.splits > 1)  // the join passes these rows by
+      for (int64_t i = tid; i < int64_t(n - p.max_q_len) * p.h_q; i += kThreads)
+        p.l_part[(int64_t(t0) + p.max_q_len) * p.h_q + i] = -1.f;
+  }
+  if (int(blockIdx.y) >= n_tiles_rows) return;
+  const int r0 = (n_tiles_rows - 1 - int(blockIdx.y)) * C::kRows;
+  const int nr = min(C::kRows, rows - r0);
+  const int L = p.seq_lens[b];
+  // the last key that any of the rows sees, and this piece of the tiles up to there
+  const int last = min(L - 1, p.causal ? L - n + (r0 + nr - 1) / p.h_r : L - 1);
+  const int tiles = last >= 0 ? last / BN + 1 : 0;
+  const int each = (tiles + p.splits - 1) / p.splits;
+  const int first_tile = min(tiles, piece * each);
+  const int nt = min(tiles, first_tile + each) - first_tile;
+  const int k0 = first_tile * BN;
+  const int k_end = min(L, (first_tile + nt) * BN);  // keys from here on are not this CTA's
+
+  if (tid == 0) {
+    for (int s = 0; s < kKStages; ++s) {
+      tc::mbar_init(bar(ctl.k_full[s]), 1);
+      tc::mbar_init(bar(ctl.k_empty[s]), 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      tc::mbar_init(bar(ctl.vr_full[s]), 1);
+      tc::mbar_init(bar(ctl.vr_empty[s]), 32 * C::kConvWarps);
+      tc::mbar_init(bar(ctl.vf_full[s]), 32 * C::kConvWarps);
+      tc::mbar_init(bar(ctl.vf_empty[s]), 1);
+      tc::mbar_init(bar(ctl.s_full[s]), 1);
+      tc::mbar_init(bar(ctl.p_full[s]), 128);
+      tc::mbar_init(bar(ctl.o_done[s]), 1);
+      tc::mbar_init(bar(ctl.e_full[s]), 1);
+      tc::mbar_init(bar(ctl.e_empty[s]), 4 * NT);
+    }
+    tc::mbar_init(bar(ctl.q_ready), 128 * NT);
+    tc::mbar_init(bar(ctl.drain), 1);
+    ctl.abort = 0;
+    tc::fence_mbar_init();
+  }
+  if (warp == 12 && lane == 0) {
+    tc::prefetch_tmap(&tmap_k);
+    tc::prefetch_tmap(&tmap_v);
+  }
+  if (warp == 13) {
+    tc::tmem_alloc(tc::smem_u32(&ctl.tmem), 512);
+    tc::tmem_relinquish();
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tmem = ctl.tmem;
+  volatile int* abort = &ctl.abort;
+
+  if (warp < 4 * NT) {
+    // ======================= softmax: thread = row ============================
+    const int a = warp >> 2, quad = warp & 3;
+    const int R = r0 + 128 * a + 32 * quad + lane;
+    const bool real = R < rows;
+    const int64_t tok = t0 + int64_t(real ? R / p.h_r : 0), head = int64_t(g) * p.h_r + (real ? R % p.h_r : 0);
+    const uint32_t lanes = uint32_t(32 * quad) << 16;
+    float ck;  // logits (log2 units) = S * ck * 2^ek
+    {
+      // Q row: x' = x * 2^(127 - e), the largest finite |x'| in (224, 448]; hi = e4m3(x'), lo = e4m3(x' - hi)
+      const uint4* src = reinterpret_cast<const uint4*>(p.q + tok * p.q_ts + head * p.q_hs);
+      uint32_t am = 0;
+      if (real) {
+#pragma unroll 8
+        for (int c = 0; c < D / 8; ++c) {
+          const uint4 v = __ldcg(src + c);
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t lo = w[k] & 0x7FFFu, hi = (w[k] >> 16) & 0x7FFFu;
+            am = max(am, max(lo < 0x7F80u ? lo : 0u, hi < 0x7F80u ? hi : 0u));
+          }
+        }
+      }
+      // (e not below 64: ck 2^ek stays above 0, and a hidden key's -inf times it -inf)
+      const int e = max(64, int(((am << 16) + 0x1FFFFFu) >> 23) - 8);
+      const float inv = __int_as_float((254 - e) << 23);
+      ck = __int_as_float(e << 23) * p.scale_log2;
+      const int r = 32 * quad + lane;
+#pragma unroll 2
+      for (int c = 0; c < D / 16; ++c) {
+        uint4 v[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
+        if (real) {
+          v[0] = __ldcg(src + 2 * c);
+          v[1] = __ldcg(src + 2 * c + 1);
+        }
+        uint32_t hw[4], lw[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint4 u = v[k >> 1];
+          const uint32_t w0 = (k & 1) ? u.z : u.x, w1 = (k & 1) ? u.w : u.y;
+          float x[4] = {__uint_as_float(w0 << 16) * inv, __uint_as_float(w0 & 0xFFFF0000u) * inv,
+                        __uint_as_float(w1 << 16) * inv, __uint_as_float(w1 & 0xFFFF0000u) * inv};
+          hw[k] = lw[k] = 0u;
+#pragma unroll
+          for (int j = 0; j < 4; j += 2) {
+            if (!(fabsf(x[j]) < INFINITY)) x[j] = NAN;
+            if (!(fabsf(x[j + 1]) < INFINITY)) x[j + 1] = NAN;
+            const __nv_fp8x2_storage_t h2 = __nv_cvt_float2_to_fp8x2(make_float2(x[j], x[j + 1]), __NV_SATFINITE, __NV_E4M3);
+            const float2 hv = e4m3x2_to_float2(h2);
+            const __nv_fp8x2_storage_t l2 =
+                __nv_cvt_float2_to_fp8x2(make_float2(x[j] - hv.x, x[j + 1] - hv.y), __NV_SATFINITE, __NV_E4M3);
+            hw[k] |= uint32_t(h2) << (8 * j);
+            lw[k] |= uint32_t(l2) << (8 * j);
+          }
+        }
+        const int dh = c >> 3;
+        uint8_t* at = smem + (a * 2 * DH + dh) * kTile + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+        *reinterpret_cast<uint4*>(at) = make_uint4(hw[0], hw[1], hw[2], hw[3]);
+        *reinterpret_cast<uint4*>(at + DH * kTile) = make_uint4(lw[0], lw[1], lw[2], lw[3]);
+      }
+      tc::fence_async_smem();
+      tc::mbar_arrive(bar(ctl.q_ready));
+    }
+    // the last key this row sees
+    const int lim = real ? min(k_end - 1, p.causal ? L - n + R / p.h_r : k_end - 1) : -1;
+    float m = -INFINITY, l = 0.f;
+    bool ok = true;
+    for (int i = 0; i < nt; ++i) {
+      const int buf = NT == 2 ? a : (i & 1);
+      const uint32_t tS = tmem + lanes + uint32_t(buf * BN);
+      const int bat = i / TB;
+      if (i % TB == 0) ok = tc::mbar_wait(bar(ctl.e_full[bat & 1]), uint32_t(bat >> 1) & 1u, abort, kWaitNs);
+      ok = ok && tc::mbar_wait(bar(ctl.s_full[buf]), uint32_t(NT == 2 ? i : i >> 1) & 1u, abort, kWaitNs);
+      ok = __all_sync(~0u, ok);
+      if (!ok) break;
+      tc::tc_fence_after();
+      const float4* sc = &ctl.scale[bat & 1][(i % TB) * NB];
+      const int key0 = k0 + i * BN;
+      // column c of the tile is hidden from c = seen on
+      const int seen = lim - key0 + 1;
+      const bool masked = __any_sync(~0u, seen < BN);
+
+      // pass 1: the tile's largest u
+      float top = -INFINITY;
+#pragma unroll
+      for (int c = 0; c < BN / 32; ++c) {
+        uint32_t r[32];
+        tmem_ld32(tS + 32 * c, r);
+        tmem_wait_ld32(r);
+        if (masked) {
+#pragma unroll
+          for (int k = 0; k < 32; ++k)
+            if (32 * c + k >= seen) r[k] = 0xFF800000u;
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float mx = fmaxf(__uint_as_float(r[16 * h]), __uint_as_float(r[16 * h + 1]));
+#pragma unroll
+          for (int k = 2; k < 16; k += 2) mx = fmaxf(mx, fmaxf(__uint_as_float(r[16 * h + k]), __uint_as_float(r[16 * h + k + 1])));
+          const float4 s = sc[2 * c + h];
+          top = fmaxf(top, fmaf(mx, ck * s.x, s.y));
+        }
+      }
+      // the reference
+      float by = 1.f;
+      bool move = false;
+      if (top > m + kTau) {
+        by = fast_exp2(m - top);
+        move = m != -INFINITY;
+        m = top;
+        l *= by;
+      }
+      if (__any_sync(~0u, move)) {
+        // O holds the products up to tile i - 1: rescale it before this tile's
+        ok = __all_sync(~0u, tc::mbar_wait(bar(ctl.o_done[NT == 2 ? a : 0]), uint32_t(i - 1) & 1u, abort, kWaitNs));
+        if (!ok) break;
+        tc::tc_fence_after();
+        const uint32_t tO = tmem + lanes + C::kO + uint32_t(a * D);
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          uint32_t v[32];
+          tmem_ld32(tO + c, v);
+          tmem_wait_ld32(v);
+#pragma unroll
+          for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * by);
+          tmem_st32(tO + c, v);
+        }
+      }
+      // pass 2: P in place of S (columns 16 c .. of what was read up to column 32 c)
+      const float lift = kLift - (m == -INFINITY ? 0.f : m);
+#pragma unroll
+      for (int c = 0; c < BN / 32; ++c) {
+        uint32_t r[32];
+        tmem_ld32(tS + 32 * c, r);
+        tmem_wait_ld32(r);
+        if (masked) {
+#pragma unroll
+          for (int k = 0; k < 32; ++k)
+            if (32 * c + k >= seen) r[k] = 0xFF800000u;
+        }
+        uint32_t w[16];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float4 s = sc[2 * c + h];
+          const float2 mul = make_float2(ck * s.x, ck * s.x), add = make_float2(s.y + lift, s.y + lift);
+          float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int k = 0; k < 16; k += 2) {
+            float2 u = fma2(make_float2(__uint_as_float(r[16 * h + k]), __uint_as_float(r[16 * h + k + 1])), mul, add);
+            u.x = fast_exp2(u.x);
+            u.y = fast_exp2(u.y);
+            sum = add2(sum, u);
+            w[8 * h + k / 2] = f16x2(u.x, u.y);
+          }
+          l = fmaf(sum.x + sum.y, s.z, l);
+        }
+        tmem_st16u(tS + 16 * c, w);
+      }
+      tc::tmem_wait_st();
+      tc::tc_fence_before();
+      tc::mbar_arrive(bar(ctl.p_full[buf]));
+      if ((i % TB == TB - 1 || i == nt - 1)) {
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(bar(ctl.e_empty[bat & 1]));
+      }
+    }
+    // The last product. With two S buffers the one before it may still run, and a wait for
+    // phase nt - 1 passes on phase nt - 3's parity: wait for phase nt - 2 first (phase nt - 3 is
+    // over: the last scores were issued behind it).
+    if (NT == 1 && nt > 1) ok = ok && tc::mbar_wait(bar(ctl.o_done[0]), uint32_t(nt - 2) & 1u, abort, kWaitNs);
+    if (nt > 0) ok = ok && tc::mbar_wait(bar(ctl.o_done[NT == 2 ? a : 0]), uint32_t(nt - 1) & 1u, abort, kWaitNs);
+    if (__all_sync(~0u, ok)) {
+      tc::tc_fence_after();
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      const bool some = nt > 0 && !(l == 0.f);
+      const int64_t unit = tok * p.h_q + head, part = int64_t(piece) * p.num_tokens * p.h_q + unit;
+#pragma unroll 1
+      for (int c = 0; c < D; c += 32) {
+        uint32_t r[32];
+        if (nt > 0) {
+          tmem_ld32(tmem + lanes + C::kO + uint32_t(a * D + c), r);
+          tmem_wait_ld32(r);
+        }
+        if (!real) continue;
+        if (p.splits > 1) {
+          if (!some) continue;
+          float4* dst = reinterpret_cast<float4*>(p.o_part + part * D + c);
+#pragma unroll
+          for (int k = 0; k < 32; k += 4)
+            dst[k / 4] = make_float4(__uint_as_float(r[k]) * inv, __uint_as_float(r[k + 1]) * inv,
+                                     __uint_as_float(r[k + 2]) * inv, __uint_as_float(r[k + 3]) * inv);
+        } else {
+          uint4* dst = reinterpret_cast<uint4*>(p.out + tok * p.out_ts + head * p.out_hs + c);
+#pragma unroll
+          for (int k = 0; k < 32; k += 8) {
+            uint32_t o[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              o[j] = some ? uint32_t(float_to_out_bits(__uint_as_float(r[k + 2 * j]) * inv, p.out_f16)) |
+                                (uint32_t(float_to_out_bits(__uint_as_float(r[k + 2 * j + 1]) * inv, p.out_f16)) << 16)
+                          : 0u;
+            dst[k / 8] = make_uint4(o[0], o[1], o[2], o[3]);
+          }
+        }
+      }
+      if (real) {
+        if (p.splits > 1) {
+          // m counts V's scales in, l does not: together 2^m l = sum 2^t
+          p.m_part[part] = some ? fmaxf(m, -1e30f) - kLift : -INFINITY;
+          p.l_part[part] = some ? l : 0.f;
+        } else if (p.lse) {
+          p.lse[unit] = some ? (m - kLift + fast_log2(l)) * kLn2 : -INFINITY;
+        }
+      }
+    }
+  } else if (warp < 12) {
+    // ======================= V to fp16 ========================================
+    // [key][128 codes] 128-byte swizzled -> [64 channels][key][64 fp16] likewise
+    const int ct = tid - 32 * C::kConvWarp0;
+    bool ok = true;
+    for (int i = 0; i < nt; ++i) {
+      const int s = i & 1;
+      const uint32_t ph = uint32_t(i >> 1) & 1u;
+      ok = tc::mbar_wait(bar(ctl.vr_full[s]), ph, abort, kWaitNs) && tc::mbar_wait(bar(ctl.vf_empty[s]), ph ^ 1u, abort, kWaitNs);
+      if (!ok) break;
+      const uint8_t* src = smem + C::kVr + s * kTile;
+      uint8_t* dst = smem + C::kVf + s * 2 * kTile;
+      const int live = k_end - (k0 + i * BN);  // rows from here on are no key's: zeros (they may hold NaN codes)
+#pragma unroll 4
+      for (int c = ct; c < kTile / 16; c += 32 * C::kConvWarps) {
+        const int sub = c / (BN * 8), row = (c >> 3) % BN, ch = c & 7;  // 128-channel half, key, 16-channel chunk
+        uint4 v = *reinterpret_cast<const uint4*>(src + sub * (BN * 128) + row * 128 + ((ch ^ (row & 7)) << 4));
+        if (row >= live) v = make_uint4(0u, 0u, 0u, 0u);
+        const uint4 lo = make_uint4(e4m3x2_f16x2(v.x), e4m3x2_f16x2(v.x >> 16), e4m3x2_f16x2(v.y), e4m3x2_f16x2(v.y >> 16));
+        const uint4 hi = make_uint4(e4m3x2_f16x2(v.z), e4m3x2_f16x2(v.z >> 16), e4m3x2_f16x2(v.w), e4m3x2_f16x2(v.w >> 16));
+        // the upper 64 channels' lanes store their halves the other way round: eight lanes then cover eight banks' groups
+        uint8_t* at = dst + (2 * sub + (ch >> 2)) * (BN * 128) + row * 128;
+        const int q = (ch & 3) * 2, swap = ch >> 2;
+        *reinterpret_cast<uint4*>(at + (((q + swap) ^ (row & 7)) << 4)) = swap ? hi : lo;
+        *reinterpret_cast<uint4*>(at + (((q + 1 - swap) ^ (row & 7)) << 4)) = swap ? lo : hi;
+      }
+      tc::fence_async_smem();
+      tc::mbar_arrive(bar(ctl.vr_empty[s]));
+      tc::mbar_arrive(bar(ctl.vf_full[s]));
+    }
+  } else if (warp == 12) {
+    // ======================= TMA: K and V tiles ===============================
+    const int box = min(BN, 1 << p.page_shift);  // rows of a copy
+    const int per = BN / box;                    // copies a tile, one lane each
+    const uint64_t pol = tc::l2_policy_evict_normal();
+    auto page_of = [&](int i) {  // of this lane's copy of tile i
+      const int64_t key = int64_t(k0) + int64_t(i) * BN + lane * box;
+      const int64_t e = key >> p.page_shift;
+      return lane < per && key < k_end && e < p.bt_len ? p.block_table[b * p.bt_stride + e] : -1;
+    };
+    int pg = nt > 0 ? page_of(0) : -1;
+    bool ok = true;
+    int issued = 0;
+    for (int i = 0; i < nt && ok; ++i) {
+      const int next = i + 1 < nt ? page_of(i + 1) : -1;
+      const int key0 = k0 + i * BN;
+      const int valid = min(per, (k_end - key0 + box - 1) / box);
+      const int row = (key0 + lane * box) & ((1 << p.page_shift) - 1);
+      auto load = [&](const CUtensorMap* map, uint32_t dst, uint32_t full, uint32_t empty, uint32_t parity) {
+        ok = tc::mbar_wait(empty, parity, abort, kWaitNs);
+        ok = __all_sync(~0u, ok);
+        if (!ok) return;
+        if (lane == 0) tc::mbar_arrive_expect_tx(full, uint32_t(valid * box * D));
+        __syncwarp();
+        if (lane < valid) {
+#pragma unroll
+          for (int dh = 0; dh < DH; ++dh) {
+            const uint32_t at = dst + uint32_t(dh * BN * 128 + lane * box * 128);
+            if (p.tma_head_inner)
+              tc::tma_load_4d(at, map, full, 128 * dh, g, row, pg, pol);
+            else
+              tc::tma_load_4d(at, map, full, 128 * dh, row, g, pg, pol);
+          }
+        }
+        ++issued;
+      };
+      const int ks = i % kKStages, vs = i & 1;
+      load(&tmap_k, base + C::kK + ks * kTile, bar(ctl.k_full[ks]), bar(ctl.k_empty[ks]), (uint32_t(i / kKStages) & 1u) ^ 1u);
+      if (ok)
+        load(&tmap_v, base + C::kVr + vs * kTile, bar(ctl.vr_full[vs]), bar(ctl.vr_empty[vs]), (uint32_t(i >> 1) & 1u) ^ 1u);
+      pg = next;
+    }
+    if (*abort && lane == 0) {
+      // wait (bounded) for the copies in flight before the CTA exits: copy j of tile j / 2, K then V
+      const uint64_t start = tc::globaltimer_ns();
+      for (int j = max(0, issued - 2 * kKStages); j < issued; ++j) {
+        const int i = j >> 1;
+        const uint32_t full = (j & 1) ? bar(ctl.vr_full[i & 1]) : bar(ctl.k_full[i % kKStages]);
+        const uint32_t par = (j & 1) ? uint32_t(i >> 1) & 1u : uint32_t(i / kKStages) & 1u;
+        while (!tc::mbar_try_wait(full, par) && tc::globaltimer_ns() - start < kDrainNs) {
+        }
+      }
+    }
+  } else if (warp == 13) {
+    // ======================= MMA ==============================================
+    constexpr uint32_t idesc_qk = tc::idesc_e4m3(128, BN, false, false);
+    constexpr uint32_t idesc_pv = idesc_f16(128, D);
+    const uint64_t qd = tc::smem_desc(base, 16, 1024, tc::kSwizzle128B);
+    const uint64_t kd = tc::smem_desc(base + C::kK, 16, 1024, tc::kSwizzle128B);
+    // V: 64-channel columns of blocks BN * 128 bytes apart, 8-key groups 1024
+    const uint64_t vd = tc::smem_desc(base + C::kVf, BN * 128, 1024, tc::kSwizzle128B);
+    // (votes: the products below are issued by whole warps)
+    bool ok = __all_sync(~0u, tc::mbar_wait(bar(ctl.q_ready), 0, abort, kWaitNs));
+    auto qk = [&](int a, int buf, int i) {
+      const uint32_t d = tmem + uint32_t(buf * BN);
+      const uint64_t k1 = kd + uint64_t((i % kKStages) * (kTile >> 4));
+#pragma unroll
+      for (int term = 0; term < 2; ++term)
+#pragma unroll
+        for (int dh = 0; dh < DH; ++dh)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            tc::umma_f8f6f4_warp(d, qd + uint64_t(((a * 2 + term) * DH + dh) * (kTile >> 4) + 2 * k),
+                                 k1 + uint64_t(dh * (BN * 128 >> 4) + 2 * k), idesc_qk, term > 0 || dh > 0 || k > 0);
+      tc::umma_commit_warp(bar(ctl.s_full[buf]));
+    };
+    auto pv = [&](int a, int buf, int i) {
+      const uint64_t v1 = vd + uint64_t((i & 1) * (2 * kTile >> 4));
+#pragma unroll
+      for (int k = 0; k < NB; ++k)
+        umma_f16_ts_warp(tmem + C::kO + uint32_t(a * D), tmem + uint32_t(buf * BN + 8 * k), v1 + uint64_t(128 * k), idesc_pv,
+                         i > 0 || k > 0);
+      tc::umma_commit_warp(bar(ctl.o_done[a]));
+    };
+    auto wait_k = [&](int i) {
+      ok = ok && __all_sync(~0u, tc::mbar_wait(bar(ctl.k_full[i % kKStages]), uint32_t(i / kKStages) & 1u, abort, kWaitNs));
+      tc::tc_fence_after();
+      return ok;
+    };
+    auto wait_v = [&](int i) {
+      ok = ok && __all_sync(~0u, tc::mbar_wait(bar(ctl.vf_full[i & 1]), uint32_t(i >> 1) & 1u, abort, kWaitNs));
+      return ok;
+    };
+    auto wait_p = [&](int buf, int parity) {
+      ok = ok && __all_sync(~0u, tc::mbar_wait(bar(ctl.p_full[buf]), uint32_t(parity) & 1u, abort, kWaitNs));
+      tc::tc_fence_after();
+      return ok;
+    };
+    // Products run in the order they are issued, so a tile's next scores may be asked
+    // for right behind the product that reads its weights from the same columns.
+    if (nt > 0 && wait_k(0)) {
+#pragma unroll
+      for (int a = 0; a < NT; ++a) qk(a, a, 0);
+      tc::umma_commit_warp(bar(ctl.k_empty[0]));
+      for (int i = 0; i < nt && ok; ++i) {
+        const int j = i + 1;
+        if constexpr (NT == 2) {
+#pragma unroll
+          for (int a = 0; a < 2; ++a) {
+            if (a == 0 && !wait_v(i)) break;
+            if (!wait_p(a, i)) break;
+            pv(a, a, i);
+            if (a == 1) tc::umma_commit_warp(bar(ctl.vf_empty[i & 1]));
+            if (j < nt) {
+              if (a == 0 && !wait_k(j)) break;
+              qk(a, a, j);
+              if (a == 1) tc::umma_commit_warp(bar(ctl.k_empty[j % kKStages]));
+            }
+          }
+        } else {
+          if (j < nt) {
+            if (!wait_k(j)) break;
+            qk(0, j & 1, j);
+            tc::umma_commit_warp(bar(ctl.k_empty[j % kKStages]));
+          }
+          if (!wait_v(i) || !wait_p(i & 1, i >> 1)) break;
+          pv(0, i & 1, i);
+          tc::umma_commit_warp(bar(ctl.vf_empty[i & 1]));
+        }
+      }
+    }
+    if (!ok) {
+      // wait (bounded) until every product issued so far is done
+      tc::umma_commit_warp(bar(ctl.drain));
+      const uint64_t start = tc::globaltimer_ns();
+      while (!tc::mbar_try_wait(bar(ctl.drain), 0) && tc::globaltimer_ns() - start < kDrainNs) {
+      }
+    }
+  } else if (warp == 14) {
+    // ======================= the blocks' scales ================================
+    for (int q = 0; q * TB < nt; ++q) {
+      const int64_t key = int64_t(k0) + int64_t(q) * TB * BN + lane * 16;
+      const int64_t e = key >> p.page_shift;
+      int ke = 127, ve = 127;
+      if (key < k_end) {
+        const int pg = e < p.bt_len ? p.block_table[b * p.bt_stride + e] : -1;
+        if (pg >= 0 && pg < p.num_pages) {
+          const int at = (int(key) & ((1 << p.page_shift) - 1)) >> p.block_shift;
+          ke = block_exp(p.side[0].exps[pg * p.side[0].esp + g * p.side[0].esh + at]);
+          ve = block_exp(p.side[1].exps[pg * p.side[1].esp + g * p.side[1].esh + at]);
+        } else {
+          atomicOr(p.status, kStatusBadPage);
+        }
+      }
+      if (!__all_sync(~0u, tc::mbar_wait(bar(ctl.e_empty[q & 1]), (uint32_t(q >> 1) & 1u) ^ 1u, abort, kWaitNs))) break;
+      ctl.scale[q & 1][lane] = make_float4(__int_as_float(ke << 23), float(ve - 127), __int_as_float((254 - ve) << 23), 0.f);
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(bar(ctl.e_full[q & 1]));
+    }
+  }
+
+  // ---- teardown ------------------------------------------------------------
+  tc::tc_fence_before();
+  __syncthreads();
+  if (*abort && tid == 0) atomicOr(p.status, kStatusTimeout);
+  if (warp == 13) {
+    tc::tc_fence_after();
+    tc::tmem_dealloc(tmem, 512);
+  }
+}
+
+// The cache side as a 4-D byte tensor (channel, token, head, page), the smaller of
+// the token and head strides first; a copy is 128 channels of `rows` tokens.
+bool encode(CUtensorMap* map, const BlockSide& s, const BlockPromptParams& p, int rows) {
+  auto fn = tensor_map_encode_fn();
+  if (!fn) return false;
+  const int page = 1 << p.page_shift;
+  const bool hi = p.tma_head_inner;
+  const int64_t sh = p.h_k == 1 ? (hi ? 32 : s.sp) : s.sh;
+  const cuuint64_t dims[4] = {cuuint64_t(p.d), cuuint64_t(hi ? p.h_k : page), cuuint64_t(hi ? page : p.h_k),
+                              cuuint64_t(p.num_pages)};
+  const cuuint64_t strides[3] = {cuuint64_t(hi ? sh : s.st), cuuint64_t(hi ? s.st : sh), cuuint64_t(s.sp)};
+  const cuuint32_t box[4] = {128, cuuint32_t(hi ? 1 : rows), cuuint32_t(hi ? rows : 1), 1}, one[4] = {1, 1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, s.codes, dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D>
+cudaError_t launch(const CUtensorMap& mk, const CUtensorMap& mv, const BlockPromptParams& p, cudaStream_t stream) {
+  constexpr int bytes = Cfg<D>::kBytes + 1024;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  const dim3 grid(unsigned((int64_t(p.max_q_len) * p.h_r + kRows - 1) / kRows), unsigned(p.h_k * p.splits), unsigned(p.num_seqs));
-  block_prompt_kernel<D><<<grid, 32 * kWarps, bytes, stream>>>(p);
-  return cudaGetLastError();
+  static std::atomic<int> configured[64];  // the shared-memory limit is raised once per device
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!configured[dev].load(std::memory_order_acquire)) {
+    e = cudaFuncSetAttribute(block_prompt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+    configured[dev].store(1, std::memory_order_release);
+  }
+  const int64_t tiles = (int64_t(p.max_q_len) * p.h_r + Cfg<D>::kRows - 1) / Cfg<D>::kRows;
+  if (tiles > 65535) return cudaErrorInvalidConfiguration;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(p.h_k * p.splits), unsigned(tiles), unsigned(p.num_seqs));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = bytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, block_prompt_kernel<D>, mk, mv, p);
 }
 
 }  // namespace
 
-cudaError_t launch_block_prompt(const BlockPromptParams& p, cudaStream_t stream) {
-  return p.d == 256 ? launch<256>(p, stream) : launch<128>(p, stream);
+int block_prompt_rows(int d) { return d == 256 ? Cfg<256>::kRows : Cfg<128>::kRows; }
+
+cudaError_t launch_block_prompt(BlockPromptParams p, cudaStream_t stream, bool* unsupported) {
+  const BlockSide &k = p.side[0], &v = p.side[1];
+  p.tma_head_inner = k.sh < k.st ? 1 : 0;
+  const int rows = std::min(p.d == 256 ? Cfg<256>::BN : Cfg<128>::BN, 1 << p.page_shift);
+  CUtensorMap mk, mv;
+  *unsupported = k.sp == 0 || v.sp == 0 || (v.sh < v.st) != (k.sh < k.st) || !encode(&mk, k, p, rows) || !encode(&mv, v, p, rows);
+  if (*unsupported) return cudaSuccess;
+  return p.d == 256 ? launch<256>(mk, mv, p, stream) : launch<128>(mk, mv, p, stream);
 }
 
 }  // namespace mj

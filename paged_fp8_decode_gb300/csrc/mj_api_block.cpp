@@ -22,8 +22,8 @@ int status_of(cudaError_t e) { return e == cudaSuccess ? MJ_OK : MJ_ERR_CUDA; }
 bool size_ok(int n) { return n == 16 || n == 32 || n == 64 || n == 128; }
 
 constexpr int kMaxTokens = 1 << 30;
-// A prompt's row tile, and the least keys of a piece worth a CTA of its own.
-constexpr int64_t kPromptRows = 256, kPromptMinKeys = 1024;
+// The least keys of a prompt's piece worth a CTA of its own.
+constexpr int64_t kPromptMinKeys = 1024;
 constexpr int64_t kMaxRows = 1 << 20;  // query rows of a request and KV head
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -362,7 +362,7 @@ int mj_block_prompt_splits(int sm_count, int num_seqs, int max_q_len, int max_le
   if (sm_count < 1 || num_seqs < 1 || max_q_len < 1 || max_len < 1 || h_k < 1 || h_q < h_k || h_q % h_k || !mj::head_dim_ok(d))
     return 1;
   const int64_t rows = int64_t(max_q_len) * (h_q / h_k);
-  const int64_t ctas = ceil_div(rows, kPromptRows) * h_k * num_seqs;
+  const int64_t ctas = ceil_div(rows, mj::block_prompt_rows(d)) * h_k * num_seqs;
   const int64_t by_keys = std::max<int64_t>(1, max_len / kPromptMinKeys);
   return int(std::min<int64_t>({MJ_BLOCK_MAX_SPLITS, by_keys, std::max<int64_t>(1, sm_count / ctas)}));
 }
@@ -388,7 +388,8 @@ int mj_block_prompt(const mj_block_prompt_args* a, void* stream) {
   st = mj_block_prompt_workspace_size(a->num_tokens, a->h_q, c.d, a->splits, &bytes);
   if (st != MJ_OK) return st;
   const int h_r = a->h_q / c.h_k;
-  if (a->num_seqs > 65535 || int64_t(c.h_k) * a->splits > 65535) return MJ_ERR_UNSUPPORTED;
+  if (a->num_seqs > 65535 || ceil_div(int64_t(a->max_q_len) * h_r, mj::block_prompt_rows(c.d)) > 65535)
+    return MJ_ERR_UNSUPPORTED;
   if (a->num_seqs == 0 || a->num_tokens == 0 || a->max_q_len == 0) return MJ_OK;
   st = check_rows(a->q, a->q_tok_stride, a->q_head_stride);
   if (st == MJ_OK) st = check_rows(a->out, a->out_tok_stride, a->out_head_stride);
@@ -434,7 +435,9 @@ int mj_block_prompt(const mj_block_prompt_args* a, void* stream) {
   p.o_part = reinterpret_cast<float*>(ws + mj::kWsHeader);
   p.m_part = p.o_part + parts * c.d;
   p.l_part = p.m_part + parts;
-  cudaError_t e = mj::launch_block_prompt(p, static_cast<cudaStream_t>(stream));
+  bool unsupported = false;
+  cudaError_t e = mj::launch_block_prompt(p, static_cast<cudaStream_t>(stream), &unsupported);
+  if (unsupported) return MJ_ERR_UNSUPPORTED;
   if (e != cudaSuccess || a->splits == 1) return status_of(e);
   mj::BlockJoinParams j = {};
   j.d = c.d;

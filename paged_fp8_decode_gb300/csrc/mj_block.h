@@ -94,10 +94,13 @@ struct BlockPromptParams {
   uint32_t* status;
   float* o_part;              // splits > 1: [splits][num_tokens][h_q][d], then m and l alike
   float* m_part;
-  float* l_part;
+  float* l_part;              // -1: a row that was not computed (piece 0's)
+  int tma_head_inner;
 };
 
-cudaError_t launch_block_prompt(const BlockPromptParams& p, cudaStream_t stream);
+// Sets *unsupported (and launches nothing) where TMA cannot take the cache's strides.
+cudaError_t launch_block_prompt(BlockPromptParams p, cudaStream_t stream, bool* unsupported);
+int block_prompt_rows(int d);  // query rows of a CTA
 cudaError_t launch_block_write(BlockWriteParams p, int d, cudaStream_t stream);
 cudaError_t launch_block_read(const BlockReadParams& p, int d, cudaStream_t stream);
 cudaError_t launch_block_join(const BlockJoinParams& p, cudaStream_t stream);
