@@ -101,15 +101,19 @@ __device__ __forceinline__ void tmem_wait_ld32(uint32_t (&r)[32]) {
                  "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory");
 }
 
-__device__ __forceinline__ void tmem_st32(uint32_t at, const uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(at),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]),
-      "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
-      "r"(r[30]), "r"(r[31])
-      : "memory");
+// The same without the wait: for loads that an earlier wait covers.
+__device__ __forceinline__ void tmem_pass32(uint32_t (&r)[32]) {
+  asm volatile(""
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+                 "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]),
+                 "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]),
+                 "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31]));
+}
+
+__device__ __forceinline__ void tmem_wait_ld16(float (&v)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]), "+f"(v[8]),
+                 "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15])::"memory");
 }
 
 __device__ __forceinline__ void tmem_st16u(uint32_t at, const uint32_t (&r)[16]) {
@@ -225,7 +229,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = ctl.tmem;
   volatile int* abort = &ctl.abort;
 
+  // Registers: 128 a thread at launch. With two row tiles a softmax thread keeps a row's 128
+  // scores; 2 x 176 + 64 + 96 = 4 x 128 for the four warpgroups.
   if (warp < 4 * NT) {
+    if constexpr (NT == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
     // ======================= softmax: thread = row ============================
     const int a = warp >> 2, quad = warp & 3;
     const int R = r0 + 128 * a + 32 * quad + lane;
@@ -308,26 +315,27 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int seen = lim - key0 + 1;
       const bool masked = __any_sync(~0u, seen < BN);
 
-      // pass 1: the tile's largest u
+      // the tile's largest u
+      uint32_t r[BN / 32][32];
+#pragma unroll
+      for (int c = 0; c < BN / 32; ++c) tmem_ld32(tS + 32 * c, r[c]);
+      tmem_wait_ld32(r[0]);
+#pragma unroll
+      for (int c = 1; c < BN / 32; ++c) tmem_pass32(r[c]);
+      if (masked) {
+#pragma unroll
+        for (int k = 0; k < BN; ++k)
+          if (k >= seen) r[k / 32][k % 32] = 0xFF800000u;
+      }
       float top = -INFINITY;
 #pragma unroll
-      for (int c = 0; c < BN / 32; ++c) {
-        uint32_t r[32];
-        tmem_ld32(tS + 32 * c, r);
-        tmem_wait_ld32(r);
-        if (masked) {
+      for (int h = 0; h < NB; ++h) {
+        const uint32_t* x = &r[h / 2][16 * (h & 1)];
+        float mx = fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1]));
 #pragma unroll
-          for (int k = 0; k < 32; ++k)
-            if (32 * c + k >= seen) r[k] = 0xFF800000u;
-        }
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          float mx = fmaxf(__uint_as_float(r[16 * h]), __uint_as_float(r[16 * h + 1]));
-#pragma unroll
-          for (int k = 2; k < 16; k += 2) mx = fmaxf(mx, fmaxf(__uint_as_float(r[16 * h + k]), __uint_as_float(r[16 * h + k + 1])));
-          const float4 s = sc[2 * c + h];
-          top = fmaxf(top, fmaf(mx, ck * s.x, s.y));
-        }
+        for (int k = 2; k < 16; k += 2) mx = fmaxf(mx, fmaxf(__uint_as_float(x[k]), __uint_as_float(x[k + 1])));
+        const float4 e = sc[h];
+        top = fmaxf(top, fmaf(mx, ck * e.x, e.y));
       }
       // the reference
       float by = 1.f;
@@ -345,42 +353,34 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::tc_fence_after();
         const uint32_t tO = tmem + lanes + C::kO + uint32_t(a * D);
 #pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
-          uint32_t v[32];
-          tmem_ld32(tO + c, v);
-          tmem_wait_ld32(v);
+        for (int c = 0; c < D; c += 16) {
+          float v[16];
+          tc::tmem_ld16(tO + c, v);
+          tmem_wait_ld16(v);
 #pragma unroll
-          for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * by);
-          tmem_st32(tO + c, v);
+          for (int k = 0; k < 16; ++k) v[k] *= by;
+          tc::tmem_st16(tO + c, v);
         }
       }
-      // pass 2: P in place of S (columns 16 c .. of what was read up to column 32 c)
+      // P in place of S
       const float lift = kLift - (m == -INFINITY ? 0.f : m);
 #pragma unroll
       for (int c = 0; c < BN / 32; ++c) {
-        uint32_t r[32];
-        tmem_ld32(tS + 32 * c, r);
-        tmem_wait_ld32(r);
-        if (masked) {
-#pragma unroll
-          for (int k = 0; k < 32; ++k)
-            if (32 * c + k >= seen) r[k] = 0xFF800000u;
-        }
         uint32_t w[16];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const float4 s = sc[2 * c + h];
-          const float2 mul = make_float2(ck * s.x, ck * s.x), add = make_float2(s.y + lift, s.y + lift);
+          const float4 e = sc[2 * c + h];
+          const float2 mul = make_float2(ck * e.x, ck * e.x), add = make_float2(e.y + lift, e.y + lift);
           float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
           for (int k = 0; k < 16; k += 2) {
-            float2 u = fma2(make_float2(__uint_as_float(r[16 * h + k]), __uint_as_float(r[16 * h + k + 1])), mul, add);
+            float2 u = fma2(make_float2(__uint_as_float(r[c][16 * h + k]), __uint_as_float(r[c][16 * h + k + 1])), mul, add);
             u.x = fast_exp2(u.x);
             u.y = fast_exp2(u.y);
             sum = add2(sum, u);
             w[8 * h + k / 2] = f16x2(u.x, u.y);
           }
-          l = fmaf(sum.x + sum.y, s.z, l);
+          l = fmaf(sum.x + sum.y, e.z, l);
         }
         tmem_st16u(tS + 16 * c, w);
       }
@@ -442,6 +442,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp < 12) {
+    if constexpr (NT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     // ======================= V to fp16 ========================================
     // [key][128 codes] 128-byte swizzled -> [64 channels][key][64 fp16] likewise
     const int ct = tid - 32 * C::kConvWarp0;
@@ -471,7 +472,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::mbar_arrive(bar(ctl.vr_empty[s]));
       tc::mbar_arrive(bar(ctl.vf_full[s]));
     }
-  } else if (warp == 12) {
+  } else {
+    if constexpr (NT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
+  if (warp == 12) {
     // ======================= TMA: K and V tiles ===============================
     const int box = min(BN, 1 << p.page_shift);  // rows of a copy
     const int per = BN / box;                    // copies a tile, one lane each
@@ -630,6 +633,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(bar(ctl.e_full[q & 1]));
     }
+  }
   }
 
   // ---- teardown ------------------------------------------------------------
