@@ -671,7 +671,7 @@ typedef struct mj_block_cache {
  * ones written are of no value until they are written. The result does not
  * depend on the tokens' order.
  * The call's slots are distinct, and its tokens of one block follow one another
- * (padding tokens between two of them: at most 128): a block's tokens that do
+ * (padding tokens may lie between them): a block's tokens that do
  * not are written as if by several calls at once, in no order. Negative slots
  * are padding, a slot past the pool is skipped and reported (status bit 1). The
  * rows of a cache, and its exponent bytes, lie apart: each stride holds all

@@ -142,6 +142,12 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   return d;
 }
+// the largest of three (NaN does not count)
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
 // lo and hi to fp16, packed
 __device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
   uint32_t r;
@@ -322,7 +328,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       tmem_wait_ld32(r[0]);
 #pragma unroll
       for (int c = 1; c < BN / 32; ++c) tmem_pass32(r[c]);
-      if (masked) {
+      if (masked) {  // (the asm keeps this a branch: as selects it would cost every tile)
+        asm volatile("" ::: "memory");
 #pragma unroll
         for (int k = 0; k < BN; ++k)
           if (k >= seen) r[k / 32][k % 32] = 0xFF800000u;
@@ -331,9 +338,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int h = 0; h < NB; ++h) {
         const uint32_t* x = &r[h / 2][16 * (h & 1)];
-        float mx = fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1]));
+        float mx = __uint_as_float(x[0]), my = __uint_as_float(x[1]);
 #pragma unroll
-        for (int k = 2; k < 16; k += 2) mx = fmaxf(mx, fmaxf(__uint_as_float(x[k]), __uint_as_float(x[k + 1])));
+        for (int k = 2; k < 14; k += 4) {
+          mx = max3(mx, __uint_as_float(x[k]), __uint_as_float(x[k + 1]));
+          my = max3(my, __uint_as_float(x[k + 2]), __uint_as_float(x[k + 3]));
+        }
+        mx = fmaxf(max3(mx, __uint_as_float(x[14]), __uint_as_float(x[15])), my);
         const float4 e = sc[h];
         top = fmaxf(top, fmaf(mx, ck * e.x, e.y));
       }
@@ -446,27 +457,33 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ======================= V to fp16 ========================================
     // [key][128 codes] 128-byte swizzled -> [64 channels][key][64 fp16] likewise
     const int ct = tid - 32 * C::kConvWarp0;
+    constexpr int RI = 4 * C::kConvWarps;  // rows the warps take at once, a thread 16 channels: row & 7 is a thread's own
+    const int row0 = ct >> 3, ch = ct & 7, x7 = row0 & 7;
+    // The upper 64 channels' lanes store their halves the other way round: eight
+    // lanes of a row then cover all of shared memory's banks.
+    const int swap = ch >> 2, q = (ch & 3) * 2;
+    const uint8_t* src0 = smem + C::kVr + row0 * 128 + ((ch ^ x7) << 4);
+    uint8_t* dst0 = smem + C::kVf + swap * (BN * 128) + row0 * 128;
+    const int at0 = ((q + swap) ^ x7) << 4, at1 = ((q + 1 - swap) ^ x7) << 4;
     bool ok = true;
     for (int i = 0; i < nt; ++i) {
       const int s = i & 1;
       const uint32_t ph = uint32_t(i >> 1) & 1u;
       ok = tc::mbar_wait(bar(ctl.vr_full[s]), ph, abort, kWaitNs) && tc::mbar_wait(bar(ctl.vf_empty[s]), ph ^ 1u, abort, kWaitNs);
       if (!ok) break;
-      const uint8_t* src = smem + C::kVr + s * kTile;
-      uint8_t* dst = smem + C::kVf + s * 2 * kTile;
+      const uint8_t* src = src0 + s * kTile;
+      uint8_t* dst = dst0 + s * 2 * kTile;
       const int live = k_end - (k0 + i * BN);  // rows from here on are no key's: zeros (they may hold NaN codes)
-#pragma unroll 4
-      for (int c = ct; c < kTile / 16; c += 32 * C::kConvWarps) {
-        const int sub = c / (BN * 8), row = (c >> 3) % BN, ch = c & 7;  // 128-channel half, key, 16-channel chunk
-        uint4 v = *reinterpret_cast<const uint4*>(src + sub * (BN * 128) + row * 128 + ((ch ^ (row & 7)) << 4));
-        if (row >= live) v = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+      for (int it = 0; it < DH * BN / RI; ++it) {
+        const int sub = it / (BN / RI), row = RI * (it % (BN / RI));  // 128-channel half; beside row0
+        uint4 v = *reinterpret_cast<const uint4*>(src + sub * (BN * 128) + row * 128);
+        if (row0 + row >= live) v = make_uint4(0u, 0u, 0u, 0u);
         const uint4 lo = make_uint4(e4m3x2_f16x2(v.x), e4m3x2_f16x2(v.x >> 16), e4m3x2_f16x2(v.y), e4m3x2_f16x2(v.y >> 16));
         const uint4 hi = make_uint4(e4m3x2_f16x2(v.z), e4m3x2_f16x2(v.z >> 16), e4m3x2_f16x2(v.w), e4m3x2_f16x2(v.w >> 16));
-        // the upper 64 channels' lanes store their halves the other way round: eight lanes then cover eight banks' groups
-        uint8_t* at = dst + (2 * sub + (ch >> 2)) * (BN * 128) + row * 128;
-        const int q = (ch & 3) * 2, swap = ch >> 2;
-        *reinterpret_cast<uint4*>(at + (((q + swap) ^ (row & 7)) << 4)) = swap ? hi : lo;
-        *reinterpret_cast<uint4*>(at + (((q + 1 - swap) ^ (row & 7)) << 4)) = swap ? lo : hi;
+        uint8_t* at = dst + 2 * sub * (BN * 128) + row * 128;
+        *reinterpret_cast<uint4*>(at + at0) = swap ? hi : lo;
+        *reinterpret_cast<uint4*>(at + at1) = swap ? lo : hi;
       }
       tc::fence_async_smem();
       tc::mbar_arrive(bar(ctl.vr_empty[s]));

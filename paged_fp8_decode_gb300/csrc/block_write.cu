@@ -8,7 +8,7 @@
 // is exact and the only rounding is the one to e4m3.
 //
 // The call's tokens of a block form a run (they follow one another, padding
-// tokens aside). A CTA looks through a window of tokens for runs that begin
+// tokens aside, however many). A CTA looks through a window of tokens for runs that begin
 // there; its warps then take the run's (KV head, K or V) pairs in turn, each
 // warp 16 rows of the block in registers: one read of the input, one maximum
 // over the warp (over the block's warps where it has more than 16 rows), one
@@ -50,6 +50,26 @@ __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
          (uint32_t(__nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3)) << 16);
 }
 
+// The first live token of the call at or after `from` (DIR 1) or at or before it
+// (DIR -1); -1 where there is none. For a whole warp: 256 tokens a step.
+template <int DIR>
+__device__ __noinline__ int64_t find_live(const int64_t* slots, int64_t from, int64_t num_tokens, int64_t num_slots, int lane) {
+  for (int64_t t0 = from; t0 >= 0 && t0 < num_tokens; t0 += DIR * 256) {
+    int64_t s[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int64_t t = t0 + DIR * (32 * u + lane);
+      s[u] = t >= 0 && t < num_tokens ? slots[t] : -1;
+    }
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const unsigned m = __ballot_sync(~0u, s[u] >= 0 && s[u] < num_slots);
+      if (m) return t0 + DIR * (32 * u + __ffs(m) - 1);
+    }
+  }
+  return -1;
+}
+
 // G warps share a block of 16 G rows.
 template <int D, int G>
 __global__ void __launch_bounds__(kThreads) block_write_kernel(BlockWriteParams p) {
@@ -69,8 +89,8 @@ __global__ void __launch_bounds__(kThreads) block_write_kernel(BlockWriteParams 
 
   const int64_t w0 = int64_t(blockIdx.x) * p.window, w1 = min(T, w0 + p.window);
   for (int64_t t0 = w0; t0 < w1; t0 += 32) {
-    // lane l: token t0 + l, and whether a run begins there: no live token of its
-    // block right before it (kBlockPad padding tokens aside)
+    // lane l: token t0 + l, and whether a run begins there: the live token before it
+    // is of another block
     const int64_t t = t0 + lane;
     const int64_t s = t < w1 ? p.slots[t] : -1;
     const bool live = alive(s);
@@ -79,31 +99,17 @@ __global__ void __launch_bounds__(kThreads) block_write_kernel(BlockWriteParams 
     if (!mask) continue;
     const int64_t b = s >> p.block_shift;
     const unsigned below = mask & ((1u << lane) - 1u);
-    const int from = below ? 31 - __clz(below) : 0;
-    int64_t pb = __shfl_sync(~0u, b, from), pt = t0 + from;  // the live token before, its block
-    bool has = below != 0;
-    {  // the window's first live token looks back past its begin
-      const int head = __ffs(mask) - 1;
-      int64_t hb = 0, ht = 0;
-      bool found = false;
-      for (int64_t e = t0; e > 0 && !found && t0 + head - e <= kBlockPad; e -= 32) {
-        const int64_t q = e - 1 - lane;
-        const int64_t qs = q >= 0 ? p.slots[q] : -1;
-        const unsigned qm = __ballot_sync(~0u, alive(qs));
-        if (qm) {
-          const int l = __ffs(qm) - 1;
-          hb = __shfl_sync(~0u, qs >> p.block_shift, l);
-          ht = e - 1 - l;
-          found = true;
-        }
+    int64_t pb = __shfl_sync(~0u, b, below ? 31 - __clz(below) : 0);
+    if (lane == __ffs(mask) - 1) pb = -1;
+    if (t0 > 0) {  // the window's first live token looks back past its begin
+      int64_t at = t0 - 1, before = p.slots[at];
+      if (!alive(before)) {
+        at = find_live<-1>(p.slots, at, T, p.num_slots, lane);
+        before = at >= 0 ? p.slots[at] : -1;
       }
-      if (lane == head) {
-        has = found;
-        pb = hb;
-        pt = ht;
-      }
+      if (lane == __ffs(mask) - 1 && before >= 0) pb = before >> p.block_shift;
     }
-    unsigned leaders = __ballot_sync(~0u, live && !(has && pb == b && t - pt <= kBlockPad + 1));
+    unsigned leaders = __ballot_sync(~0u, live && pb != b);
 
     while (leaders) {
       const int l = __ffs(leaders) - 1;
@@ -113,22 +119,21 @@ __global__ void __launch_bounds__(kThreads) block_write_kernel(BlockWriteParams 
       if (lane < kRowsWarp) map[warp][lane] = 0;
       __syncwarp();
       int first = block;
-      int64_t last = t0 + l;
-      for (int64_t c0 = t0 + l; c0 < T; c0 += 32) {
+      for (int64_t c0 = t0 + l; c0 >= 0 && c0 < T;) {
         const int64_t c = c0 + lane;
         const int64_t cs = c < T ? p.slots[c] : -1;
         const bool cl = alive(cs), same = cl && (cs >> p.block_shift) == B;
         const unsigned other = __ballot_sync(~0u, cl && !same);
         unsigned mine = __ballot_sync(~0u, same);
         if (other) mine &= (other & (0u - other)) - 1u;  // up to the next block's first token
-        if (mine && c0 + __ffs(mine) - 1 - last > kBlockPad + 1) break;
         if (mine >> lane & 1u) {
           const int row = int(cs) & (block - 1);
           first = min(first, row);
           if ((row >> 4) == part) map[warp][row & (kRowsWarp - 1)] = int(c) + 1;
         }
-        if (mine) last = c0 + 31 - __clz(mine);
-        if (other || c0 + 32 - last > kBlockPad + 1) break;
+        if (other) break;
+        c0 += 32;
+        if (!mine && c0 < T) c0 = find_live<1>(p.slots, c0, T, p.num_slots, lane);
       }
       first = __reduce_min_sync(~0u, first);
       __syncwarp();

@@ -6,8 +6,6 @@
 
 namespace mj {
 
-constexpr int kBlockPad = 128;  // padding tokens that may lie between two tokens of one block in a write
-
 // One side (K or V) of the cache, as the kernels see it.
 struct BlockSide {
   uint8_t* codes;

@@ -99,16 +99,15 @@ def test_padding_inside_a_run(gap):
     check_write(*make_write([(0, 40)], pad=range(21, 21 + gap), seed=gap, page=128, block=128))
 
 
-def test_far_padding_loses_no_token():
-    # past the 128 tokens that a run may be interrupted for, tokens of one block are written as by two calls: nothing is lost
-    import paged_fp8_decode_gb300 as mj
+@pytest.mark.parametrize("gap", [129, 255, 256, 257, 289, 1000, 5000])
+def test_far_padding_inside_a_run(gap):
+    check_write(*make_write([(20, 9)], pad=range(4, 4 + gap), seed=gap))
+    check_write(*make_write([(0, 40), (60, 70)], pad=range(21, 21 + gap), seed=gap, page=128, block=128))
 
-    for gap in (129, 140, 160, 161, 200):
-        b, k, v, slots = make_write([(16, 8)], pad=range(4, 4 + gap), seed=gap)
-        kv = b.kv()
-        kv.k_cache[1] = 0x7F
-        mj.mj_block_write_kv(mj.block_write_args(k, v, up(slots), kv))
-        assert not ((kv.k_cache[1, :8] & 0x7F) == 0x7F).any() and ((kv.k_cache[1, 8:]) == 0x7F).all()
+
+def test_padding_before_and_behind():
+    check_write(*make_write([(20, 40)], pad=list(range(700)) + list(range(740, 1500)), seed=1))
+    check_write(*make_write([(20, 3), (39, 2)], pad=list(range(3, 400)) + list(range(402, 1500)), seed=2, block=16))
 
 
 def test_rows_left_out_inside_a_run():
