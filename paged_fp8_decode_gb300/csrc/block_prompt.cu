@@ -13,17 +13,27 @@
 // and a product per 16 keys and row. m is the row's running reference of u: it moves
 // only where a tile's largest u is more than 8 above it (P stays below 2^14 + 1), and
 // O, kept in tensor memory, is rescaled then. Weights keep 11 bits down to 20 binades
-// below the reference, and lose less than 2^-31 of it each below. The sum l wants 2^t: P's float32 times 2^-ev.
+// below the reference, and lose less than 2^-31 of it each below. The sum l wants 2^t: P's float32
+// times 2^-ev.
 //
-// Head size 128: two row tiles (256 rows) and 128 keys a step; while one tile's softmax
-// runs, the tensor cores work on the other's products. Head size 256: tensor memory
-// holds one row tile's O; 64 keys a step, two S buffers, so that the next scores
-// are ready when a softmax ends. What bounds it is the 16-bit tensor rate.
+// Head size 128: two row tiles (256 rows), 128 keys a step; tensor memory is full (two S and two
+// O), so a tile's next scores wait for its weights' product, and the other tile's
+// products fill that time. Head size 256: one row tile, 64 keys a step, two S buffers.
 //
-// Warps: 0-3 and 4-7 softmax of the row tiles (a thread a row), 8-11 widen V (4-11 at head size 256),
-// 12 TMA, 13 MMA, 14 the blocks' scales. Every wait is bounded (2 s): a timeout sets a status
-// bit, and the CTA drains its copies and products, frees its tensor memory and returns.
+// What bounds it (4096 tokens after 12288, 32/8 heads: 808 us, 1190 TFLOP/s, 61% of the
+// measured bf16 rate; clock stamps of a CTA's steps): a row tile's chain, 3100 cycles a
+// step where both tiles' products take 2050. Softmax 1500 (scores read 60, largest u 400, exponentials 1000),
+// products of the weights 700, scores 580, from their end to the softmax 350. Measured and not kept:
+// 64 keys a step with two S buffers a tile (980 us: at 64 columns the scores' operands
+// bound shared memory), the same with Q in tensor memory and one buffer (977 us), two
+// threads a row (940 us). The products are issued four at an election, their
+// barriers waited for a step ahead: 864 -> 808 us; scores read once into registers instead of twice: 1040 -> 864.
+//
+// Warps: 0 TMA, 1 MMA, 2 the blocks' scales, then softmax (a thread a row) and the
+// warps that widen V. Every wait is bounded (2 s): a timeout sets a status bit, and the CTA
+// drains its copies and products, frees its tensor memory and returns.
 #include <atomic>
+#include <type_traits>
 
 #include "latent_ptx.cuh"
 #include "mj_block.h"
@@ -36,7 +46,7 @@ namespace {
 constexpr int kThreads = 512;
 constexpr uint64_t kWaitNs = 2000000000ull, kDrainNs = 100000000ull;
 constexpr float kTau = 8.f, kLift = 6.f;  // log2 units
-constexpr int kKStages = 3;
+constexpr int kKStages = 4;              // (a multiple of V's two: the MMA loop's period)
 constexpr int kTile = 16384;              // bytes: 128 rows of 128, and a K or V tile
 
 template <int D>
@@ -46,33 +56,60 @@ struct Cfg {
   static constexpr int DH = D / 128;
   static constexpr int NB = BN / 16;            // 16-key groups of a tile
   static constexpr int TB = 32 / NB;            // tiles a batch of scales covers
-  static constexpr int kConvWarp0 = 4 * NT, kConvWarps = 12 - kConvWarp0;
+  // warps: 0 TMA, 1 MMA, 2 the blocks' scales, 4 .. softmax, then the ones that widen V
+  static constexpr int kConvWarp0 = 4 + 4 * NT, kConvWarps = 16 - kConvWarp0;
   static constexpr int kRows = 128 * NT;
   static constexpr uint32_t kO = 256;           // O's first column; S (and P) buffers from 0, BN columns each
   static constexpr int kQ = NT * 2 * DH * kTile;
   static constexpr int kK = kQ, kVr = kK + kKStages * kTile, kVf = kVr + 2 * kTile, kCtrl = kVf + 4 * kTile;
   static constexpr int kBytes = kCtrl + 2048;
 };
-static_assert(Cfg<128>::kBytes == Cfg<256>::kBytes && Cfg<128>::kBytes + 1024 <= 227 * 1024, "shared memory");
+static_assert(Cfg<128>::kBytes == Cfg<256>::kBytes && Cfg<128>::kBytes + 1024 <= 227 * 1024 && kKStages % 2 == 0, "shared memory");
 
 struct Ctrl {
   uint64_t k_full[kKStages], k_empty[kKStages];
   uint64_t vr_full[2], vr_empty[2], vf_full[2], vf_empty[2];
-  uint64_t s_full[2], p_full[2], o_done[2];
+  uint64_t s_full[2], p_full[2][2];  // (P in halves of its keys)
+  uint64_t o_done;  // one row tile: a product on V is done
   uint64_t e_full[2], e_empty[2];
-  uint64_t q_ready, drain;
+  uint64_t q_ready, drain, o_last[2];  // o_last: a row tile's last product
   uint32_t tmem;
   int abort;
   alignas(16) float4 scale[2][32];  // batches of TB tiles: 2^ek, ev, 2^-ev of each 16-key group
 };
 static_assert(sizeof(Ctrl) <= 2048, "control block");
 
-// D[tmem] (+)= A[tmem] B[smem desc], fp16 operands; called by a converged warp (one elected lane issues).
-__device__ __forceinline__ void umma_f16_ts_warp(uint32_t d, uint32_t a, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+// The two products, four instructions at a time, called by a converged warp: one elected
+// lane issues (the same each time). A descriptor's upper half is constant; offsets are
+// added here. (One election for four: elected one by one the products were issued
+// 43 cycles apart, and the issue bounded the kernel.)
+// D[tmem] (+)= A[smem desc] B[smem desc], e4m3: 128 channels, 32 bytes of the rows a step.
+__device__ __forceinline__ void umma_qk4(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t hi, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p, e;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p, e;\n\t.reg .b64 w, x, y, z, a0, a1, a2, a3;\n\t.reg .b32 t, u, v, r, s, q;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+      "add.u32 t, %2, 2;\n\tadd.u32 u, %2, 4;\n\tadd.u32 v, %2, 6;\n\tadd.u32 r, %1, 2;\n\tadd.u32 s, %1, 4;\n\t"
+      "add.u32 q, %1, 6;\n\tmov.b64 w, {%2, %3};\n\tmov.b64 x, {t, %3};\n\tmov.b64 y, {u, %3};\n\tmov.b64 z, {v, %3};\n\t"
+      "mov.b64 a0, {%1, %3};\n\tmov.b64 a1, {r, %3};\n\tmov.b64 a2, {s, %3};\n\tmov.b64 a3, {q, %3};\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a0, w, %4, p;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a1, x, %4, 1;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a2, y, %4, 1;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a3, z, %4, 1;\n\t}" ::"r"(d),
+      "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// D[tmem] (+)= A[tmem] B[smem desc], fp16: 64 keys, 8 columns of A and 16 rows of B a step.
+__device__ __forceinline__ void umma_pv4(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t hi, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t.reg .b64 w, x, y, z;\n\t.reg .b32 t, u, v, a1, a2, a3;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+      "add.u32 t, %2, 128;\n\tadd.u32 u, %2, 256;\n\tadd.u32 v, %2, 384;\n\tadd.u32 a1, %1, 8;\n\tadd.u32 a2, %1, 16;\n\t"
+      "add.u32 a3, %1, 24;\n\tmov.b64 w, {%2, %3};\n\tmov.b64 x, {t, %3};\n\tmov.b64 y, {u, %3};\n\tmov.b64 z, {v, %3};\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], w, %4, p;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], x, %4, 1;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], y, %4, 1;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], z, %4, 1;\n\t}" ::"r"(d),
+      "r"(a), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate)
       : "memory");
 }
 
@@ -125,6 +162,27 @@ __device__ __forceinline__ void tmem_st16u(uint32_t at, const uint32_t (&r)[16])
       : "memory");
 }
 
+// As tc::mbar_wait, with naps of NAP ns between the looks: most warps here wait most of
+// the time, and their polls take issue slots and shared memory from those that work.
+template <int NAP>
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int* abort) {
+  if (tc::mbar_try_wait(bar, parity)) return true;
+  uint64_t t0 = 0;
+  for (uint32_t it = 0;; ++it) {
+    if constexpr (NAP > 0) __nanosleep(NAP);
+    if (tc::mbar_try_wait(bar, parity)) return true;
+    if ((it & 63u) != 63u) continue;
+    if (*abort) return false;
+    const uint64_t now = tc::globaltimer_ns();
+    if (t0 == 0) {
+      t0 = now;
+    } else if (now - t0 > kWaitNs) {
+      *abort = 1;
+      return false;
+    }
+  }
+}
+
 // two float32 at once: a * b + c
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   float2 d;
@@ -168,11 +226,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   using C = Cfg<D>;
   constexpr int NT = C::NT, BN = C::BN, DH = C::DH, NB = C::NB, TB = C::TB;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  // (32-bit shared addresses throughout, from constants: what the products are issued with stays in uniform registers)
+  const uint32_t raw = tc::smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
+  uint8_t* smem = smem_raw + (base - raw);
   Ctrl& ctl = *reinterpret_cast<Ctrl*>(smem + C::kCtrl);
-  const uint32_t base = tc::smem_u32(smem);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  auto bar = [](uint64_t& b) { return tc::smem_u32(&b); };
+  auto bar = [&](uint64_t& b) {
+    return base + uint32_t(C::kCtrl) + uint32_t(reinterpret_cast<char*>(&b) - reinterpret_cast<char*>(&ctl));
+  };
 
   tc::grid_dependency_wait();
   // The CTA's rows. blockIdx: (KV head and piece, row tiles from the last one on: with a causal
@@ -211,36 +272,37 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::mbar_init(bar(ctl.vf_full[s]), 32 * C::kConvWarps);
       tc::mbar_init(bar(ctl.vf_empty[s]), 1);
       tc::mbar_init(bar(ctl.s_full[s]), 1);
-      tc::mbar_init(bar(ctl.p_full[s]), 128);
-      tc::mbar_init(bar(ctl.o_done[s]), 1);
+      for (int h = 0; h < 2; ++h) tc::mbar_init(bar(ctl.p_full[s][h]), 128);
+      tc::mbar_init(bar(ctl.o_last[s]), 1);
       tc::mbar_init(bar(ctl.e_full[s]), 1);
       tc::mbar_init(bar(ctl.e_empty[s]), 4 * NT);
     }
     tc::mbar_init(bar(ctl.q_ready), 128 * NT);
     tc::mbar_init(bar(ctl.drain), 1);
+    tc::mbar_init(bar(ctl.o_done), 1);
     ctl.abort = 0;
     tc::fence_mbar_init();
   }
-  if (warp == 12 && lane == 0) {
+  if (warp == 0 && lane == 0) {
     tc::prefetch_tmap(&tmap_k);
     tc::prefetch_tmap(&tmap_v);
   }
-  if (warp == 13) {
+  if (warp == 1) {
     tc::tmem_alloc(tc::smem_u32(&ctl.tmem), 512);
     tc::tmem_relinquish();
   }
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
-  const uint32_t tmem = ctl.tmem;
+  constexpr uint32_t tmem = 0;  // all 512 columns: the allocation begins at 0
   volatile int* abort = &ctl.abort;
 
   // Registers: 128 a thread at launch. With two row tiles a softmax thread keeps a row's 128
-  // scores; 2 x 176 + 64 + 96 = 4 x 128 for the four warpgroups.
-  if (warp < 4 * NT) {
-    if constexpr (NT == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
+  // scores; 2 x 192 + 64 + 64 = 4 x 128 for the four warpgroups.
+  if (warp >= 4 && warp < C::kConvWarp0) {
+    if constexpr (NT == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
     // ======================= softmax: thread = row ============================
-    const int a = warp >> 2, quad = warp & 3;
+    const int a = (warp - 4) >> 2, quad = warp & 3;
     const int R = r0 + 128 * a + 32 * quad + lane;
     const bool real = R < rows;
     const int64_t tok = t0 + int64_t(real ? R / p.h_r : 0), head = int64_t(g) * p.h_r + (real ? R % p.h_r : 0);
@@ -302,24 +364,34 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::fence_async_smem();
       tc::mbar_arrive(bar(ctl.q_ready));
     }
-    // the last key this row sees
-    const int lim = real ? min(k_end - 1, p.causal ? L - n + R / p.h_r : k_end - 1) : -1;
+    // The last key this row sees (a row past the end computes something that nobody reads).
+    // The first `open` tiles hide nothing from the warp's rows: their code has no
+    // masks (as selects or predicated they would cost every tile).
+    const int lim = real && p.causal ? min(k_end - 1, L - n + R / p.h_r) : k_end - 1;
+    const int open = max(0, __reduce_min_sync(~0u, lim + 1 - k0)) / BN;
     float m = -INFINITY, l = 0.f;
     bool ok = true;
-    for (int i = 0; i < nt; ++i) {
+    // one tile; false: give up
+    auto tile = [&](auto with_mask, int i) -> bool {
+      constexpr bool masked = decltype(with_mask)::value;
       const int buf = NT == 2 ? a : (i & 1);
       const uint32_t tS = tmem + lanes + uint32_t(buf * BN);
       const int bat = i / TB;
-      if (i % TB == 0) ok = tc::mbar_wait(bar(ctl.e_full[bat & 1]), uint32_t(bat >> 1) & 1u, abort, kWaitNs);
-      ok = ok && tc::mbar_wait(bar(ctl.s_full[buf]), uint32_t(NT == 2 ? i : i >> 1) & 1u, abort, kWaitNs);
+      if (i % TB == 0) ok = wait_bar<0>(bar(ctl.e_full[bat & 1]), uint32_t(bat >> 1) & 1u, abort);
+      // the groups' scales, before the scores are there: the products' operands keep
+      // shared memory busy, and a load from it in the middle of the arithmetic would take long
+      float4 sc[NB];
+#pragma unroll
+      for (int h = 0; h < NB; ++h) {
+        sc[h] = ctl.scale[bat & 1][(i % TB) * NB + h];
+        sc[h].x *= ck;
+      }
+      ok = ok && wait_bar<0>(bar(ctl.s_full[buf]), uint32_t(NT == 2 ? i : i >> 1) & 1u, abort);
       ok = __all_sync(~0u, ok);
-      if (!ok) break;
+      if (!ok) return false;
       tc::tc_fence_after();
-      const float4* sc = &ctl.scale[bat & 1][(i % TB) * NB];
-      const int key0 = k0 + i * BN;
       // column c of the tile is hidden from c = seen on
-      const int seen = lim - key0 + 1;
-      const bool masked = __any_sync(~0u, seen < BN);
+      const int seen = lim - (k0 + i * BN) + 1;
 
       // the tile's largest u
       uint32_t r[BN / 32][32];
@@ -328,13 +400,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       tmem_wait_ld32(r[0]);
 #pragma unroll
       for (int c = 1; c < BN / 32; ++c) tmem_pass32(r[c]);
-      if (masked) {  // (the asm keeps this a branch: as selects it would cost every tile)
-        asm volatile("" ::: "memory");
+      if constexpr (masked) {
 #pragma unroll
         for (int k = 0; k < BN; ++k)
           if (k >= seen) r[k / 32][k % 32] = 0xFF800000u;
       }
-      float top = -INFINITY;
+      float t[NB];
 #pragma unroll
       for (int h = 0; h < NB; ++h) {
         const uint32_t* x = &r[h / 2][16 * (h & 1)];
@@ -345,9 +416,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           my = max3(my, __uint_as_float(x[k + 2]), __uint_as_float(x[k + 3]));
         }
         mx = fmaxf(max3(mx, __uint_as_float(x[14]), __uint_as_float(x[15])), my);
-        const float4 e = sc[h];
-        top = fmaxf(top, fmaf(mx, ck * e.x, e.y));
+        t[h] = fmaf(mx, sc[h].x, sc[h].y);
       }
+      float top = fmaxf(max3(t[0], t[1], t[2]), t[3]);
+      if constexpr (NB == 8) top = max3(top, max3(t[4], t[5], t[6]), t[7]);
       // the reference
       float by = 1.f;
       bool move = false;
@@ -358,10 +430,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         l *= by;
       }
       if (__any_sync(~0u, move)) {
-        // O holds the products up to tile i - 1: rescale it before this tile's
-        ok = __all_sync(~0u, tc::mbar_wait(bar(ctl.o_done[NT == 2 ? a : 0]), uint32_t(i - 1) & 1u, abort, kWaitNs));
-        if (!ok) break;
-        tc::tc_fence_after();
+        // O holds the products up to tile i - 1: rescale it before this tile's. (With two row
+        // tiles this tile's scores were issued behind the last of them. With one they
+        // were issued before it.)
+        if constexpr (NT == 1) {
+          ok = __all_sync(~0u, wait_bar<0>(bar(ctl.o_done), uint32_t(i - 1) & 1u, abort));
+          if (!ok) return false;
+          tc::tc_fence_after();
+        }
         const uint32_t tO = tmem + lanes + C::kO + uint32_t(a * D);
 #pragma unroll 1
         for (int c = 0; c < D; c += 16) {
@@ -373,41 +449,65 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc::tmem_st16(tO + c, v);
         }
       }
-      // P in place of S
+      // P in place of S, 32 keys at a time; a group's sums and stores come behind the
+      // exponentials of the next, which do not wait for them
       const float lift = kLift - (m == -INFINITY ? 0.f : m);
-#pragma unroll
-      for (int c = 0; c < BN / 32; ++c) {
-        uint32_t w[16];
+      auto exps = [&](int c) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const float4 e = sc[2 * c + h];
-          const float2 mul = make_float2(ck * e.x, ck * e.x), add = make_float2(e.y + lift, e.y + lift);
-          float2 sum = make_float2(0.f, 0.f);
+          const float2 mul = make_float2(e.x, e.x), add = make_float2(e.y + lift, e.y + lift);
 #pragma unroll
-          for (int k = 0; k < 16; k += 2) {
-            float2 u = fma2(make_float2(__uint_as_float(r[c][16 * h + k]), __uint_as_float(r[c][16 * h + k + 1])), mul, add);
-            u.x = fast_exp2(u.x);
-            u.y = fast_exp2(u.y);
-            sum = add2(sum, u);
-            w[8 * h + k / 2] = f16x2(u.x, u.y);
+          for (int k = 16 * h; k < 16 * h + 16; k += 2) {
+            const float2 u = fma2(make_float2(__uint_as_float(r[c][k]), __uint_as_float(r[c][k + 1])), mul, add);
+            r[c][k] = __float_as_uint(fast_exp2(u.x));
+            r[c][k + 1] = __float_as_uint(fast_exp2(u.y));
           }
-          l = fmaf(sum.x + sum.y, e.z, l);
+        }
+      };
+      auto store = [&](int c) {
+        uint32_t w[16];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float2 x[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            x[k] = make_float2(__uint_as_float(r[c][16 * h + 2 * k]), __uint_as_float(r[c][16 * h + 2 * k + 1]));
+            w[8 * h + k] = f16x2(x[k].x, x[k].y);
+          }
+#pragma unroll
+          for (int d = 4; d > 0; d >>= 1)
+#pragma unroll
+            for (int k = 0; k < d; ++k) x[k] = add2(x[k], x[k + d]);
+          l = fmaf(x[0].x + x[0].y, sc[2 * c + h].z, l);
         }
         tmem_st16u(tS + 16 * c, w);
+        if (c % (BN / 64) == BN / 64 - 1) {  // half of the keys
+          tc::tmem_wait_st();
+          tc::tc_fence_before();
+          tc::mbar_arrive(bar(ctl.p_full[buf][c / (BN / 64)]));
+        }
+      };
+      exps(0);
+#pragma unroll
+      for (int c = 1; c < BN / 32; ++c) {
+        exps(c);
+        store(c - 1);
       }
-      tc::tmem_wait_st();
-      tc::tc_fence_before();
-      tc::mbar_arrive(bar(ctl.p_full[buf]));
-      if ((i % TB == TB - 1 || i == nt - 1)) {
+      store(BN / 32 - 1);
+      if (i % TB == TB - 1 || i == nt - 1) {
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(bar(ctl.e_empty[bat & 1]));
       }
+      return true;
+    };
+    {
+      int i = 0;
+      bool go = true;
+      for (; i < min(open, nt) && go; ++i) go = tile(std::false_type{}, i);
+      for (; i < nt && go; ++i) go = tile(std::true_type{}, i);
     }
-    // The last product. With two S buffers the one before it may still run, and a wait for
-    // phase nt - 1 passes on phase nt - 3's parity: wait for phase nt - 2 first (phase nt - 3 is
-    // over: the last scores were issued behind it).
-    if (NT == 1 && nt > 1) ok = ok && tc::mbar_wait(bar(ctl.o_done[0]), uint32_t(nt - 2) & 1u, abort, kWaitNs);
-    if (nt > 0) ok = ok && tc::mbar_wait(bar(ctl.o_done[NT == 2 ? a : 0]), uint32_t(nt - 1) & 1u, abort, kWaitNs);
+    if (nt > 0) ok = ok && wait_bar<0>(bar(ctl.o_last[a]), 0, abort);
     if (__all_sync(~0u, ok)) {
       tc::tc_fence_after();
       const float inv = l == 0.f ? 0.f : 1.f / l;
@@ -452,7 +552,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-  } else if (warp < 12) {
+  } else if (warp >= C::kConvWarp0) {
     if constexpr (NT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     // ======================= V to fp16 ========================================
     // [key][128 codes] 128-byte swizzled -> [64 channels][key][64 fp16] likewise
@@ -469,7 +569,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < nt; ++i) {
       const int s = i & 1;
       const uint32_t ph = uint32_t(i >> 1) & 1u;
-      ok = tc::mbar_wait(bar(ctl.vr_full[s]), ph, abort, kWaitNs) && tc::mbar_wait(bar(ctl.vf_empty[s]), ph ^ 1u, abort, kWaitNs);
+      ok = wait_bar<100>(bar(ctl.vr_full[s]), ph, abort) && wait_bar<100>(bar(ctl.vf_empty[s]), ph ^ 1u, abort);
       if (!ok) break;
       const uint8_t* src = src0 + s * kTile;
       uint8_t* dst = dst0 + s * 2 * kTile;
@@ -490,8 +590,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::mbar_arrive(bar(ctl.vf_full[s]));
     }
   } else {
-    if constexpr (NT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
-  if (warp == 12) {
+    if constexpr (NT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+  if (warp == 0) {
     // ======================= TMA: K and V tiles ===============================
     const int box = min(BN, 1 << p.page_shift);  // rows of a copy
     const int per = BN / box;                    // copies a tile, one lane each
@@ -510,7 +610,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int valid = min(per, (k_end - key0 + box - 1) / box);
       const int row = (key0 + lane * box) & ((1 << p.page_shift) - 1);
       auto load = [&](const CUtensorMap* map, uint32_t dst, uint32_t full, uint32_t empty, uint32_t parity) {
-        ok = tc::mbar_wait(empty, parity, abort, kWaitNs);
+        ok = wait_bar<100>(empty, parity, abort);
         ok = __all_sync(~0u, ok);
         if (!ok) return;
         if (lane == 0) tc::mbar_arrive_expect_tx(full, uint32_t(valid * box * D));
@@ -544,7 +644,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-  } else if (warp == 13) {
+  } else if (warp == 1) {
     // ======================= MMA ==============================================
     constexpr uint32_t idesc_qk = tc::idesc_e4m3(128, BN, false, false);
     constexpr uint32_t idesc_pv = idesc_f16(128, D);
@@ -553,73 +653,73 @@ __global__ void __launch_bounds__(kThreads, 1)
     // V: 64-channel columns of blocks BN * 128 bytes apart, 8-key groups 1024
     const uint64_t vd = tc::smem_desc(base + C::kVf, BN * 128, 1024, tc::kSwizzle128B);
     // (votes: the products below are issued by whole warps)
-    bool ok = __all_sync(~0u, tc::mbar_wait(bar(ctl.q_ready), 0, abort, kWaitNs));
-    auto qk = [&](int a, int buf, int i) {
-      const uint32_t d = tmem + uint32_t(buf * BN);
-      const uint64_t k1 = kd + uint64_t((i % kKStages) * (kTile >> 4));
+    bool ok = __all_sync(~0u, wait_bar<0>(bar(ctl.q_ready), 0, abort));
+    // Stages and buffers are constants at every issue (the loop runs over four tiles).
+    auto qk = [&](auto a, auto buf, auto stage) {
 #pragma unroll
       for (int term = 0; term < 2; ++term)
 #pragma unroll
         for (int dh = 0; dh < DH; ++dh)
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            tc::umma_f8f6f4_warp(d, qd + uint64_t(((a * 2 + term) * DH + dh) * (kTile >> 4) + 2 * k),
-                                 k1 + uint64_t(dh * (BN * 128 >> 4) + 2 * k), idesc_qk, term > 0 || dh > 0 || k > 0);
+          umma_qk4(tmem + uint32_t(buf * BN), uint32_t(qd) + ((a * 2 + term) * DH + dh) * (kTile >> 4),
+                   uint32_t(kd) + stage * (kTile >> 4) + dh * (BN * 128 >> 4), uint32_t(kd >> 32), idesc_qk, term > 0 || dh > 0);
       tc::umma_commit_warp(bar(ctl.s_full[buf]));
     };
-    auto pv = [&](int a, int buf, int i) {
-      const uint64_t v1 = vd + uint64_t((i & 1) * (2 * kTile >> 4));
+    auto wait_for = [&](uint64_t& barrier, int use) {
+      ok = ok && __all_sync(~0u, wait_bar<0>(bar(barrier), uint32_t(use) & 1u, abort));
+      return ok;
+    };
+    // row tile a's weights in buffer buf, on V stage vs, as the softmax hands them over
+    auto weigh = [&](auto a, auto buf, auto vs, int i, int use) {
 #pragma unroll
-      for (int k = 0; k < NB; ++k)
-        umma_f16_ts_warp(tmem + C::kO + uint32_t(a * D), tmem + uint32_t(buf * BN + 8 * k), v1 + uint64_t(128 * k), idesc_pv,
-                         i > 0 || k > 0);
-      tc::umma_commit_warp(bar(ctl.o_done[a]));
+      for (int k = 0; k < NB; k += 4) {
+        if (k % (NB / 2) == 0 && !wait_for(ctl.p_full[buf][k / (NB / 2)], use)) return false;
+        if (NB == 4 && !wait_for(ctl.p_full[buf][1], use)) return false;
+        tc::tc_fence_after();
+        umma_pv4(tmem + C::kO + uint32_t(a * D), tmem + uint32_t(buf * BN + 8 * k), uint32_t(vd) + vs * (2 * kTile >> 4) + 128 * k,
+                 uint32_t(vd >> 32), idesc_pv, k > 0 || i > 0);
+      }
+      if (i == nt - 1) tc::umma_commit_warp(bar(ctl.o_last[a]));
+      return true;
     };
-    auto wait_k = [&](int i) {
-      ok = ok && __all_sync(~0u, tc::mbar_wait(bar(ctl.k_full[i % kKStages]), uint32_t(i / kKStages) & 1u, abort, kWaitNs));
-      tc::tc_fence_after();
-      return ok;
+    using I0 = std::integral_constant<int, 0>;
+    using I1 = std::integral_constant<int, 1>;
+    // Tile i's weights, tile i + 1's scores; U = i modulo the period. Products run in the
+    // order they are issued, so a row tile's next scores may be asked for right behind
+    // the product that reads its weights from the same columns. What is sure to come is
+    // waited for at the end of the step before: only the softmaxes' barriers are left
+    // between the products.
+    auto step = [&](auto u, int i) {
+      constexpr int U = decltype(u)::value;
+      using Vs = std::integral_constant<int, U & 1>;
+      using Ks = std::integral_constant<int, (U + 1) % kKStages>;
+      const bool more = i + 1 < nt;
+      if constexpr (NT == 2) {
+        if (!weigh(I0{}, I0{}, Vs{}, i, i)) return;
+        if (more) qk(I0{}, I0{}, Ks{});
+        if (!weigh(I1{}, I1{}, Vs{}, i, i)) return;
+        if (more) qk(I1{}, I1{}, Ks{});
+      } else {
+        if (more) qk(I0{}, std::integral_constant<int, (U + 1) & 1>{}, Ks{});
+        if (!weigh(I0{}, Vs{}, Vs{}, i, i >> 1)) return;
+        tc::umma_commit_warp(bar(ctl.o_done));
+      }
+      if (!more) return;
+      tc::umma_commit_warp(bar(ctl.vf_empty[Vs::value]));
+      tc::umma_commit_warp(bar(ctl.k_empty[Ks::value]));
+      wait_for(ctl.vf_full[(U + 1) & 1], (i + 1) >> 1);
+      if (i + 2 < nt) wait_for(ctl.k_full[(U + 2) % kKStages], (i + 2) / kKStages);
     };
-    auto wait_v = [&](int i) {
-      ok = ok && __all_sync(~0u, tc::mbar_wait(bar(ctl.vf_full[i & 1]), uint32_t(i >> 1) & 1u, abort, kWaitNs));
-      return ok;
-    };
-    auto wait_p = [&](int buf, int parity) {
-      ok = ok && __all_sync(~0u, tc::mbar_wait(bar(ctl.p_full[buf]), uint32_t(parity) & 1u, abort, kWaitNs));
-      tc::tc_fence_after();
-      return ok;
-    };
-    // Products run in the order they are issued, so a tile's next scores may be asked
-    // for right behind the product that reads its weights from the same columns.
-    if (nt > 0 && wait_k(0)) {
-#pragma unroll
-      for (int a = 0; a < NT; ++a) qk(a, a, 0);
+    if (nt > 0 && wait_for(ctl.k_full[0], 0)) {
+      qk(I0{}, I0{}, I0{});
+      if constexpr (NT == 2) qk(I1{}, I1{}, I0{});
       tc::umma_commit_warp(bar(ctl.k_empty[0]));
-      for (int i = 0; i < nt && ok; ++i) {
-        const int j = i + 1;
-        if constexpr (NT == 2) {
-#pragma unroll
-          for (int a = 0; a < 2; ++a) {
-            if (a == 0 && !wait_v(i)) break;
-            if (!wait_p(a, i)) break;
-            pv(a, a, i);
-            if (a == 1) tc::umma_commit_warp(bar(ctl.vf_empty[i & 1]));
-            if (j < nt) {
-              if (a == 0 && !wait_k(j)) break;
-              qk(a, a, j);
-              if (a == 1) tc::umma_commit_warp(bar(ctl.k_empty[j % kKStages]));
-            }
-          }
-        } else {
-          if (j < nt) {
-            if (!wait_k(j)) break;
-            qk(0, j & 1, j);
-            tc::umma_commit_warp(bar(ctl.k_empty[j % kKStages]));
-          }
-          if (!wait_v(i) || !wait_p(i & 1, i >> 1)) break;
-          pv(0, i & 1, i);
-          tc::umma_commit_warp(bar(ctl.vf_empty[i & 1]));
-        }
+      wait_for(ctl.vf_full[0], 0);
+      if (nt > 1) wait_for(ctl.k_full[1], 0);
+      for (int i = 0; i < nt && ok; i += kKStages) {
+        step(I0{}, i);
+        if (ok && i + 1 < nt) step(I1{}, i + 1);
+        if (ok && i + 2 < nt) step(std::integral_constant<int, 2>{}, i + 2);
+        if (ok && i + 3 < nt) step(std::integral_constant<int, 3>{}, i + 3);
       }
     }
     if (!ok) {
@@ -629,7 +729,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       while (!tc::mbar_try_wait(bar(ctl.drain), 0) && tc::globaltimer_ns() - start < kDrainNs) {
       }
     }
-  } else if (warp == 14) {
+  } else if (warp == 2) {
     // ======================= the blocks' scales ================================
     for (int q = 0; q * TB < nt; ++q) {
       const int64_t key = int64_t(k0) + int64_t(q) * TB * BN + lane * 16;
@@ -645,7 +745,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           atomicOr(p.status, kStatusBadPage);
         }
       }
-      if (!__all_sync(~0u, tc::mbar_wait(bar(ctl.e_empty[q & 1]), (uint32_t(q >> 1) & 1u) ^ 1u, abort, kWaitNs))) break;
+      if (!__all_sync(~0u, wait_bar<100>(bar(ctl.e_empty[q & 1]), (uint32_t(q >> 1) & 1u) ^ 1u, abort))) break;
       ctl.scale[q & 1][lane] = make_float4(__int_as_float(ke << 23), float(ve - 127), __int_as_float((254 - ve) << 23), 0.f);
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(bar(ctl.e_full[q & 1]));
@@ -657,7 +757,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc::tc_fence_before();
   __syncthreads();
   if (*abort && tid == 0) atomicOr(p.status, kStatusTimeout);
-  if (warp == 13) {
+  if (warp == 1) {
     tc::tc_fence_after();
     tc::tmem_dealloc(tmem, 512);
   }

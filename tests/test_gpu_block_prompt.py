@@ -257,3 +257,23 @@ def test_the_same_bits_twice():
     for splits in (1, 4):
         one, _, _, q = run(b, [600, 100], 8, splits=splits)
         assert torch.equal(one, run(b, [600, 100], 8, q=q, splits=splits)[0])
+
+
+@pytest.mark.parametrize("d", [128, 256])
+def test_many_calls_in_a_row(d):
+    # every wait of every CTA ends by itself, whatever the order in which its warps come to it
+    import paged_fp8_decode_gb300 as mj
+
+    new = [40, 300, 130, 200, 7]
+    b = Batch([900, 669, 130, 777, 7], d=d, h_k=8, seed=15)
+    kv = b.kv()
+    starts = up(np.concatenate([[0], np.cumsum(new)]).astype(np.int32))
+    q = queries(b, sum(new), 16)
+    out = torch.empty(sum(new), 16, d, dtype=torch.bfloat16, device="cuda")
+    step = mj.PromptStep(max_tokens=sum(new), max_num_seqs=5, max_q_len=300, max_len=900, h_q=16, h_k=8, d=d, splits=1)
+    args = step.args(q, out, kv, b.table_dev, b.lens_dev, starts, 5, d ** -0.5)
+    mj.mj_block_prompt(args)
+    first = out.clone()
+    for _ in range(300):
+        mj.mj_block_prompt(args)
+    assert mj.mj_workspace_status(step.workspace) == 0 and torch.equal(out, first)
