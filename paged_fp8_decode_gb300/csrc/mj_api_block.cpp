@@ -71,10 +71,15 @@ void sides(const mj_block_cache& c, mj::BlockSide (&s)[2]) {
           c.v_exp_stride_head};
 }
 
-int64_t work_rows(int slots, int max_num_seqs) { return max_num_seqs < slots ? slots : int64_t(slots) + max_num_seqs; }
+// A plan's pieces have at least half a slot's share of all tiles: at most two a slot
+// and one a request, and of split requests (over one piece each) at most four a slot.
+int64_t work_rows(int slots, int max_num_seqs) { return 2 * int64_t(slots) + max_num_seqs; }
+int64_t part_cap(int slots) { return 4 * int64_t(slots); }
 
-// Partial rows (a piece of a split request) that a plan can have: at most 2 a slot.
-int64_t part_cap(int slots) { return 2 * int64_t(slots); }
+// What starting, ending and joining a piece costs, in tiles, and how much of the
+// longest piece the slots that end early wait for the last one. Fitted to the batches
+// of mj_block_plan's comment.
+constexpr double kPieceTiles = 4, kTail = 0.2;
 
 bool slots_ok(int slots) { return slots >= 1 && slots <= (1 << 20); }
 
@@ -175,33 +180,53 @@ int mj_block_plan(const int32_t* seq_lens_host, int num_seqs, int max_num_seqs, 
   auto tiles = [&](int b) -> int64_t {
     return seq_lens_host[b] > 0 ? ceil_div(int64_t(seq_lens_host[b]) + margin, mj::kKvTile) : 0;
   };
-  int64_t total = 0, longest = 1, live = 0;
+  int64_t total = 0, longest = 1;
   for (int b = 0; b < num_seqs; ++b) {
     const int64_t t = tiles(b);
     total += t;
     longest = std::max(longest, t);
-    live += t > 0;
   }
-  // Tiles a piece has at most. With fewer requests than slots: the least with which
-  // all pieces run at once (one wave). With more: a slot's share, so that no piece
-  // outlasts the rest; requests of up to a share stay whole.
-  auto pieces = [&](int64_t c) {
+  // Tiles a piece has at most: between half a slot's share of all and the longest
+  // request, where the last slot is expected to end first. If all pieces run at once (one a
+  // slot), that is the longest piece; else the slots' common load and part of the longest. Few or equal requests
+  // stay in one wave that way; a long request among short ones is cut however many there are
+  // (34 requests of 200 to 16384 tokens, 16 query rows, 38 slots: XX us in one wave, YY so).
+  const int64_t least = std::max<int64_t>(1, (total + 2 * int64_t(slots) - 1) / (2 * int64_t(slots)));
+  auto pieces = [&](int64_t c, int64_t* most) {
     int64_t n = 0;
-    for (int b = 0; b < num_seqs; ++b) n += ceil_div(tiles(b), c);
+    *most = 1;
+    for (int b = 0; b < num_seqs; ++b) {
+      const int64_t t = tiles(b), k = ceil_div(t, c);
+      n += k;
+      if (k > 0) *most = std::max(*most, ceil_div(t, k));
+    }
     return n;
   };
-  int64_t chunk = std::max<int64_t>(1, ceil_div(total, slots));
-  if (live <= slots) {
-    int64_t lo = chunk, hi = longest;  // pieces(longest) = live
+  int64_t chunk = std::max(longest, least);
+  double best = 1e300;
+  auto consider = [&](int64_t c) {
+    int64_t most;
+    const int64_t n = pieces(c, &most);
+    const double end = n <= slots ? double(most) + kPieceTiles
+                                  : (double(total) + kPieceTiles * double(n)) / slots + kTail * double(most);
+    if (end < best) {
+      best = end;
+      chunk = c;
+    }
+  };
+  for (int64_t c = chunk; c > least; c = std::min(c - 1, c * 15 / 16)) consider(std::max(c, least));
+  consider(least);
+  int64_t lo = least, hi = std::max(longest, least);  // the least with which one wave holds all
+  if (int64_t most; pieces(hi, &most) <= slots) {
     while (lo < hi) {
       const int64_t mid = lo + (hi - lo) / 2;
-      if (pieces(mid) <= slots)
+      if (pieces(mid, &most) <= slots)
         hi = mid;
       else
         lo = mid + 1;
     }
-    chunk = std::max(lo, chunk);
   }
+  consider(lo);
   const int64_t rows = work_rows(slots, max_num_seqs);
   int32_t* work = plan_host;
   int32_t* req = plan_host + 4 * rows;
@@ -217,7 +242,7 @@ int mj_block_plan(const int32_t* seq_lens_host, int num_seqs, int max_num_seqs, 
     r[3] = int32_t(t);
     if (r[1] > 1) part += r[1];
   }
-  if (part > part_cap(slots)) return MJ_ERR_CAPACITY;  // cannot be: a split request has over one share
+  if (part > part_cap(slots)) return MJ_ERR_CAPACITY;  // cannot be
   // the longest pieces first, so that the last to start are short ones
   struct Row {
     int32_t b, begin, end, s;
@@ -227,7 +252,7 @@ int mj_block_plan(const int32_t* seq_lens_host, int num_seqs, int max_num_seqs, 
   for (int b = 0; b < num_seqs; ++b) {
     const int32_t* r = req + 4 * int64_t(b);
     for (int s = 0; s < r[1]; ++s) {
-      if (at >= rows) return MJ_ERR_CAPACITY;  // cannot be: a request has at most one piece that is no full share
+      if (at >= rows) return MJ_ERR_CAPACITY;  // cannot be
       out[at++] = {b, s * r[2], int32_t(std::min<int64_t>((s + int64_t(1)) * r[2], r[3])), s};
     }
   }
