@@ -725,13 +725,15 @@ MJ_API int mj_block_read_kv(const mj_block_read_args* args, void* stream);
 /* ------------------------------------------------------------------------
  * The block-scaled plan: like mj_plan_split_kv's, but every request is cut into
  * pieces of its own equal length, so that a long request among short ones is
- * split however many requests there are. slots: mj_slots(...). The plan is one
+ * split however many requests there are. slots: mj_block_slots(...), the pieces of a KV head that
+ * sm_count SMs run at once. The plan is one
  * buffer of mj_block_plan_size() int32 words (a multiple of 4): copy it with
  * mj_plan_upload(plan_host, NULL, plan_dev, NULL, words / 4, 0, stream). Lengths
  * are exact or an upper bound (margin: tokens added to each that is not 0).
  * mj_block_workspace_size: bytes of mj_block_attention's workspace, the status
  * header (mj_workspace_init, mj_workspace_status) and the pieces' partials.
  * ---------------------------------------------------------------------- */
+MJ_API int mj_block_slots(int sm_count, int q_len, int h_q, int h_k, int d);
 MJ_API int mj_block_plan_size(int slots, int max_num_seqs, size_t* words);
 MJ_API int mj_block_plan(const int32_t* seq_lens_host, int num_seqs, int max_num_seqs, int slots, int margin,
                   int32_t* plan_host, size_t plan_words);

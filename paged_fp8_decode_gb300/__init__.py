@@ -53,7 +53,7 @@ EXPORTS = (
     "mj_plan_upload", "mj_decode_kernel",
     "mj_rope_turns", "mj_rope_write_kv", "mj_latent_write", "mj_latent_slots", "mj_latent_plan_size",
     "mj_latent_plan", "mj_latent_workspace_size", "mj_latent_attention",
-    "mj_block_write_kv", "mj_block_read_kv", "mj_block_plan_size", "mj_block_plan", "mj_block_workspace_size",
+    "mj_block_write_kv", "mj_block_read_kv", "mj_block_slots", "mj_block_plan_size", "mj_block_plan", "mj_block_workspace_size",
     "mj_block_attention", "mj_block_prompt_splits", "mj_block_prompt_workspace_size", "mj_block_prompt",
 )
 
@@ -288,6 +288,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.mj_latent_attention.argtypes = [ctypes.POINTER(mj_latent_args), vp]
     lib.mj_block_write_kv.argtypes = [ctypes.POINTER(mj_block_write_args), vp]
     lib.mj_block_read_kv.argtypes = [ctypes.POINTER(mj_block_read_args), vp]
+    lib.mj_block_slots.argtypes = [i32, i32, i32, i32, i32]
     lib.mj_block_plan_size.argtypes = [i32, i32, ctypes.POINTER(sz)]
     lib.mj_block_plan.argtypes = [vp, i32, i32, i32, i32, vp, sz]
     lib.mj_block_workspace_size.argtypes = [i32, i32, i32, i32, i32, ctypes.POINTER(sz)]
@@ -581,6 +582,10 @@ def mj_block_read_kv(args: mj_block_read_args, stream=None):
     """Bring cached tokens back as rows (:func:`block_read_args` builds ``args``)."""
     _on_device(args)
     _check("mj_block_read_kv", load_library().mj_block_read_kv(ctypes.byref(args), _stream(stream)))
+
+
+def mj_block_slots(sm_count: int, q_len: int, h_q: int, h_k: int, d: int) -> int:
+    return load_library().mj_block_slots(sm_count, q_len, h_q, h_k, d)
 
 
 def mj_block_plan_size(slots: int, max_num_seqs: int) -> int:

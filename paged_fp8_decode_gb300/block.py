@@ -17,8 +17,8 @@ import torch
 
 from . import (MJ_OUT_BF16, MJ_OUT_F16, _check, _same_device, _stream, load_library, mj_block_args, mj_block_attention,
                mj_block_cache, mj_block_plan, mj_block_plan_size, mj_block_prompt, mj_block_prompt_args,
-               mj_block_prompt_splits, mj_block_prompt_workspace_size, mj_block_read_args, mj_block_workspace_size,
-               mj_block_write_args, mj_slots, mj_workspace_init)
+               mj_block_prompt_splits, mj_block_prompt_workspace_size, mj_block_read_args, mj_block_slots,
+               mj_block_workspace_size, mj_block_write_args, mj_workspace_init)
 from .step import _flat, _hold, _rows, _tensor
 
 
@@ -153,14 +153,14 @@ class BlockStep:
     need a BlockStep each (they share its workspace)."""
 
     def __init__(self, *, max_num_seqs: int, q_len: int, h_q: int, h_k: int, d: int, sm_count: int | None = None,
-                 ctas_per_sm: int = 2, margin: int = 0, causal: bool = True, evict_first: bool = True, device="cuda",
+                 margin: int = 0, causal: bool = True, evict_first: bool = True, device="cuda",
                  with_lse: bool = False):
         self.device = torch.device(device)
         if sm_count is None:
             sm_count = torch.cuda.get_device_properties(self.device).multi_processor_count
         self.max_num_seqs, self.q_len, self.h_q, self.h_k, self.d = max_num_seqs, q_len, h_q, h_k, d
         self.margin, self.causal, self.evict_first = margin, causal, evict_first
-        self.slots = mj_slots(sm_count, ctas_per_sm, h_k, q_len, h_q)
+        self.slots = mj_block_slots(sm_count, q_len, h_q, h_k, d)
         words = mj_block_plan_size(self.slots, max_num_seqs)
         self.plan_dev = torch.zeros(words, dtype=torch.int32, device=self.device)
         self.plan_host = torch.zeros(words, dtype=torch.int32).pin_memory()

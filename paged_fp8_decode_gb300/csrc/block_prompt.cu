@@ -43,28 +43,29 @@ namespace mj {
 
 namespace {
 
-constexpr int kThreads = 512;
 constexpr uint64_t kWaitNs = 2000000000ull, kDrainNs = 100000000ull;
 constexpr float kTau = 8.f, kLift = 6.f;  // log2 units
 constexpr int kKStages = 4;              // (a multiple of V's two: the MMA loop's period)
 constexpr int kTile = 16384;              // bytes: 128 rows of 128, and a K or V tile
 
-template <int D>
+// Row tiles of 128: head size 128 has two where a CTA has that many rows, else one.
+template <int D, int NT_>
 struct Cfg {
-  static constexpr int NT = D == 128 ? 2 : 1;   // row tiles
+  static constexpr int NT = NT_;
   static constexpr int BN = D == 128 ? 128 : 64;
   static constexpr int DH = D / 128;
   static constexpr int NB = BN / 16;            // 16-key groups of a tile
   static constexpr int TB = 32 / NB;            // tiles a batch of scales covers
   // warps: 0 TMA, 1 MMA, 2 the blocks' scales, 4 .. softmax, then the ones that widen V
-  static constexpr int kConvWarp0 = 4 + 4 * NT, kConvWarps = 16 - kConvWarp0;
+  static constexpr int kConvWarp0 = 4 + 4 * NT, kConvWarps = 16 - kConvWarp0, kThreads = 512;
   static constexpr int kRows = 128 * NT;
   static constexpr uint32_t kO = 256;           // O's first column; S (and P) buffers from 0, BN columns each
   static constexpr int kQ = NT * 2 * DH * kTile;
   static constexpr int kK = kQ, kVr = kK + kKStages * kTile, kVf = kVr + 2 * kTile, kCtrl = kVf + 4 * kTile;
   static constexpr int kBytes = kCtrl + 2048;
 };
-static_assert(Cfg<128>::kBytes == Cfg<256>::kBytes && Cfg<128>::kBytes + 1024 <= 227 * 1024 && kKStages % 2 == 0, "shared memory");
+static_assert(Cfg<128, 2>::kBytes + 1024 <= 227 * 1024 && Cfg<256, 1>::kBytes + 1024 <= 227 * 1024 && kKStages % 2 == 0,
+              "shared memory");
 
 struct Ctrl {
   uint64_t k_full[kKStages], k_empty[kKStages];
@@ -183,6 +184,15 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile
   }
 }
 
+// This warpgroup's registers a thread from here on.
+template <bool MORE, int N>
+__device__ __forceinline__ void set_regs() {
+  if constexpr (MORE)
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+  else
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 // two float32 at once: a * b + c
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   float2 d;
@@ -219,12 +229,12 @@ __device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t two) {
   return r;
 }
 
-template <int D>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int D, int NT>
+__global__ void __launch_bounds__(512, 1)
     block_prompt_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
                         BlockPromptParams p) {
-  using C = Cfg<D>;
-  constexpr int NT = C::NT, BN = C::BN, DH = C::DH, NB = C::NB, TB = C::TB;
+  using C = Cfg<D, NT>;
+  constexpr int BN = C::BN, DH = C::DH, NB = C::NB, TB = C::TB;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   // (32-bit shared addresses throughout, from constants: what the products are issued with stays in uniform registers)
   const uint32_t raw = tc::smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
@@ -236,30 +246,57 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
 
   tc::grid_dependency_wait();
-  // The CTA's rows. blockIdx: (KV head and piece, row tiles from the last one on: with a causal
-  // limit the longest, request)
-  const int piece = int(blockIdx.x) % p.splits, g = int(blockIdx.x) / p.splits, b = blockIdx.z;
-  const int t0 = max(0, p.q_starts[b]), n = min(p.q_starts[b + 1], p.num_tokens) - t0;
-  const int rows = min(n, p.max_q_len) * p.h_r;
-  const int n_tiles_rows = (rows + C::kRows - 1) / C::kRows;
-  if (n > p.max_q_len && blockIdx.x == 0 && blockIdx.y == 0) {
-    if (tid == 0) atomicOr(p.status, kStatusBadPlan);
-    if (p.splits > 1)  // the join passes these rows by
-      for (int64_t i = tid; i < int64_t(n - p.max_q_len) * p.h_q; i += kThreads)
-        p.l_part[(int64_t(t0) + p.max_q_len) * p.h_q + i] = -1.f;
+  // The CTA's rows r0 .. of request b and KV head g, the request's first query token t0 of n, and
+  // its keys: k0 .. k_end - 1, nt tiles. parts: where the rows' partials begin (-1: there is one piece).
+  int b, g, t0, n, rows, r0, L, k0, k_end;
+  int64_t parts = -1;
+  if (p.work) {
+    // decode: work row and KV head, row tile
+    g = int(blockIdx.x % unsigned(p.h_k));
+    const int4 w = p.work[blockIdx.x / unsigned(p.h_k)];
+    if (w.z <= w.y || w.x < 0 || w.x >= p.num_seqs) return;
+    b = w.x;
+    const int4 rq = p.req[b];  // first partial, pieces, tiles a piece, tiles planned
+    L = p.seq_lens[b];
+    const bool bad = w.w < 0 || w.w >= rq.y || (rq.y > 1 && (rq.x < 0 || int64_t(rq.x) + rq.y > p.part_cap));
+    if (tid == 0 && (bad || (w.w == 0 && int64_t(L) > int64_t(rq.w) * kKvTile))) atomicOr(p.status, kStatusBadPlan);
+    n = p.max_q_len;
+    t0 = b * n;
+    rows = n * p.h_r;
+    r0 = int(blockIdx.y) * C::kRows;
+    k0 = w.y * kKvTile;
+    if (bad || L <= k0) return;  // (a piece without keys: the join does not count it)
+    k_end = int(min(int64_t(L), int64_t(w.z) * kKvTile));
+    if (rq.y > 1) parts = ((int64_t(rq.x) + w.w) * p.h_k + g) * rows;
+  } else {
+    // prompt: KV head and piece, row tiles from the last one on (with a causal limit the longest), request
+    const int piece = int(blockIdx.x) % p.splits;
+    g = int(blockIdx.x) / p.splits;
+    b = blockIdx.z;
+    t0 = max(0, p.q_starts[b]);
+    n = min(p.q_starts[b + 1], p.num_tokens) - t0;
+    rows = min(n, p.max_q_len) * p.h_r;
+    const int row_tiles = (rows + C::kRows - 1) / C::kRows;
+    if (n > p.max_q_len && blockIdx.x == 0 && blockIdx.y == 0) {
+      if (tid == 0) atomicOr(p.status, kStatusBadPlan);
+      if (p.splits > 1)  // the join passes these rows by
+        for (int64_t i = tid; i < int64_t(n - p.max_q_len) * p.h_q; i += C::kThreads)
+          p.l_part[(int64_t(t0) + p.max_q_len) * p.h_q + i] = -1.f;
+    }
+    if (int(blockIdx.y) >= row_tiles) return;
+    r0 = (row_tiles - 1 - int(blockIdx.y)) * C::kRows;
+    L = p.seq_lens[b];
+    // this piece of the tiles up to the last key that any of the rows sees
+    const int last = min(L - 1, p.causal ? L - n + (min(rows, r0 + C::kRows) - 1) / p.h_r : L - 1);
+    const int tiles = last >= 0 ? last / BN + 1 : 0;
+    const int each = (tiles + p.splits - 1) / p.splits;
+    k0 = min(tiles, piece * each) * BN;
+    k_end = min(L, min(tiles, (piece + 1) * each) * BN);
+    if (p.splits > 1) parts = (int64_t(piece) * p.num_tokens + t0) * p.h_q;
   }
-  if (int(blockIdx.y) >= n_tiles_rows) return;
-  const int r0 = (n_tiles_rows - 1 - int(blockIdx.y)) * C::kRows;
-  const int nr = min(C::kRows, rows - r0);
-  const int L = p.seq_lens[b];
-  // the last key that any of the rows sees, and this piece of the tiles up to there
-  const int last = min(L - 1, p.causal ? L - n + (r0 + nr - 1) / p.h_r : L - 1);
-  const int tiles = last >= 0 ? last / BN + 1 : 0;
-  const int each = (tiles + p.splits - 1) / p.splits;
-  const int first_tile = min(tiles, piece * each);
-  const int nt = min(tiles, first_tile + each) - first_tile;
-  const int k0 = first_tile * BN;
-  const int k_end = min(L, (first_tile + nt) * BN);  // keys from here on are not this CTA's
+  if (r0 >= rows) return;
+  if (p.causal) k_end = min(k_end, L - n + (min(rows, r0 + C::kRows) - 1) / p.h_r + 1);
+  const int nt = k_end > k0 ? (k_end - k0 + BN - 1) / BN : 0;
 
   if (tid == 0) {
     for (int s = 0; s < kKStages; ++s) {
@@ -297,10 +334,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr uint32_t tmem = 0;  // all 512 columns: the allocation begins at 0
   volatile int* abort = &ctl.abort;
 
-  // Registers: 128 a thread at launch. With two row tiles a softmax thread keeps a row's 128
-  // scores; 2 x 192 + 64 + 64 = 4 x 128 for the four warpgroups.
+  // Registers: 128 a thread at launch. At head size 128 a softmax thread keeps a row's 128
+  // scores: 2 x 192 + 2 x 64, or 224 + 3 x 96, = 4 x 128 for the four warpgroups.
   if (warp >= 4 && warp < C::kConvWarp0) {
-    if constexpr (NT == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+    if constexpr (D == 128) set_regs<true, NT == 2 ? 192 : 224>();
     // ======================= softmax: thread = row ============================
     const int a = (warp - 4) >> 2, quad = warp & 3;
     const int R = r0 + 128 * a + 32 * quad + lane;
@@ -512,7 +549,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::tc_fence_after();
       const float inv = l == 0.f ? 0.f : 1.f / l;
       const bool some = nt > 0 && !(l == 0.f);
-      const int64_t unit = tok * p.h_q + head, part = int64_t(piece) * p.num_tokens * p.h_q + unit;
+      // the row's place in its partials and in the LSE
+      const int64_t part = parts + (p.work ? R : (tok - t0) * p.h_q + head);
+      const int64_t lse_at = p.work ? (int64_t(b) * p.h_k + g) * rows + R : tok * p.h_q + head;
 #pragma unroll 1
       for (int c = 0; c < D; c += 32) {
         uint32_t r[32];
@@ -521,7 +560,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_wait_ld32(r);
         }
         if (!real) continue;
-        if (p.splits > 1) {
+        if (parts >= 0) {
           if (!some) continue;
           float4* dst = reinterpret_cast<float4*>(p.o_part + part * D + c);
 #pragma unroll
@@ -543,17 +582,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (real) {
-        if (p.splits > 1) {
+        if (parts >= 0) {
           // m counts V's scales in, l does not: together 2^m l = sum 2^t
           p.m_part[part] = some ? fmaxf(m, -1e30f) - kLift : -INFINITY;
           p.l_part[part] = some ? l : 0.f;
         } else if (p.lse) {
-          p.lse[unit] = some ? (m - kLift + fast_log2(l)) * kLn2 : -INFINITY;
+          p.lse[lse_at] = some ? (m - kLift + fast_log2(l)) * kLn2 : -INFINITY;
         }
       }
     }
   } else if (warp >= C::kConvWarp0) {
-    if constexpr (NT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    if constexpr (D == 128) set_regs<false, NT == 2 ? 64 : 96>();
     // ======================= V to fp16 ========================================
     // [key][128 codes] 128-byte swizzled -> [64 channels][key][64 fp16] likewise
     const int ct = tid - 32 * C::kConvWarp0;
@@ -590,12 +629,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::mbar_arrive(bar(ctl.vf_full[s]));
     }
   } else {
-    if constexpr (NT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    if constexpr (D == 128) set_regs<false, NT == 2 ? 64 : 96>();
   if (warp == 0) {
     // ======================= TMA: K and V tiles ===============================
     const int box = min(BN, 1 << p.page_shift);  // rows of a copy
     const int per = BN / box;                    // copies a tile, one lane each
-    const uint64_t pol = tc::l2_policy_evict_normal();
+    const uint64_t pol = p.evict_first ? tc::l2_policy_evict_first() : tc::l2_policy_evict_normal();
     auto page_of = [&](int i) {  // of this lane's copy of tile i
       const int64_t key = int64_t(k0) + int64_t(i) * BN + lane * box;
       const int64_t e = key >> p.page_shift;
@@ -779,24 +818,26 @@ bool encode(CUtensorMap* map, const BlockSide& s, const BlockPromptParams& p, in
             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D>
+template <int D, int NT>
 cudaError_t launch(const CUtensorMap& mk, const CUtensorMap& mv, const BlockPromptParams& p, cudaStream_t stream) {
-  constexpr int bytes = Cfg<D>::kBytes + 1024;
+  using C = Cfg<D, NT>;
+  constexpr int bytes = C::kBytes + 1024;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   static std::atomic<int> configured[64];  // the shared-memory limit is raised once per device
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!configured[dev].load(std::memory_order_acquire)) {
-    e = cudaFuncSetAttribute(block_prompt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    e = cudaFuncSetAttribute(block_prompt_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
     configured[dev].store(1, std::memory_order_release);
   }
-  const int64_t tiles = (int64_t(p.max_q_len) * p.h_r + Cfg<D>::kRows - 1) / Cfg<D>::kRows;
-  if (tiles > 65535) return cudaErrorInvalidConfiguration;
+  const int64_t tiles = (int64_t(p.max_q_len) * p.h_r + C::kRows - 1) / C::kRows;
+  const int64_t x = p.work ? int64_t(p.num_work) * p.h_k : int64_t(p.h_k) * p.splits;
+  if (tiles > 65535 || x > INT32_MAX) return cudaErrorInvalidConfiguration;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(p.h_k * p.splits), unsigned(tiles), unsigned(p.num_seqs));
-  cfg.blockDim = dim3(kThreads);
+  cfg.gridDim = dim3(unsigned(x), unsigned(tiles), p.work ? 1u : unsigned(p.num_seqs));
+  cfg.blockDim = dim3(C::kThreads);
   cfg.dynamicSmemBytes = bytes;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -804,21 +845,23 @@ cudaError_t launch(const CUtensorMap& mk, const CUtensorMap& mv, const BlockProm
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, block_prompt_kernel<D>, mk, mv, p);
+  return cudaLaunchKernelEx(&cfg, block_prompt_kernel<D, NT>, mk, mv, p);
 }
 
 }  // namespace
 
-int block_prompt_rows(int d) { return d == 256 ? Cfg<256>::kRows : Cfg<128>::kRows; }
+int block_prompt_rows(int d, int64_t rows) { return d == 128 && rows > 128 ? 256 : 128; }
 
 cudaError_t launch_block_prompt(BlockPromptParams p, cudaStream_t stream, bool* unsupported) {
   const BlockSide &k = p.side[0], &v = p.side[1];
   p.tma_head_inner = k.sh < k.st ? 1 : 0;
-  const int rows = std::min(p.d == 256 ? Cfg<256>::BN : Cfg<128>::BN, 1 << p.page_shift);
+  const int rows = std::min(p.d == 256 ? Cfg<256, 1>::BN : Cfg<128, 2>::BN, 1 << p.page_shift);
   CUtensorMap mk, mv;
   *unsupported = k.sp == 0 || v.sp == 0 || (v.sh < v.st) != (k.sh < k.st) || !encode(&mk, k, p, rows) || !encode(&mv, v, p, rows);
   if (*unsupported) return cudaSuccess;
-  return p.d == 256 ? launch<256>(mk, mv, p, stream) : launch<128>(mk, mv, p, stream);
+  if (p.d == 256) return launch<256, 1>(mk, mv, p, stream);
+  return block_prompt_rows(p.d, int64_t(p.max_q_len) * p.h_r) == 256 ? launch<128, 2>(mk, mv, p, stream)
+                                                                       : launch<128, 1>(mk, mv, p, stream);
 }
 
 }  // namespace mj

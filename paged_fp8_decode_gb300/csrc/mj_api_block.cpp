@@ -81,6 +81,10 @@ int64_t part_cap(int slots) { return 4 * int64_t(slots); }
 // of mj_block_plan's comment.
 constexpr double kPieceTiles = 4, kTail = 0.2;
 
+// Which kernel attends: the decode kernel (keys on the tensor cores' rows, so that a few
+// query rows fill them) or the prompt's (query rows there, 128 at a time). Measured, see there.
+bool by_rows(int d, int64_t n_q) { return d == 128 ? n_q > 8 : n_q > 8; }
+
 bool slots_ok(int slots) { return slots >= 1 && slots <= (1 << 20); }
 
 }  // namespace
@@ -158,6 +162,14 @@ int mj_block_read_kv(const mj_block_read_args* a, void* stream) {
   p.side0 = a->k_out ? 0 : 1;
   p.status = a->status;
   return status_of(mj::launch_block_read(p, c.d, static_cast<cudaStream_t>(stream)));
+}
+
+int mj_block_slots(int sm_count, int q_len, int h_q, int h_k, int d) {
+  if (sm_count < 1 || q_len < 1 || h_k < 1 || h_q < h_k || h_q % h_k || !mj::head_dim_ok(d)) return 1;
+  const int64_t n_q = int64_t(q_len) * (h_q / h_k);
+  if (!by_rows(d, n_q)) return mj_slots(sm_count, 2, h_k, q_len, h_q);
+  const int64_t tiles = ceil_div(n_q, mj::block_prompt_rows(d, n_q));
+  return int(std::max<int64_t>(1, sm_count / (h_k * tiles)));
 }
 
 int mj_block_plan_size(int slots, int max_num_seqs, size_t* words) {
@@ -298,87 +310,130 @@ int mj_block_attention(const mj_block_args* a, void* stream) {
   if (a->num_seqs == 0) return MJ_OK;
 
   const int h_r = a->h_q / c.h_k, n_q = a->q_len * h_r;
-  mj::DecodeParams p = {};
-  p.num_seqs = a->num_seqs;
-  p.q_len = a->q_len;
-  p.h_q = a->h_q;
-  p.h_k = c.h_k;
-  p.h_r = h_r;
-  p.n_q = n_q;
-  p.d = c.d;
-  p.causal = a->causal ? 1 : 0;
-  p.kv_format = MJ_KV_E4M3;
-  p.page_size = c.page_size;
-  p.row_bytes = c.d;
-  p.num_pages = c.num_pages;
-  p.tw = mj_tile_width(n_q);
-  p.n_row_tiles = int(ceil_div(n_q, p.tw));
-  p.q_mode = mj::kQBlock;
-  p.q_bf16 = static_cast<const uint16_t*>(a->q);
-  p.q_ts = a->q_tok_stride;
-  p.q_hs = a->q_head_stride;
-  p.k_cache = static_cast<const uint8_t*>(c.k_cache);
-  p.v_cache = static_cast<const uint8_t*>(c.v_cache);
-  p.k_sp = c.k_stride_page;
-  p.k_st = c.k_stride_token;
-  p.k_sh = c.k_stride_head;
-  p.v_sp = c.v_stride_page;
-  p.v_st = c.v_stride_token;
-  p.v_sh = c.v_stride_head;
-  p.k_exp = c.k_exp;
-  p.v_exp = c.v_exp;
-  p.ke_sp = c.k_exp_stride_page;
-  p.ke_sh = c.k_exp_stride_head;
-  p.ve_sp = c.v_exp_stride_page;
-  p.ve_sh = c.v_exp_stride_head;
-  p.page_shift = mj::page_shift(c.page_size);
-  p.block_shift = mj::page_shift(c.block);
-  p.block_table = a->block_table;
-  p.bt_stride = a->block_table_stride;
-  p.bt_len = a->block_table_len;
-  p.seq_lens = a->seq_lens;
-  const int64_t rows = work_rows(a->slots, a->max_num_seqs);
-  p.work = a->plan;
-  p.req = reinterpret_cast<const int4*>(a->plan + 4 * rows);
-  p.num_work = int(rows);
-  p.with_reduction = 1;
-  p.part_cap = int(part_cap(a->slots));
-  p.qk_scale_log2 = a->softmax_scale * 1.4426950408889634f;
-  p.v_fmt = 1.f;
-  p.out = static_cast<uint16_t*>(a->out);
-  p.out_f16 = a->out_dtype == MJ_OUT_F16 ? 1 : 0;
-  p.out_ts = a->out_tok_stride;
-  p.out_hs = a->out_head_stride;
-  p.lse = a->lse;
   char* ws = static_cast<char*>(a->workspace);
-  p.status = reinterpret_cast<uint32_t*>(ws);
-  const int64_t parts = part_cap(a->slots) * c.h_k * n_q;
-  p.o_part = reinterpret_cast<float*>(ws + mj::kWsHeader);
-  p.m_part = p.o_part + parts * c.d;
-  p.l_part = p.m_part + parts;
-  p.evict_first = a->evict_first;
+  const int64_t parts = part_cap(a->slots) * c.h_k * n_q, rows = work_rows(a->slots, a->max_num_seqs);
+  float* o_part = reinterpret_cast<float*>(ws + mj::kWsHeader);
+  const int4* req = reinterpret_cast<const int4*>(a->plan + 4 * rows);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
   bool unsupported = false;
-  cudaError_t e = mj::launch_decode_block(p, static_cast<cudaStream_t>(stream), &unsupported);
+  cudaError_t e = cudaSuccess;
+  if (by_rows(c.d, n_q)) {
+    mj::BlockPromptParams p = {};
+    p.num_seqs = a->num_seqs;
+    p.num_tokens = a->num_seqs * a->q_len;
+    p.max_q_len = a->q_len;
+    p.splits = 1;
+    p.h_q = a->h_q;
+    p.h_k = c.h_k;
+    p.h_r = h_r;
+    p.d = c.d;
+    p.causal = a->causal ? 1 : 0;
+    p.scale_log2 = a->softmax_scale * 1.4426950408889634f;
+    p.q = static_cast<const uint16_t*>(a->q);
+    p.q_ts = a->q_tok_stride;
+    p.q_hs = a->q_head_stride;
+    p.page_shift = mj::page_shift(c.page_size);
+    p.block_shift = mj::page_shift(c.block);
+    p.num_pages = c.num_pages;
+    sides(c, p.side);
+    p.block_table = a->block_table;
+    p.bt_stride = a->block_table_stride;
+    p.bt_len = a->block_table_len;
+    p.seq_lens = a->seq_lens;
+    p.out = static_cast<uint16_t*>(a->out);
+    p.out_f16 = a->out_dtype == MJ_OUT_F16 ? 1 : 0;
+    p.out_ts = a->out_tok_stride;
+    p.out_hs = a->out_head_stride;
+    p.lse = a->lse;
+    p.status = reinterpret_cast<uint32_t*>(ws);
+    p.o_part = o_part;
+    p.m_part = o_part + parts * c.d;
+    p.l_part = p.m_part + parts;
+    p.evict_first = a->evict_first;
+    p.work = reinterpret_cast<const int4*>(a->plan);
+    p.req = req;
+    p.num_work = int(rows);
+    p.part_cap = int(part_cap(a->slots));
+    e = mj::launch_block_prompt(p, s, &unsupported);
+  } else {
+    mj::DecodeParams p = {};
+    p.num_seqs = a->num_seqs;
+    p.q_len = a->q_len;
+    p.h_q = a->h_q;
+    p.h_k = c.h_k;
+    p.h_r = h_r;
+    p.n_q = n_q;
+    p.d = c.d;
+    p.causal = a->causal ? 1 : 0;
+    p.kv_format = MJ_KV_E4M3;
+    p.page_size = c.page_size;
+    p.row_bytes = c.d;
+    p.num_pages = c.num_pages;
+    p.tw = mj_tile_width(n_q);
+    p.n_row_tiles = int(ceil_div(n_q, p.tw));
+    p.q_mode = mj::kQBlock;
+    p.q_bf16 = static_cast<const uint16_t*>(a->q);
+    p.q_ts = a->q_tok_stride;
+    p.q_hs = a->q_head_stride;
+    p.k_cache = static_cast<const uint8_t*>(c.k_cache);
+    p.v_cache = static_cast<const uint8_t*>(c.v_cache);
+    p.k_sp = c.k_stride_page;
+    p.k_st = c.k_stride_token;
+    p.k_sh = c.k_stride_head;
+    p.v_sp = c.v_stride_page;
+    p.v_st = c.v_stride_token;
+    p.v_sh = c.v_stride_head;
+    p.k_exp = c.k_exp;
+    p.v_exp = c.v_exp;
+    p.ke_sp = c.k_exp_stride_page;
+    p.ke_sh = c.k_exp_stride_head;
+    p.ve_sp = c.v_exp_stride_page;
+    p.ve_sh = c.v_exp_stride_head;
+    p.page_shift = mj::page_shift(c.page_size);
+    p.block_shift = mj::page_shift(c.block);
+    p.block_table = a->block_table;
+    p.bt_stride = a->block_table_stride;
+    p.bt_len = a->block_table_len;
+    p.seq_lens = a->seq_lens;
+    p.work = a->plan;
+    p.req = req;
+    p.num_work = int(rows);
+    p.with_reduction = 1;
+    p.part_cap = int(part_cap(a->slots));
+    p.qk_scale_log2 = a->softmax_scale * 1.4426950408889634f;
+    p.v_fmt = 1.f;
+    p.out = static_cast<uint16_t*>(a->out);
+    p.out_f16 = a->out_dtype == MJ_OUT_F16 ? 1 : 0;
+    p.out_ts = a->out_tok_stride;
+    p.out_hs = a->out_head_stride;
+    p.lse = a->lse;
+    p.status = reinterpret_cast<uint32_t*>(ws);
+    p.o_part = o_part;
+    p.m_part = o_part + parts * c.d;
+    p.l_part = p.m_part + parts;
+    p.evict_first = a->evict_first;
+    e = mj::launch_decode_block(p, s, &unsupported);
+  }
   if (unsupported) return MJ_ERR_UNSUPPORTED;
   if (e != cudaSuccess) return MJ_ERR_CUDA;
   mj::BlockJoinParams j = {};
   j.d = c.d;
   j.units = int64_t(a->num_seqs) * c.h_k * n_q;
-  j.o_part = p.o_part;
-  j.m_part = p.m_part;
-  j.l_part = p.l_part;
-  j.out = p.out;
-  j.out_f16 = p.out_f16;
-  j.out_ts = p.out_ts;
-  j.out_hs = p.out_hs;
-  j.lse = p.lse;
-  j.plan = p.req;
-  j.seq_lens = p.seq_lens;
+  j.o_part = o_part;
+  j.m_part = o_part + parts * c.d;
+  j.l_part = j.m_part + parts;
+  j.out = static_cast<uint16_t*>(a->out);
+  j.out_f16 = a->out_dtype == MJ_OUT_F16 ? 1 : 0;
+  j.out_ts = a->out_tok_stride;
+  j.out_hs = a->out_head_stride;
+  j.lse = a->lse;
+  j.plan = req;
+  j.seq_lens = a->seq_lens;
   j.h_k = c.h_k;
   j.h_r = h_r;
   j.n_q = n_q;
   j.q_len = a->q_len;
-  return status_of(mj::launch_block_join(j, static_cast<cudaStream_t>(stream)));
+  return status_of(mj::launch_block_join(j, s));
 }
 
 // Pieces of a row tile's keys: as many as give every SM a CTA, none below
@@ -387,7 +442,7 @@ int mj_block_prompt_splits(int sm_count, int num_seqs, int max_q_len, int max_le
   if (sm_count < 1 || num_seqs < 1 || max_q_len < 1 || max_len < 1 || h_k < 1 || h_q < h_k || h_q % h_k || !mj::head_dim_ok(d))
     return 1;
   const int64_t rows = int64_t(max_q_len) * (h_q / h_k);
-  const int64_t ctas = ceil_div(rows, mj::block_prompt_rows(d)) * h_k * num_seqs;
+  const int64_t ctas = ceil_div(rows, mj::block_prompt_rows(d, rows)) * h_k * num_seqs;
   const int64_t by_keys = std::max<int64_t>(1, max_len / kPromptMinKeys);
   return int(std::min<int64_t>({MJ_BLOCK_MAX_SPLITS, by_keys, std::max<int64_t>(1, sm_count / ctas)}));
 }
@@ -413,7 +468,7 @@ int mj_block_prompt(const mj_block_prompt_args* a, void* stream) {
   st = mj_block_prompt_workspace_size(a->num_tokens, a->h_q, c.d, a->splits, &bytes);
   if (st != MJ_OK) return st;
   const int h_r = a->h_q / c.h_k;
-  if (a->num_seqs > 65535 || ceil_div(int64_t(a->max_q_len) * h_r, mj::block_prompt_rows(c.d)) > 65535)
+  if (a->num_seqs > 65535 || ceil_div(int64_t(a->max_q_len) * h_r, mj::block_prompt_rows(c.d, int64_t(a->max_q_len) * h_r)) > 65535)
     return MJ_ERR_UNSUPPORTED;
   if (a->num_seqs == 0 || a->num_tokens == 0 || a->max_q_len == 0) return MJ_OK;
   st = check_rows(a->q, a->q_tok_stride, a->q_head_stride);

@@ -94,11 +94,17 @@ struct BlockPromptParams {
   float* m_part;
   float* l_part;              // -1: a row that was not computed (piece 0's)
   int tma_head_inner;
+  int evict_first;
+  // decode (work != null): the plan's pieces (request, first tile, end tile, piece) in place of
+  // the grid's; max_q_len query tokens a request, `out` and `lse` laid out by request
+  const int4* work;
+  const int4* req;            // per request: first partial, pieces, tiles a piece, tiles planned
+  int num_work, part_cap;
 };
 
 // Sets *unsupported (and launches nothing) where TMA cannot take the cache's strides.
 cudaError_t launch_block_prompt(BlockPromptParams p, cudaStream_t stream, bool* unsupported);
-int block_prompt_rows(int d);  // query rows of a CTA
+int block_prompt_rows(int d, int64_t rows);  // query rows of a CTA, of so many of a request and KV head
 cudaError_t launch_block_write(BlockWriteParams p, int d, cudaStream_t stream);
 cudaError_t launch_block_read(const BlockReadParams& p, int d, cudaStream_t stream);
 cudaError_t launch_block_join(const BlockJoinParams& p, cudaStream_t stream);
