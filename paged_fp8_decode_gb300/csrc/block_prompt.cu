@@ -59,8 +59,12 @@ struct Cfg {
   // warps: 0 TMA, 1 MMA, 2 the blocks' scales, 4 .. softmax, then the ones that widen V
   static constexpr int kConvWarp0 = 4 + 4 * NT, kConvWarps = 16 - kConvWarp0, kThreads = 512;
   static constexpr int kRows = 128 * NT;
-  static constexpr uint32_t kO = 256;           // O's first column; S (and P) buffers from 0, BN columns each
-  static constexpr int kQ = NT * 2 * DH * kTile;
+  // Tensor memory: S (and P) buffers of BN columns from 0; with one row tile Q's terms behind them
+  // (D / 4 columns each), so that the scores' product reads shared memory for K alone; O
+  static constexpr bool kQt = NT == 1;
+  static constexpr uint32_t kQcol = 2 * BN, kO = NT == 1 && D == 128 ? 384 : 256;
+  static_assert(!kQt || (kQcol + D / 2 <= kO && kO + D <= 512), "tensor memory");
+  static constexpr int kQ = kQt ? 0 : NT * 2 * DH * kTile;
   static constexpr int kK = kQ, kVr = kK + kKStages * kTile, kVf = kVr + 2 * kTile, kCtrl = kVf + 4 * kTile;
   static constexpr int kBytes = kCtrl + 2048;
 };
@@ -97,6 +101,20 @@ __device__ __forceinline__ void umma_qk4(uint32_t d, uint32_t a_lo, uint32_t b_l
       "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a2, y, %4, 1;\n\t"
       "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a3, z, %4, 1;\n\t}" ::"r"(d),
       "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// D[tmem] (+)= A[tmem] B[smem desc], e4m3: 128 channels, 8 columns of A and 32 bytes of B's rows a step.
+__device__ __forceinline__ void umma_qk4_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t hi, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t.reg .b64 w, x, y, z;\n\t.reg .b32 t, u, v, a1, a2, a3;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+      "add.u32 t, %2, 2;\n\tadd.u32 u, %2, 4;\n\tadd.u32 v, %2, 6;\n\tadd.u32 a1, %1, 8;\n\tadd.u32 a2, %1, 16;\n\t"
+      "add.u32 a3, %1, 24;\n\tmov.b64 w, {%2, %3};\n\tmov.b64 x, {t, %3};\n\tmov.b64 y, {u, %3};\n\tmov.b64 z, {v, %3};\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], w, %4, p;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [a1], x, %4, 1;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [a2], y, %4, 1;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [a3], z, %4, 1;\n\t}" ::"r"(d),
+      "r"(a), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate)
       : "memory");
 }
 // D[tmem] (+)= A[tmem] B[smem desc], fp16: 64 keys, 8 columns of A and 16 rows of B a step.
@@ -365,40 +383,60 @@ __global__ void __launch_bounds__(512, 1)
       const int e = max(64, int(((am << 16) + 0x1FFFFFu) >> 23) - 8);
       const float inv = __int_as_float((254 - e) << 23);
       ck = __int_as_float(e << 23) * p.scale_log2;
-      const int r = 32 * quad + lane;
-#pragma unroll 2
-      for (int c = 0; c < D / 16; ++c) {
-        uint4 v[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
-        if (real) {
-          v[0] = __ldcg(src + 2 * c);
-          v[1] = __ldcg(src + 2 * c + 1);
+      // four channels' codes of both terms
+      auto terms = [&](uint32_t w0, uint32_t w1, uint32_t& hw, uint32_t& lw) {
+        float x[4] = {__uint_as_float(w0 << 16) * inv, __uint_as_float(w0 & 0xFFFF0000u) * inv,
+                      __uint_as_float(w1 << 16) * inv, __uint_as_float(w1 & 0xFFFF0000u) * inv};
+        hw = lw = 0u;
+#pragma unroll
+        for (int j = 0; j < 4; j += 2) {
+          if (!(fabsf(x[j]) < INFINITY)) x[j] = NAN;
+          if (!(fabsf(x[j + 1]) < INFINITY)) x[j + 1] = NAN;
+          const __nv_fp8x2_storage_t h2 = __nv_cvt_float2_to_fp8x2(make_float2(x[j], x[j + 1]), __NV_SATFINITE, __NV_E4M3);
+          const float2 hv = e4m3x2_to_float2(h2);
+          const __nv_fp8x2_storage_t l2 =
+              __nv_cvt_float2_to_fp8x2(make_float2(x[j] - hv.x, x[j + 1] - hv.y), __NV_SATFINITE, __NV_E4M3);
+          hw |= uint32_t(h2) << (8 * j);
+          lw |= uint32_t(l2) << (8 * j);
         }
-        uint32_t hw[4], lw[4];
+      };
+      if constexpr (C::kQt) {
+#pragma unroll 1
+        for (int c = 0; c < D / 64; ++c) {
+          uint32_t hw[16], lw[16];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint4 u = v[k >> 1];
-          const uint32_t w0 = (k & 1) ? u.z : u.x, w1 = (k & 1) ? u.w : u.y;
-          float x[4] = {__uint_as_float(w0 << 16) * inv, __uint_as_float(w0 & 0xFFFF0000u) * inv,
-                        __uint_as_float(w1 << 16) * inv, __uint_as_float(w1 & 0xFFFF0000u) * inv};
-          hw[k] = lw[k] = 0u;
-#pragma unroll
-          for (int j = 0; j < 4; j += 2) {
-            if (!(fabsf(x[j]) < INFINITY)) x[j] = NAN;
-            if (!(fabsf(x[j + 1]) < INFINITY)) x[j + 1] = NAN;
-            const __nv_fp8x2_storage_t h2 = __nv_cvt_float2_to_fp8x2(make_float2(x[j], x[j + 1]), __NV_SATFINITE, __NV_E4M3);
-            const float2 hv = e4m3x2_to_float2(h2);
-            const __nv_fp8x2_storage_t l2 =
-                __nv_cvt_float2_to_fp8x2(make_float2(x[j] - hv.x, x[j + 1] - hv.y), __NV_SATFINITE, __NV_E4M3);
-            hw[k] |= uint32_t(h2) << (8 * j);
-            lw[k] |= uint32_t(l2) << (8 * j);
+          for (int k = 0; k < 16; k += 2) {
+            const uint4 u = real ? __ldcg(src + 8 * c + k / 2) : make_uint4(0u, 0u, 0u, 0u);
+            terms(u.x, u.y, hw[k], lw[k]);
+            terms(u.z, u.w, hw[k + 1], lw[k + 1]);
           }
+          tmem_st16u(tmem + lanes + C::kQcol + uint32_t(16 * c), hw);
+          tmem_st16u(tmem + lanes + C::kQcol + uint32_t(D / 4 + 16 * c), lw);
         }
-        const int dh = c >> 3;
-        uint8_t* at = smem + (a * 2 * DH + dh) * kTile + r * 128 + (((c & 7) ^ (r & 7)) << 4);
-        *reinterpret_cast<uint4*>(at) = make_uint4(hw[0], hw[1], hw[2], hw[3]);
-        *reinterpret_cast<uint4*>(at + DH * kTile) = make_uint4(lw[0], lw[1], lw[2], lw[3]);
+        tc::tmem_wait_st();
+        tc::tc_fence_before();
+      } else {
+        const int r = 32 * quad + lane;
+#pragma unroll 2
+        for (int c = 0; c < D / 16; ++c) {
+          uint4 v[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
+          if (real) {
+            v[0] = __ldcg(src + 2 * c);
+            v[1] = __ldcg(src + 2 * c + 1);
+          }
+          uint32_t hw[4], lw[4];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            terms(v[k].x, v[k].y, hw[2 * k], lw[2 * k]);
+            terms(v[k].z, v[k].w, hw[2 * k + 1], lw[2 * k + 1]);
+          }
+          const int dh = c >> 3;
+          uint8_t* at = smem + (a * 2 * DH + dh) * kTile + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+          *reinterpret_cast<uint4*>(at) = make_uint4(hw[0], hw[1], hw[2], hw[3]);
+          *reinterpret_cast<uint4*>(at + DH * kTile) = make_uint4(lw[0], lw[1], lw[2], lw[3]);
+        }
+        tc::fence_async_smem();
       }
-      tc::fence_async_smem();
       tc::mbar_arrive(bar(ctl.q_ready));
     }
     // The last key this row sees (a row past the end computes something that nobody reads).
@@ -693,14 +731,21 @@ __global__ void __launch_bounds__(512, 1)
     const uint64_t vd = tc::smem_desc(base + C::kVf, BN * 128, 1024, tc::kSwizzle128B);
     // (votes: the products below are issued by whole warps)
     bool ok = __all_sync(~0u, wait_bar<0>(bar(ctl.q_ready), 0, abort));
+    tc::tc_fence_after();
     // Stages and buffers are constants at every issue (the loop runs over four tiles).
     auto qk = [&](auto a, auto buf, auto stage) {
 #pragma unroll
       for (int term = 0; term < 2; ++term)
 #pragma unroll
         for (int dh = 0; dh < DH; ++dh)
-          umma_qk4(tmem + uint32_t(buf * BN), uint32_t(qd) + ((a * 2 + term) * DH + dh) * (kTile >> 4),
-                   uint32_t(kd) + stage * (kTile >> 4) + dh * (BN * 128 >> 4), uint32_t(kd >> 32), idesc_qk, term > 0 || dh > 0);
+          if constexpr (C::kQt)
+            umma_qk4_ts(tmem + uint32_t(buf * BN), tmem + C::kQcol + uint32_t(term * (D / 4) + 32 * dh),
+                        uint32_t(kd) + stage * (kTile >> 4) + dh * (BN * 128 >> 4), uint32_t(kd >> 32), idesc_qk,
+                        term > 0 || dh > 0);
+          else
+            umma_qk4(tmem + uint32_t(buf * BN), uint32_t(qd) + ((a * 2 + term) * DH + dh) * (kTile >> 4),
+                     uint32_t(kd) + stage * (kTile >> 4) + dh * (BN * 128 >> 4), uint32_t(kd >> 32), idesc_qk,
+                     term > 0 || dh > 0);
       tc::umma_commit_warp(bar(ctl.s_full[buf]));
     };
     auto wait_for = [&](uint64_t& barrier, int use) {
