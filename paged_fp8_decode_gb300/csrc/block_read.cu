@@ -95,8 +95,8 @@ __global__ void __launch_bounds__(kThreads) block_read_kernel(BlockReadParams p)
         o[2 * k + 1] = out2<F16>(f[2] * by, f[3] * by);
       }
       uint4* dst = reinterpret_cast<uint4*>(out + int64_t((i0 + u) * kRowsIt + sub) * p.ts[v]);
-      dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
-      dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+      __stcs(dst, make_uint4(o[0], o[1], o[2], o[3]));
+      __stcs(dst + 1, make_uint4(o[4], o[5], o[6], o[7]));
     }
   }
 }

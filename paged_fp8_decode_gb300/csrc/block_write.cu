@@ -10,8 +10,8 @@
 // The call's tokens of a block form a run (they follow one another, padding
 // tokens aside, however many). A CTA looks through a window of tokens for runs that begin
 // there; its warps then take the run's (KV head, K or V) pairs in turn, each
-// warp 16 rows of the block in registers: one read of the input, one maximum
-// over the warp (over the block's warps where it has more than 16 rows), one
+// warp 4 KB of the input in registers: one read of the input, one maximum
+// over the warp (over the block's warps where it takes several), one
 // write. HBM bounds it: 2 bytes read and 1 written a channel.
 #include <atomic>
 
@@ -24,8 +24,9 @@ namespace mj {
 
 namespace {
 
-constexpr int kWarps = 8, kThreads = 32 * kWarps;
-constexpr int kRowsWarp = 16;
+// Rows of a warp: 4 KB of input, 32 registers a thread.
+__host__ __device__ constexpr int rows_warp(int d) { return 2048 / d; }
+__host__ __device__ constexpr int warps_cta(int g) { return g > 8 ? g : 8; }
 
 __device__ __forceinline__ uint4 load16(const uint16_t* at) { return __ldcg(reinterpret_cast<const uint4*>(at)); }
 
@@ -70,9 +71,13 @@ __device__ __noinline__ int64_t find_live(const int64_t* slots, int64_t from, in
   return -1;
 }
 
-// G warps share a block of 16 G rows.
+// G warps share a block of G rows_warp(D) rows. (Three CTAs an SM where they hold 8 warps: left to
+// itself the compiler takes 127 registers, and a call too small to fill the GPU
+// by much is bound by the latency of few warps; 16 rows of 256 channels a warp took 215: 15.9 us
+// for the ragged call below.)
 template <int D, int G>
-__global__ void __launch_bounds__(kThreads) block_write_kernel(BlockWriteParams p) {
+__global__ void __launch_bounds__(32 * warps_cta(G), 24 / warps_cta(G)) block_write_kernel(BlockWriteParams p) {
+  constexpr int kWarps = warps_cta(G), kRowsWarp = rows_warp(D);
   constexpr int kLanesRow = D / 8;             // lanes a row: 8 channels, 16 bytes of input each
   constexpr int kRowsIt = 32 / kLanesRow;      // rows a warp takes at once
   constexpr int kIts = kRowsWarp / kRowsIt;
@@ -129,7 +134,7 @@ __global__ void __launch_bounds__(kThreads) block_write_kernel(BlockWriteParams 
         if (mine >> lane & 1u) {
           const int row = int(cs) & (block - 1);
           first = min(first, row);
-          if ((row >> 4) == part) map[warp][row & (kRowsWarp - 1)] = int(c) + 1;
+          if (row / kRowsWarp == part) map[warp][row & (kRowsWarp - 1)] = int(c) + 1;
         }
         if (other) break;
         c0 += 32;
@@ -223,7 +228,7 @@ __global__ void __launch_bounds__(kThreads) block_write_kernel(BlockWriteParams 
 
 template <int D, int G>
 cudaError_t launch(BlockWriteParams p, cudaStream_t stream) {
-  constexpr int kGroups = kWarps / G;
+  constexpr int kWarps = warps_cta(G), kGroups = kWarps / G;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -239,12 +244,12 @@ cudaError_t launch(BlockWriteParams p, cudaStream_t stream) {
   // pairs, then from shorter windows; a window is never longer than a block.
   const int64_t want = 6 * int64_t(sms), pairs = (2 * int64_t(p.h_k) + kGroups - 1) / kGroups;
   const int64_t y_max = std::min<int64_t>(pairs, 65535);
-  p.window = kRowsWarp * G;
+  p.window = rows_warp(D) * G;
   while (p.window > 1 && (int64_t(p.num_tokens) + p.window - 1) / p.window * y_max < want) p.window /= 2;
   const int64_t ctas = (int64_t(p.num_tokens) + p.window - 1) / p.window;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(ctas), unsigned(std::min(y_max, (want + ctas - 1) / ctas)));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(32 * kWarps);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -257,10 +262,10 @@ cudaError_t launch(BlockWriteParams p, cudaStream_t stream) {
 template <int D>
 cudaError_t launch_block(const BlockWriteParams& p, cudaStream_t stream) {
   switch (p.block_shift) {
-    case 4: return launch<D, 1>(p, stream);
-    case 5: return launch<D, 2>(p, stream);
-    case 6: return launch<D, 4>(p, stream);
-    default: return launch<D, 8>(p, stream);
+    case 4: return launch<D, 16 / rows_warp(D)>(p, stream);
+    case 5: return launch<D, 32 / rows_warp(D)>(p, stream);
+    case 6: return launch<D, 64 / rows_warp(D)>(p, stream);
+    default: return launch<D, 128 / rows_warp(D)>(p, stream);
   }
 }
 

@@ -1346,7 +1346,7 @@ cudaError_t launch_tc(const CUtensorMap& mk, const CUtensorMap& mv, const Decode
 // row (two pairs of e4m3 terms).
 template <int KF, int QM, int D = 128>
 cudaError_t launch_rows(const CUtensorMap& mk, const CUtensorMap& mv, const DecodeParams& p, cudaStream_t stream) {
-  constexpr int K = QM == 1 || QM == kQBlock ? 2 : 1;
+  constexpr int K = QM == 1 ? 2 : 1;
   if (p.tw <= 16) {
     if (p.n_q <= 4) return launch_tc<16, 16, 4, KF, QM, D>(mk, mv, p, stream);
     if (p.n_q <= 8) return launch_tc<16, 32, 8, KF, QM, D>(mk, mv, p, stream);

@@ -82,8 +82,10 @@ int64_t part_cap(int slots) { return 4 * int64_t(slots); }
 constexpr double kPieceTiles = 4, kTail = 0.2;
 
 // Which kernel attends: the decode kernel (keys on the tensor cores' rows, so that a few
-// query rows fill them) or the prompt's (query rows there, 128 at a time). Measured, see there.
-bool by_rows(int d, int64_t n_q) { return d == 128 ? n_q > 8 : n_q > 8; }
+// query rows fill them) or the prompt's (query rows there, 128 at a time). 64 x 4096 tokens, in us:
+// head size 128, 8 KV heads: 16 rows 184 and 163, 32 rows 455 and 168; head size 256, 4 KV heads:
+// 16 rows 126 and 136, 32 rows 306 and 141. At 8 rows the decode kernel takes 103 and 93.
+bool by_rows(int d, int64_t n_q) { return n_q > (d == 128 ? 8 : 16); }
 
 bool slots_ok(int slots) { return slots >= 1 && slots <= (1 << 20); }
 
