@@ -71,12 +71,12 @@ __device__ __noinline__ int64_t find_live(const int64_t* slots, int64_t from, in
   return -1;
 }
 
-// G warps share a block of G rows_warp(D) rows. (Three CTAs an SM where they hold 8 warps: left to
+// G warps share a block of G rows_warp(D) rows. (Two CTAs an SM where they hold 8 warps: left to
 // itself the compiler takes 127 registers, and a call too small to fill the GPU
 // by much is bound by the latency of few warps; 16 rows of 256 channels a warp took 215: 15.9 us
 // for the ragged call below.)
 template <int D, int G>
-__global__ void __launch_bounds__(32 * warps_cta(G), 24 / warps_cta(G)) block_write_kernel(BlockWriteParams p) {
+__global__ void __launch_bounds__(32 * warps_cta(G), 16 / warps_cta(G)) block_write_kernel(BlockWriteParams p) {
   constexpr int kWarps = warps_cta(G), kRowsWarp = rows_warp(D);
   constexpr int kLanesRow = D / 8;             // lanes a row: 8 channels, 16 bytes of input each
   constexpr int kRowsIt = 32 / kLanesRow;      // rows a warp takes at once

@@ -288,6 +288,16 @@ __global__ void __launch_bounds__(KF != MJ_KV_E4M3 ? kThreadsTcFp6 : kThreadsTc,
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
+  if constexpr (BS) {
+    // Past the first wave a CTA without work leaves before it takes barriers and tensor
+    // memory (there the preceding kernel is long done, and its wait costs nothing).
+    if (int64_t(blockIdx.x) + int64_t(gridDim.x) * blockIdx.y >= p.first_wave) {
+      tc::grid_dependency_wait();
+      const int4 w = reinterpret_cast<const int4*>(p.work)[blockIdx.x / unsigned(p.h_k)];
+      if (w.z <= w.y) return;
+    }
+  }
+
   // ---- set-up: barriers, TMEM, Q tile ------------------------------------
   if (tid == 0) {
     for (int s = 0; s < stages; ++s) {
@@ -349,10 +359,20 @@ __global__ void __launch_bounds__(KF != MJ_KV_E4M3 ? kThreadsTcFp6 : kThreadsTc,
       if (blockIdx.y == 0 && wp.z > wp.y && wp.x >= 0 && wp.x < p.num_seqs) {
         const int ppt = kKvTile / p.page_size;
         const int64_t grid = int64_t(gridDim.x) * gridDim.y;
+        // the CTAs with work: the grid, but that the block-scaled plan's rows are padded far
+        // past them, live ones first
+        auto grid_within = [&](int64_t n) {
+          if constexpr (!BS) return grid <= n;
+          const int64_t row = n / p.h_k;
+          if (row >= p.num_work) return true;
+          const int4 r = reinterpret_cast<const int4*>(p.work)[row];
+          return r.z <= r.y;
+        };
+        const bool split = BS ? p.req[wp.x].y > 1 : p.with_reduction;
         const bool deep = int64_t(blockIdx.x) + int64_t(gridDim.x) * blockIdx.y < p.first_wave &&
-                          (!p.with_reduction || grid <= p.first_wave);
+                          (!split || grid_within(p.first_wave));
         const int depth = !deep ? kPrefetchTiles
-                                : (grid <= 2 * int64_t(p.first_wave) ? kPrefetchTilesShortGrid : kPrefetchTilesFirstWave);
+                                : (grid_within(2 * int64_t(p.first_wave)) ? kPrefetchTilesShortGrid : kPrefetchTilesFirstWave);
         const int n = min(depth, wp.z - wp.y) * ppt;  // pages
         const CUtensorMap* map = warp == 0 ? &tmap_k : &tmap_v;
         for (int k = lane; k < n; k += 32) {
@@ -375,7 +395,8 @@ __global__ void __launch_bounds__(KF != MJ_KV_E4M3 ? kThreadsTcFp6 : kThreadsTc,
     // may launch now: its CTAs take the SMs this grid's last CTAs leave and
     // run their set-up and prefetches meanwhile. (After a split the merge's
     // CTAs would sit on those SMs instead, and the step is slower.)
-    if (!p.with_reduction) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    // (The block-scaled join always follows; where nothing was split it has nothing to do.)
+    if (BS || !p.with_reduction) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     tc::grid_dependency_wait();
   }
 

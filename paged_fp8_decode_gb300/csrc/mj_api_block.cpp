@@ -71,9 +71,10 @@ void sides(const mj_block_cache& c, mj::BlockSide (&s)[2]) {
           c.v_exp_stride_head};
 }
 
-// A plan's pieces have at least half a slot's share of all tiles: at most two a slot
-// and one a request, and of split requests (over one piece each) at most four a slot.
-int64_t work_rows(int slots, int max_num_seqs) { return 2 * int64_t(slots) + max_num_seqs; }
+// A plan has at most a piece a slot and one a request (each launch has a CTA for every
+// row that there could be), and a piece at least half a slot's share of all tiles: of
+// split requests, over one piece each, at most four a slot.
+int64_t work_rows(int slots, int max_num_seqs) { return int64_t(slots) + max_num_seqs; }
 int64_t part_cap(int slots) { return 4 * int64_t(slots); }
 
 // What starting, ending and joining a piece costs, in tiles, and how much of the
@@ -221,6 +222,7 @@ int mj_block_plan(const int32_t* seq_lens_host, int num_seqs, int max_num_seqs, 
   auto consider = [&](int64_t c) {
     int64_t most;
     const int64_t n = pieces(c, &most);
+    if (n > work_rows(slots, max_num_seqs)) return;
     const double end = n <= slots ? double(most) + kPieceTiles
                                   : (double(total) + kPieceTiles * double(n)) / slots + kTail * double(most);
     if (end < best) {
