@@ -67,6 +67,7 @@ struct Cfg {
   static constexpr int kQ = kQt ? 0 : NT * 2 * DH * kTile;
   static constexpr int kK = kQ, kVr = kK + kKStages * kTile, kVf = kVr + 2 * kTile, kCtrl = kVf + 4 * kTile;
   static constexpr int kBytes = kCtrl + 2048;
+  static_assert(NT > 1 || 4 * D * 32 * 4 + 1024 <= kCtrl, "the copies' join");
 };
 static_assert(Cfg<128, 2>::kBytes + 1024 <= 227 * 1024 && Cfg<256, 1>::kBytes + 1024 <= 227 * 1024 && kKStages % 2 == 0,
               "shared memory");
@@ -137,7 +138,7 @@ __host__ __device__ constexpr uint32_t idesc_f16(int M, int N) {
   return (1u << 4) | (1u << 16) | (uint32_t(N >> 3) << 17) | (uint32_t(M >> 4) << 24);
 }
 
-__device__ __forceinline__ void tmem_ld32(uint32_t at, uint32_t (&r)[32]) {
+__device__ __forceinline__ void tmem_ld32(uint32_t at, uint32_t* r) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
       "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
@@ -148,17 +149,32 @@ __device__ __forceinline__ void tmem_ld32(uint32_t at, uint32_t (&r)[32]) {
       : "r"(at));
 }
 
-// Wait for the thread's TMEM loads; the values pass through, so that nothing uses them earlier.
-__device__ __forceinline__ void tmem_wait_ld32(uint32_t (&r)[32]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
-                 "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]),
-                 "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]),
-                 "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory");
+__device__ __forceinline__ void tmem_ld16u(uint32_t at, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(at));
+}
+
+// Wait for the thread's TMEM loads; N of the values pass through, so that nothing uses them earlier.
+template <int N>
+__device__ __forceinline__ void tmem_wait_ld(uint32_t* r) {
+  static_assert(N == 16 || N == 32, "values");
+  if constexpr (N == 32)
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+                   "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]),
+                   "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]),
+                   "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory");
+  else
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+                   "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
 }
 
 // The same without the wait: for loads that an earlier wait covers.
-__device__ __forceinline__ void tmem_pass32(uint32_t (&r)[32]) {
+__device__ __forceinline__ void tmem_pass32(uint32_t* r) {
   asm volatile(""
                : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
                  "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]),
@@ -166,19 +182,20 @@ __device__ __forceinline__ void tmem_pass32(uint32_t (&r)[32]) {
                  "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31]));
 }
 
-__device__ __forceinline__ void tmem_wait_ld16(float (&v)[16]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]), "+f"(v[8]),
-                 "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15])::"memory");
-}
-
-__device__ __forceinline__ void tmem_st16u(uint32_t at, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-      "%15, %16};" ::"r"(at),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
+template <int N>
+__device__ __forceinline__ void tmem_st(uint32_t at, const uint32_t* r) {
+  static_assert(N == 8 || N == 16, "columns");
+  if constexpr (N == 16)
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16};" ::"r"(at),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+  else
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(at), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
 }
 
 // As tc::mbar_wait, with naps of NAP ns between the looks: most warps here wait most of
@@ -247,12 +264,18 @@ __device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t two) {
   return r;
 }
 
-template <int D, int NT>
+template <int D, int NT, bool SPREAD>
 __global__ void __launch_bounds__(512, 1)
     block_prompt_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
                         BlockPromptParams p) {
   using C = Cfg<D, NT>;
   constexpr int BN = C::BN, DH = C::DH, NB = C::NB, TB = C::TB;
+  // With at most 32 rows (SPREAD) the row tile holds them four times, once for each softmax warp
+  // (a warp reaches 32 of the tile's rows), and a copy takes a quarter of a tile's keys: its P is 0
+  // for the others. Each copy has a reference, a sum and an output of its own; they are joined
+  // at the end, as pieces of the keys are.
+  static_assert(!SPREAD || NT == 1, "one row tile");
+  constexpr int HC = SPREAD ? BN / 4 : BN, HB = HC / 16;  // columns (keys) of a softmax thread, 16-key groups
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   // (32-bit shared addresses throughout, from constants: what the products are issued with stays in uniform registers)
   const uint32_t raw = tc::smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
@@ -355,10 +378,11 @@ __global__ void __launch_bounds__(512, 1)
   // Registers: 128 a thread at launch. At head size 128 a softmax thread keeps a row's 128
   // scores: 2 x 192 + 2 x 64, or 224 + 3 x 96, = 4 x 128 for the four warpgroups.
   if (warp >= 4 && warp < C::kConvWarp0) {
-    if constexpr (D == 128) set_regs<true, NT == 2 ? 192 : 224>();
+    if constexpr (D == 128 && !SPREAD) set_regs<true, NT == 2 ? 192 : 224>();
     // ======================= softmax: thread = row ============================
     const int a = (warp - 4) >> 2, quad = warp & 3;
-    const int R = r0 + 128 * a + 32 * quad + lane;
+    const int R = SPREAD ? r0 + lane : r0 + 128 * a + 32 * quad + lane;
+    const int col = SPREAD ? quad * HC : 0;  // the thread's first column
     const bool real = R < rows;
     const int64_t tok = t0 + int64_t(real ? R / p.h_r : 0), head = int64_t(g) * p.h_r + (real ? R % p.h_r : 0);
     const uint32_t lanes = uint32_t(32 * quad) << 16;
@@ -410,8 +434,8 @@ __global__ void __launch_bounds__(512, 1)
             terms(u.x, u.y, hw[k], lw[k]);
             terms(u.z, u.w, hw[k + 1], lw[k + 1]);
           }
-          tmem_st16u(tmem + lanes + C::kQcol + uint32_t(16 * c), hw);
-          tmem_st16u(tmem + lanes + C::kQcol + uint32_t(D / 4 + 16 * c), lw);
+          tmem_st<16>(tmem + lanes + C::kQcol + uint32_t(16 * c), hw);
+          tmem_st<16>(tmem + lanes + C::kQcol + uint32_t(D / 4 + 16 * c), lw);
         }
         tc::tmem_wait_st();
         tc::tc_fence_before();
@@ -455,35 +479,40 @@ __global__ void __launch_bounds__(512, 1)
       if (i % TB == 0) ok = wait_bar<0>(bar(ctl.e_full[bat & 1]), uint32_t(bat >> 1) & 1u, abort);
       // the groups' scales, before the scores are there: the products' operands keep
       // shared memory busy, and a load from it in the middle of the arithmetic would take long
-      float4 sc[NB];
+      float4 sc[HB];
 #pragma unroll
-      for (int h = 0; h < NB; ++h) {
-        sc[h] = ctl.scale[bat & 1][(i % TB) * NB + h];
+      for (int h = 0; h < HB; ++h) {
+        sc[h] = ctl.scale[bat & 1][(i % TB) * NB + (SPREAD ? quad * HB : 0) + h];
         sc[h].x *= ck;
       }
       ok = ok && wait_bar<0>(bar(ctl.s_full[buf]), uint32_t(NT == 2 ? i : i >> 1) & 1u, abort);
       ok = __all_sync(~0u, ok);
       if (!ok) return false;
       tc::tc_fence_after();
-      // column c of the tile is hidden from c = seen on
-      const int seen = lim - (k0 + i * BN) + 1;
+      // column c of the thread's is hidden from c = seen on
+      const int seen = lim - (k0 + i * BN + col) + 1;
 
       // the tile's largest u
-      uint32_t r[BN / 32][32];
+      uint32_t r[HC];
+      if constexpr (HC == 16) {
+        tmem_ld16u(tS + col, r);
+        tmem_wait_ld<16>(r);
+      } else {
 #pragma unroll
-      for (int c = 0; c < BN / 32; ++c) tmem_ld32(tS + 32 * c, r[c]);
-      tmem_wait_ld32(r[0]);
+        for (int c = 0; c < HC; c += 32) tmem_ld32(tS + col + c, r + c);
+        tmem_wait_ld<32>(r);
 #pragma unroll
-      for (int c = 1; c < BN / 32; ++c) tmem_pass32(r[c]);
+        for (int c = 32; c < HC; c += 32) tmem_pass32(r + c);
+      }
       if constexpr (masked) {
 #pragma unroll
-        for (int k = 0; k < BN; ++k)
-          if (k >= seen) r[k / 32][k % 32] = 0xFF800000u;
+        for (int k = 0; k < HC; ++k)
+          if (k >= seen) r[k] = 0xFF800000u;
       }
-      float t[NB];
+      float t[HB];
 #pragma unroll
-      for (int h = 0; h < NB; ++h) {
-        const uint32_t* x = &r[h / 2][16 * (h & 1)];
+      for (int h = 0; h < HB; ++h) {
+        const uint32_t* x = r + 16 * h;
         float mx = __uint_as_float(x[0]), my = __uint_as_float(x[1]);
 #pragma unroll
         for (int k = 2; k < 14; k += 4) {
@@ -493,8 +522,10 @@ __global__ void __launch_bounds__(512, 1)
         mx = fmaxf(max3(mx, __uint_as_float(x[14]), __uint_as_float(x[15])), my);
         t[h] = fmaf(mx, sc[h].x, sc[h].y);
       }
-      float top = fmaxf(max3(t[0], t[1], t[2]), t[3]);
-      if constexpr (NB == 8) top = max3(top, max3(t[4], t[5], t[6]), t[7]);
+      float top = t[0];
+      if constexpr (HB == 2) top = fmaxf(t[0], t[1]);
+      if constexpr (HB >= 4) top = fmaxf(max3(t[0], t[1], t[2]), t[3]);
+      if constexpr (HB == 8) top = max3(top, max3(t[4], t[5], t[6]), t[7]);
       // the reference
       float by = 1.f;
       bool move = false;
@@ -516,60 +547,81 @@ __global__ void __launch_bounds__(512, 1)
         const uint32_t tO = tmem + lanes + C::kO + uint32_t(a * D);
 #pragma unroll 1
         for (int c = 0; c < D; c += 16) {
-          float v[16];
-          tc::tmem_ld16(tO + c, v);
-          tmem_wait_ld16(v);
+          uint32_t v[16];
+          tmem_ld16u(tO + c, v);
+          tmem_wait_ld<16>(v);
 #pragma unroll
-          for (int k = 0; k < 16; ++k) v[k] *= by;
-          tc::tmem_st16(tO + c, v);
+          for (int k = 0; k < 16; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * by);
+          tmem_st<16>(tO + c, v);
         }
       }
       // P in place of S, 32 keys at a time; a group's sums and stores come behind the
       // exponentials of the next, which do not wait for them
       const float lift = kLift - (m == -INFINITY ? 0.f : m);
-      auto exps = [&](int c) {
+      auto exps = [&](int h) {  // of 16 keys
+        const float4 e = sc[h];
+        const float2 mul = make_float2(e.x, e.x), add = make_float2(e.y + lift, e.y + lift);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float4 e = sc[2 * c + h];
-          const float2 mul = make_float2(e.x, e.x), add = make_float2(e.y + lift, e.y + lift);
-#pragma unroll
-          for (int k = 16 * h; k < 16 * h + 16; k += 2) {
-            const float2 u = fma2(make_float2(__uint_as_float(r[c][k]), __uint_as_float(r[c][k + 1])), mul, add);
-            r[c][k] = __float_as_uint(fast_exp2(u.x));
-            r[c][k + 1] = __float_as_uint(fast_exp2(u.y));
-          }
+        for (int k = 16 * h; k < 16 * h + 16; k += 2) {
+          const float2 u = fma2(make_float2(__uint_as_float(r[k]), __uint_as_float(r[k + 1])), mul, add);
+          r[k] = __float_as_uint(fast_exp2(u.x));
+          r[k + 1] = __float_as_uint(fast_exp2(u.y));
         }
       };
-      auto store = [&](int c) {
-        uint32_t w[16];
+      auto pack = [&](int h, uint32_t* w) {
+        float2 x[8];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          float2 x[8];
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            x[k] = make_float2(__uint_as_float(r[c][16 * h + 2 * k]), __uint_as_float(r[c][16 * h + 2 * k + 1]));
-            w[8 * h + k] = f16x2(x[k].x, x[k].y);
-          }
-#pragma unroll
-          for (int d = 4; d > 0; d >>= 1)
-#pragma unroll
-            for (int k = 0; k < d; ++k) x[k] = add2(x[k], x[k + d]);
-          l = fmaf(x[0].x + x[0].y, sc[2 * c + h].z, l);
+        for (int k = 0; k < 8; ++k) {
+          x[k] = make_float2(__uint_as_float(r[16 * h + 2 * k]), __uint_as_float(r[16 * h + 2 * k + 1]));
+          w[k] = f16x2(x[k].x, x[k].y);
         }
-        tmem_st16u(tS + 16 * c, w);
-        if (c % (BN / 64) == BN / 64 - 1) {  // half of the keys
-          tc::tmem_wait_st();
-          tc::tc_fence_before();
-          tc::mbar_arrive(bar(ctl.p_full[buf][c / (BN / 64)]));
-        }
+#pragma unroll
+        for (int d = 4; d > 0; d >>= 1)
+#pragma unroll
+          for (int k = 0; k < d; ++k) x[k] = add2(x[k], x[k + d]);
+        l = fmaf(x[0].x + x[0].y, sc[h].z, l);
       };
-      exps(0);
+      auto give = [&](int h) {  // a half of the tile's keys
+        tc::tmem_wait_st();
+        tc::tc_fence_before();
+        tc::mbar_arrive(bar(ctl.p_full[buf][h]));
+      };
+      if constexpr (SPREAD) {
+        uint32_t w[HC / 2];
+        uint32_t none[HC / 2];
 #pragma unroll
-      for (int c = 1; c < BN / 32; ++c) {
-        exps(c);
-        store(c - 1);
+        for (int k = 0; k < HC / 2; ++k) none[k] = 0u;
+#pragma unroll
+        for (int h = 0; h < HB; ++h) exps(h);
+#pragma unroll
+        for (int h = 0; h < HB; ++h) pack(h, w + 8 * h);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if (k == quad)
+            tmem_st<HC / 2>(tS + k * (HC / 2), w);
+          else
+            tmem_st<HC / 2>(tS + k * (HC / 2), none);
+        }
+        give(0);
+        tc::mbar_arrive(bar(ctl.p_full[buf][1]));
+      } else {
+        auto store = [&](int c) {
+          uint32_t w[16];
+          pack(2 * c, w);
+          pack(2 * c + 1, w + 8);
+          tmem_st<16>(tS + 16 * c, w);
+          if (c % (BN / 64) == BN / 64 - 1) give(c / (BN / 64));
+        };
+        exps(0);
+        exps(1);
+#pragma unroll
+        for (int c = 1; c < BN / 32; ++c) {
+          exps(2 * c);
+          exps(2 * c + 1);
+          store(c - 1);
+        }
+        store(BN / 32 - 1);
       }
-      store(BN / 32 - 1);
       if (i % TB == TB - 1 || i == nt - 1) {
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(bar(ctl.e_empty[bat & 1]));
@@ -583,19 +635,54 @@ __global__ void __launch_bounds__(512, 1)
       for (; i < nt && go; ++i) go = tile(std::true_type{}, i);
     }
     if (nt > 0) ok = ok && wait_bar<0>(bar(ctl.o_last[a]), 0, abort);
-    if (__all_sync(~0u, ok)) {
-      tc::tc_fence_after();
+    ok = __all_sync(~0u, ok);
+    tc::tc_fence_after();
+    if constexpr (SPREAD) {
+      // Join the copies in shared memory, whose tiles are consumed by now: [copy][channel][row].
+      // (All four warps come here whatever happened.)
+      float* all = reinterpret_cast<float*>(smem);
+      float2* ml = reinterpret_cast<float2*>(all + 4 * D * 32);
+      ml[32 * quad + lane] = ok ? make_float2(m, l) : make_float2(-INFINITY, 0.f);
+      tc::named_bar_sync(1, 128);
+      float M = -INFINITY, sum = 0.f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) M = fmaxf(M, ml[32 * k + lane].x);
+      const float top = M == -INFINITY ? 0.f : M;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) sum = fmaf(fast_exp2(ml[32 * k + lane].x - top), ml[32 * k + lane].y, sum);
+      const float f = fast_exp2(m - top);
+#pragma unroll 1
+      for (int c = 0; c < D; c += 32) {
+        uint32_t r[32];
+        if (ok && nt > 0) {
+          tmem_ld32(tmem + lanes + C::kO + uint32_t(c), r);
+          tmem_wait_ld<32>(r);
+        }
+#pragma unroll
+        for (int k = 0; k < 32; ++k) all[(quad * D + c + k) * 32 + lane] = nt > 0 ? __uint_as_float(r[k]) * f : 0.f;
+      }
+      tc::named_bar_sync(1, 128);
+      m = M;
+      l = sum;
+    }
+    if (ok) {
       const float inv = l == 0.f ? 0.f : 1.f / l;
       const bool some = nt > 0 && !(l == 0.f);
       // the row's place in its partials and in the LSE
       const int64_t part = parts + (p.work ? R : (tok - t0) * p.h_q + head);
       const int64_t lse_at = p.work ? (int64_t(b) * p.h_k + g) * rows + R : tok * p.h_q + head;
+      // (of joined copies each thread writes a quarter of the row)
 #pragma unroll 1
-      for (int c = 0; c < D; c += 32) {
+      for (int c = SPREAD ? quad * (D / 4) : 0; c < (SPREAD ? (quad + 1) * (D / 4) : D); c += 32) {
         uint32_t r[32];
-        if (nt > 0) {
+        if constexpr (SPREAD) {
+          const float* all = reinterpret_cast<const float*>(smem) + lane;
+#pragma unroll
+          for (int k = 0; k < 32; ++k)
+            r[k] = __float_as_uint((all[(c + k) * 32] + all[(D + c + k) * 32]) + (all[(2 * D + c + k) * 32] + all[(3 * D + c + k) * 32]));
+        } else if (nt > 0) {
           tmem_ld32(tmem + lanes + C::kO + uint32_t(a * D + c), r);
-          tmem_wait_ld32(r);
+          tmem_wait_ld<32>(r);
         }
         if (!real) continue;
         if (parts >= 0) {
@@ -619,7 +706,7 @@ __global__ void __launch_bounds__(512, 1)
           }
         }
       }
-      if (real) {
+      if (real && (!SPREAD || quad == 0)) {
         if (parts >= 0) {
           // m counts V's scales in, l does not: together 2^m l = sum 2^t
           p.m_part[part] = some ? fmaxf(m, -1e30f) - kLift : -INFINITY;
@@ -630,7 +717,7 @@ __global__ void __launch_bounds__(512, 1)
       }
     }
   } else if (warp >= C::kConvWarp0) {
-    if constexpr (D == 128) set_regs<false, NT == 2 ? 64 : 96>();
+    if constexpr (D == 128 && !SPREAD) set_regs<false, NT == 2 ? 64 : 96>();
     // ======================= V to fp16 ========================================
     // [key][128 codes] 128-byte swizzled -> [64 channels][key][64 fp16] likewise
     const int ct = tid - 32 * C::kConvWarp0;
@@ -667,7 +754,7 @@ __global__ void __launch_bounds__(512, 1)
       tc::mbar_arrive(bar(ctl.vf_full[s]));
     }
   } else {
-    if constexpr (D == 128) set_regs<false, NT == 2 ? 64 : 96>();
+    if constexpr (D == 128 && !SPREAD) set_regs<false, NT == 2 ? 64 : 96>();
   if (warp == 0) {
     // ======================= TMA: K and V tiles ===============================
     const int box = min(BN, 1 << p.page_shift);  // rows of a copy
@@ -863,7 +950,7 @@ bool encode(CUtensorMap* map, const BlockSide& s, const BlockPromptParams& p, in
             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, int NT>
+template <int D, int NT, bool SPREAD>
 cudaError_t launch(const CUtensorMap& mk, const CUtensorMap& mv, const BlockPromptParams& p, cudaStream_t stream) {
   using C = Cfg<D, NT>;
   constexpr int bytes = C::kBytes + 1024;
@@ -873,7 +960,7 @@ cudaError_t launch(const CUtensorMap& mk, const CUtensorMap& mv, const BlockProm
   static std::atomic<int> configured[64];  // the shared-memory limit is raised once per device
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!configured[dev].load(std::memory_order_acquire)) {
-    e = cudaFuncSetAttribute(block_prompt_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    e = cudaFuncSetAttribute(block_prompt_kernel<D, NT, SPREAD>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
     configured[dev].store(1, std::memory_order_release);
   }
@@ -890,7 +977,7 @@ cudaError_t launch(const CUtensorMap& mk, const CUtensorMap& mv, const BlockProm
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, block_prompt_kernel<D, NT>, mk, mv, p);
+  return cudaLaunchKernelEx(&cfg, block_prompt_kernel<D, NT, SPREAD>, mk, mv, p);
 }
 
 }  // namespace
@@ -904,9 +991,10 @@ cudaError_t launch_block_prompt(BlockPromptParams p, cudaStream_t stream, bool* 
   CUtensorMap mk, mv;
   *unsupported = k.sp == 0 || v.sp == 0 || (v.sh < v.st) != (k.sh < k.st) || !encode(&mk, k, p, rows) || !encode(&mv, v, p, rows);
   if (*unsupported) return cudaSuccess;
-  if (p.d == 256) return launch<256, 1>(mk, mv, p, stream);
-  return block_prompt_rows(p.d, int64_t(p.max_q_len) * p.h_r) == 256 ? launch<128, 2>(mk, mv, p, stream)
-                                                                       : launch<128, 1>(mk, mv, p, stream);
+  const int64_t n = int64_t(p.max_q_len) * p.h_r;
+  if (p.d == 256) return n <= 32 ? launch<256, 1, true>(mk, mv, p, stream) : launch<256, 1, false>(mk, mv, p, stream);
+  if (n <= 32) return launch<128, 1, true>(mk, mv, p, stream);
+  return block_prompt_rows(p.d, n) == 256 ? launch<128, 2, false>(mk, mv, p, stream) : launch<128, 1, false>(mk, mv, p, stream);
 }
 
 }  // namespace mj
