@@ -66,7 +66,9 @@ struct Cfg {
   static_assert(!kQt || (kQcol + D / 2 <= kO && kO + D <= 512), "tensor memory");
   static constexpr int kQ = kQt ? 0 : NT * 2 * DH * kTile;
   static constexpr int kK = kQ, kVr = kK + kKStages * kTile, kVf = kVr + 2 * kTile, kCtrl = kVf + 4 * kTile;
-  static constexpr int kBytes = kCtrl + 2048;
+  // (SPREAD) the rows' codes on their way to the copies, and their largest values
+  static constexpr int kQs = kCtrl + 2048, kQrow = D + 16;
+  static constexpr int kBytes = kQs + (NT == 1 ? 2 * 32 * kQrow + 512 : 0);
   static_assert(NT > 1 || 4 * D * 32 * 4 + 1024 <= kCtrl, "the copies' join");
 };
 static_assert(Cfg<128, 2>::kBytes + 1024 <= 227 * 1024 && Cfg<256, 1>::kBytes + 1024 <= 227 * 1024 && kKStages % 2 == 0,
@@ -390,11 +392,15 @@ __global__ void __launch_bounds__(512, 1)
     {
       // Q row: x' = x * 2^(127 - e), the largest finite |x'| in (224, 448]; hi = e4m3(x'), lo = e4m3(x' - hi)
       const uint4* src = reinterpret_cast<const uint4*>(p.q + tok * p.q_ts + head * p.q_hs);
+      // (SPREAD: each copy's warp takes a quarter of the channels, and the codes are handed
+      // round: the rows are read once a CTA, not four times. Every CTA of a split request reads the same.)
+      constexpr int kC0 = SPREAD ? D / 32 : D / 8;  // 16-byte pieces of the thread's
+      const int c0 = SPREAD ? quad * kC0 : 0;
       uint32_t am = 0;
       if (real) {
 #pragma unroll 8
-        for (int c = 0; c < D / 8; ++c) {
-          const uint4 v = __ldcg(src + c);
+        for (int c = 0; c < kC0; ++c) {
+          const uint4 v = __ldcg(src + c0 + c);
           const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
@@ -402,6 +408,14 @@ __global__ void __launch_bounds__(512, 1)
             am = max(am, max(lo < 0x7F80u ? lo : 0u, hi < 0x7F80u ? hi : 0u));
           }
         }
+      }
+      uint8_t* qs = smem + C::kQs;
+      if constexpr (SPREAD) {
+        uint32_t* tops = reinterpret_cast<uint32_t*>(qs + 2 * 32 * C::kQrow);
+        tops[32 * quad + lane] = am;
+        tc::named_bar_sync(1, 128);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) am = max(am, tops[32 * k + lane]);
       }
       // (e not below 64: ck 2^ek stays above 0, and a hidden key's -inf times it -inf)
       const int e = max(64, int(((am << 16) + 0x1FFFFFu) >> 23) - 8);
@@ -424,7 +438,41 @@ __global__ void __launch_bounds__(512, 1)
           lw |= uint32_t(l2) << (8 * j);
         }
       };
-      if constexpr (C::kQt) {
+      if constexpr (SPREAD) {
+#pragma unroll 1
+        for (int c = 0; c < D / 64; ++c) {  // 16 channels
+          uint4 u[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
+          if (real) {
+            u[0] = __ldcg(src + c0 + 2 * c);
+            u[1] = __ldcg(src + c0 + 2 * c + 1);
+          }
+          uint4 h, l4;
+          terms(u[0].x, u[0].y, h.x, l4.x);
+          terms(u[0].z, u[0].w, h.y, l4.y);
+          terms(u[1].x, u[1].y, h.z, l4.z);
+          terms(u[1].z, u[1].w, h.w, l4.w);
+          uint8_t* at = qs + lane * C::kQrow + quad * (D / 4) + 16 * c;
+          *reinterpret_cast<uint4*>(at) = h;
+          *reinterpret_cast<uint4*>(at + 32 * C::kQrow) = l4;
+        }
+        tc::named_bar_sync(1, 128);
+#pragma unroll 1
+        for (int c = 0; c < 2 * D / 64; ++c) {  // 64 codes: of hi, then of lo
+          const uint4* at = reinterpret_cast<const uint4*>(qs + (c / (D / 64)) * 32 * C::kQrow + lane * C::kQrow + c % (D / 64) * 64);
+          uint32_t w[16];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint4 u = at[k];
+            w[4 * k] = u.x;
+            w[4 * k + 1] = u.y;
+            w[4 * k + 2] = u.z;
+            w[4 * k + 3] = u.w;
+          }
+          tmem_st<16>(tmem + lanes + C::kQcol + uint32_t(16 * c), w);
+        }
+        tc::tmem_wait_st();
+        tc::tc_fence_before();
+      } else if constexpr (C::kQt) {
 #pragma unroll 1
         for (int c = 0; c < D / 64; ++c) {
           uint32_t hw[16], lw[16];
