@@ -747,17 +747,19 @@ MJ_API int mj_block_workspace_size(int slots, int q_len, int h_q, int h_k, int d
  * Requests with seq_lens[b] == 0 are padding: nothing is written for them. A
  * causal row that sees no key writes 0 (LSE -inf).
  *
- * Accuracy: a query enters the tensor cores as two 8-bit terms, exact down to
- * 2^-14 of the largest |q| among the rows of its request and KV head (within 2^-22
- * of it below); a value's weight, softmax weight times its block's scale, as two 8-bit
- * terms, within 2^-8 of itself down to 10 binades below its row's largest (below
- * that, where such keys are many, by two more terms, down to 28 binades). A row of
- * N keys is off by at most (2^-7 + N 2^-28) times its largest weight times 448. A query that is not finite makes its
- * row NaN; a NaN code of a cached token reaches every row of its request, also
- * one whose causal limit hides it.
+ * Accuracy. Up to 8 query rows a request and KV head (16 at head size 256), rows =
+ * q_len * h_q / h_k: a query enters the tensor cores as two 8-bit terms, exact down
+ * to 2^-14 of the largest |q| of those rows (within 2^-22 of it below); a value's
+ * weight, softmax weight times its block's scale, as two 8-bit terms, within 2^-8
+ * of itself down to 10 binades below its row's largest (below that, where such keys
+ * are many, by two more terms, down to 28 binades): a row of N keys is off by at
+ * most (2^-7 + N 2^-28) times its largest weight times 448. More rows: as
+ * mj_block_prompt. A query that is not finite makes its row NaN; a NaN code of a
+ * cached token reaches every row of its request, also one whose causal limit hides it.
  * Status bits (workspace): as mj_workspace_status lists them; bit 1 also for a
  * token past block_table_len, bit 4 also where a request's device length reaches
- * past the plan's tiles of it (the tokens past them are not attended to).
+ * past the plan's tiles of it (the tokens past them are not attended to, and a request
+ * that the plan has as padding is not written).
  * Two calls that may run at once (other streams, two captured graphs) need a
  * workspace each. out overlaps nothing that the call reads; its rows lie apart.
  * Make one call of each head size and row count before capturing.
@@ -801,11 +803,12 @@ MJ_API int mj_block_attention(const mj_block_args* args, void* stream);
  * what mj_block_prompt_splits gives, which fills sm_count SMs where the chunks
  * alone do not (max_len: the longest request).
  *
- * Accuracy: queries as in mj_block_attention, but exact down to 2^-10 of the
- * row's largest |q| (within 2^-18 of it below); weights in fp16, relative to a
- * running reference of their row, so that keys down to 24 binades below its largest count;
- * sums in float32. What that call says about values that are not finite, status
- * bits, workspaces and overlaps holds here.
+ * Accuracy: a query is exact down to 2^-10 of its row's largest |q| (within 2^-18
+ * of it below); weights in fp16 relative to a running reference of their row, within 2^-12 of
+ * themselves down to 20 binades below it and 2^-31 of it lower; sums in float32. What
+ * mj_block_attention says about values that are not finite, status bits,
+ * workspaces, overlaps and first calls holds here.
+ * Alignment: as mj_block_attention's.
  * ---------------------------------------------------------------------- */
 typedef struct mj_block_prompt_args {
   int num_seqs;

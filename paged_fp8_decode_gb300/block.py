@@ -65,7 +65,7 @@ def _set_cache(c: mj_block_cache, kv: BlockKV):
 
 
 def _status(status):
-    return None if status is None else _flat("status", status, status.dtype, 1).data_ptr()
+    return None if status is None else _flat("status", status, torch.int32, 1).data_ptr()
 
 
 def _held(kv: BlockKV):

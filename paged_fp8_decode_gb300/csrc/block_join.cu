@@ -39,6 +39,8 @@ __global__ void __launch_bounds__(32 * kWarps) block_join_kernel(BlockJoinParams
     const int g = int(bg % p.h_k), b = int(bg / p.h_k);
     const int4 rq = p.plan[b];
     const int L = p.seq_lens[b];
+    // a length past the tiles that the plan has of the request
+    if (lane == 0 && row == 0 && g == 0 && int64_t(L) > int64_t(rq.w) * kKvTile) atomicOr(p.status, kStatusBadPlan);
     if (rq.y <= 1 || L <= 0) return;  // in one piece: already written
     const int64_t span = int64_t(rq.z) * kKvTile;
     n = int(min(int64_t(rq.y), (int64_t(L) + span - 1) / span));  // pieces with a key

@@ -302,7 +302,7 @@ __global__ void __launch_bounds__(512, 1)
     const int4 rq = p.req[b];  // first partial, pieces, tiles a piece, tiles planned
     L = p.seq_lens[b];
     const bool bad = w.w < 0 || w.w >= rq.y || (rq.y > 1 && (rq.x < 0 || int64_t(rq.x) + rq.y > p.part_cap));
-    if (tid == 0 && (bad || (w.w == 0 && int64_t(L) > int64_t(rq.w) * kKvTile))) atomicOr(p.status, kStatusBadPlan);
+    if (tid == 0 && bad) atomicOr(p.status, kStatusBadPlan);
     n = p.max_q_len;
     t0 = b * n;
     rows = n * p.h_r;

@@ -424,10 +424,6 @@ __global__ void __launch_bounds__(KF != MJ_KV_E4M3 ? kThreadsTcFp6 : kThreadsTc,
     active = false;
   }
   const int L = active ? p.seq_lens[b] : 0;
-  if constexpr (BS) {
-    // a length past the plan's tiles of the request, seen by its first piece
-    if (active && w.w == 0 && threadIdx.x == 0 && int64_t(L) > int64_t(req.w) * kKvTile) atomicOr(p.status, kStatusBadPlan);
-  }
   const int64_t k0 = int64_t(w.y) * kKvTile;
   const int64_t k1 = min(int64_t(w.z) * kKvTile, int64_t(L));
   const int r0 = blockIdx.y * p.tw;

@@ -55,8 +55,9 @@ struct BlockJoinParams {
   int out_f16;
   int64_t out_ts, out_hs;
   float* lse;
+  uint32_t* status;
   // decode (plan != null): unit = (request, KV head, row)
-  const int4* plan;           // per request: first partial, pieces, tiles a piece
+  const int4* plan;           // per request: first partial, pieces, tiles a piece, tiles planned
   const int32_t* seq_lens;
   int h_k, h_r, n_q, q_len;
   // prompt: unit = (token, query head), `pieces` pieces each, lying `units` rows apart

@@ -476,3 +476,80 @@ def test_a_query_of_nan_over_split_requests():
 
 def step_lse(lse, B, h_q):
     return lse.reshape(B, h_q)
+
+
+@pytest.mark.parametrize("h_q,h_k,q_len,d", [(36, 1, 1, 128), (128, 1, 1, 128), (43, 1, 3, 128), (64, 1, 5, 128), (40, 1, 1, 256), (43, 1, 3, 256)])
+def test_decode_of_many_rows(h_q, h_k, q_len, d):
+    # 33 rows and more a KV head: one row tile, one of 256 rows, several
+    b = Batch([1, 0, 2, 130, 900, 5000], h_k=h_k, d=d, page=32, block=16, seed=h_q)
+    q = queries(b, b.B * q_len, h_q)
+    for causal in (True, False):
+        out, lse, status = decode(b, q, q_len, h_q, causal=causal)
+        assert status == 0
+        check_decode(b, q, out, lse, q_len, h_q, causal=causal)
+
+
+@pytest.mark.parametrize("h_q", [8, 32])
+def test_a_request_that_was_not_planned_is_reported(h_q):
+    b = Batch([300, 200], seed=16)
+    q = queries(b, 2, h_q)
+    out, lse, status = decode(b, q, 1, h_q, lens=np.array([300, 0], np.int32))
+    assert status == 4 and (out[1] == SENTINEL).all() and (out[0] != SENTINEL).all()
+    b.lens[1] = 0
+    b.lens_dev.copy_(up(b.lens))
+    out, lse, status = decode(b, q, 1, h_q)
+    assert status == 0
+    check_decode(b, q, out, lse, 1, h_q)
+
+
+@pytest.mark.parametrize("h_q", [8, 32])
+def test_two_steps_at_once_on_two_streams(h_q):
+    import paged_fp8_decode_gb300 as mj
+
+    batches = [Batch([20000, 300], h_k=2, page=64, block=32, seed=17), Batch([50, 9000, 1], h_k=2, page=64, block=32, seed=18)]
+    qs = [queries(b, b.B, h_q, seed=i) for i, b in enumerate(batches)]
+    want = [decode(b, q, 1, h_q)[0][:b.B].clone() for b, q in zip(batches, qs)]
+    steps, args, outs = [], [], []
+    for b, q in zip(batches, qs):
+        step = mj.BlockStep(max_num_seqs=b.B, q_len=1, h_q=h_q, h_k=2, d=128)
+        step.plan(b.lens, b.B)
+        outs.append(torch.zeros(b.B, h_q, 128, dtype=torch.bfloat16, device="cuda"))
+        args.append(step.args(q, outs[-1], b.kv(), b.table_dev, b.lens_dev, b.B, 128 ** -0.5))
+        steps.append(step)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in batches]
+    for _ in range(20):
+        for s, a in zip(streams, args):
+            mj.mj_block_attention(a, s)
+    torch.cuda.synchronize()
+    for o, w, st in zip(outs, want, steps):
+        assert torch.equal(o, w) and mj.mj_workspace_status(st.workspace) == 0
+
+
+def test_the_plan_lengths_and_table_rewritten_right_before():
+    # what the call reads early is only a guess: the batch before it lies in other pages, with other lengths
+    import paged_fp8_decode_gb300 as mj
+
+    for h_q in (8, 32):
+        b = Batch([4000, 130, 0, 77], h_k=2, seed=19)
+        kv = b.kv()
+        q = queries(b, 4, h_q)
+        step = mj.BlockStep(max_num_seqs=4, q_len=1, h_q=h_q, h_k=2, d=128, with_lse=True)
+        out = torch.full((4 + 2, h_q, 128), SENTINEL, dtype=torch.bfloat16, device="cuda")
+        table, lens = torch.zeros_like(b.table_dev), torch.zeros_like(b.lens_dev)
+        args = step.args(q, out, kv, table, lens, 4, 128 ** -0.5)
+        step.plan(np.array([50, 3000, 900, 0], np.int32), 4)
+        mj.mj_block_attention(args)
+        out.fill_(SENTINEL)
+        step.lse.fill_(SENTINEL)
+        step.plan(b.lens, 4)
+        new = step.plan_dev.clone()
+        step.plan(np.array([50, 3000, 900, 0], np.int32), 4)
+        mj.mj_workspace_status(step.workspace)
+        table.copy_(b.table_dev)
+        lens.copy_(b.lens_dev)
+        step.plan_dev.copy_(new)
+        mj.mj_block_attention(args)
+        torch.cuda.synchronize()
+        assert mj.mj_workspace_status(step.workspace) == 0
+        check_decode(b, q, out, step.lse, 1, h_q)

@@ -100,6 +100,18 @@ def test_a_longer_chunk(d):
     check(b, new, out, lse, q)
 
 
+@pytest.mark.parametrize("d", [128, 256])
+@pytest.mark.parametrize("h_q,longest", [(2, 9), (2, 33), (4, 30), (4, 70)])
+def test_rows_of_every_tile_shape(h_q, longest, d):
+    # the longest chunk's rows choose the kernel: up to 32 rows, up to 128, more
+    new = [longest, 1, longest // 2, 0]
+    b = Batch([900, 1, longest // 2, 50], h_k=1, d=d, page=32, block=32, seed=longest)
+    for splits in (1, 3):
+        out, lse, status, q = run(b, new, h_q, splits=splits)
+        assert status == 0
+        check(b, new, out, lse, q)
+
+
 def test_without_a_causal_limit():
     new = [40, 7]
     b = Batch([333, 7], seed=2)
