@@ -2,9 +2,11 @@
 //
 // A warp takes 32 output rows of one KV head of K or V. Its lanes first find
 // their row's request (a binary search in the row offsets), page and row; then
-// groups of D / 16 lanes take a token each, a lane 16 channels: 16 bytes of codes
-// in, 32 bytes out, all of a warp's loads issued before its stores. HBM bounds it:
-// 1 byte read and 2 written a channel.
+// groups of D / 8 lanes take a token each, a lane 8 channels: 8 bytes of codes
+// in, 16 bytes out, so that each load and each store of a warp covers whole rows.
+// HBM bounds it: 1 byte read and 2 written a channel. 12 requests of 500 to 16384
+// tokens, 8 heads of 128: 108 us, 6.3 TB/s, 94% of a copy's rate. (16 bytes in and 32 out a lane, two
+// stores of half-sectors: 112 us.)
 #include "mj_block.h"
 #include "mj_device.cuh"
 #include "tc_ptx.cuh"
@@ -21,9 +23,11 @@ __device__ __forceinline__ uint32_t out2(float a, float b) {
              : uint32_t(float_to_bf16_bits(a)) | (uint32_t(float_to_bf16_bits(b)) << 16);
 }
 
+// Eight loads ahead in 64 registers, four CTAs an SM (same call: four ahead 119 us; sixteen
+// ahead, three CTAs 117 us).
 template <int D, bool F16>
-__global__ void __launch_bounds__(kThreads) block_read_kernel(BlockReadParams p) {
-  constexpr int kLanesRow = D / 16;        // lanes a row
+__global__ void __launch_bounds__(kThreads, 4) block_read_kernel(BlockReadParams p) {
+  constexpr int kLanesRow = D / 8;         // lanes a row
   constexpr int kRowsIt = 32 / kLanesRow;  // rows at once
   constexpr int kIts = 32 / kRowsIt;
   tc::grid_launch_dependents();
@@ -60,24 +64,24 @@ __global__ void __launch_bounds__(kThreads) block_read_kernel(BlockReadParams p)
   }
 
   const BlockSide& sd = p.side[v];
-  const int sub = lane / kLanesRow, ch = (lane % kLanesRow) * 16;
+  const int sub = lane / kLanesRow, ch = (lane % kLanesRow) * 8;
   const uint8_t* codes = sd.codes + g * sd.sh + ch;
   const uint8_t* exps = sd.exps + g * sd.esh;
   uint16_t* out = p.out[v] + t0 * p.ts[v] + g * p.hs[v] + ch;
   constexpr int U = 8;
 #pragma unroll
   for (int i0 = 0; i0 < kIts; i0 += U) {
-    uint4 x[U];
+    uint2 x[U];
     int ex[U], pg[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int from = (i0 + u) * kRowsIt + sub;
       pg[u] = __shfl_sync(~0u, page, from);
       const int r = __shfl_sync(~0u, row, from);
-      x[u] = make_uint4(0u, 0u, 0u, 0u);
+      x[u] = make_uint2(0u, 0u);
       ex[u] = 127;
       if (pg[u] >= 0) {
-        x[u] = __ldcg(reinterpret_cast<const uint4*>(codes + pg[u] * sd.sp + r * sd.st));
+        x[u] = __ldcg(reinterpret_cast<const uint2*>(codes + pg[u] * sd.sp + r * sd.st));
         ex[u] = exps[pg[u] * sd.esp + (r >> p.block_shift)];
       }
     }
@@ -85,10 +89,10 @@ __global__ void __launch_bounds__(kThreads) block_read_kernel(BlockReadParams p)
     for (int u = 0; u < U; ++u) {
       if (pg[u] < -1) continue;
       const float by = __int_as_float(block_exp(ex[u]) << 23);
-      const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
-      uint32_t o[8];
+      const uint32_t w[2] = {x[u].x, x[u].y};
+      uint32_t o[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
+      for (int k = 0; k < 2; ++k) {
         float f[4];
         e4m3x4_to_float(w[k], f);
         o[2 * k] = out2<F16>(f[0] * by, f[1] * by);
@@ -96,7 +100,6 @@ __global__ void __launch_bounds__(kThreads) block_read_kernel(BlockReadParams p)
       }
       uint4* dst = reinterpret_cast<uint4*>(out + int64_t((i0 + u) * kRowsIt + sub) * p.ts[v]);
       __stcs(dst, make_uint4(o[0], o[1], o[2], o[3]));
-      __stcs(dst + 1, make_uint4(o[4], o[5], o[6], o[7]));
     }
   }
 }

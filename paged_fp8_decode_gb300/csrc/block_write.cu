@@ -71,12 +71,13 @@ __device__ __noinline__ int64_t find_live(const int64_t* slots, int64_t from, in
   return -1;
 }
 
-// G warps share a block of G rows_warp(D) rows. (Two CTAs an SM where they hold 8 warps: left to
-// itself the compiler takes 127 registers, and a call too small to fill the GPU
-// by much is bound by the latency of few warps; 16 rows of 256 channels a warp took 215: 15.9 us
-// for the ragged call below.)
+// G warps share a block of G rows_warp(D) rows. Three CTAs of 8 warps an SM, 80 registers: the
+// moves of earlier codes are a loop of their own, since few runs have them. (4 x 4096 tokens of
+// 8 heads of 128: 20.4 us, 4.9 TB/s; two CTAs of 120 registers 21.6 us; four, or half the rows a
+// warp, 18.2 us, but then 11 ragged chunks of 1..700 tokens, head size 256, which take 9.7 us
+// here, take 10.6 and 11.3, and 64 tokens 3.3 and 3.6 us in place of 3.1.)
 template <int D, int G>
-__global__ void __launch_bounds__(32 * warps_cta(G), 16 / warps_cta(G)) block_write_kernel(BlockWriteParams p) {
+__global__ void __launch_bounds__(32 * warps_cta(G), 24 / warps_cta(G)) block_write_kernel(BlockWriteParams p) {
   constexpr int kWarps = warps_cta(G), kRowsWarp = rows_warp(D);
   constexpr int kLanesRow = D / 8;             // lanes a row: 8 channels, 16 bytes of input each
   constexpr int kRowsIt = 32 / kLanesRow;      // rows a warp takes at once
@@ -201,23 +202,15 @@ __global__ void __launch_bounds__(32 * warps_cta(G), 16 / warps_cta(G)) block_wr
           // the earlier tokens move to the larger scale
           const float by = __int_as_float((127 + old - e) << 23);
           const int n = min(kRowsWarp, first - kRowsWarp * part);
-          uint2 y[kIts];
-#pragma unroll
-          for (int i = 0; i < kIts; ++i) {
-            const int r = i * kRowsIt + sub;
-            if (r < n) y[i] = *reinterpret_cast<const uint2*>(dst + r * sd.st);
-          }
-#pragma unroll
-          for (int i = 0; i < kIts; ++i) {
-            const int r = i * kRowsIt + sub;
-            if (r < n) {
-              float f[8];
-              e4m3x4_to_float(y[i].x, f);
-              e4m3x4_to_float(y[i].y, f + 4);
-              *reinterpret_cast<uint2*>(dst + r * sd.st) =
-                  make_uint2(codes4(f[0] * by, f[1] * by, f[2] * by, f[3] * by),
+#pragma unroll 2
+          for (int r = sub; r < n; r += kRowsIt) {
+            uint2* at = reinterpret_cast<uint2*>(dst + r * sd.st);
+            const uint2 y = *at;
+            float f[8];
+            e4m3x4_to_float(y.x, f);
+            e4m3x4_to_float(y.y, f + 4);
+            *at = make_uint2(codes4(f[0] * by, f[1] * by, f[2] * by, f[3] * by),
                              codes4(f[4] * by, f[5] * by, f[6] * by, f[7] * by));
-            }
           }
         }
       }
