@@ -66,23 +66,22 @@ struct Cfg {
   static_assert(!kQt || (kQcol + D / 2 <= kO && kO + D <= 512), "tensor memory");
   static constexpr int kQ = kQt ? 0 : NT * 2 * DH * kTile;
   static constexpr int kK = kQ, kVr = kK + kKStages * kTile, kVf = kVr + 2 * kTile, kCtrl = kVf + 4 * kTile;
-  // (SPREAD) the rows' codes on their way to the copies, and their largest values
-  static constexpr int kQs = kCtrl + 2048, kQrow = D + 16;
-  static constexpr int kBytes = kQs + (NT == 1 ? 2 * 32 * kQrow + 512 : 0);
+  static constexpr int kBytes = kCtrl + 2048;
   static_assert(NT > 1 || 4 * D * 32 * 4 + 1024 <= kCtrl, "the copies' join");
 };
 static_assert(Cfg<128, 2>::kBytes + 1024 <= 227 * 1024 && Cfg<256, 1>::kBytes + 1024 <= 227 * 1024 && kKStages % 2 == 0,
               "shared memory");
 
 struct Ctrl {
-  uint64_t k_full[kKStages], k_empty[kKStages];
-  uint64_t vr_full[2], vr_empty[2], vf_full[2], vf_empty[2];
+  uint64_t k_full[kKStages];
+  uint64_t vr_full[2], vr_empty[2], vf_full[2];
   uint64_t s_full[2], p_full[2][2];  // (P in halves of its keys)
-  uint64_t o_done;  // one row tile: a product on V is done
+  uint64_t done[4];  // of step i modulo 4: tile i's products on V, and tile i + 1's scores
   uint64_t e_full[2], e_empty[2];
   uint64_t q_ready, drain, o_last[2];  // o_last: a row tile's last product
   uint32_t tmem;
   int abort;
+  uint8_t q_exp[256];  // the rows' exponents
   alignas(16) float4 scale[2][32];  // batches of TB tiles: 2^ek, ev, 2^-ev of each 16-key group
 };
 static_assert(sizeof(Ctrl) <= 2048, "control block");
@@ -259,11 +258,25 @@ __device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
+// lo and hi to bf16, packed
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
 // two e4m3 codes to fp16, exactly
 __device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t two) {
   uint32_t r;
   asm("{\n\t.reg .b16 x, y;\n\tmov.b32 {x, y}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, x;\n\t}" : "=r"(r) : "r"(two));
   return r;
+}
+
+// x (two fp16) = hi + lo, two e4m3 codes each
+__device__ __forceinline__ void split_e4m3(uint32_t x, uint32_t& hi, uint32_t& lo) {
+  asm("{\n\t.reg .b16 h, l;\n\t.reg .b32 y;\n\tcvt.rn.satfinite.e4m3x2.f16x2 h, %2;\n\tcvt.rn.f16x2.e4m3x2 y, h;\n\t"
+      "sub.rn.f16x2 y, %2, y;\n\tcvt.rn.satfinite.e4m3x2.f16x2 l, y;\n\tcvt.u32.u16 %0, h;\n\tcvt.u32.u16 %1, l;\n\t}"
+      : "=r"(hi), "=r"(lo)
+      : "r"(x));
 }
 
 template <int D, int NT, bool SPREAD>
@@ -277,6 +290,7 @@ __global__ void __launch_bounds__(512, 1)
   // for the others. Each copy has a reference, a sum and an output of its own; they are joined
   // at the end, as pieces of the keys are.
   static_assert(!SPREAD || NT == 1, "one row tile");
+  constexpr int kHalves = BN == 128 && !SPREAD ? 2 : 1;  // P is handed over in halves of its keys
   constexpr int HC = SPREAD ? BN / 4 : BN, HB = HC / 16;  // columns (keys) of a softmax thread, 16-key groups
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   // (32-bit shared addresses throughout, from constants: what the products are issued with stays in uniform registers)
@@ -342,24 +356,20 @@ __global__ void __launch_bounds__(512, 1)
   const int nt = k_end > k0 ? (k_end - k0 + BN - 1) / BN : 0;
 
   if (tid == 0) {
-    for (int s = 0; s < kKStages; ++s) {
-      tc::mbar_init(bar(ctl.k_full[s]), 1);
-      tc::mbar_init(bar(ctl.k_empty[s]), 1);
-    }
+    for (int s = 0; s < kKStages; ++s) tc::mbar_init(bar(ctl.k_full[s]), 1);
+    for (int s = 0; s < 4; ++s) tc::mbar_init(bar(ctl.done[s]), 1);
     for (int s = 0; s < 2; ++s) {
       tc::mbar_init(bar(ctl.vr_full[s]), 1);
-      tc::mbar_init(bar(ctl.vr_empty[s]), 32 * C::kConvWarps);
-      tc::mbar_init(bar(ctl.vf_full[s]), 32 * C::kConvWarps);
-      tc::mbar_init(bar(ctl.vf_empty[s]), 1);
+      tc::mbar_init(bar(ctl.vr_empty[s]), C::kConvWarps);
+      tc::mbar_init(bar(ctl.vf_full[s]), C::kConvWarps);
       tc::mbar_init(bar(ctl.s_full[s]), 1);
-      for (int h = 0; h < 2; ++h) tc::mbar_init(bar(ctl.p_full[s][h]), 128);
+      for (int h = 0; h < 2; ++h) tc::mbar_init(bar(ctl.p_full[s][h]), 4);
       tc::mbar_init(bar(ctl.o_last[s]), 1);
       tc::mbar_init(bar(ctl.e_full[s]), 1);
       tc::mbar_init(bar(ctl.e_empty[s]), 4 * NT);
     }
     tc::mbar_init(bar(ctl.q_ready), 128 * NT);
     tc::mbar_init(bar(ctl.drain), 1);
-    tc::mbar_init(bar(ctl.o_done), 1);
     ctl.abort = 0;
     tc::fence_mbar_init();
   }
@@ -377,6 +387,114 @@ __global__ void __launch_bounds__(512, 1)
   constexpr uint32_t tmem = 0;  // all 512 columns: the allocation begins at 0
   volatile int* abort = &ctl.abort;
 
+  // Q's rows, by the twelve warps that have nothing else to do yet, 8 channels a lane: x' = x *
+  // 2^(127 - e), the row's largest finite |x'| in (224, 448]; hi = e4m3(x'), lo = e4m3(x' - hi). In fp16
+  // both are exact: what fp16 rounds of x' is far below e4m3's smallest step. (By the softmax
+  // threads, each its own row, this took 12000 cycles a CTA at head size 256.)
+  if (warp >= 4) {
+    constexpr int kRowLanes = D / 8, kRowsLd = 32 / kRowLanes, kMine = SPREAD ? 32 : C::kRows;
+    const int j0 = (warp - 4) * kRowsLd + lane / kRowLanes, ch = lane % kRowLanes * 8;
+    // The rows as they are, all on their way at once, to where V's first tiles are widened to later; a
+    // thread reads back what it copied. (Short loops: a CTA of the first wave waits for its code, too.)
+    const uint32_t in = base + uint32_t(C::kVf + lane % kRowLanes * 16);
+    {
+      // a row's token and head, from the CTA's first row's (exact: rem + j is far below 2^21)
+      const int tq = r0 / p.h_r, rem = r0 - tq * p.h_r;
+      const float recip = 1.f / float(p.h_r);
+#pragma unroll 4
+      for (int j = j0; j < kMine; j += 12 * kRowsLd) {
+        const int dt = int((float(rem + j) + 0.5f) * recip);
+        const bool real = r0 + j < rows;
+        const uint16_t* src = p.q + ch;
+        if (real) src += int64_t(t0 + tq + dt) * p.q_ts + (int64_t(g) * p.h_r + (rem + j - dt * p.h_r)) * p.q_hs;
+        tc::cp_async16(in + uint32_t(j * (2 * D)), src, real ? 16u : 0u);
+      }
+    }
+    tc::cp_async_wait_all();
+    // (four rows abreast: one row's shuffles and conversions are a chain of 600 cycles)
+    constexpr int kAbreast = SPREAD ? 3 : 4;
+#pragma unroll 1
+    for (int jj = j0; jj < kMine; jj += 12 * kRowsLd * kAbreast) {
+      uint32_t w[kAbreast][4], am[kAbreast], odd[kAbreast];
+#pragma unroll
+      for (int u = 0; u < kAbreast; ++u) {
+        const int j = jj + u * 12 * kRowsLd < kMine ? jj + u * 12 * kRowsLd : jj;  // (past the end: not written)
+        const uint4 v = *reinterpret_cast<const uint4*>(smem + C::kVf + lane % kRowLanes * 16 + j * (2 * D));
+        w[u][0] = v.x;
+        w[u][1] = v.y;
+        w[u][2] = v.z;
+        w[u][3] = v.w;
+      }
+      auto largest = [&] {
+#pragma unroll
+        for (int u = 0; u < kAbreast; ++u) {
+          uint32_t m = 0;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) m = __vmaxu2(m, w[u][k] & 0x7FFF7FFFu);
+          am[u] = max(m & 0xFFFFu, m >> 16);
+        }
+#pragma unroll
+        for (int o = kRowLanes / 2; o > 0; o >>= 1)
+#pragma unroll
+          for (int u = 0; u < kAbreast; ++u) am[u] = max(am[u], __shfl_xor_sync(~0u, am[u], o));
+      };
+      largest();
+      uint32_t any = 0;
+#pragma unroll
+      for (int u = 0; u < kAbreast; ++u) {
+        any = max(any, am[u]);
+        odd[u] = 0;
+      }
+      if (__any_sync(~0u, any >= 0x7F80u)) {  // infinities or NaN: NaN codes; they do not count above
+#pragma unroll
+        for (int u = 0; u < kAbreast; ++u)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            if ((w[u][k] & 0x7FFFu) >= 0x7F80u) {
+              w[u][k] &= 0xFFFF0000u;
+              odd[u] |= 1u << (2 * k);
+            }
+            if ((w[u][k] & 0x7FFF0000u) >= 0x7F800000u) {
+              w[u][k] &= 0xFFFFu;
+              odd[u] |= 2u << (2 * k);
+            }
+          }
+        largest();
+      }
+      __syncwarp();  // (in place: the rows have been read)
+#pragma unroll
+      for (int u = 0; u < kAbreast; ++u) {
+        const int j = jj + u * 12 * kRowsLd;
+        // (e not below 64: ck 2^ek stays above 0, and a hidden key's -inf times it -inf)
+        const int e = max(64, int(((am[u] << 16) + 0x1FFFFFu) >> 23) - 8);
+        const float inv = __int_as_float((254 - e) << 23);
+        uint32_t hw[4], lw[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          split_e4m3(f16x2(__uint_as_float(w[u][k] << 16) * inv, __uint_as_float(w[u][k] & 0xFFFF0000u) * inv), hw[k], lw[k]);
+        uint2 hi = make_uint2(__byte_perm(hw[0], hw[1], 0x5410), __byte_perm(hw[2], hw[3], 0x5410));
+        const uint2 lo = make_uint2(__byte_perm(lw[0], lw[1], 0x5410), __byte_perm(lw[2], lw[3], 0x5410));
+        if (odd[u]) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            if (odd[u] >> k & 1u) hi.x |= 0x7Fu << (8 * k);
+            if (odd[u] >> (k + 4) & 1u) hi.y |= 0x7Fu << (8 * k);
+          }
+        }
+        if (j >= kMine) break;
+        // One row tile: [row][hi, lo] in place, on their way to tensor memory. 16-byte pieces
+        // swizzled by the row in both places.
+        uint8_t* at = smem + (C::kQt ? C::kVf + j * (2 * D) : (j >> 7) * (2 * kTile) + (j & 127) * 128) +
+                      (((ch >> 4) ^ (j & 7)) << 4) + (ch & 8);
+        *reinterpret_cast<uint2*>(at) = hi;
+        *reinterpret_cast<uint2*>(at + (C::kQt ? D : kTile)) = lo;
+        if (ch == 0) ctl.q_exp[j] = uint8_t(e);
+      }
+    }
+    if constexpr (!C::kQt) tc::fence_async_smem();
+    tc::named_bar_sync(1, 384);
+  }
+
   // Registers: 128 a thread at launch. At head size 128 a softmax thread keeps a row's 128
   // scores: 2 x 192 + 2 x 64, or 224 + 3 x 96, = 4 x 128 for the four warpgroups.
   if (warp >= 4 && warp < C::kConvWarp0) {
@@ -390,79 +508,15 @@ __global__ void __launch_bounds__(512, 1)
     const uint32_t lanes = uint32_t(32 * quad) << 16;
     float ck;  // logits (log2 units) = S * ck * 2^ek
     {
-      // Q row: x' = x * 2^(127 - e), the largest finite |x'| in (224, 448]; hi = e4m3(x'), lo = e4m3(x' - hi)
-      const uint4* src = reinterpret_cast<const uint4*>(p.q + tok * p.q_ts + head * p.q_hs);
-      // (SPREAD: each copy's warp takes a quarter of the channels, and the codes are handed
-      // round: the rows are read once a CTA, not four times. Every CTA of a split request reads the same.)
-      constexpr int kC0 = SPREAD ? D / 32 : D / 8;  // 16-byte pieces of the thread's
-      const int c0 = SPREAD ? quad * kC0 : 0;
-      uint32_t am = 0;
-      if (real) {
-#pragma unroll 8
-        for (int c = 0; c < kC0; ++c) {
-          const uint4 v = __ldcg(src + c0 + c);
-          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint32_t lo = w[k] & 0x7FFFu, hi = (w[k] >> 16) & 0x7FFFu;
-            am = max(am, max(lo < 0x7F80u ? lo : 0u, hi < 0x7F80u ? hi : 0u));
-          }
-        }
-      }
-      uint8_t* qs = smem + C::kQs;
-      if constexpr (SPREAD) {
-        uint32_t* tops = reinterpret_cast<uint32_t*>(qs + 2 * 32 * C::kQrow);
-        tops[32 * quad + lane] = am;
-        tc::named_bar_sync(1, 128);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) am = max(am, tops[32 * k + lane]);
-      }
-      // (e not below 64: ck 2^ek stays above 0, and a hidden key's -inf times it -inf)
-      const int e = max(64, int(((am << 16) + 0x1FFFFFu) >> 23) - 8);
-      const float inv = __int_as_float((254 - e) << 23);
-      ck = __int_as_float(e << 23) * p.scale_log2;
-      // four channels' codes of both terms
-      auto terms = [&](uint32_t w0, uint32_t w1, uint32_t& hw, uint32_t& lw) {
-        float x[4] = {__uint_as_float(w0 << 16) * inv, __uint_as_float(w0 & 0xFFFF0000u) * inv,
-                      __uint_as_float(w1 << 16) * inv, __uint_as_float(w1 & 0xFFFF0000u) * inv};
-        hw = lw = 0u;
-#pragma unroll
-        for (int j = 0; j < 4; j += 2) {
-          if (!(fabsf(x[j]) < INFINITY)) x[j] = NAN;
-          if (!(fabsf(x[j + 1]) < INFINITY)) x[j + 1] = NAN;
-          const __nv_fp8x2_storage_t h2 = __nv_cvt_float2_to_fp8x2(make_float2(x[j], x[j + 1]), __NV_SATFINITE, __NV_E4M3);
-          const float2 hv = e4m3x2_to_float2(h2);
-          const __nv_fp8x2_storage_t l2 =
-              __nv_cvt_float2_to_fp8x2(make_float2(x[j] - hv.x, x[j + 1] - hv.y), __NV_SATFINITE, __NV_E4M3);
-          hw |= uint32_t(h2) << (8 * j);
-          lw |= uint32_t(l2) << (8 * j);
-        }
-      };
-      if constexpr (SPREAD) {
-#pragma unroll 1
-        for (int c = 0; c < D / 64; ++c) {  // 16 channels
-          uint4 u[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
-          if (real) {
-            u[0] = __ldcg(src + c0 + 2 * c);
-            u[1] = __ldcg(src + c0 + 2 * c + 1);
-          }
-          uint4 h, l4;
-          terms(u[0].x, u[0].y, h.x, l4.x);
-          terms(u[0].z, u[0].w, h.y, l4.y);
-          terms(u[1].x, u[1].y, h.z, l4.z);
-          terms(u[1].z, u[1].w, h.w, l4.w);
-          uint8_t* at = qs + lane * C::kQrow + quad * (D / 4) + 16 * c;
-          *reinterpret_cast<uint4*>(at) = h;
-          *reinterpret_cast<uint4*>(at + 32 * C::kQrow) = l4;
-        }
-        tc::named_bar_sync(1, 128);
-#pragma unroll 1
+      const uint8_t* qs = smem + C::kVf + (SPREAD ? 0 : quad * (64 * D));
+      ck = __int_as_float(int(ctl.q_exp[SPREAD ? lane : 32 * (warp - 4) + lane]) << 23) * p.scale_log2;
+      if constexpr (C::kQt) {
+#pragma unroll 4
         for (int c = 0; c < 2 * D / 64; ++c) {  // 64 codes: of hi, then of lo
-          const uint4* at = reinterpret_cast<const uint4*>(qs + (c / (D / 64)) * 32 * C::kQrow + lane * C::kQrow + c % (D / 64) * 64);
           uint32_t w[16];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const uint4 u = at[k];
+            const uint4 u = *reinterpret_cast<const uint4*>(qs + lane * (2 * D) + (((4 * c + k) ^ (lane & 7)) << 4));
             w[4 * k] = u.x;
             w[4 * k + 1] = u.y;
             w[4 * k + 2] = u.z;
@@ -472,42 +526,6 @@ __global__ void __launch_bounds__(512, 1)
         }
         tc::tmem_wait_st();
         tc::tc_fence_before();
-      } else if constexpr (C::kQt) {
-#pragma unroll 1
-        for (int c = 0; c < D / 64; ++c) {
-          uint32_t hw[16], lw[16];
-#pragma unroll
-          for (int k = 0; k < 16; k += 2) {
-            const uint4 u = real ? __ldcg(src + 8 * c + k / 2) : make_uint4(0u, 0u, 0u, 0u);
-            terms(u.x, u.y, hw[k], lw[k]);
-            terms(u.z, u.w, hw[k + 1], lw[k + 1]);
-          }
-          tmem_st<16>(tmem + lanes + C::kQcol + uint32_t(16 * c), hw);
-          tmem_st<16>(tmem + lanes + C::kQcol + uint32_t(D / 4 + 16 * c), lw);
-        }
-        tc::tmem_wait_st();
-        tc::tc_fence_before();
-      } else {
-        const int r = 32 * quad + lane;
-#pragma unroll 2
-        for (int c = 0; c < D / 16; ++c) {
-          uint4 v[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
-          if (real) {
-            v[0] = __ldcg(src + 2 * c);
-            v[1] = __ldcg(src + 2 * c + 1);
-          }
-          uint32_t hw[4], lw[4];
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            terms(v[k].x, v[k].y, hw[2 * k], lw[2 * k]);
-            terms(v[k].z, v[k].w, hw[2 * k + 1], lw[2 * k + 1]);
-          }
-          const int dh = c >> 3;
-          uint8_t* at = smem + (a * 2 * DH + dh) * kTile + r * 128 + (((c & 7) ^ (r & 7)) << 4);
-          *reinterpret_cast<uint4*>(at) = make_uint4(hw[0], hw[1], hw[2], hw[3]);
-          *reinterpret_cast<uint4*>(at + DH * kTile) = make_uint4(lw[0], lw[1], lw[2], lw[3]);
-        }
-        tc::fence_async_smem();
       }
       tc::mbar_arrive(bar(ctl.q_ready));
     }
@@ -588,7 +606,7 @@ __global__ void __launch_bounds__(512, 1)
         // tiles this tile's scores were issued behind the last of them. With one they
         // were issued before it.)
         if constexpr (NT == 1) {
-          ok = __all_sync(~0u, wait_bar<0>(bar(ctl.o_done), uint32_t(i - 1) & 1u, abort));
+          ok = __all_sync(~0u, wait_bar<0>(bar(ctl.done[(i - 1) & 3]), uint32_t((i - 1) >> 2) & 1u, abort));
           if (!ok) return false;
           tc::tc_fence_after();
         }
@@ -629,10 +647,11 @@ __global__ void __launch_bounds__(512, 1)
           for (int k = 0; k < d; ++k) x[k] = add2(x[k], x[k + d]);
         l = fmaf(x[0].x + x[0].y, sc[h].z, l);
       };
-      auto give = [&](int h) {  // a half of the tile's keys
+      auto give = [&](int h) {
         tc::tmem_wait_st();
         tc::tc_fence_before();
-        tc::mbar_arrive(bar(ctl.p_full[buf][h]));
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(bar(ctl.p_full[buf][h]));
       };
       if constexpr (SPREAD) {
         uint32_t w[HC / 2];
@@ -651,14 +670,17 @@ __global__ void __launch_bounds__(512, 1)
             tmem_st<HC / 2>(tS + k * (HC / 2), none);
         }
         give(0);
-        tc::mbar_arrive(bar(ctl.p_full[buf][1]));
       } else {
         auto store = [&](int c) {
           uint32_t w[16];
           pack(2 * c, w);
           pack(2 * c + 1, w + 8);
           tmem_st<16>(tS + 16 * c, w);
-          if (c % (BN / 64) == BN / 64 - 1) give(c / (BN / 64));
+          if constexpr (kHalves == 2) {
+            if (c & 1) give(c >> 1);
+          } else {
+            if (c == BN / 32 - 1) give(0);
+          }
         };
         exps(0);
         exps(1);
@@ -691,7 +713,7 @@ __global__ void __launch_bounds__(512, 1)
       float* all = reinterpret_cast<float*>(smem);
       float2* ml = reinterpret_cast<float2*>(all + 4 * D * 32);
       ml[32 * quad + lane] = ok ? make_float2(m, l) : make_float2(-INFINITY, 0.f);
-      tc::named_bar_sync(1, 128);
+      tc::named_bar_sync(2, 128);
       float M = -INFINITY, sum = 0.f;
 #pragma unroll
       for (int k = 0; k < 4; ++k) M = fmaxf(M, ml[32 * k + lane].x);
@@ -709,7 +731,7 @@ __global__ void __launch_bounds__(512, 1)
 #pragma unroll
         for (int k = 0; k < 32; ++k) all[(quad * D + c + k) * 32 + lane] = nt > 0 ? __uint_as_float(r[k]) * f : 0.f;
       }
-      tc::named_bar_sync(1, 128);
+      tc::named_bar_sync(2, 128);
       m = M;
       l = sum;
     }
@@ -718,41 +740,85 @@ __global__ void __launch_bounds__(512, 1)
       const bool some = nt > 0 && !(l == 0.f);
       // the row's place in its partials and in the LSE
       const int64_t part = parts + (p.work ? R : (tok - t0) * p.h_q + head);
+      auto out2 = [&](float x, float y) {  // (0 for a row that sees nothing)
+        return some ? (p.out_f16 ? f16x2(x, y) : bf16x2(x, y)) : 0u;
+      };
       const int64_t lse_at = p.work ? (int64_t(b) * p.h_k + g) * rows + R : tok * p.h_q + head;
-      // (of joined copies each thread writes a quarter of the row)
+      if constexpr (SPREAD) {  // each thread writes a quarter of the row
+        const float* all = reinterpret_cast<const float*>(smem) + lane;
 #pragma unroll 1
-      for (int c = SPREAD ? quad * (D / 4) : 0; c < (SPREAD ? (quad + 1) * (D / 4) : D); c += 32) {
-        uint32_t r[32];
-        if constexpr (SPREAD) {
-          const float* all = reinterpret_cast<const float*>(smem) + lane;
+        for (int c = quad * (D / 4); c < (quad + 1) * (D / 4); c += 32) {
+          float o[32];
 #pragma unroll
           for (int k = 0; k < 32; ++k)
-            r[k] = __float_as_uint((all[(c + k) * 32] + all[(D + c + k) * 32]) + (all[(2 * D + c + k) * 32] + all[(3 * D + c + k) * 32]));
-        } else if (nt > 0) {
-          tmem_ld32(tmem + lanes + C::kO + uint32_t(a * D + c), r);
-          tmem_wait_ld<32>(r);
-        }
-        if (!real) continue;
-        if (parts >= 0) {
-          if (!some) continue;
-          float4* dst = reinterpret_cast<float4*>(p.o_part + part * D + c);
+            o[k] = ((all[(c + k) * 32] + all[(D + c + k) * 32]) + (all[(2 * D + c + k) * 32] + all[(3 * D + c + k) * 32])) * inv;
+          if (!real) continue;
+          if (parts >= 0) {
+            if (!some) continue;
+            float4* dst = reinterpret_cast<float4*>(p.o_part + part * D + c);
 #pragma unroll
-          for (int k = 0; k < 32; k += 4)
-            dst[k / 4] = make_float4(__uint_as_float(r[k]) * inv, __uint_as_float(r[k + 1]) * inv,
-                                     __uint_as_float(r[k + 2]) * inv, __uint_as_float(r[k + 3]) * inv);
-        } else {
-          uint4* dst = reinterpret_cast<uint4*>(p.out + tok * p.out_ts + head * p.out_hs + c);
+            for (int k = 0; k < 32; k += 4) dst[k / 4] = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+          } else {
+            uint4* dst = reinterpret_cast<uint4*>(p.out + tok * p.out_ts + head * p.out_hs + c);
 #pragma unroll
-          for (int k = 0; k < 32; k += 8) {
-            uint32_t o[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              o[j] = some ? uint32_t(float_to_out_bits(__uint_as_float(r[k + 2 * j]) * inv, p.out_f16)) |
-                                (uint32_t(float_to_out_bits(__uint_as_float(r[k + 2 * j + 1]) * inv, p.out_f16)) << 16)
-                          : 0u;
-            dst[k / 8] = make_uint4(o[0], o[1], o[2], o[3]);
+            for (int k = 0; k < 32; k += 8)
+              dst[k / 8] = make_uint4(out2(o[k], o[k + 1]), out2(o[k + 2], o[k + 3]), out2(o[k + 4], o[k + 5]), out2(o[k + 6], o[k + 7]));
           }
         }
+      } else {
+        // Through shared memory, whose tiles are consumed by now, so that a warp writes whole rows (a
+        // thread writing its own, 32 lines a store, took 6500 cycles a CTA at head size 256). 512 bytes
+        // of a row at most, its 16-byte pieces swizzled by the row.
+        uint8_t* st = smem + C::kK + (warp - 4) * (32 * 512);
+        const int64_t at = parts >= 0 ? part * D : tok * p.out_ts + head * p.out_hs;  // where the row begins
+        const unsigned wanted = __ballot_sync(~0u, real && (some || parts < 0));
+        auto rows_out = [&](auto partial) {
+          constexpr bool f32 = decltype(partial)::value;
+          constexpr int kCh = f32 ? 128 : D, kPieces = kCh * (f32 ? 4 : 2) / 16, kRowsSt = 32 / kPieces;
+#pragma unroll 1
+          for (int c0 = 0; c0 < D; c0 += kCh) {
+#pragma unroll 1
+            for (int c = c0; c < c0 + kCh; c += 64) {
+              uint32_t r[64];
+              if (nt > 0) {
+                tmem_ld32(tmem + lanes + C::kO + uint32_t(a * D + c), r);
+                tmem_ld32(tmem + lanes + C::kO + uint32_t(a * D + c + 32), r + 32);
+                tmem_wait_ld<32>(r);
+                tmem_pass32(r + 32);
+              }
+              float o[64];
+#pragma unroll
+              for (int k = 0; k < 64; ++k) o[k] = __uint_as_float(r[k]) * inv;
+              constexpr int kPer = f32 ? 4 : 8;  // channels a piece
+#pragma unroll
+              for (int k = 0; k < 64; k += kPer) {
+                uint4 v;
+                if constexpr (f32)
+                  v = make_uint4(__float_as_uint(o[k]), __float_as_uint(o[k + 1]), __float_as_uint(o[k + 2]), __float_as_uint(o[k + 3]));
+                else
+                  v = make_uint4(out2(o[k], o[k + 1]), out2(o[k + 2], o[k + 3]), out2(o[k + 4], o[k + 5]), out2(o[k + 6], o[k + 7]));
+                *reinterpret_cast<uint4*>(st + lane * 512 + ((((c - c0 + k) / kPer) ^ (lane & 7)) << 4)) = v;
+              }
+            }
+            __syncwarp();
+#pragma unroll 8
+            for (int j0 = 0; j0 < 32; j0 += kRowsSt) {
+              const int j = j0 + lane / kPieces, pc = lane % kPieces;
+              const int64_t to = __shfl_sync(~0u, at, j) + c0;
+              const uint4 v = *reinterpret_cast<const uint4*>(st + j * 512 + ((pc ^ (j & 7)) << 4));
+              if (!(wanted >> j & 1u)) continue;
+              if constexpr (f32)
+                *reinterpret_cast<uint4*>(p.o_part + to + 4 * pc) = v;
+              else
+                *reinterpret_cast<uint4*>(p.out + to + 8 * pc) = v;
+            }
+            __syncwarp();
+          }
+        };
+        if (parts >= 0)
+          rows_out(std::true_type{});
+        else
+          rows_out(std::false_type{});
       }
       if (real && (!SPREAD || quad == 0)) {
         if (parts >= 0) {
@@ -777,11 +843,13 @@ __global__ void __launch_bounds__(512, 1)
     const uint8_t* src0 = smem + C::kVr + row0 * 128 + ((ch ^ x7) << 4);
     uint8_t* dst0 = smem + C::kVf + swap * (BN * 128) + row0 * 128;
     const int at0 = ((q + swap) ^ x7) << 4, at1 = ((q + 1 - swap) ^ x7) << 4;
-    bool ok = true;
-    for (int i = 0; i < nt; ++i) {
+    // (one row tile: Q's codes pass through here first)
+    bool ok = NT == 2 || wait_bar<100>(bar(ctl.q_ready), 0, abort);
+    for (int i = 0; i < nt && ok; ++i) {
       const int s = i & 1;
       const uint32_t ph = uint32_t(i >> 1) & 1u;
-      ok = wait_bar<100>(bar(ctl.vr_full[s]), ph, abort) && wait_bar<100>(bar(ctl.vf_empty[s]), ph ^ 1u, abort);
+      ok = wait_bar<100>(bar(ctl.vr_full[s]), ph, abort) &&
+           (i < 2 || wait_bar<100>(bar(ctl.done[(i - 2) & 3]), uint32_t((i - 2) >> 2) & 1u, abort));
       if (!ok) break;
       const uint8_t* src = src0 + s * kTile;
       uint8_t* dst = dst0 + s * 2 * kTile;
@@ -798,8 +866,11 @@ __global__ void __launch_bounds__(512, 1)
         *reinterpret_cast<uint4*>(at + at1) = swap ? lo : hi;
       }
       tc::fence_async_smem();
-      tc::mbar_arrive(bar(ctl.vr_empty[s]));
-      tc::mbar_arrive(bar(ctl.vf_full[s]));
+      __syncwarp();
+      if (lane == 0) {
+        tc::mbar_arrive(bar(ctl.vf_full[s]));
+        tc::mbar_arrive(bar(ctl.vr_empty[s]));
+      }
     }
   } else {
     if constexpr (D == 128 && !SPREAD) set_regs<false, NT == 2 ? 64 : 96>();
@@ -821,8 +892,8 @@ __global__ void __launch_bounds__(512, 1)
       const int key0 = k0 + i * BN;
       const int valid = min(per, (k_end - key0 + box - 1) / box);
       const int row = (key0 + lane * box) & ((1 << p.page_shift) - 1);
-      auto load = [&](const CUtensorMap* map, uint32_t dst, uint32_t full, uint32_t empty, uint32_t parity) {
-        ok = wait_bar<100>(empty, parity, abort);
+      auto load = [&](const CUtensorMap* map, uint32_t dst, uint32_t full, bool used, uint32_t empty, uint32_t parity) {
+        ok = !used || wait_bar<100>(empty, parity, abort);
         ok = __all_sync(~0u, ok);
         if (!ok) return;
         if (lane == 0) tc::mbar_arrive_expect_tx(full, uint32_t(valid * box * D));
@@ -840,9 +911,10 @@ __global__ void __launch_bounds__(512, 1)
         ++issued;
       };
       const int ks = i % kKStages, vs = i & 1;
-      load(&tmap_k, base + C::kK + ks * kTile, bar(ctl.k_full[ks]), bar(ctl.k_empty[ks]), (uint32_t(i / kKStages) & 1u) ^ 1u);
+      const int kd = i == kKStages ? 0 : i - kKStages - 1;  // the step that used K's stage last
+      load(&tmap_k, base + C::kK + ks * kTile, bar(ctl.k_full[ks]), i >= kKStages, bar(ctl.done[kd & 3]), uint32_t(kd >> 2) & 1u);
       if (ok)
-        load(&tmap_v, base + C::kVr + vs * kTile, bar(ctl.vr_full[vs]), bar(ctl.vr_empty[vs]), (uint32_t(i >> 1) & 1u) ^ 1u);
+        load(&tmap_v, base + C::kVr + vs * kTile, bar(ctl.vr_full[vs]), true, bar(ctl.vr_empty[vs]), (uint32_t(i >> 1) & 1u) ^ 1u);
       pg = next;
     }
     if (*abort && lane == 0) {
@@ -891,9 +963,10 @@ __global__ void __launch_bounds__(512, 1)
     auto weigh = [&](auto a, auto buf, auto vs, int i, int use) {
 #pragma unroll
       for (int k = 0; k < NB; k += 4) {
-        if (k % (NB / 2) == 0 && !wait_for(ctl.p_full[buf][k / (NB / 2)], use)) return false;
-        if (NB == 4 && !wait_for(ctl.p_full[buf][1], use)) return false;
-        tc::tc_fence_after();
+        if (k == 0 || (kHalves == 2 && k == NB / 2)) {
+          if (!wait_for(ctl.p_full[buf][k == 0 ? 0 : 1], use)) return false;
+          tc::tc_fence_after();
+        }
         umma_pv4(tmem + C::kO + uint32_t(a * D), tmem + uint32_t(buf * BN + 8 * k), uint32_t(vd) + vs * (2 * kTile >> 4) + 128 * k,
                  uint32_t(vd >> 32), idesc_pv, k > 0 || i > 0);
       }
@@ -920,18 +993,17 @@ __global__ void __launch_bounds__(512, 1)
       } else {
         if (more) qk(I0{}, std::integral_constant<int, (U + 1) & 1>{}, Ks{});
         if (!weigh(I0{}, Vs{}, Vs{}, i, i >> 1)) return;
-        tc::umma_commit_warp(bar(ctl.o_done));
       }
       if (!more) return;
-      tc::umma_commit_warp(bar(ctl.vf_empty[Vs::value]));
-      tc::umma_commit_warp(bar(ctl.k_empty[Ks::value]));
-      wait_for(ctl.vf_full[(U + 1) & 1], (i + 1) >> 1);
-      if (i + 2 < nt) wait_for(ctl.k_full[(U + 2) % kKStages], (i + 2) / kKStages);
+      tc::umma_commit_warp(bar(ctl.done[U]));
+      // (both at once, by different lanes)
+      const bool k = (lane & 1) && i + 2 < nt;
+      ok = ok && __all_sync(~0u, wait_bar<0>(k ? bar(ctl.k_full[(U + 2) % kKStages]) : bar(ctl.vf_full[(U + 1) & 1]),
+                                             uint32_t(k ? (i + 2) / kKStages : (i + 1) >> 1) & 1u, abort));
     };
     if (nt > 0 && wait_for(ctl.k_full[0], 0)) {
       qk(I0{}, I0{}, I0{});
       if constexpr (NT == 2) qk(I1{}, I1{}, I0{});
-      tc::umma_commit_warp(bar(ctl.k_empty[0]));
       wait_for(ctl.vf_full[0], 0);
       if (nt > 1) wait_for(ctl.k_full[1], 0);
       for (int i = 0; i < nt && ok; i += kKStages) {
