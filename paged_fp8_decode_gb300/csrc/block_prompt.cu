@@ -64,8 +64,10 @@ struct Cfg {
   static constexpr bool kQt = NT == 1;
   static constexpr uint32_t kQcol = 2 * BN, kO = NT == 1 && D == 128 ? 384 : 256;
   static_assert(!kQt || (kQcol + D / 2 <= kO && kO + D <= 512), "tensor memory");
+  // widened V tiles: with one row tile there is room for four, and the warps that widen run ahead
+  static constexpr int kVStages = NT == 1 ? 4 : 2;
   static constexpr int kQ = kQt ? 0 : NT * 2 * DH * kTile;
-  static constexpr int kK = kQ, kVr = kK + kKStages * kTile, kVf = kVr + 2 * kTile, kCtrl = kVf + 4 * kTile;
+  static constexpr int kK = kQ, kVr = kK + kKStages * kTile, kVf = kVr + 2 * kTile, kCtrl = kVf + kVStages * 2 * kTile;
   static constexpr int kBytes = kCtrl + 2048;
   static_assert(NT > 1 || 4 * D * 32 * 4 + 1024 <= kCtrl, "the copies' join");
 };
@@ -74,7 +76,7 @@ static_assert(Cfg<128, 2>::kBytes + 1024 <= 227 * 1024 && Cfg<256, 1>::kBytes + 
 
 struct Ctrl {
   uint64_t k_full[kKStages];
-  uint64_t vr_full[2], vr_empty[2], vf_full[2];
+  uint64_t vr_full[2], vr_empty[2], vf_full[4];
   uint64_t s_full[2], p_full[2][2];  // (P in halves of its keys)
   uint64_t done[4];  // of step i modulo 4: tile i's products on V, and tile i + 1's scores
   uint64_t e_full[2], e_empty[2];
@@ -284,7 +286,7 @@ __global__ void __launch_bounds__(512, 1)
     block_prompt_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
                         BlockPromptParams p) {
   using C = Cfg<D, NT>;
-  constexpr int BN = C::BN, DH = C::DH, NB = C::NB, TB = C::TB;
+  constexpr int BN = C::BN, DH = C::DH, NB = C::NB, TB = C::TB, NV = C::kVStages;
   // With at most 32 rows (SPREAD) the row tile holds them four times, once for each softmax warp
   // (a warp reaches 32 of the tile's rows), and a copy takes a quarter of a tile's keys: its P is 0
   // for the others. Each copy has a reference, a sum and an output of its own; they are joined
@@ -357,11 +359,13 @@ __global__ void __launch_bounds__(512, 1)
 
   if (tid == 0) {
     for (int s = 0; s < kKStages; ++s) tc::mbar_init(bar(ctl.k_full[s]), 1);
-    for (int s = 0; s < 4; ++s) tc::mbar_init(bar(ctl.done[s]), 1);
+    for (int s = 0; s < 4; ++s) {
+      tc::mbar_init(bar(ctl.done[s]), 1);
+      tc::mbar_init(bar(ctl.vf_full[s]), C::kConvWarps);
+    }
     for (int s = 0; s < 2; ++s) {
       tc::mbar_init(bar(ctl.vr_full[s]), 1);
       tc::mbar_init(bar(ctl.vr_empty[s]), C::kConvWarps);
-      tc::mbar_init(bar(ctl.vf_full[s]), C::kConvWarps);
       tc::mbar_init(bar(ctl.s_full[s]), 1);
       for (int h = 0; h < 2; ++h) tc::mbar_init(bar(ctl.p_full[s][h]), 4);
       tc::mbar_init(bar(ctl.o_last[s]), 1);
@@ -849,10 +853,10 @@ __global__ void __launch_bounds__(512, 1)
       const int s = i & 1;
       const uint32_t ph = uint32_t(i >> 1) & 1u;
       ok = wait_bar<100>(bar(ctl.vr_full[s]), ph, abort) &&
-           (i < 2 || wait_bar<100>(bar(ctl.done[(i - 2) & 3]), uint32_t((i - 2) >> 2) & 1u, abort));
+           (i < NV || wait_bar<100>(bar(ctl.done[(i - NV) & 3]), uint32_t((i - NV) >> 2) & 1u, abort));
       if (!ok) break;
       const uint8_t* src = src0 + s * kTile;
-      uint8_t* dst = dst0 + s * 2 * kTile;
+      uint8_t* dst = dst0 + (i & (NV - 1)) * 2 * kTile;
       const int live = k_end - (k0 + i * BN);  // rows from here on are no key's: zeros (they may hold NaN codes)
 #pragma unroll
       for (int it = 0; it < DH * BN / RI; ++it) {
@@ -868,7 +872,7 @@ __global__ void __launch_bounds__(512, 1)
       tc::fence_async_smem();
       __syncwarp();
       if (lane == 0) {
-        tc::mbar_arrive(bar(ctl.vf_full[s]));
+        tc::mbar_arrive(bar(ctl.vf_full[i & (NV - 1)]));
         tc::mbar_arrive(bar(ctl.vr_empty[s]));
       }
     }
@@ -982,7 +986,8 @@ __global__ void __launch_bounds__(512, 1)
     // between the products.
     auto step = [&](auto u, int i) {
       constexpr int U = decltype(u)::value;
-      using Vs = std::integral_constant<int, U & 1>;
+      using Sb = std::integral_constant<int, U & 1>;
+      using Vs = std::integral_constant<int, U & (NV - 1)>;
       using Ks = std::integral_constant<int, (U + 1) % kKStages>;
       const bool more = i + 1 < nt;
       if constexpr (NT == 2) {
@@ -992,14 +997,14 @@ __global__ void __launch_bounds__(512, 1)
         if (more) qk(I1{}, I1{}, Ks{});
       } else {
         if (more) qk(I0{}, std::integral_constant<int, (U + 1) & 1>{}, Ks{});
-        if (!weigh(I0{}, Vs{}, Vs{}, i, i >> 1)) return;
+        if (!weigh(I0{}, Sb{}, Vs{}, i, i >> 1)) return;
       }
       if (!more) return;
       tc::umma_commit_warp(bar(ctl.done[U]));
       // (both at once, by different lanes)
       const bool k = (lane & 1) && i + 2 < nt;
-      ok = ok && __all_sync(~0u, wait_bar<0>(k ? bar(ctl.k_full[(U + 2) % kKStages]) : bar(ctl.vf_full[(U + 1) & 1]),
-                                             uint32_t(k ? (i + 2) / kKStages : (i + 1) >> 1) & 1u, abort));
+      ok = ok && __all_sync(~0u, wait_bar<0>(k ? bar(ctl.k_full[(U + 2) % kKStages]) : bar(ctl.vf_full[(U + 1) & (NV - 1)]),
+                                             uint32_t(k ? (i + 2) / kKStages : (i + 1) / NV) & 1u, abort));
     };
     if (nt > 0 && wait_for(ctl.k_full[0], 0)) {
       qk(I0{}, I0{}, I0{});
