@@ -18,16 +18,25 @@
 //
 // Head size 128: two row tiles (256 rows), 128 keys a step; tensor memory is full (two S and two
 // O), so a tile's next scores wait for its weights' product, and the other tile's
-// products fill that time. Head size 256: one row tile, 64 keys a step, two S buffers.
+// products fill that time. One row tile (head size 256, or 128 rows and fewer): two S
+// buffers, Q in tensor memory, 64 keys a step at head size 256. At most 32 rows, as a decode
+// of more query rows than the decode kernel takes: SPREAD, below.
 //
-// What bounds it (4096 tokens after 12288, 32/8 heads: 808 us, 1190 TFLOP/s, 61% of the
-// measured bf16 rate; clock stamps of a CTA's steps): a row tile's chain, 3100 cycles a
-// step where both tiles' products take 2050. Softmax 1500 (scores read 60, largest u 400, exponentials 1000),
-// products of the weights 700, scores 580, from their end to the softmax 350. Measured and not kept:
-// 64 keys a step with two S buffers a tile (980 us: at 64 columns the scores' operands
-// bound shared memory), the same with Q in tensor memory and one buffer (977 us), two
-// threads a row (940 us). The products are issued four at an election, their
-// barriers waited for a step ahead: 864 -> 808 us; scores read once into registers instead of twice: 1040 -> 864.
+// What bounds it. 4096 tokens after 12288, 32/8 heads: 727 us, 1320 TFLOP/s, 67% of the
+// measured bf16 rate: a row tile's chain, 3100 cycles a step where both tiles' products take
+// 2050 (clock stamps: softmax 1500 - scores read 60, largest u 400, exponentials 1000 -, products of the
+// weights 700, scores 580, from their end to the softmax 350). One row tile: 1400 to 1900 cycles a step where
+// the products take 1024: softmax 900, and a step's barriers in the MMA warp. Short chunks (5 of 20 to 700
+// tokens, head size 256: 45 us): the CTA's ends, 12000 cycles to the first scores, 5000 to write the rows.
+// 64 x 4096 cached tokens, 16 and 32 rows: 133 and 136 us, 4.0 TB/s.
+//
+// What it took (the long chunk, us): four products at an election, their barriers waited for a step
+// ahead 864 -> 808; scores read once into registers instead of twice 1040 -> 864; Q split by twelve
+// warps and rows written whole 790 -> 735; one arrival a warp instead of one a thread, one
+// barrier for all that a step frees 735 -> 727.
+// Not kept: 64 keys a step with two S buffers a tile (980: at 64 columns the scores' operands
+// bound shared memory), the same with Q in tensor memory and one buffer (977), two
+// threads a row (940), a step's waits between the products (756).
 //
 // Warps: 0 TMA, 1 MMA, 2 the blocks' scales, then softmax (a thread a row) and the
 // warps that widen V. Every wait is bounded (2 s): a timeout sets a status bit, and the CTA
@@ -290,7 +299,7 @@ __global__ void __launch_bounds__(512, 1)
   // With at most 32 rows (SPREAD) the row tile holds them four times, once for each softmax warp
   // (a warp reaches 32 of the tile's rows), and a copy takes a quarter of a tile's keys: its P is 0
   // for the others. Each copy has a reference, a sum and an output of its own; they are joined
-  // at the end, as pieces of the keys are.
+  // at the end, as pieces of the keys are. (64 x 4096 tokens, 16 rows: 163 -> 139 us when it was added.)
   static_assert(!SPREAD || NT == 1, "one row tile");
   constexpr int kHalves = BN == 128 && !SPREAD ? 2 : 1;  // P is handed over in halves of its keys
   constexpr int HC = SPREAD ? BN / 4 : BN, HB = HC / 16;  // columns (keys) of a softmax thread, 16-key groups
@@ -392,9 +401,9 @@ __global__ void __launch_bounds__(512, 1)
   volatile int* abort = &ctl.abort;
 
   // Q's rows, by the twelve warps that have nothing else to do yet, 8 channels a lane: x' = x *
-  // 2^(127 - e), the row's largest finite |x'| in (224, 448]; hi = e4m3(x'), lo = e4m3(x' - hi). In fp16
-  // both are exact: what fp16 rounds of x' is far below e4m3's smallest step. (By the softmax
-  // threads, each its own row, this took 12000 cycles a CTA at head size 256.)
+  // 2^(127 - e), the row's largest finite |x'| in (224, 448]; hi = e4m3(x'), lo = e4m3(x' - hi). x' goes
+  // through fp16: it keeps x' of 2^-17 and more exactly, and less gives code 0 either way. (By the softmax
+  // threads, each its own row, this took 12000 cycles a CTA at head size 256, now 9000.)
   if (warp >= 4) {
     constexpr int kRowLanes = D / 8, kRowsLd = 32 / kRowLanes, kMine = SPREAD ? 32 : C::kRows;
     const int j0 = (warp - 4) * kRowsLd + lane / kRowLanes, ch = lane % kRowLanes * 8;
@@ -499,7 +508,7 @@ __global__ void __launch_bounds__(512, 1)
     tc::named_bar_sync(1, 384);
   }
 
-  // Registers: 128 a thread at launch. At head size 128 a softmax thread keeps a row's 128
+  // Registers: 128 a thread at launch. At head size 128 (without copies) a softmax thread keeps a row's 128
   // scores: 2 x 192 + 2 x 64, or 224 + 3 x 96, = 4 x 128 for the four warpgroups.
   if (warp >= 4 && warp < C::kConvWarp0) {
     if constexpr (D == 128 && !SPREAD) set_regs<true, NT == 2 ? 192 : 224>();

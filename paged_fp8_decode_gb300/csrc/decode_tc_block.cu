@@ -1,5 +1,6 @@
 // tcgen05 decode kernel instances for the block-scaled cache (e4m3 codes): up to 8 query
-// rows at head size 128, 16 at 256 (more go to the prompt's kernel, mj_api_block.cpp).
+// rows (more go to the prompt's kernel, mj_api_block.cpp). 64 x 4096 tokens, 8 heads of 128: 4 rows
+// 89 us (6.0 TB/s, 0.90 of a copy's rate), 8 rows 103; 1 x 131072 tokens 47 (5.7 TB/s, start and join).
 #include "decode_tc_kernel.cuh"
 
 namespace mj {
@@ -8,9 +9,8 @@ cudaError_t launch_tc_block(const CUtensorMap& mk, const CUtensorMap& mv, const 
   if (p.d == 128)
     return p.n_q <= 4 ? launch_tc<16, 16, 4, MJ_KV_E4M3, kQBlock, 128>(mk, mv, p, stream)
                       : launch_tc<16, 32, 8, MJ_KV_E4M3, kQBlock, 128>(mk, mv, p, stream);
-  if (p.n_q <= 4) return launch_tc<16, 16, 4, MJ_KV_E4M3, kQBlock, 256>(mk, mv, p, stream);
-  if (p.n_q <= 8) return launch_tc<16, 32, 8, MJ_KV_E4M3, kQBlock, 256>(mk, mv, p, stream);
-  return launch_tc<32, 64, 16, MJ_KV_E4M3, kQBlock, 256>(mk, mv, p, stream);
+  return p.n_q <= 4 ? launch_tc<16, 16, 4, MJ_KV_E4M3, kQBlock, 256>(mk, mv, p, stream)
+                    : launch_tc<16, 32, 8, MJ_KV_E4M3, kQBlock, 256>(mk, mv, p, stream);
 }
 
 }  // namespace mj

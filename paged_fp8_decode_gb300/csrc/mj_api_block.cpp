@@ -83,10 +83,11 @@ int64_t part_cap(int slots) { return 4 * int64_t(slots); }
 constexpr double kPieceTiles = 4, kTail = 0.2;
 
 // Which kernel attends: the decode kernel (keys on the tensor cores' rows, so that a few
-// query rows fill them) or the prompt's (query rows there, 128 at a time). 64 x 4096 tokens, in us:
-// head size 128, 8 KV heads: 16 rows 184 and 163, 32 rows 455 and 168; head size 256, 4 KV heads:
-// 16 rows 126 and 136, 32 rows 306 and 141. At 8 rows the decode kernel takes 103 and 93.
-bool by_rows(int d, int64_t n_q) { return n_q > (d == 128 ? 8 : 16); }
+// query rows fill them) or the prompt's (query rows there, up to 32 of them four times over). In us, the decode
+// kernel's time first, where both were built: head size 128, 64 x 4096 tokens, 8 KV heads: 8 rows 103 and
+// 133, 16 rows 184 and 133; head size 256, 4 KV heads: 8 rows 95 and 125, 12 rows 125 and 125, 16 rows 137
+// and 126; 16 rows, 1 x 65536 tokens, 37 and 21, 40 ragged requests 181 and 133.
+bool by_rows(int64_t n_q) { return n_q > 8; }
 
 bool slots_ok(int slots) { return slots >= 1 && slots <= (1 << 20); }
 
@@ -170,7 +171,7 @@ int mj_block_read_kv(const mj_block_read_args* a, void* stream) {
 int mj_block_slots(int sm_count, int q_len, int h_q, int h_k, int d) {
   if (sm_count < 1 || q_len < 1 || h_k < 1 || h_q < h_k || h_q % h_k || !mj::head_dim_ok(d)) return 1;
   const int64_t n_q = int64_t(q_len) * (h_q / h_k);
-  if (!by_rows(d, n_q)) return mj_slots(sm_count, 2, h_k, q_len, h_q);
+  if (!by_rows(n_q)) return mj_slots(sm_count, 2, h_k, q_len, h_q);
   const int64_t tiles = ceil_div(n_q, mj::block_prompt_rows(d, n_q));
   return int(std::max<int64_t>(1, sm_count / (h_k * tiles)));
 }
@@ -323,7 +324,7 @@ int mj_block_attention(const mj_block_args* a, void* stream) {
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   bool unsupported = false;
   cudaError_t e = cudaSuccess;
-  if (by_rows(c.d, n_q)) {
+  if (by_rows(n_q)) {
     mj::BlockPromptParams p = {};
     p.num_seqs = a->num_seqs;
     p.num_tokens = a->num_seqs * a->q_len;

@@ -216,7 +216,7 @@ def test_plan_refusals():
 def test_slots_and_splits():
     assert mj.mj_block_slots(152, 1, 32, 8, 128) == 38      # two CTAs an SM
     assert mj.mj_block_slots(152, 4, 32, 8, 128) == 19      # by rows: one
-    assert mj.mj_block_slots(152, 4, 16, 4, 256) == 76 and mj.mj_block_slots(152, 9, 16, 4, 256) == 38
+    assert mj.mj_block_slots(152, 2, 16, 4, 256) == 76 and mj.mj_block_slots(152, 9, 16, 4, 256) == 38
     assert mj.mj_block_slots(152, 100, 64, 64, 128) == 2    # 100 rows in one tile
     assert mj.mj_block_slots(0, 1, 32, 8, 128) == 1
     assert mj.mj_block_prompt_splits(152, 1, 8192, 8192, 32, 8, 128) == 1
