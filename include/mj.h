@@ -697,9 +697,9 @@ MJ_API int mj_block_write_kv(const mj_block_write_args* args, void* stream);
  * mj_block_read_kv — bring cached tokens back: row starts[b] + i of k_out and
  * v_out, for i < starts[b + 1] - starts[b], is the value of token first[b] + i of
  * request b (token i without `first`), as bf16 (exact) or fp16 (to nearest even). Rows
- * from starts[num_seqs] on, and
- * rows past num_rows, are left as they are. A page outside the pool or the block table reads as zeros
- * and is reported (status bit 1), as is a token past the table.
+ * from starts[num_seqs] on, and rows past num_rows, are left as they are. A page
+ * outside the pool or the block table reads as zeros and is reported (status bit 1),
+ * as is a token past the table.
  * starts rises from 0; num_rows is at least starts[num_seqs] and sizes the grid.
  * Alignment: outputs 16 bytes, their strides multiples of 8 elements; the
  * outputs' rows lie apart.
@@ -747,7 +747,7 @@ MJ_API int mj_block_workspace_size(int slots, int q_len, int h_q, int h_k, int d
  * Requests with seq_lens[b] == 0 are padding: nothing is written for them. A
  * causal row that sees no key writes 0 (LSE -inf).
  *
- * Accuracy. Up to 8 query rows a request and KV head (16 at head size 256), rows =
+ * Accuracy. Up to 8 query rows a request and KV head, rows =
  * q_len * h_q / h_k: a query enters the tensor cores as two 8-bit terms, exact down
  * to 2^-14 of the largest |q| of those rows (within 2^-22 of it below); a value's
  * weight, softmax weight times its block's scale, as two 8-bit terms, within 2^-8
@@ -803,7 +803,7 @@ MJ_API int mj_block_attention(const mj_block_args* args, void* stream);
  * what mj_block_prompt_splits gives, which fills sm_count SMs where the chunks
  * alone do not (max_len: the longest request).
  *
- * Accuracy: a query is exact down to 2^-10 of its row's largest |q| (within 2^-18
+ * Accuracy: a query is exact down to 2^-10 of its row's largest |q| (within 2^-17
  * of it below); weights in fp16 relative to a running reference of their row, within 2^-12 of
  * themselves down to 20 binades below it and 2^-31 of it lower; sums in float32. What
  * mj_block_attention says about values that are not finite, status bits,

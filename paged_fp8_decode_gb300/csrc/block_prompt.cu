@@ -1014,6 +1014,7 @@ __global__ void __launch_bounds__(512, 1)
       const bool k = (lane & 1) && i + 2 < nt;
       ok = ok && __all_sync(~0u, wait_bar<0>(k ? bar(ctl.k_full[(U + 2) % kKStages]) : bar(ctl.vf_full[(U + 1) & (NV - 1)]),
                                              uint32_t(k ? (i + 2) / kKStages : (i + 1) / NV) & 1u, abort));
+      __syncwarp();  // (what one lane has seen holds for the one that issues)
     };
     if (nt > 0 && wait_for(ctl.k_full[0], 0)) {
       qk(I0{}, I0{}, I0{});

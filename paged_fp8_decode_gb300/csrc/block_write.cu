@@ -99,6 +99,7 @@ __global__ void __launch_bounds__(32 * warps_cta(G), 24 / warps_cta(G)) block_wr
     // is of another block
     const int64_t t = t0 + lane;
     const int64_t s = t < w1 ? p.slots[t] : -1;
+    int64_t at = t0 - 1, before = t0 > 0 ? p.slots[at] : -1;  // (on its way together with s)
     const bool live = alive(s);
     if (p.status && s >= p.num_slots && blockIdx.y == 0 && warp == 0) atomicOr(p.status, kStatusBadPage);
     const unsigned mask = __ballot_sync(~0u, live);
@@ -108,7 +109,6 @@ __global__ void __launch_bounds__(32 * warps_cta(G), 24 / warps_cta(G)) block_wr
     int64_t pb = __shfl_sync(~0u, b, below ? 31 - __clz(below) : 0);
     if (lane == __ffs(mask) - 1) pb = -1;
     if (t0 > 0) {  // the window's first live token looks back past its begin
-      int64_t at = t0 - 1, before = p.slots[at];
       if (!alive(before)) {
         at = find_live<-1>(p.slots, at, T, p.num_slots, lane);
         before = at >= 0 ? p.slots[at] : -1;

@@ -463,6 +463,24 @@ def test_two_steps_of_one_batch_give_the_same_bits():
     assert torch.equal(one, two)
 
 
+@pytest.mark.parametrize("d", [128, 256])
+@pytest.mark.parametrize("q_len", [1, 2, 4])  # 8, 16 and 32 rows
+def test_any_channel_of_a_query_that_is_not_finite(q_len, d):
+    b = Batch([40, 300, 17], h_k=1, d=d, seed=21)
+    q = queries(b, 3 * q_len, 8)
+    out0, lse0, _ = decode(b, q, q_len, 8, causal=False)
+    bad = q.clone()
+    for n in range(3 * q_len * 4):
+        bad[n // 4, 2 * (n % 4), (n * 9) % d] = [float("inf"), float("-inf"), float("nan")][n % 3]
+    out, lse, status = decode(b, bad, q_len, 8, causal=False)
+    hit = ~torch.isfinite(bad).all(2)
+    rows = hit.view(3, 1, q_len * 8)  # (query token, head), as the sums of weights
+    assert status == 0 and torch.isnan(out[:3 * q_len][hit]).all() and torch.isfinite(out[:3 * q_len][~hit]).all()
+    assert torch.isnan(lse[rows]).all() and torch.isfinite(lse[~rows]).all()
+    if q_len > 1:  # (a row's own scale: the others keep their bits)
+        assert torch.equal(out[:3 * q_len][~hit], out0[:3 * q_len][~hit]) and torch.equal(lse[~rows], lse0[~rows])
+
+
 def test_a_query_of_nan_over_split_requests():
     b = Batch([9000, 40], h_k=1, page=64, block=32, seed=15)
     q = queries(b, 2, 8)

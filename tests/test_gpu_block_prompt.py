@@ -1,7 +1,7 @@
 """Prompt attention over the block-scaled cache on the GPU against oracle.block (float64).
 
-Tolerance. Queries are exact down to 2^-10 of their row's largest value and within 2^-18 of it
-below, keys exact: a logit is off by at most 2^-18 |q|max sum|k| scale, below 2e-4 here, in the
+Tolerance. Queries are exact down to 2^-10 of their row's largest value and within 2^-17 of it
+below, keys exact: a logit is off by at most 2^-17 |q|max sum|k| scale, below 4e-4 here, in the
 sum at random far less; float32 sums as in the decode attention: LSE within 6e-4. Weights in fp16:
 2^-12 rms of themselves; the output's rounding 0.0017 rms (bf16), 0.0002 (fp16): 0.0025 in the 2-norm for bf16, 0.0006 for
 fp16. Elementwise: a weight within 2^-11 of itself, the rounding 2^-9 (2^-12 fp16): 0.003 of the
@@ -174,6 +174,33 @@ def test_queries_that_are_not_finite_and_zeros():
         out[3, 1], out[250, 2] = run(b, [200, 140], 4, q=ref, splits=splits)[0][[3, 250], [1, 2]]
         lse[3, 1], lse[250, 2] = run(b, [200, 140], 4, q=ref, splits=splits)[1][[3, 250], [1, 2]]
         check(b, [200, 140], out, lse, ref)
+
+
+@pytest.mark.parametrize("d", [128, 256])
+@pytest.mark.parametrize("new", [2, 9, 40])  # 32, 144 and 640 rows
+def test_any_channel_that_is_not_finite(new, d):
+    """Each place of a 16-byte piece, in every second row: that row is NaN, the others keep their bits."""
+    b = Batch([50], h_k=1, d=d, seed=16)
+    out0, lse0, _, q = run(b, [new], 16, extra=0)
+    bad = q.clone()
+    n = 0
+    for t in range(new):
+        for h in range(t % 2, 16, 2):
+            bad[t, h, (n * 9) % d] = [float("inf"), float("-inf"), float("nan")][n % 3]
+            n += 1
+    out, lse, status, _ = run(b, [new], 16, q=bad, extra=0)
+    hit = ~torch.isfinite(bad).all(2)
+    assert status == 0 and int(hit.sum()) == 8 * new
+    assert torch.isnan(out[hit]).all() and torch.isnan(lse[hit]).all()
+    assert torch.equal(out[~hit], out0[~hit]) and torch.equal(lse[~hit], lse0[~hit])
+
+
+@pytest.mark.parametrize("d", [128, 256])
+def test_hundreds_of_heads_a_kv_head(d):
+    b = Batch([70, 20], h_k=1, d=d, seed=17)
+    out, lse, status, q = run(b, [3, 2], 300)
+    assert status == 0
+    check(b, [3, 2], out, lse, q)
 
 
 def test_rows_of_very_different_size():
