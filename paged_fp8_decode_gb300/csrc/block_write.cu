@@ -73,8 +73,8 @@ __device__ __noinline__ int64_t find_live(const int64_t* slots, int64_t from, in
 
 // G warps share a block of G rows_warp(D) rows. Three CTAs of 8 warps an SM, 80 registers: the
 // moves of earlier codes are a loop of their own, since few runs have them. (4 x 4096 tokens of
-// 8 heads of 128: 20.4 us, 4.9 TB/s; two CTAs of 120 registers 21.6 us; four, or half the rows a
-// warp, 18.2 us, but then 11 ragged chunks of 1..700 tokens, head size 256, which take 9.7 us
+// 8 heads of 128: 20.0 us, 5.0 TB/s; two CTAs of 120 registers 21.6 us; four, or half the rows a
+// warp, 18.2 us, but then 11 ragged chunks of 1..700 tokens, head size 256, which take 9.4 us
 // here, take 10.6 and 11.3, and 64 tokens 3.3 and 3.6 us in place of 3.1.)
 template <int D, int G>
 __global__ void __launch_bounds__(32 * warps_cta(G), 24 / warps_cta(G)) block_write_kernel(BlockWriteParams p) {
