@@ -221,7 +221,7 @@ def test_slots_and_splits():
     assert mj.mj_block_slots(0, 1, 32, 8, 128) == 1
     assert mj.mj_block_prompt_splits(152, 1, 8192, 8192, 32, 8, 128) == 1
     assert mj.mj_block_prompt_splits(152, 1, 64, 100000, 32, 8, 128) == 19
-    assert mj.mj_block_prompt_splits(152, 1, 64, 3000, 32, 8, 128) == 2
+    assert mj.mj_block_prompt_splits(152, 1, 64, 3000, 32, 8, 128) == 9
     assert mj.mj_block_prompt_splits(152, 1, 1, 10 ** 6, 1, 1, 128) == 64
 
 
