@@ -373,11 +373,10 @@ __global__ void __launch_bounds__(KF != MJ_KV_E4M3 ? kThreadsTcFp6 : kThreadsTc,
                           (!split || grid_within(p.first_wave));
         const int depth = !deep ? kPrefetchTiles
                                 : (grid_within(2 * int64_t(p.first_wave)) ? kPrefetchTilesShortGrid : kPrefetchTilesFirstWave);
-        const int n = min(depth, wp.z - wp.y) * ppt;  // pages
+        const int n = prefetch_pages(wp.y, wp.z, depth, ppt, BS ? p.bt_len : p.bt_stride);
         const CUtensorMap* map = warp == 0 ? &tmap_k : &tmap_v;
         for (int k = lane; k < n; k += 32) {
           const int64_t e = int64_t(wp.y) * ppt + k;  // block-table entry of the page
-          if (e >= p.bt_stride) break;
           const int pg = p.block_table[int64_t(wp.x) * p.bt_stride + e];
           if (pg >= 0 && int64_t(pg) < p.num_pages) {
 #pragma unroll

@@ -155,6 +155,16 @@ cudaError_t launch_quantize_q(const QuantParams& p, cudaStream_t stream);
 cudaError_t launch_decode_simt(const DecodeParams& p, cudaStream_t stream);
 cudaError_t launch_merge(const DecodeParams& p, cudaStream_t stream);
 cudaError_t launch_write_kv(const mj_write_kv_args& a, cudaStream_t stream);
+// How many of a block-table row's `len` entries the decode kernels look up ahead for a work row
+// of tiles begin .. end - 1, `depth` of them at most, ppt pages a tile: entries begin * ppt and on.
+// (The work row may be a guess, and its last tile reaches past the request's last page.)
+__host__ __device__ inline int prefetch_pages(int begin, int end, int depth, int ppt, int64_t len) {
+  if (begin < 0 || end <= begin) return 0;
+  const int64_t held = len - int64_t(begin) * ppt;
+  const int tiles = end - begin < depth ? end - begin : depth, n = tiles * ppt;
+  return held <= 0 ? 0 : (held < n ? int(held) : n);
+}
+
 // Tensor-core kernel; sets *unsupported (and launches nothing) when the
 // arguments are outside its envelope.
 cudaError_t launch_decode_tc(DecodeParams p, cudaStream_t stream, bool* unsupported);

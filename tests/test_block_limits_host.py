@@ -1,0 +1,59 @@
+"""The block-scaled cache's calls at their limits, without a GPU: the index bounds that the kernels take from
+headers, compiled here for the host, and what the calls refuse."""
+
+import ctypes
+import subprocess
+
+import numpy as np
+import pytest
+import torch
+
+import paged_fp8_decode_gb300 as mj
+
+HOST = """
+#include "mj_block.h"
+extern "C" int prefetch_pages(int begin, int end, int depth, int ppt, long long len) {
+  return mj::prefetch_pages(begin, end, depth, ppt, len);
+}
+"""
+
+
+@pytest.fixture(scope="module")
+def bounds(tmp_path_factory):
+    """The kernels' bounds as a host library."""
+    from paged_fp8_decode_gb300 import build as B
+
+    at = tmp_path_factory.mktemp("bounds")
+    (at / "bounds.cu").write_text(HOST)
+    subprocess.run([B._nvcc(), "-std=c++17", "-shared", "-Xcompiler", "-fPIC", "-I", B.INCLUDE, "-I", B.CSRC] + B.ARCH +
+                   ["-o", str(at / "bounds.so"), str(at / "bounds.cu")], check=True, capture_output=True, text=True)
+    lib = ctypes.CDLL(str(at / "bounds.so"))
+    lib.prefetch_pages.argtypes = [ctypes.c_int] * 4 + [ctypes.c_longlong]
+    return lib
+
+
+@pytest.mark.parametrize("page", [16, 32, 64, 128])
+def test_pages_looked_up_ahead_lie_inside_the_table(bounds, page):
+    """Every work row of plans with and without a margin, over tables that end at the longest request's last page, before it and
+    after it: the entries that the decode kernel looks up before it knows the lengths."""
+    rng = np.random.default_rng(page)
+    ppt, ends = 128 // page, 0
+    for _ in range(20):
+        lens = rng.integers(1, [100, 3000, 70000][rng.integers(3)], rng.integers(1, 20)).astype(np.int32)
+        slots, margin = int(rng.integers(1, 60)), int(rng.choice([0, 1, 500]))
+        plan = mj.mj_block_plan(lens, len(lens), len(lens), slots, margin)
+        pages = -(-int(lens.max()) // page)
+        for b, begin, end, _ in plan[:4 * (slots + len(lens))].reshape(-1, 4):
+            for table in (pages, pages - 1, pages + 9, 0):
+                for depth in (4, 8, 16):
+                    n = bounds.prefetch_pages(int(begin), int(end), depth, ppt, table)
+                    want = [e for e in range(begin * ppt, min(end, begin + depth) * ppt) if e < table]
+                    assert n == len(want)
+                    ends += n < min(end - begin, depth) * ppt and n > 0
+    assert ends or page == 128  # tiles that reach past the table were among them
+
+
+def test_pages_looked_up_ahead_of_rows_that_are_no_plan(bounds):
+    for begin, end in ((-3, 5), (-2 ** 31, 2 ** 31 - 1), (7, 7), (9, 2), (2 ** 31 - 2, 2 ** 31 - 1)):
+        assert bounds.prefetch_pages(begin, end, 16, 8, 1000) == 0
+    assert bounds.prefetch_pages(0, 2 ** 31 - 1, 16, 8, 2 ** 40) == 128
