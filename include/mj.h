@@ -239,7 +239,7 @@ typedef struct mj_decode_args {
   /* paging */
   const int32_t* block_table;   /* device; page of token j of request b:
                                    block_table[b*block_table_stride + j/page_size] */
-  int64_t block_table_stride;
+  int64_t block_table_stride;   /* entries between requests; so many of each are readable, the last's too */
   const int32_t* seq_lens;      /* device [num_seqs]; exact lengths used for masking.
                                    0 = padding request: nothing is written for it. */
 

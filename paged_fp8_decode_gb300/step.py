@@ -109,6 +109,10 @@ class DecodeStep:
                         ("seq_lens", kv.seq_lens), ("q_mul", kv.q_mul), ("o_mul", kv.o_mul)):
             if t is not None and not t.is_cuda:
                 raise ValueError(f"{name} must be a CUDA tensor: the kernels read it through a device pointer")
+        bt = kv.block_table
+        if bt.storage_offset() + num_seqs * bt.stride(0) > bt.untyped_storage().nbytes() // bt.element_size():
+            # (the decode looks a request's pages up before it knows its length)
+            raise ValueError(f"block_table: its storage ends inside the last of {num_seqs} rows of {bt.stride(0)} entries")
         info = self.plan_info
         a = mj_decode_args()
         if self.q_mode in ("bf16", "fp8_fused"):

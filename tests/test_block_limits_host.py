@@ -3,12 +3,14 @@ headers, compiled here for the host, and what the calls refuse."""
 
 import ctypes
 import subprocess
+import types
 
 import numpy as np
 import pytest
 import torch
 
 import paged_fp8_decode_gb300 as mj
+from tests.test_latent_calls_host import on_gpu
 
 HOST = """
 #include "mj_block.h"
@@ -57,3 +59,20 @@ def test_pages_looked_up_ahead_of_rows_that_are_no_plan(bounds):
     for begin, end in ((-3, 5), (-2 ** 31, 2 ** 31 - 1), (7, 7), (9, 2), (2 ** 31 - 2, 2 ** 31 - 1)):
         assert bounds.prefetch_pages(begin, end, 16, 8, 1000) == 0
     assert bounds.prefetch_pages(0, 2 ** 31 - 1, 16, 8, 2 ** 40) == 128
+
+
+def test_decode_refuses_a_block_table_that_ends_inside_its_last_row():
+    """mj_decode_attention has no table length: a request's pages are looked up within block_table_stride entries."""
+    step = mj.DecodeStep.__new__(mj.DecodeStep)
+    step.plan_info, step.q_mode = None, "fp8"
+    whole, x = on_gpu(5, 12, dtype=torch.int32), on_gpu(4)
+
+    def kv(table):
+        return types.SimpleNamespace(block_table=table, k_cache=x, v_cache=x, k_descale=x, v_descale=x, seq_lens=x, q_mul=None, o_mul=None)
+
+    for table, n in ((whole[:, 4:], 5), (whole[1:, 1:], 4), (whole[4:, :1].expand(1, 1)[:, :1], 2)):
+        with pytest.raises(ValueError, match="block_table"):
+            step.args(kv(table), x, n, 0.1)
+    for table, n in ((whole, 5), (whole[:, 4:], 4), (whole[:, :3], 5), (whole[2:], 3), (whole[:1].expand(5, 12), 5)):
+        with pytest.raises((TypeError, AttributeError)):  # past the check: the step has no shape
+            step.args(kv(table), x, n, 0.1)
