@@ -42,6 +42,10 @@ __global__ void __launch_bounds__(32 * kWarps) block_join_kernel(BlockJoinParams
     // a length past the tiles that the plan has of the request
     if (lane == 0 && row == 0 && g == 0 && int64_t(L) > int64_t(rq.w) * kKvTile) atomicOr(p.status, kStatusBadPlan);
     if (rq.y <= 1 || L <= 0) return;  // in one piece: already written
+    if (!plan_entry_ok(rq.x, rq.y, rq.z, p.part_cap)) {  // not attended to
+      if (lane == 0 && row == 0 && g == 0) atomicOr(p.status, kStatusBadPlan);
+      return;
+    }
     const int64_t span = int64_t(rq.z) * kKvTile;
     n = int(min(int64_t(rq.y), (int64_t(L) + span - 1) / span));  // pieces with a key
     step = int64_t(p.h_k) * p.n_q;

@@ -326,14 +326,14 @@ __global__ void __launch_bounds__(512, 1)
     b = w.x;
     const int4 rq = p.req[b];  // first partial, pieces, tiles a piece, tiles planned
     L = p.seq_lens[b];
-    const bool bad = w.w < 0 || w.w >= rq.y || (rq.y > 1 && (rq.x < 0 || int64_t(rq.x) + rq.y > p.part_cap));
+    const bool bad = w.y < 0 || w.w < 0 || w.w >= rq.y || !plan_entry_ok(rq.x, rq.y, rq.z, p.part_cap);
     if (tid == 0 && bad) atomicOr(p.status, kStatusBadPlan);
     n = p.max_q_len;
     t0 = b * n;
     rows = n * p.h_r;
     r0 = int(blockIdx.y) * C::kRows;
+    if (bad || L <= int64_t(w.y) * kKvTile) return;  // (a piece without keys: the join does not count it)
     k0 = w.y * kKvTile;
-    if (bad || L <= k0) return;  // (a piece without keys: the join does not count it)
     k_end = int(min(int64_t(L), int64_t(w.z) * kKvTile));
     if (rq.y > 1) parts = ((int64_t(rq.x) + w.w) * p.h_k + g) * rows;
   } else {

@@ -412,8 +412,7 @@ __global__ void __launch_bounds__(KF != MJ_KV_E4M3 ? kThreadsTcFp6 : kThreadsTc,
   if constexpr (BS) {
     if (active) {
       req = p.req[b];
-      const int64_t first = req.x, n = req.y;
-      if (w.w < 0 || w.w >= n || (n > 1 && (first < 0 || first + n > p.part_cap))) {
+      if (w.y < 0 || w.w < 0 || w.w >= req.y || !plan_entry_ok(req.x, req.y, req.z, p.part_cap)) {
         if (threadIdx.x == 0) atomicOr(p.status, kStatusBadPlan);
         active = false;
       }

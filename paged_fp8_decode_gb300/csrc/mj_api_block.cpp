@@ -444,6 +444,7 @@ int mj_block_attention(const mj_block_args* a, void* stream) {
   j.h_r = h_r;
   j.n_q = n_q;
   j.q_len = a->q_len;
+  j.part_cap = int(part_cap(a->slots));
   return status_of(mj::launch_block_join(j, s));
 }
 

@@ -60,6 +60,7 @@ struct BlockJoinParams {
   const int4* plan;           // per request: first partial, pieces, tiles a piece, tiles planned
   const int32_t* seq_lens;
   int h_k, h_r, n_q, q_len;
+  int part_cap;               // partials that the workspace holds of each KV head
   // prompt: unit = (token, query head), `pieces` pieces each, lying `units` rows apart
   int pieces, h_q;
   const int32_t* q_starts;

@@ -165,6 +165,12 @@ __host__ __device__ inline int prefetch_pages(int begin, int end, int depth, int
   return held <= 0 ? 0 : (held < n ? int(held) : n);
 }
 
+// The block-scaled plan's entry of a split request (first partial, pieces, tiles a piece, tiles planned): whether
+// its partials lie in a workspace of `cap`. The attention and the join skip, and report, one whose do not.
+__host__ __device__ inline bool plan_entry_ok(int first, int pieces, int each, int64_t cap) {
+  return pieces <= 1 || (first >= 0 && each > 0 && int64_t(first) + pieces <= cap);
+}
+
 // Tensor-core kernel; sets *unsupported (and launches nothing) when the
 // arguments are outside its envelope.
 cudaError_t launch_decode_tc(DecodeParams p, cudaStream_t stream, bool* unsupported);

@@ -17,6 +17,9 @@ HOST = """
 extern "C" int prefetch_pages(int begin, int end, int depth, int ppt, long long len) {
   return mj::prefetch_pages(begin, end, depth, ppt, len);
 }
+extern "C" int plan_entry_ok(int first, int pieces, int each, long long cap) {
+  return mj::plan_entry_ok(first, pieces, each, cap);
+}
 """
 
 
@@ -31,6 +34,7 @@ def bounds(tmp_path_factory):
                    ["-o", str(at / "bounds.so"), str(at / "bounds.cu")], check=True, capture_output=True, text=True)
     lib = ctypes.CDLL(str(at / "bounds.so"))
     lib.prefetch_pages.argtypes = [ctypes.c_int] * 4 + [ctypes.c_longlong]
+    lib.plan_entry_ok.argtypes = [ctypes.c_int] * 3 + [ctypes.c_longlong]
     return lib
 
 
@@ -76,3 +80,16 @@ def test_decode_refuses_a_block_table_that_ends_inside_its_last_row():
     for table, n in ((whole, 5), (whole[:, 4:], 4), (whole[:, :3], 5), (whole[2:], 3), (whole[:1].expand(5, 12), 5)):
         with pytest.raises((TypeError, AttributeError)):  # past the check: the step has no shape
             step.args(kv(table), x, n, 0.1)
+
+
+def test_plan_entries_whose_partials_the_workspace_does_not_hold(bounds):
+    for slots in (1, 7, 304):
+        cap = 4 * slots
+        for lens in ([131072], [9000] * 5 + [20], [1, 0, 3]):
+            plan = mj.mj_block_plan(np.array(lens, np.int32), len(lens), len(lens), slots)
+            for first, pieces, each, _ in plan[4 * (slots + len(lens)):].reshape(-1, 4):
+                assert bounds.plan_entry_ok(int(first), int(pieces), int(each), cap)
+        big = 2 ** 31 - 1
+        for first, pieces, each in ((-1, 2, 1), (cap - 1, 2, 1), (0, cap + 1, 1), (0, big, 1), (big, 2, 1), (big, big, 1), (0, 2, 0), (0, 2, -5)):
+            assert not bounds.plan_entry_ok(first, pieces, each, cap)
+        assert bounds.plan_entry_ok(big, 1, 0, cap) and bounds.plan_entry_ok(cap - 2, 2, 1, cap)

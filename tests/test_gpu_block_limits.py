@@ -53,3 +53,31 @@ def test_one_row_of_a_block_table_for_all_requests(h_q):
     out, lse, status = D.decode(b, q, 1, h_q)
     assert status == 0
     D.check_decode(b, q, out, lse, 1, h_q)
+
+
+# ------------------------------------------------------------------------------------------------- plans that are not this step's
+@pytest.mark.parametrize("h_q", [8, 32])
+@pytest.mark.parametrize("word,value", [(0, -1), (0, "cap"), (0, 2 ** 31 - 1), (1, 2 ** 31 - 1), (2, 0), (2, -7)])
+def test_a_plan_whose_partials_lie_outside_the_workspace(h_q, word, value):
+    """An entry of a split request that mj_block_plan does not make: the request is left out by the attention and by the join,
+    and reported."""
+    import paged_fp8_decode_gb300 as mj
+
+    b = Batch([20000, 300, 17], seed=22, page=64, block=32)
+    kv = b.kv()
+    q = D.queries(b, 3, h_q)
+    step = mj.BlockStep(max_num_seqs=3, q_len=1, h_q=h_q, h_k=2, d=128, with_lse=True)
+    plan = step.plan(b.lens, 3).clone()
+    at = 4 * (step.slots + 3)
+    assert plan[at + 1] > 1
+    plan[at + word] = 4 * step.slots - 1 if value == "cap" else value
+    step.plan_dev.copy_(plan)
+    out = torch.full((5, h_q, 128), SENTINEL, dtype=torch.bfloat16, device="cuda")
+    step.lse.fill_(SENTINEL)
+    step.run(q, out, kv, b.table_dev, b.lens_dev, 3, 128 ** -0.5)
+    assert mj.mj_workspace_status(step.workspace) == 4
+    assert (out[0] == SENTINEL).all() and (step.lse[0] == SENTINEL).all()
+    step.plan(b.lens, 3)  # and the step is as it was
+    step.run(q, out, kv, b.table_dev, b.lens_dev, 3, 128 ** -0.5)
+    assert mj.mj_workspace_status(step.workspace) == 0
+    D.check_decode(b, q, out, step.lse, 1, h_q)
