@@ -815,7 +815,7 @@ typedef struct mj_block_prompt_args {
   int num_tokens;              /* rows of q and out (0: nothing to do) */
   int max_q_len;
   int splits;
-  int h_q;                     /* query heads (a multiple of cache.h_k) */
+  int h_q;                     /* query heads (a multiple of cache.h_k, 2^20 times it at most) */
   int causal;
   float softmax_scale;
   const void* q;               /* device bf16; (t, h, c) at q[t*q_tok_stride + h*q_head_stride + c] */

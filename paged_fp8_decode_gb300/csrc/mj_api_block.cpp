@@ -25,7 +25,7 @@ constexpr int kMaxTokens = 1 << 30;
 // The least keys of a prompt's piece worth a CTA of its own. (64 tokens after 2000, 32/8 heads of 128: 1024
 // 28.7 us, 512 23.0, 320 19.8, 192 19.5; 4 chunks of 20 after 500: 12.3, 12.3, 12.6, 16.3.)
 constexpr int64_t kPromptMinKeys = 320;
-constexpr int64_t kMaxRows = 1 << 20;  // query rows of a request and KV head
+constexpr int64_t kMaxRows = 1 << 20;  // query rows of a request and KV head; of a prompt, heads of a KV head
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
@@ -480,6 +480,7 @@ int mj_block_prompt(const mj_block_prompt_args* a, void* stream) {
   st = mj_block_prompt_workspace_size(a->num_tokens, a->h_q, c.d, a->splits, &bytes);
   if (st != MJ_OK) return st;
   const int h_r = a->h_q / c.h_k;
+  if (h_r > kMaxRows) return MJ_ERR_INVALID_ARG;  // (a row's token is found by a float32 quotient, exact up to 2^21 heads)
   if (a->num_seqs > 65535 || ceil_div(int64_t(a->max_q_len) * h_r, mj::block_prompt_rows(c.d, int64_t(a->max_q_len) * h_r)) > 65535)
     return MJ_ERR_UNSUPPORTED;
   if (a->num_seqs == 0 || a->num_tokens == 0 || a->max_q_len == 0) return MJ_OK;

@@ -10,7 +10,10 @@ import pytest
 import torch
 
 import paged_fp8_decode_gb300 as mj
+from tests import test_block_host as H
 from tests.test_latent_calls_host import on_gpu
+
+no_gpu = H.no_gpu
 
 HOST = """
 #include "mj_block.h"
@@ -21,6 +24,13 @@ extern "C" int plan_entry_ok(int first, int pieces, int each, long long cap) {
   return mj::plan_entry_ok(first, pieces, each, cap);
 }
 """
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from paged_fp8_decode_gb300.build import build
+
+    build()
 
 
 @pytest.fixture(scope="module")
@@ -93,3 +103,28 @@ def test_plan_entries_whose_partials_the_workspace_does_not_hold(bounds):
         for first, pieces, each in ((-1, 2, 1), (cap - 1, 2, 1), (0, cap + 1, 1), (0, big, 1), (big, 2, 1), (big, big, 1), (0, 2, 0), (0, 2, -5)):
             assert not bounds.plan_entry_ok(first, pieces, each, cap)
         assert bounds.plan_entry_ok(big, 1, 0, cap) and bounds.plan_entry_ok(cap - 2, 2, 1, cap)
+
+
+def token_of_row(row, h_r):
+    """The prompt kernel's quotient, as it takes it."""
+    f = np.float32
+    return int((f(row) + f(0.5)) * (f(1) / f(h_r)))
+
+
+def test_the_quotient_that_finds_a_rows_token():
+    # exact up to 2^21 heads a KV head; past that it is not, and a row would be read in front of its token's
+    for h_r in list(range(1, 300)) + [2 ** 20 - 1, 2 ** 20, 2 ** 21]:
+        for row in {0, 1, h_r - 1, h_r, h_r + 1, h_r + 255, 2 * h_r - 1 if h_r < 256 else 0}:
+            assert token_of_row(row, h_r) == row // h_r
+    assert any(token_of_row(h_r - 1, h_r) != 0 for h_r in range(2 ** 23, 2 ** 23 + 100))
+
+
+@no_gpu
+def test_prompts_refuse_more_heads_a_kv_head_than_the_quotient_takes():
+    a = H.prompt(splits=1)
+    a.cache.h_k, a.num_tokens, a.max_q_len, a.num_seqs = 1, 1, 1, 1
+    for h_q, status in ((2 ** 20, (mj.MJ_ERR_CUDA, mj.MJ_ERR_UNSUPPORTED)), (2 ** 20 + 1, (mj.MJ_ERR_INVALID_ARG,)),
+                        (2 ** 23 + 2, (mj.MJ_ERR_INVALID_ARG,))):
+        a.h_q = h_q
+        a.q_tok_stride = a.out_tok_stride = h_q * 128
+        assert H.call("mj_block_prompt", a) in status
