@@ -797,7 +797,8 @@ MJ_API int mj_block_attention(const mj_block_args* args, void* stream);
  * Rows from q_starts[num_seqs] on are left as they are; a row that sees no key
  * writes 0 (LSE -inf).
  * max_q_len bounds a request's query tokens on the host and sizes the grid; query
- * tokens past it are not computed, and reported (status bit 4). splits: into how
+ * tokens past it, or past num_tokens, are not computed, and reported (status bit 4);
+ * the others see what they would without them. splits: into how
  * many pieces the keys of a row tile are cut, each piece a CTA, joined by a second
  * launch where there is more than one: any number from 1 to MJ_BLOCK_MAX_SPLITS, or
  * what mj_block_prompt_splits gives, which fills sm_count SMs where the chunks
@@ -820,7 +821,7 @@ typedef struct mj_block_prompt_args {
   float softmax_scale;
   const void* q;               /* device bf16; (t, h, c) at q[t*q_tok_stride + h*q_head_stride + c] */
   int64_t q_tok_stride, q_head_stride;  /* elements, multiples of 8 */
-  const int32_t* q_starts;     /* device [num_seqs + 1], rising from 0 */
+  const int32_t* q_starts;     /* device [num_seqs + 1], rising from 0 to at most num_tokens */
   mj_block_cache cache;
   const int32_t* block_table;
   int64_t block_table_stride, block_table_len;

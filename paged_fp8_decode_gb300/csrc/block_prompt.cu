@@ -342,13 +342,14 @@ __global__ void __launch_bounds__(512, 1)
     g = int(blockIdx.x) / p.splits;
     b = blockIdx.z;
     t0 = max(0, p.q_starts[b]);
-    n = min(p.q_starts[b + 1], p.num_tokens) - t0;
-    rows = min(n, p.max_q_len) * p.h_r;
+    n = p.q_starts[b + 1] - t0;
+    const int held = max(0, min(n, p.num_tokens - t0));  // that are rows of q
+    rows = min(held, p.max_q_len) * p.h_r;
     const int row_tiles = (rows + C::kRows - 1) / C::kRows;
-    if (n > p.max_q_len && blockIdx.x == 0 && blockIdx.y == 0) {
+    if (n > min(held, p.max_q_len) && blockIdx.x == 0 && blockIdx.y == 0) {
       if (tid == 0) atomicOr(p.status, kStatusBadPlan);
       if (p.splits > 1)  // the join passes these rows by
-        for (int64_t i = tid; i < int64_t(n - p.max_q_len) * p.h_q; i += C::kThreads)
+        for (int64_t i = tid; i < int64_t(held - p.max_q_len) * p.h_q; i += C::kThreads)
           p.l_part[(int64_t(t0) + p.max_q_len) * p.h_q + i] = -1.f;
     }
     if (int(blockIdx.y) >= row_tiles) return;

@@ -81,3 +81,45 @@ def test_a_plan_whose_partials_lie_outside_the_workspace(h_q, word, value):
     step.run(q, out, kv, b.table_dev, b.lens_dev, 3, 128 ** -0.5)
     assert mj.mj_workspace_status(step.workspace) == 0
     D.check_decode(b, q, out, step.lse, 1, h_q)
+
+
+# ------------------------------------------------------------------------------------------------- chunks past the call's rows
+@pytest.mark.parametrize("splits", [1, 3])
+@pytest.mark.parametrize("past", [1, 7, 40])
+def test_a_chunk_that_reaches_past_the_rows_keeps_its_limits(past, splits):
+    """q_starts names more query tokens than q has rows: those that there are see what they would in the whole call, and
+    the others are reported."""
+    import paged_fp8_decode_gb300 as mj
+
+    b = Batch([90, 200], seed=past)
+    kv = b.kv()
+    q = D.queries(b, 30 + 60, 8)
+    starts = up(np.array([0, 30, 90], np.int32))
+    outs, lses, codes = [], [], []
+    for T in (90, 90 - past):
+        step = mj.PromptStep(max_tokens=90, max_num_seqs=2, max_q_len=60, max_len=200, h_q=8, h_k=2, d=128, splits=splits, with_lse=True)
+        out = torch.full((90, 8, 128), SENTINEL, dtype=torch.bfloat16, device="cuda")
+        step.lse.fill_(SENTINEL)
+        mj.mj_block_prompt(step.args(q[:T], out, kv, b.table_dev, b.lens_dev, starts, 2, 128 ** -0.5))
+        outs.append(out)
+        lses.append(step.lse)
+        codes.append(mj.mj_workspace_status(step.workspace))
+    assert codes == [0, 4]
+    T = 90 - past
+    assert torch.equal(outs[0][:T], outs[1][:T]) and torch.equal(lses[0][:T], lses[1][:T])
+    assert (outs[1][T:] == SENTINEL).all() and (lses[1][T:] == SENTINEL).all()
+
+
+@pytest.mark.parametrize("splits", [1, 2])
+def test_a_request_that_begins_past_the_rows_is_reported(splits):
+    import paged_fp8_decode_gb300 as mj
+
+    b = Batch([20, 50], seed=2)
+    kv = b.kv()
+    q = D.queries(b, 20, 8)
+    step = mj.PromptStep(max_tokens=20, max_num_seqs=2, max_q_len=20, max_len=50, h_q=8, h_k=2, d=128, splits=splits, with_lse=True)
+    out = torch.full((20, 8, 128), SENTINEL, dtype=torch.bfloat16, device="cuda")
+    mj.mj_block_prompt(step.args(q, out, kv, b.table_dev, b.lens_dev, up(np.array([0, 20, 29], np.int32)), 2, 128 ** -0.5))
+    assert mj.mj_workspace_status(step.workspace) == 4
+    want, want_lse = OB.attention(q.double().cpu().numpy(), b.rows("k", 0), b.rows("v", 0), 128 ** -0.5, True)
+    D.check_rows(out.double().cpu().numpy(), step.lse.cpu().numpy(), want, want_lse, b.vmax(0), rel=0.0025, elem=0.003, lse_tol=6e-4)
