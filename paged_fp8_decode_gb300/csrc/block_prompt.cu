@@ -479,8 +479,7 @@ __global__ void __launch_bounds__(512, 1)
 #pragma unroll
       for (int u = 0; u < kAbreast; ++u) {
         const int j = jj + u * 12 * kRowsLd;
-        // (e not below 64: ck 2^ek stays above 0, and a hidden key's -inf times it -inf)
-        const int e = max(64, int(((am[u] << 16) + 0x1FFFFFu) >> 23) - 8);
+        const int e = max(1, int(((am[u] << 16) + 0x1FFFFFu) >> 23) - 8);
         const float inv = __int_as_float((254 - e) << 23);
         uint32_t hw[4], lw[4];
 #pragma unroll
@@ -523,7 +522,9 @@ __global__ void __launch_bounds__(512, 1)
     float ck;  // logits (log2 units) = S * ck * 2^ek
     {
       const uint8_t* qs = smem + C::kVf + (SPREAD ? 0 : quad * (64 * D));
-      ck = __int_as_float(int(ctl.q_exp[SPREAD ? lane : 32 * (warp - 4) + lane]) << 23) * p.scale_log2;
+      // (not below 2^-94: ck 2^ek stays above 0, and a hidden key's -inf times it -inf. |S| is below 2^26, so that
+      // the logits of a smaller ck are within 2^-36 of 0 either way)
+      ck = fmaxf(__int_as_float(int(ctl.q_exp[SPREAD ? lane : 32 * (warp - 4) + lane]) << 23) * p.scale_log2, 0x1p-94f);
       if constexpr (C::kQt) {
 #pragma unroll 4
         for (int c = 0; c < 2 * D / 64; ++c) {  // 64 codes: of hi, then of lo

@@ -123,3 +123,73 @@ def test_a_request_that_begins_past_the_rows_is_reported(splits):
     assert mj.mj_workspace_status(step.workspace) == 4
     want, want_lse = OB.attention(q.double().cpu().numpy(), b.rows("k", 0), b.rows("v", 0), 128 ** -0.5, True)
     D.check_rows(out.double().cpu().numpy(), step.lse.cpu().numpy(), want, want_lse, b.vmax(0), rel=0.0025, elem=0.003, lse_tol=6e-4)
+
+
+# ------------------------------------------------------------------------------------------------- small softmax scales
+@pytest.mark.parametrize("scale", [1e-12, 1e-20, 1e-30, 1e-38])
+@pytest.mark.parametrize("d", [128, 256])
+def test_small_softmax_scales_and_queries_of_zero(scale, d):
+    """The logits are 0 to within 1e-8: a row's output is the mean of the V that it sees, its LSE the log of their number. Hidden
+    keys stay hidden, also for queries of zero over the smallest scales."""
+    import paged_fp8_decode_gb300 as mj
+
+    new = [70, 33]
+    b = Batch([300, 33], d=d, seed=4)
+    live = (b.exps["k"] > 0) & (b.exps["k"] < 255)
+    b.exps["k"][live] = 95
+    kv = b.kv()
+    q = D.queries(b, 103, 8)
+    q[::2] = 0
+    starts = up(np.array([0, 70, 103], np.int32))
+    for h_q, splits in ((8, 1), (8, 2), (2, 1)):
+        qh = q[:, :h_q].contiguous()
+        step = mj.PromptStep(max_tokens=103, max_num_seqs=2, max_q_len=70, max_len=300, h_q=h_q, h_k=2, d=d, splits=splits, with_lse=True)
+        out = torch.empty(103, h_q, d, dtype=torch.bfloat16, device="cuda")
+        mj.mj_block_prompt(step.args(qh, out, kv, b.table_dev, b.lens_dev, starts, 2, scale))
+        got, lse = out.double().cpu().numpy(), step.lse.cpu().numpy()
+        for i, s in enumerate((slice(0, 70), slice(70, 103))):
+            want, want_lse = OB.attention(qh[s].double().cpu().numpy(), b.rows("k", i), b.rows("v", i), scale, True)
+            D.check_rows(got[s], lse[s], want, want_lse, b.vmax(i), rel=0.0025, elem=0.003, lse_tol=6e-4)
+    for h_q, q_len in ((8, 1), (8, 4), (40, 4)):  # 4, 16 and 80 rows
+        qd = D.queries(b, 2 * q_len, h_q)
+        qd[::2] = 0
+        step = mj.BlockStep(max_num_seqs=2, q_len=q_len, h_q=h_q, h_k=2, d=d, with_lse=True)
+        step.plan(b.lens, 2)
+        out = torch.full((2 * q_len + 2, h_q, d), SENTINEL, dtype=torch.bfloat16, device="cuda")
+        step.run(qd, out, kv, b.table_dev, b.lens_dev, 2, scale)
+        got = out[:2 * q_len].double().cpu().numpy().reshape(2, q_len, h_q, d)
+        lse = step.lse.cpu().numpy().reshape(2, 2, q_len, h_q // 2).transpose(0, 2, 1, 3).reshape(2, q_len, h_q)
+        for i in range(2):
+            want, want_lse = OB.attention(qd.double().cpu().numpy().reshape(2, q_len, h_q, d)[i], b.rows("k", i), b.rows("v", i), scale, True)
+            D.check_rows(got[i], lse[i], want, want_lse, b.vmax(i))
+
+
+@pytest.mark.parametrize("by", [-100, -60, 60])
+def test_small_and_large_queries_with_the_scale_that_makes_up_for_them(by):
+    """Queries of 2^by times the usual size, the softmax scale 2^-by times: the same logits, and as exact."""
+    import paged_fp8_decode_gb300 as mj
+
+    b = Batch([300, 33], seed=23)
+    kv = b.kv()
+    scale = 128 ** -0.5 * 2.0 ** -by
+    q = D.queries(b, 103, 8, size=2.0 ** by)
+    for h_q in (8, 2):
+        qh = q[:, :h_q].contiguous()
+        step = mj.PromptStep(max_tokens=103, max_num_seqs=2, max_q_len=70, max_len=300, h_q=h_q, h_k=2, d=128, with_lse=True)
+        out = torch.empty(103, h_q, 128, dtype=torch.bfloat16, device="cuda")
+        mj.mj_block_prompt(step.args(qh, out, kv, b.table_dev, b.lens_dev, up(np.array([0, 70, 103], np.int32)), 2, scale))
+        for i, s in enumerate((slice(0, 70), slice(70, 103))):
+            want, want_lse = OB.attention(qh[s].double().cpu().numpy(), b.rows("k", i), b.rows("v", i), scale, True)
+            D.check_rows(out[s].double().cpu().numpy(), step.lse[s].cpu().numpy(), want, want_lse, b.vmax(i), rel=0.0025, elem=0.003,
+                         lse_tol=6e-4)
+    for h_q, q_len in ((8, 1), (8, 4)):
+        qd = D.queries(b, 2 * q_len, h_q, size=2.0 ** by)
+        step = mj.BlockStep(max_num_seqs=2, q_len=q_len, h_q=h_q, h_k=2, d=128, with_lse=True)
+        step.plan(b.lens, 2)
+        out = torch.empty(2 * q_len, h_q, 128, dtype=torch.bfloat16, device="cuda")
+        step.run(qd, out, kv, b.table_dev, b.lens_dev, 2, scale)
+        lse = step.lse.cpu().numpy().reshape(2, 2, q_len, h_q // 2).transpose(0, 2, 1, 3).reshape(2, q_len, h_q)
+        for i in range(2):
+            s = slice(i * q_len, (i + 1) * q_len)
+            want, want_lse = OB.attention(qd[s].double().cpu().numpy(), b.rows("k", i), b.rows("v", i), scale, True)
+            D.check_rows(out[s].double().cpu().numpy(), lse[i], want, want_lse, b.vmax(i))
