@@ -65,11 +65,15 @@ int check_table(const int32_t* table, int64_t stride, int64_t len) {
   return !table || stride < 0 || len < 0 ? MJ_ERR_INVALID_ARG : (aligned(table, 4) ? MJ_OK : MJ_ERR_ALIGNMENT);
 }
 
+// The two sides. (One head's own stride is of no use: K's and V's may differ in it, and stand in any order to
+// their tokens' strides, which the attentions want alike.)
 void sides(const mj_block_cache& c, mj::BlockSide (&s)[2]) {
   s[0] = {static_cast<uint8_t*>(c.k_cache), c.k_stride_page, c.k_stride_token, c.k_stride_head, c.k_exp, c.k_exp_stride_page,
           c.k_exp_stride_head};
   s[1] = {static_cast<uint8_t*>(c.v_cache), c.v_stride_page, c.v_stride_token, c.v_stride_head, c.v_exp, c.v_exp_stride_page,
           c.v_exp_stride_head};
+  for (mj::BlockSide& x : s)
+    if (c.h_k == 1) x.sh = x.st;
 }
 
 // A plan has at most a piece a slot and one a request (each launch has a CTA for every
@@ -385,20 +389,22 @@ int mj_block_attention(const mj_block_args* a, void* stream) {
     p.q_bf16 = static_cast<const uint16_t*>(a->q);
     p.q_ts = a->q_tok_stride;
     p.q_hs = a->q_head_stride;
-    p.k_cache = static_cast<const uint8_t*>(c.k_cache);
-    p.v_cache = static_cast<const uint8_t*>(c.v_cache);
-    p.k_sp = c.k_stride_page;
-    p.k_st = c.k_stride_token;
-    p.k_sh = c.k_stride_head;
-    p.v_sp = c.v_stride_page;
-    p.v_st = c.v_stride_token;
-    p.v_sh = c.v_stride_head;
-    p.k_exp = c.k_exp;
-    p.v_exp = c.v_exp;
-    p.ke_sp = c.k_exp_stride_page;
-    p.ke_sh = c.k_exp_stride_head;
-    p.ve_sp = c.v_exp_stride_page;
-    p.ve_sh = c.v_exp_stride_head;
+    mj::BlockSide side[2];
+    sides(c, side);
+    p.k_cache = side[0].codes;
+    p.v_cache = side[1].codes;
+    p.k_sp = side[0].sp;
+    p.k_st = side[0].st;
+    p.k_sh = side[0].sh;
+    p.v_sp = side[1].sp;
+    p.v_st = side[1].st;
+    p.v_sh = side[1].sh;
+    p.k_exp = side[0].exps;
+    p.v_exp = side[1].exps;
+    p.ke_sp = side[0].esp;
+    p.ke_sh = side[0].esh;
+    p.ve_sp = side[1].esp;
+    p.ve_sh = side[1].esh;
     p.page_shift = mj::page_shift(c.page_size);
     p.block_shift = mj::page_shift(c.block);
     p.block_table = a->block_table;

@@ -193,3 +193,38 @@ def test_small_and_large_queries_with_the_scale_that_makes_up_for_them(by):
             s = slice(i * q_len, (i + 1) * q_len)
             want, want_lse = OB.attention(qd[s].double().cpu().numpy(), b.rows("k", i), b.rows("v", i), scale, True)
             D.check_rows(out[s].double().cpu().numpy(), lse[i], want, want_lse, b.vmax(i))
+
+
+# ------------------------------------------------------------------------------------------------- layouts
+def one_head(b, order):
+    """The caches of a batch of one KV head, K's rows as ``phtd``, V's as ``order``, each with its own stride of the one head."""
+    import paged_fp8_decode_gb300 as mj
+
+    def side(c, order):
+        axes = {"p": 0, "t": 1, "h": 2}
+        perm = [axes[x] for x in order[:3]] + [3]
+        return up(c.transpose(perm)).permute(*[perm.index(i) for i in range(4)])
+
+    wide = torch.zeros(b.pages, b.page, 3, b.d, dtype=torch.uint8, device="cuda")  # (one of three heads, as a slice)
+    if order == "slice":
+        wide[:, :, 1:2] = up(b.codes["v"])
+        v = wide[:, :, 1:2]
+    else:
+        v = side(b.codes["v"], order)
+    b.table_dev, b.lens_dev = up(b.table), up(b.lens)
+    return mj.BlockKV(side(b.codes["k"], "phtd"), v, up(b.exps["k"]), up(b.exps["v"]))
+
+
+@pytest.mark.parametrize("order", ["phtd", "pthd", "slice"])
+@pytest.mark.parametrize("d", [128, 256])
+def test_one_head_whatever_its_stride(order, d):
+    b = Batch([300, 77], h_k=1, d=d, page=32, block=32, seed=5)
+    b._dev = one_head(b, order)
+    for h_q, q_len in ((8, 1), (8, 4)):
+        q = D.queries(b, 2 * q_len, h_q)
+        out, lse, status = D.decode(b, q, q_len, h_q)
+        assert status == 0
+        D.check_decode(b, q, out, lse, q_len, h_q)
+    out, lse, status, q = P.run(b, [100, 77], 4)
+    assert status == 0
+    P.check(b, [100, 77], out, lse, q)
