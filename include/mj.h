@@ -635,7 +635,10 @@ MJ_API int mj_latent_attention(const mj_latent_args* args, void* stream);
  * c * 2^(e - 127), with e from MJ_BLOCK_EXP_MIN (2^-32) to MJ_BLOCK_EXP_MAX
  * (2^32); a byte outside them is read as the nearer one. Pages of 16, 32, 64 or
  * 128 tokens hold whole blocks: block is 16, 32, 64 or 128, at most page_size.
- * Alignment: caches 16 bytes, their byte strides multiples of 16.
+ * Alignment: caches 16 bytes, their byte strides multiples of 16. Pages, tokens and
+ * heads may lie in any order; the two attentions want K's and V's alike in one thing:
+ * the smaller of the token and the head stride is of the same kind in both
+ * (MJ_ERR_UNSUPPORTED otherwise; the write and the read take any two).
  * ---------------------------------------------------------------------- */
 #define MJ_BLOCK_EXP_MIN 95
 #define MJ_BLOCK_EXP_MAX 159

@@ -25,8 +25,10 @@ from .step import _flat, _hold, _rows, _tensor
 @dataclass
 class BlockKV:
     """A block-scaled cache in device memory. Pages, tokens and heads may lie in
-    any order (views of another layout); ``k_exp`` and ``v_exp`` have a column for
-    each block of a page, which sets the block: page_size / columns tokens."""
+    any order (views of another layout); attention wants K and V alike in whether
+    a token's heads or a head's tokens lie closer together. ``k_exp`` and ``v_exp``
+    have a column for each block of a page, which sets the block: page_size / columns
+    tokens."""
 
     k_cache: torch.Tensor  # uint8 [pages, page_size, h_k, d]: e4m3 codes, channels contiguous
     v_cache: torch.Tensor

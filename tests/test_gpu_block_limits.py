@@ -228,3 +228,43 @@ def test_one_head_whatever_its_stride(order, d):
     out, lse, status, q = P.run(b, [100, 77], 4)
     assert status == 0
     P.check(b, [100, 77], out, lse, q)
+
+
+@pytest.mark.parametrize("order", ["tphd", "hptd"])
+@pytest.mark.parametrize("d", [128, 256])
+def test_attention_over_tokens_or_heads_outermost(order, d):
+    b = Batch([5, 700, 64], page=32, block=16, order=order, d=d, seed=6)
+    for h_q in (8, 32):
+        q = D.queries(b, 3, h_q)
+        out, lse, status = D.decode(b, q, 1, h_q)
+        assert status == 0
+        D.check_decode(b, q, out, lse, 1, h_q)
+    out, lse, status, q = P.run(b, [5, 200, 33], 4)
+    assert status == 0
+    P.check(b, [5, 200, 33], out, lse, q)
+
+
+def test_k_and_v_in_different_orders_are_written_and_read_but_not_attended_to():
+    import paged_fp8_decode_gb300 as mj
+
+    b, k, v, slots = D.make_write([(3, 60)], seed=7)
+    kv = b.kv()
+    kv.v_cache = kv.v_cache.contiguous()  # V's heads inside its tokens, K's outside
+    D.check_write(b, k, v, slots)
+    rows = torch.empty(60, 2, 128, dtype=torch.bfloat16, device="cuda")
+    table = torch.arange(4, dtype=torch.int32, device="cuda")[None]
+    mj.mj_block_read_kv(mj.block_read_args(kv, table, up(np.array([0, 60], np.int32)), v_out=rows, first=up(np.array([3], np.int32))))
+    b.reload()
+    assert torch.equal(rows.double().cpu(), torch.from_numpy(OB.values(b.codes["v"], b.exps["v"])[:4].reshape(64, 2, 128)[3:63]))
+    lens = up(np.array([63], np.int32))
+    for h_q in (8, 32):
+        q, out = D.queries(b, 1, h_q), torch.empty(1, h_q, 128, dtype=torch.bfloat16, device="cuda")
+        step = mj.BlockStep(max_num_seqs=1, q_len=1, h_q=h_q, h_k=2, d=128)
+        step.plan(np.array([63], np.int32), 1)
+        with pytest.raises(mj.MjError) as e:
+            step.run(q, out, kv, table, lens, 1, 0.1)
+        assert e.value.status == mj.MJ_ERR_UNSUPPORTED
+    step = mj.PromptStep(max_tokens=1, max_num_seqs=1, max_q_len=1, max_len=63, h_q=8, h_k=2, d=128)
+    with pytest.raises(mj.MjError) as e:
+        step.run(q[:, :8].contiguous(), out[:, :8].contiguous(), kv, table, lens, up(np.array([0, 1], np.int32)), 1, 0.1)
+    assert e.value.status == mj.MJ_ERR_UNSUPPORTED
