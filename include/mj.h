@@ -752,12 +752,12 @@ MJ_API int mj_block_workspace_size(int slots, int q_len, int h_q, int h_k, int d
  *
  * Accuracy. Up to 8 query rows a request and KV head, rows =
  * q_len * h_q / h_k: a query enters the tensor cores as two 8-bit terms, exact down
- * to 2^-14 of the largest |q| of those rows (within 2^-22 of it below); a value's
+ * to 2^-13.8 of the largest |q| of those rows (within 2^-21.8 of it below); a value's
  * weight, softmax weight times its block's scale, as two 8-bit terms, within 2^-8
- * of itself down to 10 binades below its row's largest (below that, where such keys
- * are many, by two more terms, down to 28 binades): a row of N keys is off by at
- * most (2^-7 + N 2^-28) times its largest weight times 448. More rows: as
- * mj_block_prompt. A query that is not finite makes its row NaN; a NaN code of a
+ * of itself down to 10 binades below its row's largest w (below that, where such keys
+ * are many, by two more terms, down to 28 binades): a row of N keys whose weights
+ * add up to S is off by at most (2^-7 S + N 2^-28 w) times 448. Sums are float32 of the
+ * unrounded weights. More rows: as mj_block_prompt. A query that is not finite makes its row NaN; a NaN code of a
  * cached token reaches every row of its request, also one whose causal limit hides it.
  * Status bits (workspace): as mj_workspace_status lists them; bit 1 also for a
  * token past block_table_len, bit 4 also where a request's device length reaches
@@ -766,7 +766,7 @@ MJ_API int mj_block_workspace_size(int slots, int q_len, int h_q, int h_k, int d
  * Two calls that may run at once (other streams, two captured graphs) need a
  * workspace each. out overlaps nothing that the call reads; its rows lie apart.
  * Make one call of each head size and row count before capturing.
- * Alignment: q, block_table, seq_lens, plan, out and workspace 16 bytes.
+ * Alignment: q, plan, out and workspace 16 bytes, block_table, seq_lens and lse 4.
  * ---------------------------------------------------------------------- */
 typedef struct mj_block_args {
   int num_seqs, max_num_seqs;  /* requests; the plan's max_num_seqs */
@@ -807,12 +807,13 @@ MJ_API int mj_block_attention(const mj_block_args* args, void* stream);
  * what mj_block_prompt_splits gives, which fills sm_count SMs where the chunks
  * alone do not (max_len: the longest request).
  *
- * Accuracy: a query is exact down to 2^-10 of its row's largest |q| (within 2^-17
- * of it below); weights in fp16 relative to a running reference of their row, within 2^-12 of
+ * Accuracy: a query is exact down to 2^-9.8 of its row's largest |q| (within 2^-17.8
+ * of it below); weights in fp16 relative to a running reference of their row, within 2^-11 of
  * themselves down to 20 binades below it and 2^-31 of it lower; sums in float32. What
- * mj_block_attention says about values that are not finite, status bits,
- * workspaces, overlaps and first calls holds here.
- * Alignment: as mj_block_attention's.
+ * mj_block_attention says about queries that are not finite, status bits,
+ * workspaces, overlaps and first calls holds here; a NaN code reaches every row that
+ * sees its token, and rows of the same chunk whose causal limit hides it.
+ * Alignment: as mj_block_attention's; q_starts 4 bytes.
  * ---------------------------------------------------------------------- */
 typedef struct mj_block_prompt_args {
   int num_seqs;

@@ -712,8 +712,8 @@ __global__ void __launch_bounds__(KF != MJ_KV_E4M3 ? kThreadsTcFp6 : kThreadsTc,
         // bf16 Q as two e4m3 terms of x' = x * 2^(127 - e), e the smallest exponent
         // byte with max |x'| <= 448 over the tile's finite values: hi = e4m3(x'),
         // lo = e4m3(16 (x' - hi)). A bf16 value has 8 significant bits, hi takes the
-        // upper four and lo the rest: exact down to |x'| = 2^-6, 2^-14 of the
-        // largest, and within 2^-14 (2^-22 of it) below. A value that is not finite
+        // upper four and lo the rest: exact down to |x'| = 2^-6, 2^-13.8 of the
+        // largest or less, and within 2^-14 (2^-21.8 of it) below. A value that is not finite
         // becomes NaN codes, which reach its own row alone.
         constexpr int EPT = NR * DH;
         const int row = (xq * EPT) / D, c0 = (xq * EPT) % D;
