@@ -3,7 +3,7 @@
 //
 // A CTA takes the query rows (tokens x the heads of one KV head) of one or two
 // 128-row tiles of a request and walks their keys once, BN at a time:
-//   S = Q K^T     kind::f8f6f4, Q as two e4m3 terms (hi + lo, exact for bf16 down to 2^-10
+//   S = Q K^T     kind::f8f6f4, Q as two e4m3 terms (hi + lo, exact for bf16 down to 2^-9.8
 //                 of the row's largest), K as it lies in the cache: 128-byte swizzled by TMA
 //   P = 2^(u - m + 6) in fp16, u = t + ev: the weight on V's codes, t = S ck 2^ek, where
 //                 2^ek and 2^ev are the scales of the key's block
@@ -28,7 +28,7 @@
 // weights 700, scores 580, from their end to the softmax 350). One row tile: 1400 to 1900 cycles a step where
 // the products take 1024: softmax 900, and a step's barriers in the MMA warp. Short chunks (5 of 20 to 700
 // tokens, head size 256: 45 us): the CTA's ends, 12000 cycles to the first scores, 5000 to write the rows.
-// 64 x 4096 cached tokens, 16 and 32 rows: 133 and 136 us, 4.0 TB/s.
+// 64 x 4096 cached tokens, 16 and 32 rows: 134 and 136 us in pages of 32 (4.0 TB/s), 155 and 157 in pages of 16.
 //
 // What it took (the long chunk, us): four products at an election, their barriers waited for a step
 // ahead 864 -> 808; scores read once into registers instead of twice 1040 -> 864; Q split by twelve

@@ -12,7 +12,9 @@
 // there; its warps then take the run's (KV head, K or V) pairs in turn, each
 // warp 4 KB of the input in registers: one read of the input, one maximum
 // over the warp (over the block's warps where it takes several), one
-// write. HBM bounds it: 2 bytes read and 1 written a channel.
+// write. It cannot do without 2 bytes read and 1 written a channel; what bounds a
+// long call is how many reads are in flight (21 warps an SM of 78 registers; DRAM 38% busy in a capture),
+// a short one the chain slots, rows, maximum, exponent.
 #include <atomic>
 
 #include "kv_codec.cuh"
@@ -73,9 +75,10 @@ __device__ __noinline__ int64_t find_live(const int64_t* slots, int64_t from, in
 
 // G warps share a block of G rows_warp(D) rows. Three CTAs of 8 warps an SM, 80 registers: the
 // moves of earlier codes are a loop of their own, since few runs have them. (4 x 4096 tokens of
-// 8 heads of 128: 20.0 us, 5.0 TB/s; two CTAs of 120 registers 21.6 us; four, or half the rows a
-// warp, 18.2 us, but then 11 ragged chunks of 1..700 tokens, head size 256, which take 9.4 us
-// here, take 10.6 and 11.3, and 64 tokens 3.3 and 3.6 us in place of 3.1.)
+// 8 heads of 128: 22.8 us over inputs that L2 does not hold, 4.4 TB/s. The others in graphs of the same
+// inputs again and again, partly in L2: 19.8 us; two CTAs of 120 registers 21.6 us; four, or half the rows a
+// warp, 18.2 us, but then 11 ragged chunks of 3..701 tokens, head size 256, which take 9.0 us
+// here (12.9 where L2 does not hold them), take 10.6 and 11.3, and 64 tokens 3.3 and 3.6 us in place of 3.1.)
 template <int D, int G>
 __global__ void __launch_bounds__(32 * warps_cta(G), 24 / warps_cta(G)) block_write_kernel(BlockWriteParams p) {
   constexpr int kWarps = warps_cta(G), kRowsWarp = rows_warp(D);

@@ -1,6 +1,6 @@
 // tcgen05 decode kernel instances for the block-scaled cache (e4m3 codes): up to 8 query
-// rows (more go to the prompt's kernel, mj_api_block.cpp). 64 x 4096 tokens, 8 heads of 128: 4 rows
-// 89 us (6.0 TB/s, 0.90 of a copy's rate), 8 rows 103; 1 x 131072 tokens 47 (5.7 TB/s, start and join).
+// rows (more go to the prompt's kernel, mj_api_block.cpp). 64 x 4096 tokens, 8 heads of 128, pages of 16: 4 rows
+// 89 us (6.0 TB/s, 0.90 of a copy's rate), 8 rows 107 (103 in pages of 32); 1 x 131072 tokens 48 (5.6 TB/s, start and join).
 #include "decode_tc_kernel.cuh"
 
 namespace mj {

@@ -91,7 +91,7 @@ constexpr double kPieceTiles = 5, kTail = 0.4;
 
 // Which kernel attends: the decode kernel (keys on the tensor cores' rows, so that a few
 // query rows fill them) or the prompt's (query rows there, up to 32 of them four times over). In us, the decode
-// kernel's time first, where both were built: head size 128, 64 x 4096 tokens, 8 KV heads: 8 rows 103 and
+// kernel's time first, where both were built, pages of 32: head size 128, 64 x 4096 tokens, 8 KV heads: 8 rows 103 and
 // 133, 16 rows 184 and 133; head size 256, 4 KV heads: 8 rows 95 and 125, 12 rows 125 and 125, 16 rows 137
 // and 126; 16 rows, 1 x 65536 tokens, 37 and 21, 40 ragged requests 181 and 133.
 bool by_rows(int64_t n_q) { return n_q > 8; }

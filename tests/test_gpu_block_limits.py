@@ -335,7 +335,8 @@ def peaked(b, rows, h_q, limit, rng):
 @pytest.mark.parametrize("d", [128, 256])
 def test_peaked_rows_one_by_one(d, dtype):
     """One key has nearly all of a row's weight, so that the weight's own error is the row's: within 2^-8 (two e4m3 terms; the sum
-    takes it unrounded) or 2^-11 (fp16) of itself, the output's rounding 2^-9 or 2^-12, the logit 4e-4, in the row's 2-norm."""
+    takes it unrounded) or 2^-11 (fp16) of itself, the logit 4e-4. The output's rounding, half a step at most, is uniform in it:
+    2^-8 / sqrt(3) of the values' power of two (fp16: 2^-11), 2^-9 of the values in the 2-norm of a row of 128 (2^-12)."""
     half = 2.0 ** -9 if dtype == torch.bfloat16 else 2.0 ** -12
     rng = np.random.default_rng(d)
     b = Batch([3000, 700, 130], d=d, seed=11, spread=(-5, -5), page=32, block=32)
